@@ -179,7 +179,7 @@ def _inputs(case, seed):
         t["w_pre"] = 1.0 + normal(h, scale=0.2, dtype=torch.float32)
         t["gate"] = {"none": lambda: None,
                      "channel": lambda: normal(h, scale=0.5, dtype=torch.float32),
-                     "token": lambda: torch.rand(n, generator=gen, device=dev),
+                     "token": lambda: torch.rand(n, 1, generator=gen, device=dev),
                      "full": lambda: normal(n, h, scale=0.5)}[case["gate"]]()
         if op == "norm":
             t["x"] = normal(n, h, scale=2.0)
@@ -427,7 +427,7 @@ def _plain(s):
         return {"dyp": dyp.view(s["dyp"].shape), "dw": dw, "dx": _rows_by_slot(s["dxp"], row_of).sum(1).to(torch.bfloat16)}
     if op in ("norm", "norm_grad"):
         gate = s["gate"]
-        wide = 1.0 if gate is None else gate.float()[:, None] if case["gate"] == "token" else gate.float()
+        wide = 1.0 if gate is None else gate.float()
         rs = case["residual_scale"]
         if op == "norm":
             post, rstd_post = _rms_norm(s["y"].float(), s["w_post"])
@@ -443,7 +443,7 @@ def _plain(s):
         dpost = dres * wide
         b = dpost * s["w_post"]
         dy = s["rstd_post"][:, None] * (b - yn * (b * yn).mean(1, keepdim=True))
-        dgate = {"none": lambda: None, "channel": lambda: dgate.sum(0), "token": lambda: dgate.sum(1),
+        dgate = {"none": lambda: None, "channel": lambda: dgate.sum(0), "token": lambda: dgate.sum(1, keepdim=True),
                  "full": lambda: dgate.to(torch.bfloat16)}[case["gate"]]()
         return {"dx": (rs * dres).to(torch.bfloat16), "dy": dy.to(torch.bfloat16),
                 "dw": torch.stack([(dpost * yn).sum(0), (dn * hn).sum(0)]), "dgate": dgate}
@@ -555,8 +555,8 @@ def exact(case, seed):
         dg = total * d["y"] * r1 * d["w_post"]
         return {"dx": rs * total, "dy": r1 * up - r1 ** 3 * d["y"] * inner / hidden,
                 "dw": torch.stack([(total * gate * d["y"] * r1).sum(0), (d["dn"] * d["h"] * r2).sum(0)]),
-                "dgate": None if s["gate"] is None else dg.sum({"channel": 0, "token": 1}[case["gate"]])
-                if case["gate"] != "full" else dg}
+                "dgate": None if s["gate"] is None else dg if case["gate"] == "full"
+                else dg.sum(0) if case["gate"] == "channel" else dg.sum(1, keepdim=True)}
     inner = case["inner"]
     gate, up = s["gu"].double().split(inner, -1)
     m = s["gu"].shape[-2]
