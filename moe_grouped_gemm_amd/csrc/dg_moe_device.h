@@ -1,0 +1,135 @@
+// Device code shared by the steps around the GEMMs: BF16 vectors, sums over
+// a wave or workgroup, and the quantisation of a 128-value block.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "dg_moe_internal.h"
+
+namespace dg {
+namespace moe {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+struct F8 {
+  float v[8];
+};
+
+__device__ __forceinline__ u32x4 load16(const void* p) { return *reinterpret_cast<const u32x4*>(p); }
+__device__ __forceinline__ void store16(void* p, u32x4 v) { *reinterpret_cast<u32x4*>(p) = v; }
+
+__device__ __forceinline__ F8 unpack8(u32x4 p) {
+  F8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r.v[2 * i] = __builtin_bit_cast(float, p[i] << 16);
+    r.v[2 * i + 1] = __builtin_bit_cast(float, p[i] & 0xFFFF0000u);
+  }
+  return r;
+}
+
+// Rounded to nearest even (v_cvt_pk_bf16_f32).
+__device__ __forceinline__ u32x4 pack8(const F8& f) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bf16x2 b = __builtin_convertvector((f32x2){f.v[2 * i], f.v[2 * i + 1]}, bf16x2);
+    r[i] = __builtin_bit_cast(uint32_t, b);
+  }
+  return r;
+}
+
+__device__ __forceinline__ F8 load_f8(const float* p) {
+  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+  return F8{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
+}
+__device__ __forceinline__ void store_f8(float* p, const F8& f) {
+  *reinterpret_cast<f32x4*>(p) = (f32x4){f.v[0], f.v[1], f.v[2], f.v[3]};
+  *reinterpret_cast<f32x4*>(p + 4) = (f32x4){f.v[4], f.v[5], f.v[6], f.v[7]};
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
+// Sum over the workgroup's waves, in every lane. `scratch` holds a float a
+// wave and is free again at the next call's barrier only if the caller
+// alternates two of them.
+__device__ __forceinline__ float block_sum(float v, float* scratch, int waves) {
+  v = wave_sum(v);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  if (lane == 0) scratch[wave] = v;
+  __syncthreads();
+  float s = 0.f;
+  for (int w = 0; w < waves; ++w) s += scratch[w];
+  return s;
+}
+
+// v rotated by N lanes within each row of 16 lanes (DPP row_ror).
+template <int N>
+__device__ __forceinline__ uint32_t ror16(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + N, 0xF, 0xF, false);
+}
+// Largest over the 16 lanes of a row, in each of them.
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+  v = max(v, ror16<8>(v));
+  v = max(v, ror16<4>(v));
+  v = max(v, ror16<2>(v));
+  return max(v, ror16<1>(v));
+}
+
+// Quantises a block of 128 values held by a row of 16 lanes, 8 a lane:
+// returns the 8 codes and the block's scale, the same in all 16 lanes.
+//   scale = max(amax, 1e-4) / 448, rounded up to a power of two with E8;
+//   code  = e4m3(x / scale).
+// amax is taken as the largest bit pattern of |x|: patterns order like the
+// values, infinity above every number and NaN above infinity, so a NaN
+// anywhere gives a NaN scale. x / scale is x * (1 / scale) with one
+// correction step, q + (x - q * scale) / scale, which gives the correctly
+// rounded quotient: codes at a rounding tie come out as the division's. It
+// needs no clamp: |x| <= amax, so |x / scale| is at most 448 but for the
+// rounding of the scale (448 (1 + 2^-23)), which the conversion rounds to 448.
+template <bool E8>
+__device__ __forceinline__ u32x2 quantize_block(const F8& x, float& scale_out) {
+  uint32_t top = 0x38D1B717u;  // 1e-4f
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __builtin_bit_cast(uint32_t, x.v[i]) & 0x7FFFFFFFu);
+  top = max16(top);
+  float scale = __builtin_bit_cast(float, top) / 448.0f;
+  if constexpr (E8) {
+    // Up to a power of two: past the mantissa, then cut (finite scales only).
+    const uint32_t s = __builtin_bit_cast(uint32_t, scale);
+    if (s < 0x7F800000u) scale = __builtin_bit_cast(float, (s + 0x7FFFFFu) & 0xFF800000u);
+  }
+  scale_out = scale;
+  F8 q;
+  if (top < 0x7F800000u) {
+    const float inv = 1.0f / scale;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float t = x.v[i] * inv;
+      q.v[i] = __builtin_fmaf(__builtin_fmaf(-t, scale, x.v[i]), inv, t);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q.v[i] = x.v[i] / scale;  // 0 or NaN
+  }
+  u32x2 r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(q.v[4 * i], q.v[4 * i + 1], 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(q.v[4 * i + 2], q.v[4 * i + 3], w, true);
+    r[i] = (uint32_t)w;
+  }
+  return r;
+}
+
+}  // namespace moe
+}  // namespace dg

@@ -1,0 +1,237 @@
+// Tokens sorted by expert into the GEMMs' row layouts, moved there (BF16, or
+// quantised to the FP8 operand) and back with weights, and the gradients.
+
+#include "dg_moe_device.h"
+
+namespace dg {
+namespace moe {
+namespace {
+
+// Lanes of the wave that hold the same key as this one (`valid` ones only):
+// one ballot per key bit.
+__device__ __forceinline__ uint64_t same_key(int key, bool valid, int bits) {
+  uint64_t m = __ballot(valid);
+  for (int b = 0; b < bits; ++b) {
+    const uint64_t ones = __ballot((key >> b) & 1);
+    m &= ((key >> b) & 1) ? ones : ~ones;
+  }
+  return m;
+}
+
+// Sorting by counting, in one workgroup: the ids are counted per group, the
+// counts scanned to the groups' first rows, and the ids then taken 1024 at a
+// time in order. Within a wave equal ids are ranked by ballots; the waves
+// take turns to advance the groups' next free rows, which keeps the order.
+constexpr int SORT_THREADS = 1024;
+
+__global__ __launch_bounds__(SORT_THREADS) void sort_kernel(RouteArgs p) {
+  __shared__ int next[MAX_GROUPS];       // counts, then the next free row of each group
+  __shared__ int first[MAX_GROUPS + 1];  // first row of each group
+  __shared__ int scan[SORT_THREADS / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int G = p.num_groups, N = p.tokens * p.top_k;
+  const long long capacity = p.layout == DG_MOE_MASKED ? (long long)G * p.rows : p.rows;
+
+  for (int g = tid; g < G; g += SORT_THREADS) next[g] = 0;
+  __syncthreads();
+  for (int i = tid; i < N; i += SORT_THREADS) {
+    const int e = p.ids[i];
+    if (e >= 0 && e < G) atomicAdd(&next[e], 1);
+  }
+  __syncthreads();
+
+  int before = 0;
+  for (int g0 = 0; g0 < G; g0 += SORT_THREADS) {
+    const int g = g0 + tid;
+    const int count = g < G ? next[g] : 0;
+    const int size = p.layout == DG_MOE_CONTIGUOUS ? (count + SEGMENT - 1) / SEGMENT * SEGMENT : count;
+    int incl = size;
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(incl, d);
+      if (lane >= d) incl += v;
+    }
+    if (lane == 63) scan[wave] = incl;
+    __syncthreads();
+    int waves_before = 0, total = 0;
+    for (int w = 0; w < SORT_THREADS / 64; ++w) {
+      if (w < wave) waves_before += scan[w];
+      total += scan[w];
+    }
+    if (g < G) {
+      const int start = p.layout == DG_MOE_MASKED ? g * p.rows : before + waves_before + incl - size;
+      const int room = p.layout == DG_MOE_MASKED ? p.rows : max(p.rows - start, 0);
+      first[g] = start;
+      next[g] = start;
+      p.group_rows[g] = min(count, room);
+    }
+    before += total;
+    __syncthreads();
+  }
+  if (tid == 0) first[G] = before;
+
+  const int bits = 32 - __builtin_clz(G);
+  for (int i0 = 0; i0 < N; i0 += SORT_THREADS) {
+    const int i = i0 + tid;
+    const int e = i < N ? p.ids[i] : -1;
+    const bool valid = e >= 0 && e < G;
+    const uint64_t peers = same_key(e, valid, bits);
+    const int rank = __popcll(peers & ((1ull << lane) - 1));
+    int base = 0;
+    for (int w = 0; w < SORT_THREADS / 64; ++w) {
+      __syncthreads();
+      if (w == wave && valid) {
+        base = next[e];
+        if (rank == 0) next[e] = base + __popcll(peers);
+      }
+    }
+    if (i < N) {
+      const int row = base + rank;
+      const bool fits = p.layout == DG_MOE_MASKED ? row - e * p.rows < p.rows : row < capacity;
+      p.row_of[i] = valid && fits ? row : -1;
+    }
+  }
+  __syncthreads();
+
+  if (p.layout == DG_MOE_CONTIGUOUS) {
+    for (int r = tid; r < p.rows; r += SORT_THREADS) {
+      int lo = 0, hi = G - 1;  // last group that starts at or before r
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first[mid] <= r) lo = mid; else hi = mid - 1;
+      }
+      p.grouped_layout[r] = r >= first[lo] && r < next[lo] ? lo : -1;
+    }
+  }
+}
+
+constexpr int MOVE_THREADS = 256;
+
+// One workgroup a token: each 16-byte piece is read once and written to the
+// rows of the token's slots.
+__global__ __launch_bounds__(MOVE_THREADS) void dispatch_kernel(RouteArgs p, const uint8_t* x, uint8_t* xp) {
+  const size_t t = blockIdx.x, bytes = (size_t)p.hidden * 2;
+  const int32_t* rows = p.row_of + t * p.top_k;
+  for (size_t c = (size_t)threadIdx.x * 16; c < bytes; c += MOVE_THREADS * 16) {
+    const u32x4 v = load16(x + t * bytes + c);
+    for (int j = 0; j < p.top_k; ++j) {
+      const int r = rows[j];
+      if (r >= 0) store16(xp + (size_t)r * bytes + c, v);
+    }
+  }
+}
+
+// The same with the token quantised, 16 lanes a 128-value block.
+template <bool E8>
+__global__ __launch_bounds__(MOVE_THREADS) void dispatch_fp8_kernel(RouteArgs p, const uint16_t* x, uint8_t* q,
+                                                                    float* sfa) {
+  const size_t t = blockIdx.x, H = p.hidden;
+  const int32_t* rows = p.row_of + t * p.top_k;
+  const int blocks = p.hidden / QBLOCK, ld = align4(p.rows);
+  for (int b = threadIdx.x >> 4; b < blocks; b += MOVE_THREADS / 16) {
+    const size_t c = (size_t)b * QBLOCK + (threadIdx.x & 15) * 8;
+    float scale;
+    const u32x2 codes = quantize_block<E8>(unpack8(load16(x + t * H + c)), scale);
+    for (int j = 0; j < p.top_k; ++j) {
+      const int r = rows[j];
+      if (r < 0) continue;
+      *reinterpret_cast<u32x2*>(q + (size_t)r * H + c) = codes;
+      if ((threadIdx.x & 15) == 0) {
+        const int g = p.layout == DG_MOE_MASKED ? r / p.rows : 0;
+        sfa[((size_t)g * blocks + b) * ld + (r - g * p.rows)] = scale;
+      }
+    }
+  }
+}
+
+__global__ __launch_bounds__(MOVE_THREADS) void combine_kernel(RouteArgs p, const uint16_t* yp, const float* w,
+                                                               uint16_t* y) {
+  const size_t t = blockIdx.x, H = p.hidden;
+  const int32_t* rows = p.row_of + t * p.top_k;
+  for (size_t c = threadIdx.x * 8; c < H; c += MOVE_THREADS * 8) {
+    F8 acc = {};
+    for (int j = 0; j < p.top_k; ++j) {
+      const int r = rows[j];
+      if (r < 0) continue;
+      const float wj = w ? w[t * p.top_k + j] : 1.0f;
+      const F8 v = unpack8(load16(yp + (size_t)r * H + c));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc.v[i] = __builtin_fmaf(wj, v.v[i], acc.v[i]);
+    }
+    store16(y + t * H + c, pack8(acc));
+  }
+}
+
+__global__ __launch_bounds__(MOVE_THREADS) void combine_bwd_kernel(RouteArgs p, const uint16_t* dy,
+                                                                   const uint16_t* yp, const float* w, uint16_t* dyp,
+                                                                   float* dw) {
+  __shared__ float scratch[2][MOVE_THREADS / 64];
+  const size_t t = blockIdx.x, H = p.hidden;
+  const int32_t* rows = p.row_of + t * p.top_k;
+  for (int j = 0; j < p.top_k; ++j) {
+    const int r = rows[j];
+    float dot = 0.f;
+    if (r >= 0) {
+      const float wj = w[t * p.top_k + j];
+      for (size_t c = threadIdx.x * 8; c < H; c += MOVE_THREADS * 8) {
+        const F8 d = unpack8(load16(dy + t * H + c));
+        F8 o;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o.v[i] = wj * d.v[i];
+        store16(dyp + (size_t)r * H + c, pack8(o));
+        if (dw) {
+          const F8 v = unpack8(load16(yp + (size_t)r * H + c));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(d.v[i], v.v[i], dot);
+        }
+      }
+    }
+    if (dw) {
+      dot = block_sum(dot, scratch[j & 1], MOVE_THREADS / 64);
+      if (threadIdx.x == 0) dw[t * p.top_k + j] = dot;
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_sort(const RouteArgs& a, hipStream_t stream) {
+  hipLaunchKernelGGL(sort_kernel, dim3(1), dim3(SORT_THREADS), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_dispatch(const RouteArgs& a, const void* x, void* xp, hipStream_t stream) {
+  if (a.ids)
+    if (hipError_t e = launch_sort(a, stream)) return e;
+  if (a.tokens == 0) return hipSuccess;
+  hipLaunchKernelGGL(dispatch_kernel, dim3(a.tokens), dim3(MOVE_THREADS), 0, stream, a,
+                     static_cast<const uint8_t*>(x), static_cast<uint8_t*>(xp));
+  return hipGetLastError();
+}
+
+hipError_t launch_dispatch_fp8(const RouteArgs& a, const void* x, void* q, float* sfa, bool ue8m0,
+                               hipStream_t stream) {
+  if (a.ids)
+    if (hipError_t e = launch_sort(a, stream)) return e;
+  if (a.tokens == 0) return hipSuccess;
+  hipLaunchKernelGGL(ue8m0 ? dispatch_fp8_kernel<true> : dispatch_fp8_kernel<false>, dim3(a.tokens),
+                     dim3(MOVE_THREADS), 0, stream, a, static_cast<const uint16_t*>(x), static_cast<uint8_t*>(q),
+                     sfa);
+  return hipGetLastError();
+}
+
+hipError_t launch_combine(const RouteArgs& a, const void* yp, const float* w, void* y, hipStream_t stream) {
+  hipLaunchKernelGGL(combine_kernel, dim3(a.tokens), dim3(MOVE_THREADS), 0, stream, a,
+                     static_cast<const uint16_t*>(yp), w, static_cast<uint16_t*>(y));
+  return hipGetLastError();
+}
+
+hipError_t launch_combine_bwd(const RouteArgs& a, const void* dy, const void* yp, const float* w, void* dyp,
+                              float* dw, hipStream_t stream) {
+  hipLaunchKernelGGL(combine_bwd_kernel, dim3(a.tokens), dim3(MOVE_THREADS), 0, stream, a,
+                     static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(yp), w,
+                     static_cast<uint16_t*>(dyp), dw);
+  return hipGetLastError();
+}
+
+}  // namespace moe
+}  // namespace dg
