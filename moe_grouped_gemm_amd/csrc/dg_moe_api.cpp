@@ -48,8 +48,7 @@ dg_status plan_sizes(const dg_moe_plan* p) {
 }
 
 long long plan_workspace(const dg_moe_plan* p) {
-  (void)p;
-  return 16;
+  return 16 + sort_workspace(p->max_tokens * p->top_k, p->num_groups);
 }
 
 dg_status plan_checks(const dg_moe_plan* p, int tokens, RouteArgs& a) {

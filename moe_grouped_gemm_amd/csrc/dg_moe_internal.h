@@ -28,6 +28,8 @@ struct RouteArgs {
   int32_t* grouped_layout;
   void* workspace;
 };
+// Bytes of workspace that sorting up to `slots` slots takes.
+long long sort_workspace(int slots, int num_groups);
 hipError_t launch_sort(const RouteArgs& a, hipStream_t stream);
 hipError_t launch_dispatch(const RouteArgs& a, const void* x, void* xp, hipStream_t stream);
 hipError_t launch_dispatch_fp8(const RouteArgs& a, const void* x, void* q, float* sfa, bool ue8m0, hipStream_t stream);

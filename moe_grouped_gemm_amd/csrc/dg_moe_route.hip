@@ -1,6 +1,8 @@
 // Tokens sorted by expert into the GEMMs' row layouts, moved there (BF16, or
 // quantised to the FP8 operand) and back with weights, and the gradients.
 
+#include <algorithm>
+
 #include "dg_moe_device.h"
 
 namespace dg {
@@ -18,32 +20,73 @@ __device__ __forceinline__ uint64_t same_key(int key, bool valid, int bits) {
   return m;
 }
 
-// Sorting by counting, in one workgroup: the ids are counted per group, the
-// counts scanned to the groups' first rows, and the ids then taken 1024 at a
-// time in order. Within a wave equal ids are ranked by ballots; the waves
-// take turns to advance the groups' next free rows, which keeps the order.
+// Sorting by counting, in two passes over chunks of the slots: the first
+// counts each chunk's ids per group, the second finds from all the counts
+// where each group starts and how many of its rows come before the chunk, and
+// ranks the chunk's slots. Within a wave equal ids are ranked by ballots; the
+// waves take turns to advance the groups' next free rows, which keeps the
+// order. Bound by latency: 2 N reads and N writes of 4 bytes are nothing, so
+// chunks are as small as keeps the table of counts small (MAX_CHUNKS rows,
+// read by every workgroup of the second pass).
 constexpr int SORT_THREADS = 1024;
+constexpr int SORT_WAVES = SORT_THREADS / 64;
+constexpr int MAX_CHUNKS = 256;
 
-__global__ __launch_bounds__(SORT_THREADS) void sort_kernel(RouteArgs p) {
-  __shared__ int next[MAX_GROUPS];       // counts, then the next free row of each group
-  __shared__ int first[MAX_GROUPS + 1];  // first row of each group
-  __shared__ int scan[SORT_THREADS / 64];
+__host__ __device__ inline int chunk_slots(int slots) {
+  const int per = (slots + MAX_CHUNKS - 1) / MAX_CHUNKS;
+  return per <= SORT_THREADS ? SORT_THREADS : (per + SORT_THREADS - 1) / SORT_THREADS * SORT_THREADS;
+}
+
+__global__ __launch_bounds__(SORT_THREADS) void count_kernel(RouteArgs p, int chunk) {
+  __shared__ int count[MAX_GROUPS];
+  const int tid = threadIdx.x, G = p.num_groups, N = p.tokens * p.top_k;
+  for (int g = tid; g < G; g += SORT_THREADS) count[g] = 0;
+  __syncthreads();
+  const int begin = blockIdx.x * chunk, end = min(begin + chunk, N);
+  for (int i = begin + tid; i < end; i += SORT_THREADS) {
+    const int e = p.ids[i];
+    if (e >= 0 && e < G) atomicAdd(&count[e], 1);
+  }
+  __syncthreads();
+  int* out = static_cast<int*>(p.workspace) + (size_t)blockIdx.x * G;
+  for (int g = tid; g < G; g += SORT_THREADS) out[g] = count[g];
+}
+
+__global__ __launch_bounds__(SORT_THREADS) void rank_kernel(RouteArgs p, int chunk, int chunks) {
+  __shared__ int next[MAX_GROUPS];   // rows of the group before this chunk, then its next free row
+  __shared__ int total[MAX_GROUPS];  // rows of the group
+  __shared__ int first[MAX_GROUPS];  // first row of the group
+  __shared__ int scan[SORT_WAVES];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int G = p.num_groups, N = p.tokens * p.top_k;
-  const long long capacity = p.layout == DG_MOE_MASKED ? (long long)G * p.rows : p.rows;
+  const int* counts = static_cast<const int*>(p.workspace);
 
-  for (int g = tid; g < G; g += SORT_THREADS) next[g] = 0;
+  for (int g = tid; g < G; g += SORT_THREADS) next[g] = total[g] = 0;
   __syncthreads();
-  for (int i = tid; i < N; i += SORT_THREADS) {
-    const int e = p.ids[i];
-    if (e >= 0 && e < G) atomicAdd(&next[e], 1);
+  // The table of counts, summed over chunks: as many chunks at once as there
+  // are threads for.
+  int width = 1;
+  while (width < G && width < SORT_THREADS) width <<= 1;
+  const int slices = SORT_THREADS / width, slice = tid / width;
+  for (int g = tid & (width - 1); g < G; g += width) {
+    int before = 0, all = 0;
+#pragma unroll 4
+    for (int c = slice; c < chunks; c += slices) {
+      const int v = counts[(size_t)c * G + g];
+      all += v;
+      before += c < (int)blockIdx.x ? v : 0;
+    }
+    if (all) {
+      atomicAdd(&total[g], all);
+      atomicAdd(&next[g], before);
+    }
   }
   __syncthreads();
 
-  int before = 0;
+  int rows_before = 0;
   for (int g0 = 0; g0 < G; g0 += SORT_THREADS) {
     const int g = g0 + tid;
-    const int count = g < G ? next[g] : 0;
+    const int count = g < G ? total[g] : 0;
     const int size = p.layout == DG_MOE_CONTIGUOUS ? (count + SEGMENT - 1) / SEGMENT * SEGMENT : count;
     int incl = size;
     for (int d = 1; d < 64; d <<= 1) {
@@ -52,54 +95,53 @@ __global__ __launch_bounds__(SORT_THREADS) void sort_kernel(RouteArgs p) {
     }
     if (lane == 63) scan[wave] = incl;
     __syncthreads();
-    int waves_before = 0, total = 0;
-    for (int w = 0; w < SORT_THREADS / 64; ++w) {
+    int waves_before = 0, sum = 0;
+    for (int w = 0; w < SORT_WAVES; ++w) {
       if (w < wave) waves_before += scan[w];
-      total += scan[w];
+      sum += scan[w];
     }
     if (g < G) {
-      const int start = p.layout == DG_MOE_MASKED ? g * p.rows : before + waves_before + incl - size;
+      const int start = p.layout == DG_MOE_MASKED ? g * p.rows : rows_before + waves_before + incl - size;
       const int room = p.layout == DG_MOE_MASKED ? p.rows : max(p.rows - start, 0);
       first[g] = start;
-      next[g] = start;
-      p.group_rows[g] = min(count, room);
+      next[g] += start;
+      if (blockIdx.x == 0) p.group_rows[g] = min(count, room);
     }
-    before += total;
+    rows_before += sum;
     __syncthreads();
   }
-  if (tid == 0) first[G] = before;
 
   const int bits = 32 - __builtin_clz(G);
-  for (int i0 = 0; i0 < N; i0 += SORT_THREADS) {
+  const int begin = blockIdx.x * chunk, end = min(begin + chunk, N);
+  for (int i0 = begin; i0 < end; i0 += SORT_THREADS) {
     const int i = i0 + tid;
-    const int e = i < N ? p.ids[i] : -1;
+    const int e = i < end ? p.ids[i] : -1;
     const bool valid = e >= 0 && e < G;
     const uint64_t peers = same_key(e, valid, bits);
     const int rank = __popcll(peers & ((1ull << lane) - 1));
     int base = 0;
-    for (int w = 0; w < SORT_THREADS / 64; ++w) {
+    for (int w = 0; w < SORT_WAVES; ++w) {
       __syncthreads();
       if (w == wave && valid) {
         base = next[e];
         if (rank == 0) next[e] = base + __popcll(peers);
       }
     }
-    if (i < N) {
+    if (i < end) {
       const int row = base + rank;
-      const bool fits = p.layout == DG_MOE_MASKED ? row - e * p.rows < p.rows : row < capacity;
-      p.row_of[i] = valid && fits ? row : -1;
+      const bool fits = valid && row < (p.layout == DG_MOE_MASKED ? (e + 1) * p.rows : p.rows);
+      p.row_of[i] = fits ? row : -1;
     }
   }
-  __syncthreads();
 
   if (p.layout == DG_MOE_CONTIGUOUS) {
-    for (int r = tid; r < p.rows; r += SORT_THREADS) {
+    for (int r = blockIdx.x * SORT_THREADS + tid; r < p.rows; r += chunks * SORT_THREADS) {
       int lo = 0, hi = G - 1;  // last group that starts at or before r
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (first[mid] <= r) lo = mid; else hi = mid - 1;
       }
-      p.grouped_layout[r] = r >= first[lo] && r < next[lo] ? lo : -1;
+      p.grouped_layout[r] = r >= first[lo] && r < first[lo] + total[lo] ? lo : -1;
     }
   }
 }
@@ -194,8 +236,19 @@ __global__ __launch_bounds__(MOVE_THREADS) void combine_bwd_kernel(RouteArgs p, 
 
 }  // namespace
 
+// Enough for any number of slots up to `slots` (fewer slots may take more,
+// smaller chunks).
+long long sort_workspace(int slots, int num_groups) {
+  const int chunks = std::min((slots + SORT_THREADS - 1) / SORT_THREADS, MAX_CHUNKS);
+  return (long long)std::max(chunks, 1) * num_groups * 4;
+}
+
 hipError_t launch_sort(const RouteArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL(sort_kernel, dim3(1), dim3(SORT_THREADS), 0, stream, a);
+  const int slots = a.tokens * a.top_k, chunk = chunk_slots(slots);
+  const int chunks = std::max((slots + chunk - 1) / chunk, 1);
+  hipLaunchKernelGGL(count_kernel, dim3(chunks), dim3(SORT_THREADS), 0, stream, a, chunk);
+  if (hipError_t e = hipGetLastError()) return e;
+  hipLaunchKernelGGL(rank_kernel, dim3(chunks), dim3(SORT_THREADS), 0, stream, a, chunk, chunks);
   return hipGetLastError();
 }
 
