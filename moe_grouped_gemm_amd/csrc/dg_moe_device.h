@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "dg_moe_internal.h"
 
 namespace dg {
@@ -15,6 +17,20 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+template <int I, int N, class F>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    static_for<I + 1, N>(f);
+  }
+}
+
+// Streaming stores: the line is not kept in L2 for its own sake.
+template <class T>
+__device__ __forceinline__ void store_stream(void* p, T v) {
+  __builtin_nontemporal_store(v, reinterpret_cast<T*>(p));
+}
 
 struct F8 {
   float v[8];
@@ -77,6 +93,11 @@ template <int N>
 __device__ __forceinline__ uint32_t ror16(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + N, 0xF, 0xF, false);
 }
+// Lane N of each row of 16 lanes, in all of them (DPP row_newbcast).
+template <int N>
+__device__ __forceinline__ int bcast16(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, 0x150 + N, 0xF, 0xF, false);
+}
 // Largest over the 16 lanes of a row, in each of them.
 __device__ __forceinline__ uint32_t max16(uint32_t v) {
   v = max(v, ror16<8>(v));
@@ -85,33 +106,38 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
   return max(v, ror16<1>(v));
 }
 
-// Quantises a block of 128 values held by a row of 16 lanes, 8 a lane:
-// returns the 8 codes and the block's scale, the same in all 16 lanes.
-//   scale = max(amax, 1e-4) / 448, rounded up to a power of two with E8;
-//   code  = e4m3(x / scale).
-// amax is taken as the largest bit pattern of |x|: patterns order like the
-// values, infinity above every number and NaN above infinity, so a NaN
-// anywhere gives a NaN scale. x / scale is x * (1 / scale) with one
-// correction step, q + (x - q * scale) / scale, which gives the correctly
-// rounded quotient: codes at a rounding tie come out as the division's. It
-// needs no clamp: |x| <= amax, so |x / scale| is at most 448 but for the
-// rounding of the scale (448 (1 + 2^-23)), which the conversion rounds to 448.
-template <bool E8>
-__device__ __forceinline__ u32x2 quantize_block(const F8& x, float& scale_out) {
-  uint32_t top = 0x38D1B717u;  // 1e-4f
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu; }
+__device__ __forceinline__ uint32_t abs_top(const F8& x) {
+  uint32_t top = abs_bits(x.v[0]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __builtin_bit_cast(uint32_t, x.v[i]) & 0x7FFFFFFFu);
-  top = max16(top);
-  float scale = __builtin_bit_cast(float, top) / 448.0f;
+  for (int i = 1; i < 8; ++i) top = max(top, abs_bits(x.v[i]));
+  return top;
+}
+
+// The scale of a 128-value block from the largest bit pattern of its |x|:
+//   scale = max(amax, 1e-4) / 448, rounded up to a power of two with E8.
+// Patterns order like the values, infinity above every number and NaN above
+// infinity, so a NaN anywhere gives a NaN scale.
+template <bool E8>
+__device__ __forceinline__ float block_scale(uint32_t top) {
+  const float scale = __builtin_bit_cast(float, max(top, 0x38D1B717u)) / 448.0f;  // 1e-4f
   if constexpr (E8) {
     // Up to a power of two: past the mantissa, then cut (finite scales only).
     const uint32_t s = __builtin_bit_cast(uint32_t, scale);
-    if (s < 0x7F800000u) scale = __builtin_bit_cast(float, (s + 0x7FFFFFu) & 0xFF800000u);
+    if (s < 0x7F800000u) return __builtin_bit_cast(float, (s + 0x7FFFFFu) & 0xFF800000u);
   }
-  scale_out = scale;
+  return scale;
+}
+
+// E4M3 codes of 8 values over their block's scale. x / scale is x * (1 / scale)
+// with one correction step, q + (x - q * scale) / scale, which gives the
+// correctly rounded quotient: codes at a rounding tie come out as the
+// division's. It needs no clamp: |x| <= amax, so |x / scale| is at most 448
+// but for the rounding of the scale (448 (1 + 2^-23)), which the conversion
+// rounds to 448.
+__device__ __forceinline__ u32x2 quantize8(const F8& x, uint32_t top, float scale, float inv) {
   F8 q;
   if (top < 0x7F800000u) {
-    const float inv = 1.0f / scale;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float t = x.v[i] * inv;
@@ -129,6 +155,14 @@ __device__ __forceinline__ u32x2 quantize_block(const F8& x, float& scale_out) {
     r[i] = (uint32_t)w;
   }
   return r;
+}
+
+// A block held by a row of 16 lanes, 8 values a lane.
+template <bool E8>
+__device__ __forceinline__ u32x2 quantize_row(const F8& x, float& scale) {
+  const uint32_t top = max16(abs_top(x));
+  scale = block_scale<E8>(top);
+  return quantize8(x, top, scale, 1.0f / scale);
 }
 
 }  // namespace moe

@@ -45,7 +45,7 @@ __global__ __launch_bounds__(GLU_THREADS) void swiglu_fp8_kernel(GluArgs p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) a.v[i] = gate.v[i] * sigmoid(gate.v[i]) * up.v[i];
     float scale;
-    *reinterpret_cast<u32x2*>(p.q + row * I + c) = quantize_block<E8>(a, scale);
+    *reinterpret_cast<u32x2*>(p.q + row * I + c) = quantize_row<E8>(a, scale);
     if ((threadIdx.x & 15) == 0) p.sfa[((size_t)g * blocks + b) * ld + r] = scale;
   }
 }

@@ -148,39 +148,66 @@ __global__ __launch_bounds__(SORT_THREADS) void rank_kernel(RouteArgs p, int chu
 
 constexpr int MOVE_THREADS = 256;
 
-// One workgroup a token: each 16-byte piece is read once and written to the
-// rows of the token's slots.
-__global__ __launch_bounds__(MOVE_THREADS) void dispatch_kernel(RouteArgs p, const uint8_t* x, uint8_t* xp) {
-  const size_t t = blockIdx.x, bytes = (size_t)p.hidden * 2;
-  const int32_t* rows = p.row_of + t * p.top_k;
-  for (size_t c = (size_t)threadIdx.x * 16; c < bytes; c += MOVE_THREADS * 16) {
-    const u32x4 v = load16(x + t * bytes + c);
-    for (int j = 0; j < p.top_k; ++j) {
-      const int r = rows[j];
-      if (r >= 0) store16(xp + (size_t)r * bytes + c, v);
+// How a token's values arrive in its rows: copied, or quantised with float32
+// or power-of-two scales.
+enum { MOVE_BF16 = 0, MOVE_FP8 = 1, MOVE_FP8_E8 = 2 };
+
+struct MoveArgs {
+  const uint16_t* x;
+  uint8_t* out;  // rows of BF16 or E4M3
+  float* sfa;    // quantised only
+};
+
+// Block b (128 values) of token t to the rows of up to 16 slots: 16 lanes, 8
+// values each; lane l16 of the 16 has the row of slot l16 or -1.
+template <int MODE>
+__device__ __forceinline__ void put_block(const RouteArgs& p, const MoveArgs& m, u32x4 raw, int b, int l16, int row,
+                                          int slots) {
+  constexpr int BYTES = MODE == MOVE_BF16 ? 2 : 1;
+  const size_t offset = ((size_t)b * QBLOCK + l16 * 8) * BYTES, stride = (size_t)p.hidden * BYTES;
+  u32x2 codes;
+  if constexpr (MODE != MOVE_BF16) {
+    float scale;
+    codes = quantize_row<MODE == MOVE_FP8_E8>(unpack8(raw), scale);
+    // Lane l16 leaves the scale of slot l16.
+    if (row >= 0) {
+      const int blocks = p.hidden / QBLOCK, ld = align4(p.rows);
+      const int g = p.layout == DG_MOE_MASKED ? row / p.rows : 0;
+      m.sfa[((size_t)g * blocks + b) * ld + (row - g * p.rows)] = scale;
     }
   }
+  static_for<0, 16>([&](auto J) {
+    constexpr int j = decltype(J)::value;
+    if (j >= slots) return;
+    const int r = bcast16<j>(row);
+    if (r < 0) return;
+    if constexpr (MODE == MOVE_BF16) store_stream(m.out + (size_t)r * stride + offset, raw);
+    else store_stream(m.out + (size_t)r * stride + offset, codes);
+  });
 }
 
-// The same with the token quantised, 16 lanes a 128-value block.
-template <bool E8>
-__global__ __launch_bounds__(MOVE_THREADS) void dispatch_fp8_kernel(RouteArgs p, const uint16_t* x, uint8_t* q,
-                                                                    float* sfa) {
-  const size_t t = blockIdx.x, H = p.hidden;
-  const int32_t* rows = p.row_of + t * p.top_k;
-  const int blocks = p.hidden / QBLOCK, ld = align4(p.rows);
-  for (int b = threadIdx.x >> 4; b < blocks; b += MOVE_THREADS / 16) {
-    const size_t c = (size_t)b * QBLOCK + (threadIdx.x & 15) * 8;
-    float scale;
-    const u32x2 codes = quantize_block<E8>(unpack8(load16(x + t * H + c)), scale);
-    for (int j = 0; j < p.top_k; ++j) {
-      const int r = rows[j];
-      if (r < 0) continue;
-      *reinterpret_cast<u32x2*>(q + (size_t)r * H + c) = codes;
-      if ((threadIdx.x & 15) == 0) {
-        const int g = p.layout == DG_MOE_MASKED ? r / p.rows : 0;
-        sfa[((size_t)g * blocks + b) * ld + (r - g * p.rows)] = scale;
-      }
+// Tokens to rows: 16 lanes a block of 128 values, read (and quantised) once
+// and written to the rows of the token's slots. Bound by memory, mostly
+// writes. Each XCD takes a contiguous range of tokens: the scales of a
+// group's consecutive rows, which lie side by side in sfa, then meet in one
+// L2, and as the codes are stored past it, stay there until their lines are
+// full.
+template <int MODE>
+__global__ __launch_bounds__(MOVE_THREADS) void dispatch_kernel(RouteArgs p, MoveArgs m) {
+  const int blocks = p.hidden / QBLOCK, l16 = threadIdx.x & 15;
+  const int tokens_per = (p.tokens + 7) / 8;
+  const int xcd = blockIdx.x & 7;
+  const int t1 = min((xcd + 1) * tokens_per, p.tokens);
+  // Block i of the XCD's tokens; a grid at its cap goes round again.
+  const long long end = (long long)max(t1 - xcd * tokens_per, 0) * blocks;
+  for (long long i = (long long)(blockIdx.x >> 3) * (MOVE_THREADS / 16) + (threadIdx.x >> 4); i < end;
+       i += (long long)(gridDim.x >> 3) * (MOVE_THREADS / 16)) {
+    const int t = xcd * tokens_per + (int)(i / blocks), b = (int)(i % blocks);
+    const u32x4 raw = load16(m.x + (size_t)t * p.hidden + b * QBLOCK + l16 * 8);
+    for (int j0 = 0; j0 < p.top_k; j0 += 16) {
+      const int slots = min(p.top_k - j0, 16);
+      const int row = l16 < slots ? p.row_of[(size_t)t * p.top_k + j0 + l16] : -1;
+      put_block<MODE>(p, m, raw, b, l16, row, slots);
     }
   }
 }
@@ -252,24 +279,30 @@ hipError_t launch_sort(const RouteArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_dispatch(const RouteArgs& a, const void* x, void* xp, hipStream_t stream) {
+namespace {
+
+template <int MODE>
+hipError_t launch_move(const RouteArgs& a, const MoveArgs& m, hipStream_t stream) {
   if (a.ids)
     if (hipError_t e = launch_sort(a, stream)) return e;
   if (a.tokens == 0) return hipSuccess;
-  hipLaunchKernelGGL(dispatch_kernel, dim3(a.tokens), dim3(MOVE_THREADS), 0, stream, a,
-                     static_cast<const uint8_t*>(x), static_cast<uint8_t*>(xp));
+  const long long groups = (long long)((a.tokens + 7) / 8) * (a.hidden / QBLOCK);
+  const int per_xcd = (int)std::min<long long>((groups + MOVE_THREADS / 16 - 1) / (MOVE_THREADS / 16), 1 << 20);
+  hipLaunchKernelGGL(dispatch_kernel<MODE>, dim3(per_xcd * 8), dim3(MOVE_THREADS), 0, stream, a, m);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_dispatch(const RouteArgs& a, const void* x, void* xp, hipStream_t stream) {
+  const MoveArgs m{static_cast<const uint16_t*>(x), static_cast<uint8_t*>(xp), nullptr};
+  return launch_move<MOVE_BF16>(a, m, stream);
 }
 
 hipError_t launch_dispatch_fp8(const RouteArgs& a, const void* x, void* q, float* sfa, bool ue8m0,
                                hipStream_t stream) {
-  if (a.ids)
-    if (hipError_t e = launch_sort(a, stream)) return e;
-  if (a.tokens == 0) return hipSuccess;
-  hipLaunchKernelGGL(ue8m0 ? dispatch_fp8_kernel<true> : dispatch_fp8_kernel<false>, dim3(a.tokens),
-                     dim3(MOVE_THREADS), 0, stream, a, static_cast<const uint16_t*>(x), static_cast<uint8_t*>(q),
-                     sfa);
-  return hipGetLastError();
+  const MoveArgs m{static_cast<const uint16_t*>(x), static_cast<uint8_t*>(q), sfa};
+  return ue8m0 ? launch_move<MOVE_FP8_E8>(a, m, stream) : launch_move<MOVE_FP8>(a, m, stream);
 }
 
 hipError_t launch_combine(const RouteArgs& a, const void* yp, const float* w, void* y, hipStream_t stream) {
