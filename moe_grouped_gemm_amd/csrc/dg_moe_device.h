@@ -69,15 +69,27 @@ __device__ __forceinline__ void store_f8(float* p, const F8& f) {
   *reinterpret_cast<f32x4*>(p + 4) = (f32x4){f.v[4], f.v[5], f.v[6], f.v[7]};
 }
 
+// Sum over the wave, in every lane: rotations within each row of 16 lanes,
+// then the four rows' sums as scalars.
+template <int N>
+__device__ __forceinline__ float add_ror16(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x120 + N, 0xF, 0xF,
+                                                                   false));
+}
 __device__ __forceinline__ float wave_sum(float v) {
+  v = add_ror16<8>(v);
+  v = add_ror16<4>(v);
+  v = add_ror16<2>(v);
+  v = add_ror16<1>(v);
+  float row[4];
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-  return v;
+  for (int i = 0; i < 4; ++i)
+    row[i] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 16 * i));
+  return (row[0] + row[1]) + (row[2] + row[3]);
 }
 
 // Sum over the workgroup's waves, in every lane. `scratch` holds a float a
-// wave and is free again at the next call's barrier only if the caller
-// alternates two of them.
+// wave and may be written again once every wave has passed a later barrier.
 __device__ __forceinline__ float block_sum(float v, float* scratch, int waves) {
   v = wave_sum(v);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;

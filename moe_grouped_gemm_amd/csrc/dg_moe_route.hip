@@ -309,51 +309,96 @@ __global__ __launch_bounds__(SMALL_THREADS) void small_kernel(RouteArgs p, MoveA
   }
 }
 
+// Rows back to tokens: a thread sums 8 columns of a token over its slots, the
+// rows of 8 slots on their way at once. Bound by memory: every row is read
+// once. A row of values is spread over workgroups too (`parts` of them), so
+// that a few hundred tokens fill the device.
+constexpr int AHEAD = 8;
+
 __global__ __launch_bounds__(MOVE_THREADS) void combine_kernel(RouteArgs p, const uint16_t* yp, const float* w,
-                                                               uint16_t* y) {
-  const size_t t = blockIdx.x, H = p.hidden;
-  const int32_t* rows = p.row_of + t * p.top_k;
-  for (size_t c = threadIdx.x * 8; c < H; c += MOVE_THREADS * 8) {
+                                                               uint16_t* y, uint32_t parts, uint32_t items) {
+  const int lane = threadIdx.x & 63;
+  for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const uint32_t t = item / parts, c = ((item - t * parts) * blockDim.x + threadIdx.x) * 8;
+    const bool inside = c < (uint32_t)p.hidden;
+    const int32_t mine = lane < p.top_k ? p.row_of[(size_t)t * p.top_k + lane] : -1;
+    const float weight = mine >= 0 ? (w ? w[(size_t)t * p.top_k + lane] : 1.0f) : 0.0f;
     F8 acc = {};
-    for (int j = 0; j < p.top_k; ++j) {
-      const int r = rows[j];
-      if (r < 0) continue;
-      const float wj = w ? w[t * p.top_k + j] : 1.0f;
-      const F8 v = unpack8(load16(yp + (size_t)r * H + c));
+    for (int j0 = 0; j0 < p.top_k; j0 += AHEAD) {
+      u32x4 v[AHEAD];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc.v[i] = __builtin_fmaf(wj, v.v[i], acc.v[i]);
+      for (int j = 0; j < AHEAD; ++j) {
+        v[j] = (u32x4){0, 0, 0, 0};
+        const int r = __builtin_amdgcn_readlane(mine, j0 + j);  // top_k <= 32: -1 past it
+        if (r >= 0 && inside) v[j] = load16(yp + (size_t)r * p.hidden + c);
+      }
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        const float wj = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, weight), j0 + j));
+        const F8 f = unpack8(v[j]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc.v[i] = __builtin_fmaf(wj, f.v[i], acc.v[i]);
+      }
     }
-    store16(y + t * H + c, pack8(acc));
+    if (inside) store16(y + (size_t)t * p.hidden + c, pack8(acc));
   }
 }
 
-__global__ __launch_bounds__(MOVE_THREADS) void combine_bwd_kernel(RouteArgs p, const uint16_t* dy,
-                                                                   const uint16_t* yp, const float* w, uint16_t* dyp,
-                                                                   float* dw) {
-  __shared__ float scratch[2][MOVE_THREADS / 64];
+// Its gradient: a workgroup a token, the token's gradient read once per 8
+// slots, their rows on the way at once. Bound by memory (rows read, rows
+// written); the sums for the weights' gradients stay in registers.
+constexpr int BWD_THREADS = 512;
+
+__global__ __launch_bounds__(BWD_THREADS) void combine_bwd_kernel(RouteArgs p, const uint16_t* dy, const uint16_t* yp,
+                                                                  const float* w, uint16_t* dyp, float* dw) {
+  __shared__ float scratch[2][BWD_THREADS / 64][AHEAD];
   const size_t t = blockIdx.x, H = p.hidden;
-  const int32_t* rows = p.row_of + t * p.top_k;
-  for (int j = 0; j < p.top_k; ++j) {
-    const int r = rows[j];
-    float dot = 0.f;
-    if (r >= 0) {
-      const float wj = w[t * p.top_k + j];
-      for (size_t c = threadIdx.x * 8; c < H; c += MOVE_THREADS * 8) {
-        const F8 d = unpack8(load16(dy + t * H + c));
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int32_t mine = lane < p.top_k ? p.row_of[t * p.top_k + lane] : -1;
+  const float weight = mine >= 0 ? w[t * p.top_k + lane] : 0.0f;
+  for (int j0 = 0; j0 < p.top_k; j0 += AHEAD) {
+    float dot[AHEAD] = {};
+    int r[AHEAD];
+    float wj[AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      r[j] = __builtin_amdgcn_readlane(mine, j0 + j);
+      wj[j] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, weight), j0 + j));
+    }
+    for (size_t c = threadIdx.x * 8; c < H; c += blockDim.x * 8) {
+      u32x4 v[AHEAD];
+      const u32x4 raw = load16(dy + t * H + c);
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        v[j] = (u32x4){0, 0, 0, 0};
+        if (r[j] >= 0 && dw) v[j] = load16(yp + (size_t)r[j] * H + c);
+      }
+      const F8 d = unpack8(raw);
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        if (r[j] < 0) continue;
+        const F8 f = unpack8(v[j]);
         F8 o;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o.v[i] = wj * d.v[i];
-        store16(dyp + (size_t)r * H + c, pack8(o));
-        if (dw) {
-          const F8 v = unpack8(load16(yp + (size_t)r * H + c));
-#pragma unroll
-          for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(d.v[i], v.v[i], dot);
+        for (int i = 0; i < 8; ++i) {
+          o.v[i] = wj[j] * d.v[i];
+          dot[j] = __builtin_fmaf(d.v[i], f.v[i], dot[j]);
         }
+        store_stream(dyp + (size_t)r[j] * H + c, pack8(o));
       }
     }
-    if (dw) {
-      dot = block_sum(dot, scratch[j & 1], MOVE_THREADS / 64);
-      if (threadIdx.x == 0) dw[t * p.top_k + j] = dot;
+    if (!dw) continue;
+    float(*s)[AHEAD] = scratch[(j0 / AHEAD) & 1];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      const float sum = wave_sum(dot[j]);
+      if (lane == j) s[wave][j] = sum;
+    }
+    __syncthreads();
+    if (wave == 0 && lane < AHEAD && j0 + lane < p.top_k) {
+      float sum = 0.f;
+      for (int i = 0; i < waves; ++i) sum += s[i][lane];
+      dw[t * p.top_k + j0 + lane] = sum;
     }
   }
 }
@@ -413,15 +458,32 @@ hipError_t launch_dispatch_fp8(const RouteArgs& a, const void* x, void* q, float
   return ue8m0 ? launch_move<MOVE_FP8_E8>(a, m, stream) : launch_move<MOVE_FP8>(a, m, stream);
 }
 
+namespace {
+
+// Threads (a multiple of 64 up to `most`) that share `pieces` of work evenly:
+// the fewest idle ones, and of those the most threads.
+int even_threads(int pieces, int most) {
+  int best = 64;
+  auto idle = [&](int n) { return (pieces + n - 1) / n * n - pieces; };
+  for (int n = 128; n <= most; n += 64)
+    if (idle(n) <= idle(best)) best = n;
+  return best;
+}
+
+}  // namespace
+
 hipError_t launch_combine(const RouteArgs& a, const void* yp, const float* w, void* y, hipStream_t stream) {
-  hipLaunchKernelGGL(combine_kernel, dim3(a.tokens), dim3(MOVE_THREADS), 0, stream, a,
-                     static_cast<const uint16_t*>(yp), w, static_cast<uint16_t*>(y));
+  const int threads = even_threads(a.hidden / 8, MOVE_THREADS);
+  const uint32_t parts = (a.hidden / 8 + threads - 1) / threads;
+  const uint32_t items = parts * (uint32_t)a.tokens;  // below 2^31: tokens take less than 2^40 bytes
+  hipLaunchKernelGGL(combine_kernel, dim3(std::min(items, 1u << 22)), dim3(threads), 0, stream, a,
+                     static_cast<const uint16_t*>(yp), w, static_cast<uint16_t*>(y), parts, items);
   return hipGetLastError();
 }
 
 hipError_t launch_combine_bwd(const RouteArgs& a, const void* dy, const void* yp, const float* w, void* dyp,
                               float* dw, hipStream_t stream) {
-  hipLaunchKernelGGL(combine_bwd_kernel, dim3(a.tokens), dim3(MOVE_THREADS), 0, stream, a,
+  hipLaunchKernelGGL(combine_bwd_kernel, dim3(a.tokens), dim3(even_threads(a.hidden / 8, BWD_THREADS)), 0, stream, a,
                      static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(yp), w,
                      static_cast<uint16_t*>(dyp), dw);
   return hipGetLastError();
