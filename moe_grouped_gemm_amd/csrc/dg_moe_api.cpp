@@ -243,7 +243,7 @@ dg_status dg_moe_block_norm(const void* x, const void* y, const float* post_weig
 
 long long dg_moe_block_norm_workspace_bytes(int tokens, int hidden) {
   if (norm_sizes(tokens, hidden, DG_MOE_GATE_NONE) != DG_OK) return -1;
-  return 16 + (long long)norm_bwd_grid(tokens, hidden) * 3 * hidden * 4;
+  return 16 + (long long)norm_bwd_grid(tokens) * 2 * hidden * 4;
 }
 
 dg_status dg_moe_block_norm_bwd(const void* dh, const void* dn, const void* h, const void* y,

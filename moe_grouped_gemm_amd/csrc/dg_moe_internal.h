@@ -81,12 +81,12 @@ struct NormBwdArgs {
   float* dpost;
   void* dgate;
   float* dpre;
-  float* partial;       // [grid][3][hidden]: dpost, dgate (channel), dpre
+  float* partial;       // [grid][2][hidden]: sums over rows of dH yn and dn hn
   float residual_scale;
   int tokens, hidden;
 };
 // Workgroups of the gradient's row loop (and rows of its partial sums).
-int norm_bwd_grid(int tokens, int hidden);
+int norm_bwd_grid(int tokens);
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t stream);
 hipError_t launch_block_norm_bwd(const NormBwdArgs& a, hipStream_t stream);
 

@@ -1,5 +1,15 @@
 // The norms before and after a block, fused with its gate and the residual
 // scale, and their gradient.
+//
+// A row is held in registers by a team of 1 to 16 waves, VPT pieces of 8
+// columns a lane; a workgroup holds as many teams as fit 1024 threads, and
+// takes rows in turn. Column vectors (weights, a channel gate) are the same
+// for every row: with one piece a lane they stay in registers for all of the
+// workgroup's rows (read per row they would be more L2 traffic than the rows
+// themselves: 3 x 4 bytes a column against 2 x 2). The next row's loads are
+// issued before a row is worked on, so the two sums a row needs (each a wave
+// sum, and through LDS where the team has more waves) run under them. Bound by
+// memory: every activation is read once and written once.
 
 #include <algorithm>
 #include <type_traits>
@@ -11,208 +21,363 @@ namespace moe {
 namespace {
 
 constexpr int MAX_THREADS = 1024;
+constexpr int MAX_WAVES = MAX_THREADS / 64;
 
-// Gate values of 8 columns of a row (column gates: `channel` already holds them).
-__device__ __forceinline__ F8 gate8(const void* gate, int kind, size_t t, size_t c, size_t hidden) {
-  if (kind == DG_MOE_GATE_CHANNEL) return load_f8(static_cast<const float*>(gate) + c);
-  if (kind == DG_MOE_GATE_FULL) return unpack8(load16(static_cast<const uint16_t*>(gate) + t * hidden + c));
-  const float v = kind == DG_MOE_GATE_TOKEN ? static_cast<const float*>(gate)[t] : 1.0f;
-  return F8{{v, v, v, v, v, v, v, v}};
+// How a workgroup shares rows: teams of `waves` waves.
+struct TeamShape {
+  int waves, teams, vpt;
+  int threads() const { return waves * teams * 64; }
+};
+
+TeamShape team_shape(int hidden) {
+  const int pieces = hidden / 8;
+  const int vpt = pieces <= 1024 ? 1 : pieces <= 2048 ? 2 : 4;
+  const int waves = ((pieces + vpt - 1) / vpt + 63) / 64;
+  return {waves, MAX_WAVES / waves, vpt};
 }
 
-// One workgroup a row, held in registers: VPT pieces of 8 columns a thread.
+// Where this thread stands.
+struct Team {
+  int waves, first_wave, lane_in_team;
+  int team, teams;
+};
+__device__ __forceinline__ Team team_of(int waves) {
+  const int wave = threadIdx.x >> 6, team = wave / waves;
+  return {waves, team * waves, (int)threadIdx.x - team * waves * 64, team, (int)(blockDim.x >> 6) / waves};
+}
+
+// Sum over the team, in every lane. Every wave of the workgroup calls it the
+// same number of times; `scratch` may be written again after a later barrier.
+__device__ __forceinline__ float team_sum(float v, const Team& tm, float* scratch) {
+  v = wave_sum(v);
+  if (tm.waves == 1) return v;
+  if ((threadIdx.x & 63) == 0) scratch[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float s = 0.f;
+  for (int w = 0; w < tm.waves; ++w) s += scratch[tm.first_wave + w];
+  return s;
+}
+
+__device__ __forceinline__ F8 splat(float v) { return F8{{v, v, v, v, v, v, v, v}}; }
+
+// A row's pieces as loaded.
 template <int VPT>
-__global__ __launch_bounds__(MAX_THREADS) void block_norm_kernel(NormArgs p) {
-  __shared__ float scratch[2][MAX_THREADS / 64];
-  const size_t t = blockIdx.x, H = p.hidden;
-  const int waves = blockDim.x >> 6;
-  const float inv_hidden = 1.0f / (float)p.hidden;
-  F8 h[VPT];
-  auto column = [&](int i) { return ((size_t)i * blockDim.x + threadIdx.x) * 8; };
-  if (p.y) {
-    F8 y[VPT];
-    float rstd = 1.0f;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      y[i] = F8{};
-      if (column(i) < H) y[i] = unpack8(load16(p.y + t * H + column(i)));
-    }
-    if (p.post_weight) {
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(y[i].v[e], y[i].v[e], ss);
-      rstd = rsqrtf(block_sum(ss, scratch[0], waves) * inv_hidden + p.eps);
-      if (p.rstd_post && threadIdx.x == 0) p.rstd_post[t] = rstd;
-    }
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      h[i] = F8{};
-      if (column(i) < H) {
-        const F8 x = unpack8(load16(p.x + t * H + column(i)));
-        const F8 gate = gate8(p.gate, p.gate_kind, t, column(i), H);
-        F8 w = {{1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f}};
-        if (p.post_weight) w = load_f8(p.post_weight + column(i));
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          h[i].v[e] = __builtin_fmaf(p.residual_scale, x.v[e], gate.v[e] * (y[i].v[e] * rstd * w.v[e]));
-        store16(p.h + t * H + column(i), pack8(h[i]));
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      h[i] = F8{};
-      if (column(i) < H) h[i] = unpack8(load16(p.x + t * H + column(i)));
-    }
-  }
-  if (!p.n) return;
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < VPT; ++i)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(h[i].v[e], h[i].v[e], ss);
-  const float rstd = rsqrtf(block_sum(ss, scratch[1], waves) * inv_hidden + p.eps);
-  if (p.rstd_pre && threadIdx.x == 0) p.rstd_pre[t] = rstd;
+__device__ __forceinline__ void load_row(u32x4 (&out)[VPT], const uint16_t* base, size_t t, int hidden, const Team& tm,
+                                         bool live) {
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    if (column(i) < H) {
-      const F8 w = load_f8(p.pre_weight + column(i));
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[i].v[e] = h[i].v[e] * rstd * w.v[e];
-      store16(p.n + t * H + column(i), pack8(h[i]));
-    }
+    const int c = (i * tm.waves * 64 + tm.lane_in_team) * 8;
+    out[i] = (u32x4){0, 0, 0, 0};
+    if (live && base && c < hidden) out[i] = load16(base + t * hidden + c);
   }
 }
 
-// The gradient: each workgroup takes rows in turn, keeps the sums over its
-// rows of the column gradients in registers, and leaves them as one row of
-// partial sums for column_sums_kernel.
+// A column vector's values at this thread's columns: kept (one piece a lane)
+// or read when asked for.
 template <int VPT>
-__global__ __launch_bounds__(MAX_THREADS) void block_norm_bwd_kernel(NormBwdArgs p) {
-  __shared__ float scratch[4][MAX_THREADS / 64];
-  const size_t H = p.hidden;
-  const int waves = blockDim.x >> 6;
-  const float inv_hidden = 1.0f / (float)p.hidden;
-  auto column = [&](int i) { return ((size_t)i * blockDim.x + threadIdx.x) * 8; };
-  F8 dpost[VPT] = {}, dgate[VPT] = {}, dpre[VPT] = {};
-  int turn = 0;
-  for (size_t t = blockIdx.x; t < (size_t)p.tokens; t += gridDim.x, turn ^= 1) {
-    F8 dres[VPT];
+struct Column {
+  F8 kept;
+  const float* base;
+  __device__ __forceinline__ void init(const float* p, int c, int hidden, float none) {
+    base = p;
+    kept = splat(none);
+    if (VPT == 1 && p && c < hidden) kept = load_f8(p + c);
+  }
+  __device__ __forceinline__ F8 at(int c, int hidden) const {
+    if (VPT == 1 || !base || c >= hidden) return kept;
+    return load_f8(base + c);
+  }
+};
+
+template <int VPT>
+__global__ __launch_bounds__(MAX_THREADS) void block_norm_kernel(NormArgs p, int waves) {
+  __shared__ float scratch[4][MAX_WAVES];
+  const Team tm = team_of(waves);
+  const int H = p.hidden;
+  const float inv_hidden = 1.0f / (float)H;
+  const bool full_gate = p.gate_kind == DG_MOE_GATE_FULL;
+  Column<VPT> post, pre, gate;
+  const int c0 = tm.lane_in_team * 8;
+  post.init(p.post_weight, c0, H, 1.0f);
+  pre.init(p.pre_weight, c0, H, 1.0f);
+  gate.init(p.gate_kind == DG_MOE_GATE_CHANNEL ? static_cast<const float*>(p.gate) : nullptr, c0, H, 1.0f);
+
+  const int step = gridDim.x * tm.teams;
+  int t = blockIdx.x + gridDim.x * tm.team;
+  const int rounds = (p.tokens + step - 1) / step;
+  u32x4 x[VPT], y[VPT], g[VPT];
+  float next_gate = 1.0f;
+  auto load = [&](int row) {
+    const bool live = row < p.tokens;
+    if (p.gate_kind == DG_MOE_GATE_TOKEN && live) next_gate = static_cast<const float*>(p.gate)[row];
+    load_row(x, p.x, row, H, tm, live);
+    load_row(y, p.y, row, H, tm, live);
+    if (full_gate) load_row(g, static_cast<const uint16_t*>(p.gate), row, H, tm, live);
+  };
+  load(t);
+  for (int round = 0; round < rounds; ++round, t += step) {
+    float* s0 = scratch[2 * (round & 1)];
+    const bool live = t < p.tokens;
+    const float row_gate = next_gate;
+    F8 h[VPT];
+    if (p.y) {
+      float rstd = 1.0f;
+      if (p.post_weight) {
+        float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      dres[i] = F8{};
-      if (p.dh && column(i) < H) dres[i] = unpack8(load16(p.dh + t * H + column(i)));
-    }
-    if (p.dn) {
-      const float rstd = p.rstd_pre[t];
-      F8 a[VPT], hn[VPT];
-      float s = 0.f;
+        for (int i = 0; i < VPT; ++i) {
+          const F8 v = unpack8(y[i]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(v.v[e], v.v[e], ss);
+        }
+        rstd = rsqrtf(team_sum(ss, tm, s0) * inv_hidden + p.eps);
+        if (p.rstd_post && live && tm.lane_in_team == 0) p.rstd_post[t] = rstd;
+      }
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        a[i] = hn[i] = F8{};
-        if (column(i) < H) {
-          const F8 dn = unpack8(load16(p.dn + t * H + column(i)));
-          const F8 h = unpack8(load16(p.h + t * H + column(i)));
-          const F8 w = load_f8(p.pre_weight + column(i));
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            hn[i].v[e] = h.v[e] * rstd;
-            a[i].v[e] = dn.v[e] * w.v[e];
-            dpre[i].v[e] = __builtin_fmaf(dn.v[e], hn[i].v[e], dpre[i].v[e]);
-            s = __builtin_fmaf(a[i].v[e], hn[i].v[e], s);
-          }
-        }
-      }
-      const float mean = block_sum(s, scratch[turn], waves) * inv_hidden;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i)
+        const int c = (i * waves * 64 + tm.lane_in_team) * 8;
+        const F8 xv = unpack8(x[i]), yv = unpack8(y[i]), w = post.at(c, H);
+        const F8 gv = full_gate ? unpack8(g[i]) : gate.at(c, H);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          dres[i].v[e] = __builtin_fmaf(rstd, __builtin_fmaf(-hn[i].v[e], mean, a[i].v[e]), dres[i].v[e]);
+          h[i].v[e] = __builtin_fmaf(p.residual_scale, xv.v[e], row_gate * gv.v[e] * (yv.v[e] * rstd * w.v[e]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) h[i] = unpack8(x[i]);
     }
+    load(t + step);
+    if (p.y) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      if (column(i) < H) {
-        F8 dx;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dx.v[e] = p.residual_scale * dres[i].v[e];
-        store16(p.dx + t * H + column(i), pack8(dx));
+      for (int i = 0; i < VPT; ++i) {
+        const int c = (i * waves * 64 + tm.lane_in_team) * 8;
+        if (live && c < H) store16(p.h + (size_t)t * H + c, pack8(h[i]));
       }
     }
-    if (!p.y) continue;
-    const float rstd = p.post_weight ? p.rstd_post[t] : 1.0f;
-    F8 b[VPT], yn[VPT];
-    float s = 0.f, token_gate = 0.f;
+    if (!p.n) continue;
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(h[i].v[e], h[i].v[e], ss);
+    // (lanes past the row hold zeros: their pieces were loaded as zeros)
+    const float rstd = rsqrtf(team_sum(ss, tm, s0 + MAX_WAVES) * inv_hidden + p.eps);
+    if (p.rstd_pre && live && tm.lane_in_team == 0) p.rstd_pre[t] = rstd;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      b[i] = yn[i] = F8{};
-      if (column(i) < H) {
-        const F8 y = unpack8(load16(p.y + t * H + column(i)));
-        const F8 gate = gate8(p.gate, p.gate_kind, t, column(i), H);
-        F8 w = {{1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f}};
-        if (p.post_weight) w = load_f8(p.post_weight + column(i));
-        F8 dg;
+      const int c = (i * waves * 64 + tm.lane_in_team) * 8;
+      const F8 w = pre.at(c, H);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          yn[i].v[e] = y.v[e] * rstd;
-          dg.v[e] = dres[i].v[e] * (yn[i].v[e] * w.v[e]);
-          const float dp = dres[i].v[e] * gate.v[e];
-          dpost[i].v[e] = __builtin_fmaf(dp, yn[i].v[e], dpost[i].v[e]);
-          dgate[i].v[e] += dg.v[e];
-          token_gate += dg.v[e];
-          b[i].v[e] = dp * w.v[e];
-          s = __builtin_fmaf(b[i].v[e], yn[i].v[e], s);
+      for (int e = 0; e < 8; ++e) h[i].v[e] = h[i].v[e] * rstd * w.v[e];
+      if (live && c < H) store16(p.n + (size_t)t * H + c, pack8(h[i]));
+    }
+  }
+}
+
+// The gradient. With hn = h rstd_pre, a = dn pre_weight, yn = y rstd_post and v
+// the weight that meets a row's dH on the way to y (gate * post_weight, without
+// the token gate, which multiplies a whole row):
+//     dH = dh + rstd_pre (a - hn m),  m = mean(a hn)
+//     dy = rstd_post token_gate (dH v - yn mean(dH v yn))
+// and sum(dH v yn) = sum((dh + rstd_pre a) v yn) - rstd_pre m sum(hn v yn), so all
+// of a row's sums are taken at once, from its inputs alone: one barrier a row.
+// The column gradients need one sum besides dpre_weight's: a channel gate and
+// post_weight are the same for every row, so both of their gradients are
+// S = sum_t dH yn times the other one (with token or full gates inside S,
+// dpost_weight is S itself). They are summed over the team's rows in
+// registers; at the end the teams' sums are added up in LDS, in order, and
+// leave the workgroup as one row of partial sums for column_sums_kernel.
+template <int VPT, bool FULL>
+__global__ __launch_bounds__(MAX_THREADS) void block_norm_bwd_kernel(NormBwdArgs p, int waves) {
+  __shared__ float scratch[2][3][MAX_WAVES];
+  extern __shared__ float column_sums[];  // [2][hidden] where there are several teams
+  const Team tm = team_of(waves);
+  const int H = p.hidden;
+  const float inv_hidden = 1.0f / (float)H;
+  const float* channel = p.gate_kind == DG_MOE_GATE_CHANNEL ? static_cast<const float*>(p.gate) : nullptr;
+  auto column = [&](int i) { return (i * waves * 64 + tm.lane_in_team) * 8; };
+  // v without a full gate, and pre_weight, at a piece's columns.
+  auto to_y = [&](int c) {
+    F8 v = splat(1.0f);
+    if (c < H) {
+      if (p.post_weight) v = load_f8(p.post_weight + c);
+      if (channel) {
+        const F8 g = load_f8(channel + c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v.v[e] *= g.v[e];
+      }
+    }
+    return v;
+  };
+  auto to_h = [&](int c) { return p.pre_weight && c < H ? load_f8(p.pre_weight + c) : splat(1.0f); };
+  F8 keep_y, keep_h;  // kept where there is one piece a lane
+  if (VPT == 1) {
+    keep_y = to_y(column(0));
+    keep_h = to_h(column(0));
+  }
+  F8 dpost[VPT] = {}, dpre[VPT] = {};
+
+  const int step = gridDim.x * tm.teams;
+  int t = blockIdx.x + gridDim.x * tm.team;
+  const int rounds = (p.tokens + step - 1) / step;
+  struct Row {
+    u32x4 dh[VPT], dn[VPT], h[VPT], y[VPT], g[FULL ? VPT : 1];
+    float rstd_pre, rstd_post, gate;
+  };
+  auto load = [&](Row& r, int row) {
+    const bool live = row < p.tokens;
+    r.rstd_pre = live && p.dn ? p.rstd_pre[row] : 0.0f;
+    r.rstd_post = live && p.post_weight ? p.rstd_post[row] : 1.0f;
+    r.gate = live && p.gate_kind == DG_MOE_GATE_TOKEN ? static_cast<const float*>(p.gate)[row] : 1.0f;
+    load_row(r.dn, p.dn, row, H, tm, live);
+    load_row(r.h, p.dn ? p.h : nullptr, row, H, tm, live);
+    load_row(r.dh, p.dh, row, H, tm, live);
+    load_row(r.y, p.y, row, H, tm, live);
+    if constexpr (FULL) load_row<VPT>(r.g, static_cast<const uint16_t*>(p.gate), row, H, tm, live);
+  };
+  Row next;
+  load(next, t);
+  for (int round = 0; round < rounds; ++round, t += step) {
+    const bool live = t < p.tokens;
+    Row r = next;
+    load(next, t + step);
+    float s_a = 0.f, s_b = 0.f, s_c = 0.f;  // of a hn, (dh + rstd_pre a) v yn, hn v yn
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const F8 d = unpack8(r.dn[i]), h = unpack8(r.h[i]), dh = unpack8(r.dh[i]), y = unpack8(r.y[i]);
+      const F8 w = VPT == 1 ? keep_h : to_h(column(i));
+      F8 v = VPT == 1 ? keep_y : to_y(column(i));
+      if constexpr (FULL) {
+        const F8 g = unpack8(r.g[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v.v[e] *= g.v[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float a = d.v[e] * w.v[e], hn = h.v[e] * r.rstd_pre, vy = v.v[e] * (y.v[e] * r.rstd_post);
+        s_a = __builtin_fmaf(a, hn, s_a);
+        s_b = __builtin_fmaf(__builtin_fmaf(r.rstd_pre, a, dh.v[e]), vy, s_b);
+        s_c = __builtin_fmaf(hn, vy, s_c);
+      }
+    }
+    s_a = wave_sum(s_a);
+    s_b = wave_sum(s_b);
+    s_c = wave_sum(s_c);
+    if (waves > 1) {
+      float(*s)[MAX_WAVES] = scratch[round & 1];
+      const int wave = threadIdx.x >> 6;
+      if ((threadIdx.x & 63) == 0) {
+        s[0][wave] = s_a;
+        s[1][wave] = s_b;
+        s[2][wave] = s_c;
+      }
+      __syncthreads();
+      s_a = s_b = s_c = 0.f;
+      for (int w = tm.first_wave; w < tm.first_wave + waves; ++w) {
+        s_a += s[0][w];
+        s_b += s[1][w];
+        s_c += s[2][w];
+      }
+    }
+    const float m = s_a * inv_hidden;
+    const float along = s_b - r.rstd_pre * m * s_c;  // sum of dH v yn
+    const float mean = p.post_weight ? along * inv_hidden : 0.0f;
+    if (p.gate_kind == DG_MOE_GATE_TOKEN && p.dgate && live && tm.lane_in_team == 0)
+      static_cast<float*>(p.dgate)[t] = along;
+    const float out_scale = r.rstd_post * r.gate;
+    // The pieces are unpacked again rather than kept as floats across the
+    // sums: those would not fit the registers, and a spilled value's reload
+    // waits for the next row's loads, which were issued before it.
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      asm volatile("" : "+v"(r.dn[i]), "+v"(r.h[i]), "+v"(r.dh[i]), "+v"(r.y[i]));
+      if constexpr (FULL) asm volatile("" : "+v"(r.g[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = column(i);
+      const F8 d = unpack8(r.dn[i]), h = unpack8(r.h[i]), dh = unpack8(r.dh[i]), y = unpack8(r.y[i]);
+      const F8 w = VPT == 1 ? keep_h : to_h(c);
+      const F8 v = VPT == 1 ? keep_y : to_y(c);
+      F8 dx, dy, dg;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float a = d.v[e] * w.v[e], hn = h.v[e] * r.rstd_pre, yn = y.v[e] * r.rstd_post;
+        const float dres = __builtin_fmaf(r.rstd_pre, __builtin_fmaf(-hn, m, a), dh.v[e]);
+        dpre[i].v[e] = __builtin_fmaf(d.v[e], hn, dpre[i].v[e]);
+        dx.v[e] = p.residual_scale * dres;
+        float gated = dres * r.gate, to = dres * v.v[e];
+        if constexpr (FULL) {
+          const float g = __builtin_bit_cast(float, e & 1 ? r.g[i][e / 2] & 0xFFFF0000u : r.g[i][e / 2] << 16);
+          dg.v[e] = to * yn;
+          gated = dres * g;
+          to *= g;
         }
-        if (p.gate_kind == DG_MOE_GATE_FULL && p.dgate)
-          store16(static_cast<uint16_t*>(p.dgate) + t * H + column(i), pack8(dg));
+        dpost[i].v[e] = __builtin_fmaf(gated, yn, dpost[i].v[e]);
+        dy.v[e] = out_scale * __builtin_fmaf(-yn, mean, to);
+      }
+      if (live && c < H) {
+        store16(p.dx + (size_t)t * H + c, pack8(dx));
+        if (p.y) store16(p.dy + (size_t)t * H + c, pack8(dy));
+        if (FULL && p.dgate) store16(static_cast<uint16_t*>(p.dgate) + (size_t)t * H + c, pack8(dg));
       }
     }
-    if (p.gate_kind == DG_MOE_GATE_TOKEN && p.dgate) {
-      token_gate = block_sum(token_gate, scratch[turn], waves);
-      if (threadIdx.x == 0) static_cast<float*>(p.dgate)[t] = token_gate;
-    }
-    float mean = 0.f;
-    if (p.post_weight) mean = block_sum(s, scratch[2 + turn], waves) * inv_hidden;
+  }
+
+  float* out = p.partial + (size_t)blockIdx.x * 2 * H;
+  for (int turn = 0; turn < tm.teams; ++turn) {
+    if (turn > 0) __syncthreads();
+    if (turn != tm.team) continue;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      if (column(i) < H) {
-        F8 dy;
+      const int c = column(i);
+      if (c >= H) continue;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dy.v[e] = rstd * __builtin_fmaf(-yn[i].v[e], mean, b[i].v[e]);
-        store16(p.dy + t * H + column(i), pack8(dy));
+      for (int k = 0; k < 2; ++k) {
+        F8 v = k == 0 ? dpost[i] : dpre[i];
+        if (turn > 0) {
+          const F8 before = load_f8(column_sums + k * H + c);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v.v[e] += before.v[e];
+        }
+        if (turn + 1 < tm.teams) store_f8(column_sums + k * H + c, v);
+        else store_f8(out + k * H + c, v);
       }
     }
   }
-  float* out = p.partial + (size_t)blockIdx.x * 3 * H;
+}
+
+// Sums the partial rows in a fixed order: the result does not depend on
+// timing. 64 columns a workgroup, 16 threads across (4 columns each) and 16
+// down, each down thread every 16th row.
+__global__ __launch_bounds__(256) void column_sums_kernel(NormBwdArgs p, int parts) {
+  __shared__ f32x4 down[16][16];
+  const int across = threadIdx.x & 15, row = threadIdx.x >> 4;
+  const bool pre = blockIdx.y == 1;
+  const int c = blockIdx.x * 64 + across * 4;
+  const float* channel = p.gate_kind == DG_MOE_GATE_CHANNEL ? static_cast<const float*>(p.gate) : nullptr;
+  float* dgate = channel ? static_cast<float*>(p.dgate) : nullptr;
+  if (pre ? !p.dpre : !p.dpost && !dgate) return;
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  if (c < p.hidden) {
+#pragma unroll 8
+    for (int i = row; i < parts; i += 16)
+      s += *reinterpret_cast<const f32x4*>(p.partial + ((size_t)i * 2 + pre) * p.hidden + c);
+  }
+  down[row][across] = s;
+  __syncthreads();
+  if (row == 0 && c < p.hidden) {
+    for (int i = 1; i < 16; ++i) s += down[i][across];
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    if (column(i) < H) {
-      store_f8(out + column(i), dpost[i]);
-      store_f8(out + H + column(i), dgate[i]);
-      store_f8(out + 2 * H + column(i), dpre[i]);
+    for (int i = 0; i < 4; ++i) {
+      if (pre) {
+        p.dpre[c + i] = s[i];
+      } else {
+        if (p.dpost) p.dpost[c + i] = s[i] * (channel ? channel[c + i] : 1.0f);
+        if (dgate) dgate[c + i] = s[i] * (p.post_weight ? p.post_weight[c + i] : 1.0f);
+      }
     }
   }
-}
-
-// Sums the partial rows, in order: the result does not depend on timing.
-__global__ __launch_bounds__(64) void column_sums_kernel(NormBwdArgs p, int parts) {
-  const int c = blockIdx.x * 64 + threadIdx.x, which = blockIdx.y;
-  float* out = which == 0 ? p.dpost
-               : which == 1 ? (p.gate_kind == DG_MOE_GATE_CHANNEL ? static_cast<float*>(p.dgate) : nullptr)
-                            : p.dpre;
-  if (!out || c >= p.hidden) return;
-  float s = 0.f;
-  for (int i = 0; i < parts; ++i) s += p.partial[((size_t)i * 3 + which) * p.hidden + c];
-  out[c] = s;
-}
-
-// Threads and pieces a thread for a row of `hidden` values.
-void row_shape(int hidden, int& threads, int& vpt) {
-  const int pieces = hidden / 8;
-  vpt = pieces <= 1024 ? 1 : pieces <= 2048 ? 2 : 4;
-  threads = ((pieces + vpt - 1) / vpt + 63) / 64 * 64;
 }
 
 template <class F>
@@ -222,33 +387,41 @@ void with_vpt(int vpt, F&& f) {
   else f(std::integral_constant<int, 4>{});
 }
 
+constexpr int CUS = 256;
+#ifndef V_FWD_WGS
+#define V_FWD_WGS 1
+#endif
+#ifndef V_BWD_WGS
+#define V_BWD_WGS 1
+#endif
+
 }  // namespace
 
-int norm_bwd_grid(int tokens, int hidden) {
-  (void)hidden;
-  return std::min(tokens, 256);
-}
+int norm_bwd_grid(int tokens) { return std::min(tokens, V_BWD_WGS * CUS); }
 
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t stream) {
-  int threads, vpt;
-  row_shape(a.hidden, threads, vpt);
-  with_vpt(vpt, [&](auto v) {
-    hipLaunchKernelGGL(block_norm_kernel<decltype(v)::value>, dim3(a.tokens), dim3(threads), 0, stream, a);
+  const TeamShape s = team_shape(a.hidden);
+  const int grid = std::min(a.tokens, V_FWD_WGS * CUS);
+  with_vpt(s.vpt, [&](auto v) {
+    hipLaunchKernelGGL(block_norm_kernel<decltype(v)::value>, dim3(grid), dim3(s.threads()), 0, stream, a, s.waves);
   });
   return hipGetLastError();
 }
 
 hipError_t launch_block_norm_bwd(const NormBwdArgs& a, hipStream_t stream) {
-  int threads, vpt;
-  row_shape(a.hidden, threads, vpt);
-  const int grid = norm_bwd_grid(a.tokens, a.hidden);
+  const TeamShape s = team_shape(a.hidden);
+  const int grid = norm_bwd_grid(a.tokens);
   if (grid > 0) {
-    with_vpt(vpt, [&](auto v) {
-      hipLaunchKernelGGL(block_norm_bwd_kernel<decltype(v)::value>, dim3(grid), dim3(threads), 0, stream, a);
+    const size_t lds = s.teams > 1 ? (size_t)2 * a.hidden * sizeof(float) : 0;
+    with_vpt(s.vpt, [&](auto v) {
+      constexpr int VPT = decltype(v)::value;
+      auto* kernel = a.gate_kind == DG_MOE_GATE_FULL ? block_norm_bwd_kernel<VPT, true>
+                                                     : block_norm_bwd_kernel<VPT, false>;
+      hipLaunchKernelGGL(kernel, dim3(grid), dim3(s.threads()), lds, stream, a, s.waves);
     });
     if (hipError_t e = hipGetLastError()) return e;
   }
-  hipLaunchKernelGGL(column_sums_kernel, dim3((a.hidden + 63) / 64, 3), dim3(64), 0, stream, a, grid);
+  hipLaunchKernelGGL(column_sums_kernel, dim3((a.hidden + 63) / 64, 2), dim3(256), 0, stream, a, grid);
   return hipGetLastError();
 }
 

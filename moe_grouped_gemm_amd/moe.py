@@ -26,7 +26,7 @@ from typing import Optional
 import torch
 
 from . import dg
-from .dg import DGError, _check, _need, _stream  # noqa: F401  (DGError: what a failed call raises)
+from .dg import DGError, _check, _need  # noqa: F401  (DGError: what a failed call raises)
 
 _LAYOUTS = {"dense": 0, "contiguous": 1, "masked": 2, "nopad": 3}
 _BF16, _F32, _I32, _FP8 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
@@ -75,13 +75,38 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-def _want(t: torch.Tensor, name: str, dtype, shape, device) -> None:
-    """As dg._need, with the whole shape."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device \
-            and t.is_contiguous():
-        return
-    _need(t, name, dtype, len(shape), device)
+# The handle of a device's current stream: a decode step's calls take a few
+# microseconds each, of which torch.cuda.current_stream(...).cuda_stream, which
+# builds a Stream object first, took 1.9 (this: 0.1).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(index: int) -> int:
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _want(t: torch.Tensor, name: str, dtype, shape, index: int) -> None:
+    """As dg._need, with the whole shape and the device by its index (the
+    cheapest way to ask: get_device() is -1 on the host)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _need(t, name, dtype, len(shape), _device(index))
     raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _device(index: int) -> torch.device:
+    return torch.device("cuda", index) if index >= 0 else torch.device("cpu")
+
+
+def _first(t: torch.Tensor, name: str, dtype, ndim: int) -> int:
+    """Checks the tensor that says where a call runs and returns its device's index."""
+    index = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if index < 0 or t.dtype is not dtype or t.dim() != ndim or not t.is_contiguous():
+        _need(t, name, dtype, ndim, _device(index))
+    return index
 
 
 # ---------------------------------------------------------------------------
@@ -127,6 +152,7 @@ class Plan:
         if device.type != "cuda":
             raise ValueError(f"a plan lives on a GPU, got {device}")
         self.device = device if device.index is not None else torch.device("cuda", torch.cuda.current_device())
+        self._index = self.device.index
         self.row_of = torch.full((self.max_tokens, self.top_k), -1, dtype=_I32, device=device)
         self.group_rows = torch.zeros(self.num_groups, dtype=_I32, device=device)
         self.grouped_layout = (torch.full((self.rows,), -1, dtype=_I32, device=device)
@@ -143,7 +169,7 @@ class Plan:
 
     def _tokens(self, t: torch.Tensor, name: str, dtype, width: int) -> int:
         """Checks a [tokens, width] tensor and returns tokens."""
-        if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype is not dtype or t.device != self.device \
+        if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype is not dtype or t.get_device() != self._index \
                 or not t.is_contiguous():
             _need(t, name, dtype, 2, self.device)
         n, w = t.shape
@@ -164,7 +190,7 @@ def sort(plan: Plan, topk_ids: torch.Tensor) -> Plan:
     """Sorts the slots of topk_ids [tokens, top_k] int32 by group, stably, into
     the plan; ids outside [0, num_groups) drop their slot."""
     n = plan._tokens(topk_ids, "topk_ids", _I32, plan.top_k)
-    _check(lib().dg_moe_sort(plan._ref, topk_ids.data_ptr(), n, _stream(topk_ids)), "dg_moe_sort")
+    _check(lib().dg_moe_sort(plan._ref, topk_ids.data_ptr(), n, _stream(plan._index)), "dg_moe_sort")
     return plan
 
 
@@ -173,8 +199,8 @@ def dispatch(plan: Plan, x, xp, topk_ids=None) -> torch.Tensor:
     xp [rows, hidden] bfloat16 (masked [G, rows, hidden]); rows without a token
     are not written. topk_ids: sorts first. Gradient: combine(plan, dxp, dx)."""
     n = plan._tokens(x, "x", _BF16, plan.hidden)
-    _want(xp, "xp", _BF16, plan.rows_shape, plan.device)
-    _check(lib().dg_moe_dispatch(plan._ref, plan._ids(topk_ids, n), x.data_ptr(), xp.data_ptr(), n, _stream(x)),
+    _want(xp, "xp", _BF16, plan.rows_shape, plan._index)
+    _check(lib().dg_moe_dispatch(plan._ref, plan._ids(topk_ids, n), x.data_ptr(), xp.data_ptr(), n, _stream(plan._index)),
            "dg_moe_dispatch")
     return xp
 
@@ -184,10 +210,10 @@ def dispatch_fp8(plan: Plan, x, q, sfa, topk_ids=None, ue8m0: bool = False):
     sfa [hidden/128, tma_aligned(rows)] float32 (masked: [G, ...]), one scale
     max(amax, 1e-4) / 448 per 128 values (ue8m0: rounded up to a power of two)."""
     n = plan._tokens(x, "x", _BF16, plan.hidden)
-    _want(q, "q", _FP8, plan.rows_shape, plan.device)
-    _want(sfa, "sfa", _F32, plan.scale_shape, plan.device)
+    _want(q, "q", _FP8, plan.rows_shape, plan._index)
+    _want(sfa, "sfa", _F32, plan.scale_shape, plan._index)
     _check(lib().dg_moe_dispatch_fp8(plan._ref, plan._ids(topk_ids, n), x.data_ptr(), q.data_ptr(), sfa.data_ptr(),
-                                     n, ue8m0, _stream(x)), "dg_moe_dispatch_fp8")
+                                     n, ue8m0, _stream(plan._index)), "dg_moe_dispatch_fp8")
     return q, sfa
 
 
@@ -196,10 +222,10 @@ def combine(plan: Plan, yp, y, weights=None) -> torch.Tensor:
     for a token without rows. yp like dispatch's xp, y [tokens, hidden]
     bfloat16, weights [tokens, top_k] float32."""
     n = plan._tokens(y, "y", _BF16, plan.hidden)
-    _want(yp, "yp", _BF16, plan.rows_shape, plan.device)
+    _want(yp, "yp", _BF16, plan.rows_shape, plan._index)
     if weights is not None:
-        _want(weights, "weights", _F32, (n, plan.top_k), plan.device)
-    _check(lib().dg_moe_combine(plan._ref, yp.data_ptr(), _ptr(weights), y.data_ptr(), n, _stream(y)),
+        _want(weights, "weights", _F32, (n, plan.top_k), plan._index)
+    _check(lib().dg_moe_combine(plan._ref, yp.data_ptr(), _ptr(weights), y.data_ptr(), n, _stream(plan._index)),
            "dg_moe_combine")
     return y
 
@@ -209,14 +235,14 @@ def combine_bwd(plan: Plan, dy, yp, weights, dyp, dweights=None):
     dweights[t, j] = <dy[t], yp[row_of[t, j]]>. dweights None: not wanted, and
     yp is not read (may be None)."""
     n = plan._tokens(dy, "dy", _BF16, plan.hidden)
-    _want(weights, "weights", _F32, (n, plan.top_k), plan.device)
-    _want(dyp, "dyp", _BF16, plan.rows_shape, plan.device)
+    _want(weights, "weights", _F32, (n, plan.top_k), plan._index)
+    _want(dyp, "dyp", _BF16, plan.rows_shape, plan._index)
     if dweights is not None:
-        _want(dweights, "dweights", _F32, (n, plan.top_k), plan.device)
+        _want(dweights, "dweights", _F32, (n, plan.top_k), plan._index)
     if dweights is not None or yp is not None:
-        _want(yp, "yp", _BF16, plan.rows_shape, plan.device)
+        _want(yp, "yp", _BF16, plan.rows_shape, plan._index)
     _check(lib().dg_moe_combine_bwd(plan._ref, dy.data_ptr(), _ptr(yp), weights.data_ptr(), dyp.data_ptr(),
-                                    _ptr(dweights), n, _stream(dy)), "dg_moe_combine_bwd")
+                                    _ptr(dweights), n, _stream(plan._index)), "dg_moe_combine_bwd")
     return dyp, dweights
 
 
@@ -225,26 +251,26 @@ def combine_bwd(plan: Plan, dy, yp, weights, dyp, dweights=None):
 # ---------------------------------------------------------------------------
 
 def _glu(gu, rows, layout: str):
-    """(layout, m, groups, inner) of a gate-and-up buffer and its row selector."""
+    """(layout, m, groups, inner, device index) of a gate-and-up buffer and its row selector."""
     if layout not in _LAYOUTS:
         raise ValueError(f"layout must be one of {', '.join(_LAYOUTS)}, got {layout!r}")
-    dev = gu.device
-    _need(gu, "gu", _BF16, 3 if layout == "masked" else 2, dev)
+    index = _first(gu, "gu", _BF16, 3 if layout == "masked" else 2)
     m, width = gu.shape[-2:]
     if width % 256:
         raise ValueError("gu must hold 2 * inner columns, inner a multiple of 128")
     if layout == "dense":
         if rows is not None:
             raise ValueError("the dense layout takes no rows")
-        return 0, m, 1, width // 2
-    _need(rows, "rows", _I32, 1, dev)
+        return 0, m, 1, width // 2, index
+    if _first(rows, "rows", _I32, 1) != index:
+        raise ValueError(f"rows must be on {gu.device}")
     if layout == "contiguous":
         if rows.shape[0] != m:
             raise ValueError("rows must be grouped_layout, one int32 a row of gu")
-        return 1, m, 1, width // 2
+        return 1, m, 1, width // 2, index
     if layout == "masked" and rows.shape[0] != gu.shape[0]:
         raise ValueError("rows must be masked_m, one int32 a group of gu")
-    return _LAYOUTS[layout], m, rows.shape[0], width // 2
+    return _LAYOUTS[layout], m, rows.shape[0], width // 2, index
 
 
 def swiglu_fp8(gu, q, sfa, rows=None, layout: str = "dense", ue8m0: bool = False):
@@ -255,24 +281,23 @@ def swiglu_fp8(gu, q, sfa, rows=None, layout: str = "dense", ue8m0: bool = False
     rows says which rows hold tokens, as the GEMM of that layout takes it:
     grouped_layout [M] (contiguous; a negative id holds none), group_rows [G]
     (nopad), masked_m [G] (masked), None (dense: all). Others are not written."""
-    kind, m, groups, inner = _glu(gu, rows, layout)
-    lead, dev = gu.shape[:-2], gu.device
-    _want(q, "q", _FP8, (*lead, m, inner), dev)
-    _want(sfa, "sfa", _F32, (*lead, inner // 128, (m + 3) // 4 * 4), dev)
+    kind, m, groups, inner, index = _glu(gu, rows, layout)
+    lead = gu.shape[:-2]
+    _want(q, "q", _FP8, (*lead, m, inner), index)
+    _want(sfa, "sfa", _F32, (*lead, inner // 128, (m + 3) // 4 * 4), index)
     _check(lib().dg_moe_swiglu_fp8(gu.data_ptr(), q.data_ptr(), sfa.data_ptr(), _ptr(rows), kind, m, groups, inner,
-                                   ue8m0, _stream(gu)), "dg_moe_swiglu_fp8")
+                                   ue8m0, _stream(index)), "dg_moe_swiglu_fp8")
     return q, sfa
 
 
 def swiglu_bwd(da, gu, dgu, rows=None, layout: str = "dense") -> torch.Tensor:
     """Gradient of silu(g) * u: da [M, I] bfloat16 (masked [G, max_m, I]) to
     dgu like gu; rows and layout as for swiglu_fp8."""
-    kind, m, groups, inner = _glu(gu, rows, layout)
-    dev = gu.device
-    _want(da, "da", _BF16, (*gu.shape[:-1], inner), dev)
-    _want(dgu, "dgu", _BF16, gu.shape, dev)
+    kind, m, groups, inner, index = _glu(gu, rows, layout)
+    _want(da, "da", _BF16, (*gu.shape[:-1], inner), index)
+    _want(dgu, "dgu", _BF16, gu.shape, index)
     _check(lib().dg_moe_swiglu_bwd(da.data_ptr(), gu.data_ptr(), dgu.data_ptr(), _ptr(rows), kind, m, groups, inner,
-                                   _stream(gu)), "dg_moe_swiglu_bwd")
+                                   _stream(index)), "dg_moe_swiglu_bwd")
     return dgu
 
 
@@ -280,21 +305,21 @@ def swiglu_bwd(da, gu, dgu, rows=None, layout: str = "dense") -> torch.Tensor:
 # The norms around the block
 # ---------------------------------------------------------------------------
 
-def _gate_kind(gate, n: int, hidden: int, device) -> int:
+def _gate_kind(gate, n: int, hidden: int, index: int) -> int:
     if gate is None:
         return 0
     if not isinstance(gate, torch.Tensor):
         raise TypeError("gate must be a torch.Tensor")
     if gate.dim() == 1:
         if gate.shape[0] == hidden:
-            _need(gate, "gate", _F32, 1, device)
+            _want(gate, "gate", _F32, (hidden,), index)
             return 1
         raise ValueError(f"a gate of one dimension is per channel ({hidden}); give one per token as ({n}, 1), "
                          f"got {tuple(gate.shape)}")
     if gate.shape == (n, 1):
-        _need(gate, "gate", _F32, 2, device)
+        _want(gate, "gate", _F32, (n, 1), index)
         return 2
-    _want(gate, "gate", _BF16, (n, hidden), device)
+    _want(gate, "gate", _BF16, (n, hidden), index)
     return 3
 
 
@@ -310,20 +335,19 @@ def block_norm(x, y, post_weight, gate, pre_weight, h, n, rstd_post=None, rstd_p
     bfloat16 or None; rstd_post, rstd_pre [tokens] float32 or None: kept for
     block_norm_bwd. y None (with post_weight, gate, h None): only n = norm(x).
     post_weight None: y is not normalised. n None (with pre_weight): only h."""
-    dev = x.device
-    _need(x, "x", _BF16, 2, dev)
+    index = _first(x, "x", _BF16, 2)
     t, hidden = shape = x.shape
     for name, v in (("y", y), ("h", h), ("n", n)):
         if v is not None:
-            _want(v, name, _BF16, shape, dev)
+            _want(v, name, _BF16, shape, index)
     for name, v, size in (("post_weight", post_weight, hidden), ("pre_weight", pre_weight, hidden),
                           ("rstd_post", rstd_post, t), ("rstd_pre", rstd_pre, t)):
         if v is not None:
-            _want(v, name, _F32, (size,), dev)
-    kind = _gate_kind(gate, t, hidden, dev)
+            _want(v, name, _F32, (size,), index)
+    kind = _gate_kind(gate, t, hidden, index)
     _check(lib().dg_moe_block_norm(x.data_ptr(), _ptr(y), _ptr(post_weight), _ptr(gate), kind, _ptr(pre_weight),
                                    _ptr(h), _ptr(n), _ptr(rstd_post), _ptr(rstd_pre), residual_scale, eps, t, hidden,
-                                   _stream(x)), "dg_moe_block_norm")
+                                   _stream(index)), "dg_moe_block_norm")
     return h, n
 
 
@@ -342,24 +366,24 @@ def block_norm_bwd(dh, dn, h, y, post_weight, gate, pre_weight, rstd_post, rstd_
     dpost_weight, dpre_weight [hidden] float32 and dgate like the gate. h, y,
     the weights, the gate and the rstd values are those of the forward call;
     dpost_weight, dgate and dpre_weight may be None where not wanted."""
-    dev = dx.device
-    _need(dx, "dx", _BF16, 2, dev)
+    index = _first(dx, "dx", _BF16, 2)
     t, hidden = shape = dx.shape
     for name, v in (("dh", dh), ("dn", dn), ("h", h), ("y", y), ("dy", dy)):
         if v is not None:
-            _want(v, name, _BF16, shape, dev)
+            _want(v, name, _BF16, shape, index)
     for name, v, size in (("post_weight", post_weight, hidden), ("pre_weight", pre_weight, hidden),
                           ("rstd_post", rstd_post, t), ("rstd_pre", rstd_pre, t),
                           ("dpost_weight", dpost_weight, hidden), ("dpre_weight", dpre_weight, hidden)):
         if v is not None:
-            _want(v, name, _F32, (size,), dev)
-    kind = _gate_kind(gate, t, hidden, dev)
+            _want(v, name, _F32, (size,), index)
+    kind = _gate_kind(gate, t, hidden, index)
     if dgate is not None and gate is not None:
-        _want(dgate, "dgate", gate.dtype, gate.shape, dev)
-    _need(workspace, "workspace", torch.uint8, 1, dev)
+        _want(dgate, "dgate", gate.dtype, gate.shape, index)
+    if _first(workspace, "workspace", torch.uint8, 1) != index:
+        raise ValueError(f"workspace must be on {dx.device}")
     _check(lib().dg_moe_block_norm_bwd(_ptr(dh), _ptr(dn), _ptr(h), _ptr(y), _ptr(post_weight), _ptr(gate), kind,
                                        _ptr(pre_weight), _ptr(rstd_post), _ptr(rstd_pre), dx.data_ptr(), _ptr(dy),
                                        _ptr(dpost_weight), _ptr(dgate), _ptr(dpre_weight), workspace.data_ptr(),
-                                       workspace.numel(), residual_scale, t, hidden, _stream(dx)),
+                                       workspace.numel(), residual_scale, t, hidden, _stream(index)),
            "dg_moe_block_norm_bwd")
     return dx, dy
