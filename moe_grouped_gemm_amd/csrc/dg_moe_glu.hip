@@ -40,12 +40,12 @@ __global__ __launch_bounds__(GLU_THREADS) void swiglu_fp8_kernel(GluArgs p) {
   const size_t row = (size_t)g * p.m + r, I = p.inner;
   for (int b = threadIdx.x >> 4; b < blocks; b += GLU_THREADS / 16) {
     const size_t c = (size_t)b * QBLOCK + (threadIdx.x & 15) * 8;
-    const F8 gate = unpack8(load16(p.gu + row * 2 * I + c)), up = unpack8(load16(p.gu + row * 2 * I + I + c));
+    const F8 gate = unpack8(load_stream16(p.gu + row * 2 * I + c)), up = unpack8(load_stream16(p.gu + row * 2 * I + I + c));
     F8 a;
 #pragma unroll
     for (int i = 0; i < 8; ++i) a.v[i] = gate.v[i] * sigmoid(gate.v[i]) * up.v[i];
     float scale;
-    *reinterpret_cast<u32x2*>(p.q + row * I + c) = quantize_row<E8>(a, scale);
+    store_stream(p.q + row * I + c, quantize_row<E8>(a, scale));
     if ((threadIdx.x & 15) == 0) p.sfa[((size_t)g * blocks + b) * ld + r] = scale;
   }
 }
@@ -55,8 +55,8 @@ __global__ __launch_bounds__(GLU_THREADS) void swiglu_bwd_kernel(GluArgs p) {
   if (!row_held(p, g, r)) return;
   const size_t row = (size_t)g * p.m + r, I = p.inner;
   for (size_t c = threadIdx.x * 8; c < I; c += GLU_THREADS * 8) {
-    const F8 gate = unpack8(load16(p.gu + row * 2 * I + c)), up = unpack8(load16(p.gu + row * 2 * I + I + c));
-    const F8 da = unpack8(load16(p.da + row * I + c));
+    const F8 gate = unpack8(load_stream16(p.gu + row * 2 * I + c)), up = unpack8(load_stream16(p.gu + row * 2 * I + I + c));
+    const F8 da = unpack8(load_stream16(p.da + row * I + c));
     F8 dg, du;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -64,8 +64,8 @@ __global__ __launch_bounds__(GLU_THREADS) void swiglu_bwd_kernel(GluArgs p) {
       dg.v[i] = t * up.v[i] * (1.0f + gate.v[i] * (1.0f - s));
       du.v[i] = t * gate.v[i];
     }
-    store16(p.dgu + row * 2 * I + c, pack8(dg));
-    store16(p.dgu + row * 2 * I + I + c, pack8(du));
+    store_stream(p.dgu + row * 2 * I + c, pack8(dg));
+    store_stream(p.dgu + row * 2 * I + I + c, pack8(du));
   }
 }
 

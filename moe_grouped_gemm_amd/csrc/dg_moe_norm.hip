@@ -68,7 +68,7 @@ __device__ __forceinline__ void load_row(u32x4 (&out)[VPT], const uint16_t* base
   for (int i = 0; i < VPT; ++i) {
     const int c = (i * tm.waves * 64 + tm.lane_in_team) * 8;
     out[i] = (u32x4){0, 0, 0, 0};
-    if (live && base && c < hidden) out[i] = load16(base + t * hidden + c);
+    if (live && base && c < hidden) out[i] = load_stream16(base + t * hidden + c);
   }
 }
 
@@ -151,7 +151,7 @@ __global__ __launch_bounds__(MAX_THREADS) void block_norm_kernel(NormArgs p, int
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int c = (i * waves * 64 + tm.lane_in_team) * 8;
-        if (live && c < H) store16(p.h + (size_t)t * H + c, pack8(h[i]));
+        if (live && c < H) store_stream(p.h + (size_t)t * H + c, pack8(h[i]));
       }
     }
     if (!p.n) continue;
@@ -169,7 +169,7 @@ __global__ __launch_bounds__(MAX_THREADS) void block_norm_kernel(NormArgs p, int
       const F8 w = pre.at(c, H);
 #pragma unroll
       for (int e = 0; e < 8; ++e) h[i].v[e] = h[i].v[e] * rstd * w.v[e];
-      if (live && c < H) store16(p.n + (size_t)t * H + c, pack8(h[i]));
+      if (live && c < H) store_stream(p.n + (size_t)t * H + c, pack8(h[i]));
     }
   }
 }
@@ -317,9 +317,9 @@ __global__ __launch_bounds__(MAX_THREADS) void block_norm_bwd_kernel(NormBwdArgs
         dy.v[e] = out_scale * __builtin_fmaf(-yn, mean, to);
       }
       if (live && c < H) {
-        store16(p.dx + (size_t)t * H + c, pack8(dx));
-        if (p.y) store16(p.dy + (size_t)t * H + c, pack8(dy));
-        if (FULL && p.dgate) store16(static_cast<uint16_t*>(p.dgate) + (size_t)t * H + c, pack8(dg));
+        store_stream(p.dx + (size_t)t * H + c, pack8(dx));
+        if (p.y) store_stream(p.dy + (size_t)t * H + c, pack8(dy));
+        if (FULL && p.dgate) store_stream(static_cast<uint16_t*>(p.dgate) + (size_t)t * H + c, pack8(dg));
       }
     }
   }

@@ -216,7 +216,8 @@ __global__ __launch_bounds__(MOVE_THREADS) void dispatch_kernel(RouteArgs p, Mov
   for (uint32_t i = (blockIdx.x >> 3) * (MOVE_THREADS / 16) + (threadIdx.x >> 4); i < end;
        i += (gridDim.x >> 3) * (MOVE_THREADS / 16)) {
     const int t = t0 + (int)(i / (uint32_t)blocks), b = (int)(i % (uint32_t)blocks);
-    const u32x4 raw = load16(m.x + (size_t)t * p.hidden + b * QBLOCK + l16 * 8);
+    const uint16_t* src = m.x + (size_t)t * p.hidden + b * QBLOCK + l16 * 8;
+    const u32x4 raw = MODE == MOVE_BF16 ? load16(src) : load_stream16(src);
     for (int j0 = 0; j0 < p.top_k; j0 += 16) {
       const int slots = min(p.top_k - j0, 16);
       const int row = l16 < slots ? p.row_of[(size_t)t * p.top_k + j0 + l16] : -1;
@@ -330,7 +331,7 @@ __global__ __launch_bounds__(MOVE_THREADS) void combine_kernel(RouteArgs p, cons
       for (int j = 0; j < AHEAD; ++j) {
         v[j] = (u32x4){0, 0, 0, 0};
         const int r = __builtin_amdgcn_readlane(mine, j0 + j);  // top_k <= 32: -1 past it
-        if (r >= 0 && inside) v[j] = load16(yp + (size_t)r * p.hidden + c);
+        if (r >= 0 && inside) v[j] = load_stream16(yp + (size_t)r * p.hidden + c);
       }
 #pragma unroll
       for (int j = 0; j < AHEAD; ++j) {
@@ -340,7 +341,7 @@ __global__ __launch_bounds__(MOVE_THREADS) void combine_kernel(RouteArgs p, cons
         for (int i = 0; i < 8; ++i) acc.v[i] = __builtin_fmaf(wj, f.v[i], acc.v[i]);
       }
     }
-    if (inside) store16(y + (size_t)t * p.hidden + c, pack8(acc));
+    if (inside) store_stream(y + (size_t)t * p.hidden + c, pack8(acc));
   }
 }
 
@@ -367,11 +368,11 @@ __global__ __launch_bounds__(BWD_THREADS) void combine_bwd_kernel(RouteArgs p, c
     }
     for (size_t c = threadIdx.x * 8; c < H; c += blockDim.x * 8) {
       u32x4 v[AHEAD];
-      const u32x4 raw = load16(dy + t * H + c);
+      const u32x4 raw = load_stream16(dy + t * H + c);
 #pragma unroll
       for (int j = 0; j < AHEAD; ++j) {
         v[j] = (u32x4){0, 0, 0, 0};
-        if (r[j] >= 0 && dw) v[j] = load16(yp + (size_t)r[j] * H + c);
+        if (r[j] >= 0 && dw) v[j] = load_stream16(yp + (size_t)r[j] * H + c);
       }
       const F8 d = unpack8(raw);
 #pragma unroll
