@@ -139,7 +139,12 @@ __device__ __forceinline__ uint32_t abs_top(const F8& x) {
 // infinity, so a NaN anywhere gives a NaN scale.
 template <bool E8>
 __device__ __forceinline__ float block_scale(uint32_t top) {
-  const float scale = __builtin_bit_cast(float, max(top, 0x38D1B717u)) / 448.0f;  // 1e-4f
+  // amax / 448, correctly rounded: the product with 1/448 and one correction
+  // (infinity and NaN pass through the product alone).
+  const float amax = __builtin_bit_cast(float, max(top, 0x38D1B717u));  // 1e-4f
+  const float near = amax * (1.0f / 448.0f);
+  float scale = __builtin_fmaf(__builtin_fmaf(-near, 448.0f, amax), 1.0f / 448.0f, near);
+  if (top >= 0x7F800000u) scale = near;
   if constexpr (E8) {
     // Up to a power of two: past the mantissa, then cut (finite scales only).
     const uint32_t s = __builtin_bit_cast(uint32_t, scale);
@@ -156,15 +161,11 @@ __device__ __forceinline__ float block_scale(uint32_t top) {
 // rounds to 448.
 __device__ __forceinline__ u32x2 quantize8(const F8& x, uint32_t top, float scale, float inv) {
   F8 q;
-  if (top < 0x7F800000u) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float t = x.v[i] * inv;
-      q.v[i] = __builtin_fmaf(__builtin_fmaf(-t, scale, x.v[i]), inv, t);
-    }
-  } else {
+  for (int i = 0; i < 8; ++i) q.v[i] = x.v[i] * inv;
+  if (top < 0x7F800000u) {  // else the scale is not finite and 1 / scale is 0 or NaN: so are the codes
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q.v[i] = x.v[i] / scale;  // 0 or NaN
+    for (int i = 0; i < 8; ++i) q.v[i] = __builtin_fmaf(__builtin_fmaf(-q.v[i], scale, x.v[i]), inv, q.v[i]);
   }
   u32x2 r;
 #pragma unroll
@@ -182,6 +183,16 @@ __device__ __forceinline__ u32x2 quantize_row(const F8& x, float& scale) {
   const uint32_t top = max16(abs_top(x));
   scale = block_scale<E8>(top);
   return quantize8(x, top, scale, 1.0f / scale);
+}
+
+// Threads (a multiple of 64 up to `most`) that share `pieces` of work evenly:
+// the fewest idle ones, and of those the most threads.
+inline int even_threads(int pieces, int most) {
+  int best = 64;
+  auto idle = [&](int n) { return (pieces + n - 1) / n * n - pieces; };
+  for (int n = 128; n <= most; n += 64)
+    if (idle(n) <= idle(best)) best = n;
+  return best;
 }
 
 }  // namespace moe

@@ -459,20 +459,6 @@ hipError_t launch_dispatch_fp8(const RouteArgs& a, const void* x, void* q, float
   return ue8m0 ? launch_move<MOVE_FP8_E8>(a, m, stream) : launch_move<MOVE_FP8>(a, m, stream);
 }
 
-namespace {
-
-// Threads (a multiple of 64 up to `most`) that share `pieces` of work evenly:
-// the fewest idle ones, and of those the most threads.
-int even_threads(int pieces, int most) {
-  int best = 64;
-  auto idle = [&](int n) { return (pieces + n - 1) / n * n - pieces; };
-  for (int n = 128; n <= most; n += 64)
-    if (idle(n) <= idle(best)) best = n;
-  return best;
-}
-
-}  // namespace
-
 hipError_t launch_combine(const RouteArgs& a, const void* yp, const float* w, void* y, hipStream_t stream) {
   const int threads = even_threads(a.hidden / 8, MOVE_THREADS);
   const uint32_t parts = (a.hidden / 8 + threads - 1) / threads;
