@@ -158,9 +158,20 @@ dg_status dg_moe_swiglu_bwd(const void* da, const void* gu, void* dgu, const int
  * rstd_post and rstd_pre may be NULL where no gradient is wanted. h may be x, and n may be y.
  * hidden % 8 == 0 and at most 32768; tokens <= 2^21; eps >= 0.
  */
-dg_status dg_moe_block_norm(const void* x, const void* y, const float* post_weight, const void* gate, int gate_kind,
-                            const float* pre_weight, void* h, void* n, float* rstd_post, float* rstd_pre,
-                            float residual_scale, float eps, int tokens, int hidden, void* stream);
+typedef struct dg_moe_norm {
+  const void* x;
+  const void* y;
+  const float* post_weight;
+  const void* gate;
+  const float* pre_weight;
+  void* h;
+  void* n;
+  float* rstd_post;
+  float* rstd_pre;
+  float residual_scale, eps;
+  int gate_kind, tokens, hidden;
+} dg_moe_norm;
+dg_status dg_moe_block_norm(const dg_moe_norm* args, void* stream);
 
 /* Bytes of the workspace of dg_moe_block_norm_bwd, or -1. */
 long long dg_moe_block_norm_workspace_bytes(int tokens, int hidden);
@@ -183,12 +194,27 @@ long long dg_moe_block_norm_workspace_bytes(int tokens, int hidden);
  * may be dh and dy may be dn. tokens == 0 gives zero weight gradients.
  * workspace: 16-byte aligned, dg_moe_block_norm_workspace_bytes() bytes.
  */
-dg_status dg_moe_block_norm_bwd(const void* dh, const void* dn, const void* h, const void* y,
-                                const float* post_weight, const void* gate, int gate_kind, const float* pre_weight,
-                                const float* rstd_post, const float* rstd_pre, void* dx, void* dy,
-                                float* dpost_weight, void* dgate, float* dpre_weight, void* workspace,
-                                long long workspace_bytes, float residual_scale, int tokens, int hidden,
-                                void* stream);
+typedef struct dg_moe_norm_bwd {
+  const void* dh;
+  const void* dn;
+  const void* h;
+  const void* y;
+  const float* post_weight;
+  const void* gate;
+  const float* pre_weight;
+  const float* rstd_post;
+  const float* rstd_pre;
+  void* dx;
+  void* dy;
+  float* dpost_weight;
+  void* dgate;
+  float* dpre_weight;
+  void* workspace;
+  long long workspace_bytes;
+  float residual_scale;
+  int gate_kind, tokens, hidden;
+} dg_moe_norm_bwd;
+dg_status dg_moe_block_norm_bwd(const dg_moe_norm_bwd* args, void* stream);
 
 #ifdef __cplusplus
 }

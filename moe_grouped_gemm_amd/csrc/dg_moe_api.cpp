@@ -206,37 +206,23 @@ dg_status dg_moe_swiglu_bwd(const void* da, const void* gu, void* dgu, const int
   return status_of(launch_swiglu_bwd(a, as_stream(stream)));
 }
 
-dg_status dg_moe_block_norm(const void* x, const void* y, const float* post_weight, const void* gate, int gate_kind,
-                            const float* pre_weight, void* h, void* n, float* rstd_post, float* rstd_pre,
-                            float residual_scale, float eps, int tokens, int hidden, void* stream) {
-  if (dg_status s = norm_sizes(tokens, hidden, gate_kind)) return s;
-  if (!(eps >= 0.0f)) return DG_ERR_SHAPE;
-  if (tokens == 0) return DG_OK;
-  if (!x || (!y && !n)) return DG_ERR_NULL;
+dg_status dg_moe_block_norm(const dg_moe_norm* args, void* stream) {
+  if (!args) return DG_ERR_NULL;
+  const dg_moe_norm& a = *args;
+  if (dg_status s = norm_sizes(a.tokens, a.hidden, a.gate_kind)) return s;
+  if (!(a.eps >= 0.0f)) return DG_ERR_SHAPE;
+  if (a.tokens == 0) return DG_OK;
+  if (!a.x || (!a.y && !a.n)) return DG_ERR_NULL;
   // What a missing part would use has to be missing too, and the rest there.
-  if ((gate_kind == DG_MOE_GATE_NONE) != (gate == nullptr)) return DG_ERR_NULL;
-  if (y && !h) return DG_ERR_NULL;
-  if (!y && (h || gate || post_weight || residual_scale != 1.0f)) return DG_ERR_NULL;
-  if (!post_weight && rstd_post) return DG_ERR_NULL;
-  if (n ? !pre_weight : (pre_weight || rstd_pre)) return DG_ERR_NULL;
-  for (const void* p : {x, y, (const void*)post_weight, (const void*)pre_weight, (const void*)h, (const void*)n})
+  if ((a.gate_kind == DG_MOE_GATE_NONE) != (a.gate == nullptr)) return DG_ERR_NULL;
+  if (a.y && !a.h) return DG_ERR_NULL;
+  if (!a.y && (a.h || a.gate || a.post_weight || a.residual_scale != 1.0f)) return DG_ERR_NULL;
+  if (!a.post_weight && a.rstd_post) return DG_ERR_NULL;
+  if (a.n ? !a.pre_weight : (a.pre_weight || a.rstd_pre)) return DG_ERR_NULL;
+  for (const void* p : {a.x, a.y, (const void*)a.post_weight, (const void*)a.pre_weight, (const void*)a.h,
+                        (const void*)a.n})
     if (!aligned16(p)) return DG_ERR_ALIGN;
-  if (!gate_aligned(gate, gate_kind) || !aligned4b(rstd_post) || !aligned4b(rstd_pre)) return DG_ERR_ALIGN;
-  NormArgs a{};
-  a.x = static_cast<const uint16_t*>(x);
-  a.y = static_cast<const uint16_t*>(y);
-  a.post_weight = post_weight;
-  a.gate = gate;
-  a.gate_kind = gate_kind;
-  a.pre_weight = pre_weight;
-  a.h = static_cast<uint16_t*>(h);
-  a.n = static_cast<uint16_t*>(n);
-  a.rstd_post = rstd_post;
-  a.rstd_pre = rstd_pre;
-  a.residual_scale = residual_scale;
-  a.eps = eps;
-  a.tokens = tokens;
-  a.hidden = hidden;
+  if (!gate_aligned(a.gate, a.gate_kind) || !aligned4b(a.rstd_post) || !aligned4b(a.rstd_pre)) return DG_ERR_ALIGN;
   if (dg_status s = device_check()) return s;
   return status_of(launch_block_norm(a, as_stream(stream)));
 }
@@ -246,49 +232,27 @@ long long dg_moe_block_norm_workspace_bytes(int tokens, int hidden) {
   return 16 + (long long)norm_bwd_grid(tokens) * 2 * hidden * 4;
 }
 
-dg_status dg_moe_block_norm_bwd(const void* dh, const void* dn, const void* h, const void* y,
-                                const float* post_weight, const void* gate, int gate_kind, const float* pre_weight,
-                                const float* rstd_post, const float* rstd_pre, void* dx, void* dy,
-                                float* dpost_weight, void* dgate, float* dpre_weight, void* workspace,
-                                long long workspace_bytes, float residual_scale, int tokens, int hidden,
-                                void* stream) {
-  if (dg_status s = norm_sizes(tokens, hidden, gate_kind)) return s;
-  if (!workspace) return DG_ERR_NULL;
-  if (tokens > 0) {
-    if ((!dh && !dn) || !dx) return DG_ERR_NULL;
-    if ((gate_kind == DG_MOE_GATE_NONE) != (gate == nullptr)) return DG_ERR_NULL;
-    if (dn ? (!h || !pre_weight || !rstd_pre) : (pre_weight || rstd_pre || dpre_weight)) return DG_ERR_NULL;
-    if (y ? !dy : (dy || gate || post_weight || residual_scale != 1.0f)) return DG_ERR_NULL;
-    if (post_weight ? !rstd_post : (rstd_post || dpost_weight)) return DG_ERR_NULL;
-    if (!gate && dgate) return DG_ERR_NULL;
+dg_status dg_moe_block_norm_bwd(const dg_moe_norm_bwd* args, void* stream) {
+  if (!args) return DG_ERR_NULL;
+  const dg_moe_norm_bwd& a = *args;
+  if (dg_status s = norm_sizes(a.tokens, a.hidden, a.gate_kind)) return s;
+  if (!a.workspace) return DG_ERR_NULL;
+  if (a.tokens > 0) {
+    if ((!a.dh && !a.dn) || !a.dx) return DG_ERR_NULL;
+    if ((a.gate_kind == DG_MOE_GATE_NONE) != (a.gate == nullptr)) return DG_ERR_NULL;
+    if (a.dn ? (!a.h || !a.pre_weight || !a.rstd_pre) : (a.pre_weight || a.rstd_pre || a.dpre_weight))
+      return DG_ERR_NULL;
+    if (a.y ? !a.dy : (a.dy || a.gate || a.post_weight || a.residual_scale != 1.0f)) return DG_ERR_NULL;
+    if (a.post_weight ? !a.rstd_post : (a.rstd_post || a.dpost_weight)) return DG_ERR_NULL;
+    if (!a.gate && a.dgate) return DG_ERR_NULL;
   }
-  for (const void* p : {dh, dn, h, y, (const void*)post_weight, (const void*)pre_weight, (const void*)dx,
-                        (const void*)dy, (const void*)workspace})
+  for (const void* p : {a.dh, a.dn, a.h, a.y, (const void*)a.post_weight, (const void*)a.pre_weight,
+                        (const void*)a.dx, (const void*)a.dy, (const void*)a.workspace})
     if (!aligned16(p)) return DG_ERR_ALIGN;
-  if (!gate_aligned(gate, gate_kind) || !gate_aligned(dgate, gate_kind)) return DG_ERR_ALIGN;
-  if (!aligned4b(rstd_post) || !aligned4b(rstd_pre) || !aligned4b(dpost_weight) || !aligned4b(dpre_weight))
+  if (!gate_aligned(a.gate, a.gate_kind) || !gate_aligned(a.dgate, a.gate_kind)) return DG_ERR_ALIGN;
+  if (!aligned4b(a.rstd_post) || !aligned4b(a.rstd_pre) || !aligned4b(a.dpost_weight) || !aligned4b(a.dpre_weight))
     return DG_ERR_ALIGN;
-  if (workspace_bytes < dg_moe_block_norm_workspace_bytes(tokens, hidden)) return DG_ERR_SHAPE;
-  NormBwdArgs a{};
-  a.dh = static_cast<const uint16_t*>(dh);
-  a.dn = static_cast<const uint16_t*>(dn);
-  a.h = static_cast<const uint16_t*>(h);
-  a.y = static_cast<const uint16_t*>(y);
-  a.post_weight = post_weight;
-  a.gate = gate;
-  a.gate_kind = gate_kind;
-  a.pre_weight = pre_weight;
-  a.rstd_post = rstd_post;
-  a.rstd_pre = rstd_pre;
-  a.dx = static_cast<uint16_t*>(dx);
-  a.dy = static_cast<uint16_t*>(dy);
-  a.dpost = dpost_weight;
-  a.dgate = dgate;
-  a.dpre = dpre_weight;
-  a.partial = static_cast<float*>(workspace);
-  a.residual_scale = residual_scale;
-  a.tokens = tokens;
-  a.hidden = hidden;
+  if (a.workspace_bytes < dg_moe_block_norm_workspace_bytes(a.tokens, a.hidden)) return DG_ERR_SHAPE;
   if (dg_status s = device_check()) return s;
   return status_of(launch_block_norm_bwd(a, as_stream(stream)));
 }

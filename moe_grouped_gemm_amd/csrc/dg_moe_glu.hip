@@ -34,8 +34,9 @@ __device__ __forceinline__ int nopad_rows(const GluArgs& p) {
 //              (32000 rows of 2048, contiguous layout).
 //   ROWS_LOOP  as many workgroups as fill the device a few times, each going on
 //              to later rows of its group: for the masked layout where G * max_m
-//              rows, most of them empty in decoding, would each cost a workgroup
-//              (about 0.25 ns, 16 us for 256 groups of 256).
+//              rows, most of them empty in decoding, would each cost a workgroup:
+//              2 rows in each of 256 groups of 256 take 10.4 us, a row a
+//              workgroup 16.8 (and full groups 114 against 109).
 //   ROWS_MANY  several rows a workgroup, 16 lanes a block, for an inner of at
 //              most 1024: 29416 rows of 256 take 10 us, a row a workgroup 25.
 enum { ROWS_ONE, ROWS_LOOP, ROWS_MANY };

@@ -51,44 +51,10 @@ hipError_t launch_swiglu_fp8(const GluArgs& a, bool ue8m0, hipStream_t stream);
 hipError_t launch_swiglu_bwd(const GluArgs& a, hipStream_t stream);
 
 // Norms around the block (dg_moe_norm.hip).
-struct NormArgs {
-  const uint16_t* x;
-  const uint16_t* y;
-  const float* post_weight;
-  const void* gate;
-  int gate_kind;
-  const float* pre_weight;
-  uint16_t* h;
-  uint16_t* n;
-  float* rstd_post;
-  float* rstd_pre;
-  float residual_scale, eps;
-  int tokens, hidden;
-};
-struct NormBwdArgs {
-  const uint16_t* dh;
-  const uint16_t* dn;
-  const uint16_t* h;
-  const uint16_t* y;
-  const float* post_weight;
-  const void* gate;
-  int gate_kind;
-  const float* pre_weight;
-  const float* rstd_post;
-  const float* rstd_pre;
-  uint16_t* dx;
-  uint16_t* dy;
-  float* dpost;
-  void* dgate;
-  float* dpre;
-  float* partial;       // [grid][2][hidden]: sums over rows of dH yn and dn hn
-  float residual_scale;
-  int tokens, hidden;
-};
 // Workgroups of the gradient's row loop (and rows of its partial sums).
 int norm_bwd_grid(int tokens);
-hipError_t launch_block_norm(const NormArgs& a, hipStream_t stream);
-hipError_t launch_block_norm_bwd(const NormBwdArgs& a, hipStream_t stream);
+hipError_t launch_block_norm(const dg_moe_norm& a, hipStream_t stream);
+hipError_t launch_block_norm_bwd(const dg_moe_norm_bwd& a, hipStream_t stream);
 
 }  // namespace moe
 }  // namespace dg

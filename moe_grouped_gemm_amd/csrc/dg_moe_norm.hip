@@ -20,6 +20,9 @@ namespace dg {
 namespace moe {
 namespace {
 
+typedef dg_moe_norm NormArgs;
+typedef dg_moe_norm_bwd NormBwdArgs;  // workspace: [workgroups][2][hidden] float32, sums over rows of dH yn and dn hn
+
 constexpr int MAX_THREADS = 1024;
 constexpr int MAX_WAVES = MAX_THREADS / 64;
 
@@ -62,13 +65,13 @@ __device__ __forceinline__ F8 splat(float v) { return F8{{v, v, v, v, v, v, v, v
 
 // A row's pieces as loaded.
 template <int VPT>
-__device__ __forceinline__ void load_row(u32x4 (&out)[VPT], const uint16_t* base, size_t t, int hidden, const Team& tm,
+__device__ __forceinline__ void load_row(u32x4 (&out)[VPT], const void* base, size_t t, int hidden, const Team& tm,
                                          bool live) {
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = (i * tm.waves * 64 + tm.lane_in_team) * 8;
     out[i] = (u32x4){0, 0, 0, 0};
-    if (live && base && c < hidden) out[i] = load_stream16(base + t * hidden + c);
+    if (live && base && c < hidden) out[i] = load_stream16(static_cast<const uint16_t*>(base) + t * hidden + c);
   }
 }
 
@@ -112,7 +115,7 @@ __global__ __launch_bounds__(MAX_THREADS) void block_norm_kernel(NormArgs p, int
     if (p.gate_kind == DG_MOE_GATE_TOKEN && live) next_gate = static_cast<const float*>(p.gate)[row];
     load_row(x, p.x, row, H, tm, live);
     load_row(y, p.y, row, H, tm, live);
-    if (full_gate) load_row(g, static_cast<const uint16_t*>(p.gate), row, H, tm, live);
+    if (full_gate) load_row(g, p.gate, row, H, tm, live);
   };
   load(t);
   for (int round = 0; round < rounds; ++round, t += step) {
@@ -151,7 +154,7 @@ __global__ __launch_bounds__(MAX_THREADS) void block_norm_kernel(NormArgs p, int
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int c = (i * waves * 64 + tm.lane_in_team) * 8;
-        if (live && c < H) store_stream(p.h + (size_t)t * H + c, pack8(h[i]));
+        if (live && c < H) store_stream(static_cast<uint16_t*>(p.h) + (size_t)t * H + c, pack8(h[i]));
       }
     }
     if (!p.n) continue;
@@ -169,7 +172,7 @@ __global__ __launch_bounds__(MAX_THREADS) void block_norm_kernel(NormArgs p, int
       const F8 w = pre.at(c, H);
 #pragma unroll
       for (int e = 0; e < 8; ++e) h[i].v[e] = h[i].v[e] * rstd * w.v[e];
-      if (live && c < H) store_stream(p.n + (size_t)t * H + c, pack8(h[i]));
+      if (live && c < H) store_stream(static_cast<uint16_t*>(p.n) + (size_t)t * H + c, pack8(h[i]));
     }
   }
 }
@@ -233,7 +236,7 @@ __global__ __launch_bounds__(MAX_THREADS) void block_norm_bwd_kernel(NormBwdArgs
     load_row(r.h, p.dn ? p.h : nullptr, row, H, tm, live);
     load_row(r.dh, p.dh, row, H, tm, live);
     load_row(r.y, p.y, row, H, tm, live);
-    if constexpr (FULL) load_row<VPT>(r.g, static_cast<const uint16_t*>(p.gate), row, H, tm, live);
+    if constexpr (FULL) load_row<VPT>(r.g, p.gate, row, H, tm, live);
   };
   Row next;
   load(next, t);
@@ -317,14 +320,14 @@ __global__ __launch_bounds__(MAX_THREADS) void block_norm_bwd_kernel(NormBwdArgs
         dy.v[e] = out_scale * __builtin_fmaf(-yn, mean, to);
       }
       if (live && c < H) {
-        store_stream(p.dx + (size_t)t * H + c, pack8(dx));
-        if (p.y) store_stream(p.dy + (size_t)t * H + c, pack8(dy));
+        store_stream(static_cast<uint16_t*>(p.dx) + (size_t)t * H + c, pack8(dx));
+        if (p.y) store_stream(static_cast<uint16_t*>(p.dy) + (size_t)t * H + c, pack8(dy));
         if (FULL && p.dgate) store_stream(static_cast<uint16_t*>(p.dgate) + (size_t)t * H + c, pack8(dg));
       }
     }
   }
 
-  float* out = p.partial + (size_t)blockIdx.x * 2 * H;
+  float* out = static_cast<float*>(p.workspace) + (size_t)blockIdx.x * 2 * H;
   for (int turn = 0; turn < tm.teams; ++turn) {
     if (turn > 0) __syncthreads();
     if (turn != tm.team) continue;
@@ -357,12 +360,12 @@ __global__ __launch_bounds__(256) void column_sums_kernel(NormBwdArgs p, int par
   const int c = blockIdx.x * 64 + across * 4;
   const float* channel = p.gate_kind == DG_MOE_GATE_CHANNEL ? static_cast<const float*>(p.gate) : nullptr;
   float* dgate = channel ? static_cast<float*>(p.dgate) : nullptr;
-  if (pre ? !p.dpre : !p.dpost && !dgate) return;
+  if (pre ? !p.dpre_weight : !p.dpost_weight && !dgate) return;
   f32x4 s = {0.f, 0.f, 0.f, 0.f};
   if (c < p.hidden) {
 #pragma unroll 8
     for (int i = row; i < parts; i += 16)
-      s += *reinterpret_cast<const f32x4*>(p.partial + ((size_t)i * 2 + pre) * p.hidden + c);
+      s += *reinterpret_cast<const f32x4*>(static_cast<float*>(p.workspace) + ((size_t)i * 2 + pre) * p.hidden + c);
   }
   down[row][across] = s;
   __syncthreads();
@@ -371,9 +374,9 @@ __global__ __launch_bounds__(256) void column_sums_kernel(NormBwdArgs p, int par
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (pre) {
-        p.dpre[c + i] = s[i];
+        p.dpre_weight[c + i] = s[i];
       } else {
-        if (p.dpost) p.dpost[c + i] = s[i] * (channel ? channel[c + i] : 1.0f);
+        if (p.dpost_weight) p.dpost_weight[c + i] = s[i] * (channel ? channel[c + i] : 1.0f);
         if (dgate) dgate[c + i] = s[i] * (p.post_weight ? p.post_weight[c + i] : 1.0f);
       }
     }

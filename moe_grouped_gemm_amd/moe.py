@@ -21,6 +21,7 @@ A block in FP8, masked layout (b1 [G, 2I, H], b2 [G, H, I] and their scales):
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional
 
 import torch
@@ -39,7 +40,7 @@ class _PlanStruct(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_longlong)]
 
 
-_vp, _i, _f, _ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong
+_vp, _i, _ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
 # (name, argtypes, restype) of every symbol include/moe/dg_moe.h declares.
 SIGNATURES = [
     ("dg_moe_workspace_bytes", [_vp], _ll),
@@ -50,10 +51,15 @@ SIGNATURES = [
     ("dg_moe_combine_bwd", [_vp, _vp, _vp, _vp, _vp, _vp, _i, _vp], _i),
     ("dg_moe_swiglu_fp8", [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp], _i),
     ("dg_moe_swiglu_bwd", [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp], _i),
-    ("dg_moe_block_norm", [_vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _f, _f, _i, _i, _vp], _i),
+    ("dg_moe_block_norm", [ctypes.c_char_p, _vp], _i),
     ("dg_moe_block_norm_workspace_bytes", [_i, _i], _ll),
-    ("dg_moe_block_norm_bwd", [_vp] * 6 + [_i] + [_vp] * 9 + [_ll, _f, _i, _i, _vp], _i),
+    ("dg_moe_block_norm_bwd", [ctypes.c_char_p, _vp], _i),
 ]
+
+# The argument structs dg_moe_norm and dg_moe_norm_bwd, packed in one go (a
+# ctypes call converts its arguments one by one, 0.1 us each).
+_NORM = struct.Struct("9P2f3i4x")
+_NORM_BWD = struct.Struct("15Pqf3i")
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -71,8 +77,8 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
-def _ptr(t) -> Optional[int]:
-    return None if t is None else t.data_ptr()
+def _ptr(t) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 # The handle of a device's current stream: a decode step's calls take a few
@@ -95,6 +101,18 @@ def _want(t: torch.Tensor, name: str, dtype, shape, index: int) -> None:
         pass
     _need(t, name, dtype, len(shape), _device(index))
     raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _optional(index: int, dtype, shape, **tensors) -> None:
+    """_want for each tensor that is given."""
+    for name, t in tensors.items():
+        if t is not None:
+            try:
+                if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+                    continue
+            except AttributeError:
+                pass
+            _want(t, name, dtype, shape, index)
 
 
 def _device(index: int) -> torch.device:
@@ -337,17 +355,13 @@ def block_norm(x, y, post_weight, gate, pre_weight, h, n, rstd_post=None, rstd_p
     post_weight None: y is not normalised. n None (with pre_weight): only h."""
     index = _first(x, "x", _BF16, 2)
     t, hidden = shape = x.shape
-    for name, v in (("y", y), ("h", h), ("n", n)):
-        if v is not None:
-            _want(v, name, _BF16, shape, index)
-    for name, v, size in (("post_weight", post_weight, hidden), ("pre_weight", pre_weight, hidden),
-                          ("rstd_post", rstd_post, t), ("rstd_pre", rstd_pre, t)):
-        if v is not None:
-            _want(v, name, _F32, (size,), index)
+    _optional(index, _BF16, shape, y=y, h=h, n=n)
+    _optional(index, _F32, (hidden,), post_weight=post_weight, pre_weight=pre_weight)
+    _optional(index, _F32, (t,), rstd_post=rstd_post, rstd_pre=rstd_pre)
     kind = _gate_kind(gate, t, hidden, index)
-    _check(lib().dg_moe_block_norm(x.data_ptr(), _ptr(y), _ptr(post_weight), _ptr(gate), kind, _ptr(pre_weight),
-                                   _ptr(h), _ptr(n), _ptr(rstd_post), _ptr(rstd_pre), residual_scale, eps, t, hidden,
-                                   _stream(index)), "dg_moe_block_norm")
+    args = _NORM.pack(x.data_ptr(), _ptr(y), _ptr(post_weight), _ptr(gate), _ptr(pre_weight), _ptr(h), _ptr(n),
+                      _ptr(rstd_post), _ptr(rstd_pre), residual_scale, eps, kind, t, hidden)
+    _check(lib().dg_moe_block_norm(args, _stream(index)), "dg_moe_block_norm")
     return h, n
 
 
@@ -368,22 +382,17 @@ def block_norm_bwd(dh, dn, h, y, post_weight, gate, pre_weight, rstd_post, rstd_
     dpost_weight, dgate and dpre_weight may be None where not wanted."""
     index = _first(dx, "dx", _BF16, 2)
     t, hidden = shape = dx.shape
-    for name, v in (("dh", dh), ("dn", dn), ("h", h), ("y", y), ("dy", dy)):
-        if v is not None:
-            _want(v, name, _BF16, shape, index)
-    for name, v, size in (("post_weight", post_weight, hidden), ("pre_weight", pre_weight, hidden),
-                          ("rstd_post", rstd_post, t), ("rstd_pre", rstd_pre, t),
-                          ("dpost_weight", dpost_weight, hidden), ("dpre_weight", dpre_weight, hidden)):
-        if v is not None:
-            _want(v, name, _F32, (size,), index)
+    _optional(index, _BF16, shape, dh=dh, dn=dn, h=h, y=y, dy=dy)
+    _optional(index, _F32, (hidden,), post_weight=post_weight, pre_weight=pre_weight, dpost_weight=dpost_weight,
+              dpre_weight=dpre_weight)
+    _optional(index, _F32, (t,), rstd_post=rstd_post, rstd_pre=rstd_pre)
     kind = _gate_kind(gate, t, hidden, index)
     if dgate is not None and gate is not None:
         _want(dgate, "dgate", gate.dtype, gate.shape, index)
     if _first(workspace, "workspace", torch.uint8, 1) != index:
         raise ValueError(f"workspace must be on {dx.device}")
-    _check(lib().dg_moe_block_norm_bwd(_ptr(dh), _ptr(dn), _ptr(h), _ptr(y), _ptr(post_weight), _ptr(gate), kind,
-                                       _ptr(pre_weight), _ptr(rstd_post), _ptr(rstd_pre), dx.data_ptr(), _ptr(dy),
-                                       _ptr(dpost_weight), _ptr(dgate), _ptr(dpre_weight), workspace.data_ptr(),
-                                       workspace.numel(), residual_scale, t, hidden, _stream(index)),
-           "dg_moe_block_norm_bwd")
+    args = _NORM_BWD.pack(_ptr(dh), _ptr(dn), _ptr(h), _ptr(y), _ptr(post_weight), _ptr(gate), _ptr(pre_weight),
+                          _ptr(rstd_post), _ptr(rstd_pre), dx.data_ptr(), _ptr(dy), _ptr(dpost_weight), _ptr(dgate),
+                          _ptr(dpre_weight), workspace.data_ptr(), workspace.numel(), residual_scale, kind, t, hidden)
+    _check(lib().dg_moe_block_norm_bwd(args, _stream(index)), "dg_moe_block_norm_bwd")
     return dx, dy

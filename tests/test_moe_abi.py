@@ -126,13 +126,21 @@ def test_glu_refusals(call):
 
 
 def _norm(x=A, y=B, post=C, gate=D, kind=1, pre=E, h=F, n=A, r1=B, r2=C, rs=0.5, eps=1e-6, tokens=4, hidden=64):
-    return moe.lib().dg_moe_block_norm(x, y, post, gate, kind, pre, h, n, r1, r2, rs, eps, tokens, hidden, None)
+    p = (0 if v is None else v for v in (x, y, post, gate, pre, h, n, r1, r2))
+    return moe.lib().dg_moe_block_norm(moe._NORM.pack(*p, rs, eps, kind, tokens, hidden), None)
 
 
 def _norm_bwd(dh=A, dn=B, h=C, y=D, post=E, gate=F, kind=1, pre=A, r1=B, r2=C, dx=D, dy=E, dpost=F, dgate=A, dpre=B,
               ws=C, ws_bytes=1 << 30, rs=0.5, tokens=4, hidden=64):
-    return moe.lib().dg_moe_block_norm_bwd(dh, dn, h, y, post, gate, kind, pre, r1, r2, dx, dy, dpost, dgate, dpre, ws,
-                                           ws_bytes, rs, tokens, hidden, None)
+    p = (0 if v is None else v for v in (dh, dn, h, y, post, gate, pre, r1, r2, dx, dy, dpost, dgate, dpre, ws))
+    return moe.lib().dg_moe_block_norm_bwd(moe._NORM_BWD.pack(*p, ws_bytes, rs, kind, tokens, hidden), None)
+
+
+def test_argument_structs_have_the_headers_size():
+    p, f, i = ctypes.sizeof(ctypes.c_void_p), 4, 4
+    assert moe._NORM.size == 9 * p + 2 * f + 3 * i + 4           # padded to a multiple of a pointer
+    assert moe._NORM_BWD.size == 15 * p + 8 + f + 3 * i
+    assert moe.lib().dg_moe_block_norm(None, None) == NULL and moe.lib().dg_moe_block_norm_bwd(None, None) == NULL
 
 
 def test_block_norm_refusals():
