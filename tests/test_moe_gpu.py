@@ -864,3 +864,32 @@ def test_refusals(dev):
         r = torch.zeros(8, device=dev)
         moe.block_norm_bwd(x, x, x, x, d["post"], None, d["pre"], r, r, h, n, None, None, None,
                            torch.zeros(16, dtype=torch.uint8, device=dev))
+
+
+def test_example_block(dev):
+    """The block of examples/moe_block.py against float32 in the three layouts,
+    and its gradients. Each FP8 operand is off by up to 2^-4 of a value, evenly
+    spread: 2^-4 / sqrt(3) = 3.6% at most in norm an operand, four operands a
+    forward pass and two more products on the way back; the residual stream
+    and the norms only dilute it. 15% would be a wrong row or weight."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_block.py")
+    spec = importlib.util.spec_from_file_location("moe_block", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    errors = mod.compare()
+    _say(errors)
+    assert len(errors) == 12 and all(e < 0.15 for e in errors.values()), errors
+
+
+def test_workspace_serves_smaller_chunks(dev):
+    """Just past 256 chunks of 1024 slots a chunk doubles: fewer slots then need
+    more rows of the workspace than the most slots do."""
+    _say("sort with more chunks than the plan's most slots take")
+    plan = moe.Plan(263_000, 1, 7, "nopad", 263_000, 128, dev)
+    for t in (262_144, 263_000):
+        ids = _ids(t, 1, 7, t)
+        moe.sort(plan, torch.from_numpy(ids).to(dev))
+        _check_sorted(plan, ids)
+    assert plan.workspace.numel() >= 256 * 7 * 4
