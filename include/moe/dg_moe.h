@@ -69,7 +69,7 @@ long long dg_moe_workspace_bytes(const dg_moe_plan* plan);
  *   contiguous:  from the next multiple of 128 after the group before it;
  * and a row at or past M is dropped. Writes row_of[0..tokens), group_rows
  * (rows kept) and, for the contiguous layout, all of grouped_layout.
- * max_tokens * top_k <= 2^23. tokens == 0 gives groups without rows.
+ * max_tokens * top_k <= 2^22. tokens == 0 gives groups without rows.
  */
 dg_status dg_moe_sort(const dg_moe_plan* plan, const int32_t* topk_ids, int tokens, void* stream);
 
@@ -126,7 +126,7 @@ dg_status dg_moe_combine_bwd(const dg_moe_plan* plan, const void* dy, const void
  *        masked_m [num_groups]; dense: NULL, every row does. Counts are
  *        clamped as by the GEMMs. Other rows do not influence the result and
  *        are not written.
- * inner % 128 == 0; m % 128 == 0 for the contiguous layout, m <= 2^23;
+ * inner % 128 == 0; m % 128 == 0 for the contiguous layout, m <= 2^22;
  * num_groups as in a plan (not read for the dense and contiguous layouts).
  */
 dg_status dg_moe_swiglu_fp8(const void* gu, void* q, float* sfa, const int32_t* rows, int layout, int m,

@@ -12,8 +12,8 @@ namespace {
 using namespace dg::moe;
 
 constexpr long long kMaxBytes = 1LL << 40;
-constexpr long long kMaxSlots = 1LL << 23;  // also keeps workgroups * threads of every grid below 2^32
-constexpr int kMaxGluRows = 1 << 23;
+constexpr long long kMaxSlots = 1LL << 22;  // this and the next two keep workgroups * threads of every grid below 2^32
+constexpr int kMaxGluRows = 1 << 22;
 constexpr int kMaxNormTokens = 1 << 21;
 constexpr int kMaxDim = 1 << 20;
 

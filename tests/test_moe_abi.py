@@ -48,7 +48,7 @@ BAD_PLANS = [
     ({"num_groups": 0}, SHAPE), ({"num_groups": 4097}, UNSUPPORTED), ({"layout": 3, "num_groups": 2049}, UNSUPPORTED),
     ({"rows": -1}, SHAPE), ({"rows": 0}, SHAPE), ({"layout": 1, "rows": 130}, SHAPE), ({"hidden": 192}, SHAPE),
     ({"hidden": 0}, SHAPE), ({"hidden": 1 << 21}, UNSUPPORTED), ({"max_tokens": -1}, SHAPE),
-    ({"max_tokens": (1 << 21) + 1}, UNSUPPORTED), ({"num_groups": 4096, "rows": 1 << 19}, UNSUPPORTED),
+    ({"max_tokens": (1 << 20) + 1}, UNSUPPORTED), ({"num_groups": 4096, "rows": 1 << 19}, UNSUPPORTED),
     ({"layout": 3, "rows": 2 ** 31 - 1, "hidden": 512}, UNSUPPORTED),
 ]
 
@@ -119,7 +119,7 @@ def test_glu_refusals(call):
     assert call(inner=0) == SHAPE and call(inner=200) == SHAPE and call(inner=1 << 21) == UNSUPPORTED
     assert call(m=-1) == SHAPE and call(m=0) == SHAPE and call(layout=1, m=100) == SHAPE and call(layout=7) == SHAPE
     assert call(groups=0) == SHAPE and call(groups=4097) == UNSUPPORTED and call(layout=3, groups=2049) == UNSUPPORTED
-    assert call(layout=3, m=(1 << 23) + 1) == UNSUPPORTED and call(layout=0, rows=None, m=1 << 24) == UNSUPPORTED
+    assert call(layout=3, m=(1 << 22) + 1) == UNSUPPORTED and call(layout=0, rows=None, m=1 << 24) == UNSUPPORTED
     assert call(layout=0, m=-1) == SHAPE
     for layout in (0, 1, 3):
         assert call(layout=layout, m=0, rows=None if layout != 3 else D) == 0
