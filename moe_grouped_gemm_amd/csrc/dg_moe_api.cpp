@@ -31,7 +31,7 @@ dg_status layout_checks(int layout, int m, int num_groups) {
   if (layout == DG_MOE_MASKED && m == 0) return DG_ERR_SHAPE;
   if (layout == DG_MOE_CONTIGUOUS && m % SEGMENT != 0) return DG_ERR_SHAPE;
   if (num_groups > (layout == DG_MOE_NOPAD ? MAX_NOPAD : MAX_GROUPS)) return DG_ERR_UNSUPPORTED;
-  if (layout == DG_MOE_MASKED && (long long)m * num_groups >= (1LL << 31)) return DG_ERR_UNSUPPORTED;
+  if (layout == DG_MOE_MASKED && (long long)m * num_groups >= (1LL << 30)) return DG_ERR_UNSUPPORTED;
   return DG_OK;
 }
 

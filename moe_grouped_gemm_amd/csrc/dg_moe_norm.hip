@@ -51,14 +51,18 @@ __device__ __forceinline__ Team team_of(int waves) {
 
 // Sum over the team, in every lane. Every wave of the workgroup calls it the
 // same number of times; `scratch` may be written again after a later barrier.
+// The waves' sums are read 16 at once, one a lane, and added by rotations: a
+// loop over them would wait for LDS once a wave.
+__device__ __forceinline__ float row_sum(float v) {
+  return add_ror16<1>(add_ror16<2>(add_ror16<4>(add_ror16<8>(v))));
+}
 __device__ __forceinline__ float team_sum(float v, const Team& tm, float* scratch) {
   v = wave_sum(v);
   if (tm.waves == 1) return v;
   if ((threadIdx.x & 63) == 0) scratch[threadIdx.x >> 6] = v;
   __syncthreads();
-  float s = 0.f;
-  for (int w = 0; w < tm.waves; ++w) s += scratch[tm.first_wave + w];
-  return s;
+  const int w = threadIdx.x & 15;
+  return row_sum(w < tm.waves ? scratch[tm.first_wave + w] : 0.f);
 }
 
 __device__ __forceinline__ F8 splat(float v) { return F8{{v, v, v, v, v, v, v, v}}; }
@@ -192,8 +196,8 @@ __global__ __launch_bounds__(MAX_THREADS) void block_norm_kernel(NormArgs p, int
 // leave the workgroup as one row of partial sums for column_sums_kernel.
 template <int VPT, bool FULL>
 __global__ __launch_bounds__(MAX_THREADS) void block_norm_bwd_kernel(NormBwdArgs p, int waves) {
-  __shared__ float scratch[2][3][MAX_WAVES];
-  extern __shared__ float column_sums[];  // [2][hidden] where there are several teams
+  __shared__ f32x4 scratch[2][MAX_WAVES];
+  extern __shared__ __align__(16) float column_sums[];  // [2][hidden] where there are several teams
   const Team tm = team_of(waves);
   const int H = p.hidden;
   const float inv_hidden = 1.0f / (float)H;
@@ -244,7 +248,7 @@ __global__ __launch_bounds__(MAX_THREADS) void block_norm_bwd_kernel(NormBwdArgs
     const bool live = t < p.tokens;
     Row r = next;
     load(next, t + step);
-    float s_a = 0.f, s_b = 0.f, s_c = 0.f;  // of a hn, (dh + rstd_pre a) v yn, hn v yn
+    float s_a = 0.f, s_b = 0.f, s_c = 0.f;  // of a h, (dh + rstd_pre a) v y, h v y: the rstd factors follow
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const F8 d = unpack8(r.dn[i]), h = unpack8(r.h[i]), dh = unpack8(r.dh[i]), y = unpack8(r.y[i]);
@@ -257,37 +261,33 @@ __global__ __launch_bounds__(MAX_THREADS) void block_norm_bwd_kernel(NormBwdArgs
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float a = d.v[e] * w.v[e], hn = h.v[e] * r.rstd_pre, vy = v.v[e] * (y.v[e] * r.rstd_post);
-        s_a = __builtin_fmaf(a, hn, s_a);
+        const float a = d.v[e] * w.v[e], vy = v.v[e] * y.v[e];
+        s_a = __builtin_fmaf(a, h.v[e], s_a);
         s_b = __builtin_fmaf(__builtin_fmaf(r.rstd_pre, a, dh.v[e]), vy, s_b);
-        s_c = __builtin_fmaf(hn, vy, s_c);
+        s_c = __builtin_fmaf(h.v[e], vy, s_c);
       }
     }
     s_a = wave_sum(s_a);
     s_b = wave_sum(s_b);
     s_c = wave_sum(s_c);
     if (waves > 1) {
-      float(*s)[MAX_WAVES] = scratch[round & 1];
-      const int wave = threadIdx.x >> 6;
-      if ((threadIdx.x & 63) == 0) {
-        s[0][wave] = s_a;
-        s[1][wave] = s_b;
-        s[2][wave] = s_c;
-      }
+      f32x4* s = scratch[round & 1];
+      if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = (f32x4){s_a, s_b, s_c, 0.f};
       __syncthreads();
-      s_a = s_b = s_c = 0.f;
-      for (int w = tm.first_wave; w < tm.first_wave + waves; ++w) {
-        s_a += s[0][w];
-        s_b += s[1][w];
-        s_c += s[2][w];
-      }
+      const int w = threadIdx.x & 15;
+      f32x4 part = {0.f, 0.f, 0.f, 0.f};
+      if (w < waves) part = s[tm.first_wave + w];
+      s_a = row_sum(part[0]);
+      s_b = row_sum(part[1]);
+      s_c = row_sum(part[2]);
     }
-    const float m = s_a * inv_hidden;
-    const float along = s_b - r.rstd_pre * m * s_c;  // sum of dH v yn
+    // dH = (dh + rstd_pre a) + to_dres h; sum of dH v yn; dy = out dH v + to_dy y
+    const float to_dres = -(s_a * r.rstd_pre * inv_hidden) * r.rstd_pre * r.rstd_pre;
+    const float along = r.rstd_post * __builtin_fmaf(to_dres, s_c, s_b);
     const float mean = p.post_weight ? along * inv_hidden : 0.0f;
     if (p.gate_kind == DG_MOE_GATE_TOKEN && p.dgate && live && tm.lane_in_team == 0)
       static_cast<float*>(p.dgate)[t] = along;
-    const float out_scale = r.rstd_post * r.gate;
+    const float out = r.rstd_post * r.gate, to_dy = -(out * mean) * r.rstd_post;
     // The pieces are unpacked again rather than kept as floats across the
     // sums: those would not fit the registers, and a spilled value's reload
     // waits for the next row's loads, which were issued before it.
@@ -305,19 +305,19 @@ __global__ __launch_bounds__(MAX_THREADS) void block_norm_bwd_kernel(NormBwdArgs
       F8 dx, dy, dg;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float a = d.v[e] * w.v[e], hn = h.v[e] * r.rstd_pre, yn = y.v[e] * r.rstd_post;
-        const float dres = __builtin_fmaf(r.rstd_pre, __builtin_fmaf(-hn, m, a), dh.v[e]);
-        dpre[i].v[e] = __builtin_fmaf(d.v[e], hn, dpre[i].v[e]);
+        const float dr = d.v[e] * r.rstd_pre;
+        const float dres = __builtin_fmaf(to_dres, h.v[e], __builtin_fmaf(dr, w.v[e], dh.v[e]));
+        dpre[i].v[e] = __builtin_fmaf(dr, h.v[e], dpre[i].v[e]);
         dx.v[e] = p.residual_scale * dres;
-        float gated = dres * r.gate, to = dres * v.v[e];
+        float gated = dres, to = dres * v.v[e];
         if constexpr (FULL) {
           const float g = __builtin_bit_cast(float, e & 1 ? r.g[i][e / 2] & 0xFFFF0000u : r.g[i][e / 2] << 16);
-          dg.v[e] = to * yn;
-          gated = dres * g;
+          dg.v[e] = to * (y.v[e] * r.rstd_post);
+          gated *= g;
           to *= g;
         }
-        dpost[i].v[e] = __builtin_fmaf(gated, yn, dpost[i].v[e]);
-        dy.v[e] = out_scale * __builtin_fmaf(-yn, mean, to);
+        dpost[i].v[e] = __builtin_fmaf(gated, y.v[e] * out, dpost[i].v[e]);
+        dy.v[e] = __builtin_fmaf(out, to, to_dy * y.v[e]);
       }
       if (live && c < H) {
         store_stream(static_cast<uint16_t*>(p.dx) + (size_t)t * H + c, pack8(dx));
@@ -391,20 +391,19 @@ void with_vpt(int vpt, F&& f) {
 }
 
 constexpr int CUS = 256;
-#ifndef V_FWD_WGS
-#define V_FWD_WGS 1
-#endif
-#ifndef V_BWD_WGS
-#define V_BWD_WGS 1
-#endif
+
+// One workgroup a CU: 2 and 4 were slower at every size (8192 rows of 7168 in 87
+// us against 92 and 97). Fewer where they need no more rounds of rows are no
+// faster: a round takes what a CU takes for its rows.
+int row_grid(int tokens) { return std::min(tokens, CUS); }
 
 }  // namespace
 
-int norm_bwd_grid(int tokens) { return std::min(tokens, V_BWD_WGS * CUS); }
+int norm_bwd_grid(int tokens) { return row_grid(tokens); }
 
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t stream) {
   const TeamShape s = team_shape(a.hidden);
-  const int grid = std::min(a.tokens, V_FWD_WGS * CUS);
+  const int grid = row_grid(a.tokens);
   with_vpt(s.vpt, [&](auto v) {
     hipLaunchKernelGGL(block_norm_kernel<decltype(v)::value>, dim3(grid), dim3(s.threads()), 0, stream, a, s.waves);
   });
@@ -413,7 +412,7 @@ hipError_t launch_block_norm(const NormArgs& a, hipStream_t stream) {
 
 hipError_t launch_block_norm_bwd(const NormBwdArgs& a, hipStream_t stream) {
   const TeamShape s = team_shape(a.hidden);
-  const int grid = norm_bwd_grid(a.tokens);
+  const int grid = row_grid(a.tokens);
   if (grid > 0) {
     const size_t lds = s.teams > 1 ? (size_t)2 * a.hidden * sizeof(float) : 0;
     with_vpt(s.vpt, [&](auto v) {
