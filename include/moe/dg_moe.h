@@ -156,7 +156,7 @@ dg_status dg_moe_swiglu_bwd(const void* da, const void* gu, void* dgu, const int
  * h, gate, post_weight and rstd_post must be NULL. post_weight NULL: y enters as
  * it is. n NULL (after the last block): pre_weight and rstd_pre must be NULL.
  * rstd_post and rstd_pre may be NULL where no gradient is wanted. h may be x, and n may be y.
- * hidden % 8 == 0 and at most 32768; tokens <= 2^21; eps >= 0.
+ * hidden % 8 == 0 and at most 16384; tokens <= 2^21; eps >= 0.
  */
 typedef struct dg_moe_norm {
   const void* x;

@@ -46,24 +46,24 @@ __device__ __forceinline__ void store_stream(void* p, T v) {
   __builtin_nontemporal_store(v, reinterpret_cast<T*>(p));
 }
 
+// The lower or upper BF16 of a pair.
+__device__ __forceinline__ float half_of(uint32_t pair, int upper) {
+  return __builtin_bit_cast(float, upper ? pair & 0xFFFF0000u : pair << 16);
+}
+// Rounded to nearest even (v_cvt_pk_bf16_f32).
+__device__ __forceinline__ uint32_t pack2(f32x2 v) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
 __device__ __forceinline__ F8 unpack8(u32x4 p) {
   F8 r;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r.v[2 * i] = __builtin_bit_cast(float, p[i] << 16);
-    r.v[2 * i + 1] = __builtin_bit_cast(float, p[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 8; ++i) r.v[i] = half_of(p[i / 2], i & 1);
   return r;
 }
-
-// Rounded to nearest even (v_cvt_pk_bf16_f32).
 __device__ __forceinline__ u32x4 pack8(const F8& f) {
   u32x4 r;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const bf16x2 b = __builtin_convertvector((f32x2){f.v[2 * i], f.v[2 * i + 1]}, bf16x2);
-    r[i] = __builtin_bit_cast(uint32_t, b);
-  }
+  for (int i = 0; i < 4; ++i) r[i] = pack2((f32x2){f.v[2 * i], f.v[2 * i + 1]});
   return r;
 }
 

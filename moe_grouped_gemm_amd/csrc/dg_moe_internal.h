@@ -15,7 +15,7 @@ constexpr int MAX_NOPAD = 2048;
 constexpr int MAX_TOP_K = 32;
 constexpr int SEGMENT = 128;     // row alignment of the contiguous layout
 constexpr int QBLOCK = 128;      // values per scale
-constexpr int MAX_NORM_HIDDEN = 32768;
+constexpr int MAX_NORM_HIDDEN = 16384;
 
 inline __host__ __device__ int align4(int m) { return (m + 3) / 4 * 4; }
 

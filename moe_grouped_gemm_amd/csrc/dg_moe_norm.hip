@@ -12,7 +12,6 @@
 // memory: every activation is read once and written once.
 
 #include <algorithm>
-#include <type_traits>
 
 #include "dg_moe_device.h"
 
@@ -34,7 +33,7 @@ struct TeamShape {
 
 TeamShape team_shape(int hidden) {
   const int pieces = hidden / 8;
-  const int vpt = pieces <= 1024 ? 1 : pieces <= 2048 ? 2 : 4;
+  const int vpt = pieces <= MAX_THREADS ? 1 : 2;
   const int waves = ((pieces + vpt - 1) / vpt + 63) / 64;
   return {waves, MAX_WAVES / waves, vpt};
 }
@@ -45,7 +44,8 @@ struct Team {
   int team, teams;
 };
 __device__ __forceinline__ Team team_of(int waves) {
-  const int wave = threadIdx.x >> 6, team = wave / waves;
+  // the same in all lanes of a wave: rows' addresses stay in scalar registers
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), team = wave / waves;
   return {waves, team * waves, (int)threadIdx.x - team * waves * 64, team, (int)(blockDim.x >> 6) / waves};
 }
 
@@ -197,7 +197,14 @@ __global__ __launch_bounds__(MAX_THREADS) void block_norm_kernel(NormArgs p, int
 template <int VPT, bool FULL>
 __global__ __launch_bounds__(MAX_THREADS) void block_norm_bwd_kernel(NormBwdArgs p, int waves) {
   __shared__ f32x4 scratch[2][MAX_WAVES];
-  extern __shared__ __align__(16) float column_sums[];  // [2][hidden] where there are several teams
+  // The column vectors in LDS where they do not fit the registers beside a full
+  // gate or a second piece a lane: to y, then to h. (Read from global memory in
+  // the loop they would wait for the next row's loads, issued before them.) At the
+  // end the same memory takes the teams' column sums, [2][hidden]; several teams
+  // have a hidden of at most 4096.
+  constexpr bool IN_LDS = FULL || VPT > 1;
+  constexpr int MOST = MAX_THREADS * 8 * VPT;
+  __shared__ __align__(16) float columns[IN_LDS ? 2 * MOST : MOST];
   const Team tm = team_of(waves);
   const int H = p.hidden;
   const float inv_hidden = 1.0f / (float)H;
@@ -217,11 +224,26 @@ __global__ __launch_bounds__(MAX_THREADS) void block_norm_bwd_kernel(NormBwdArgs
     return v;
   };
   auto to_h = [&](int c) { return p.pre_weight && c < H ? load_f8(p.pre_weight + c) : splat(1.0f); };
-  F8 keep_y, keep_h;  // kept where there is one piece a lane
-  if (VPT == 1) {
+  F8 keep_y, keep_h;
+  if constexpr (IN_LDS) {
+    for (int c = threadIdx.x * 8; c < VPT * waves * 512; c += blockDim.x * 8) {
+      store_f8(columns + c, to_y(c));
+      store_f8(columns + MOST + c, to_h(c));
+    }
+    __syncthreads();
+  } else {
     keep_y = to_y(column(0));
     keep_h = to_h(column(0));
   }
+  // Of pair q of piece i's columns.
+  auto weight_y = [&](int i, int q) {
+    if constexpr (IN_LDS) return *reinterpret_cast<const f32x2*>(columns + column(i) + 2 * q);
+    else return (f32x2){keep_y.v[2 * q], keep_y.v[2 * q + 1]};
+  };
+  auto weight_h = [&](int i, int q) {
+    if constexpr (IN_LDS) return *reinterpret_cast<const f32x2*>(columns + MOST + column(i) + 2 * q);
+    else return (f32x2){keep_h.v[2 * q], keep_h.v[2 * q + 1]};
+  };
   F8 dpost[VPT] = {}, dpre[VPT] = {};
 
   const int step = gridDim.x * tm.teams;
@@ -243,28 +265,33 @@ __global__ __launch_bounds__(MAX_THREADS) void block_norm_bwd_kernel(NormBwdArgs
     if constexpr (FULL) load_row<VPT>(r.g, p.gate, row, H, tm, live);
   };
   Row next;
-  load(next, t);
+  if constexpr (VPT == 1) load(next, t);
   for (int round = 0; round < rounds; ++round, t += step) {
     const bool live = t < p.tokens;
-    Row r = next;
-    load(next, t + step);
+    Row r;
+    if constexpr (VPT == 1) {
+      r = next;
+      load(next, t + step);
+    } else {
+      load(r, t);  // two rows' pieces would not fit the registers
+    }
     float s_a = 0.f, s_b = 0.f, s_c = 0.f;  // of a h, (dh + rstd_pre a) v y, h v y: the rstd factors follow
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const F8 d = unpack8(r.dn[i]), h = unpack8(r.h[i]), dh = unpack8(r.dh[i]), y = unpack8(r.y[i]);
-      const F8 w = VPT == 1 ? keep_h : to_h(column(i));
-      F8 v = VPT == 1 ? keep_y : to_y(column(i));
-      if constexpr (FULL) {
-        const F8 g = unpack8(r.g[i]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v.v[e] *= g.v[e];
-      }
+      for (int q = 0; q < 4; ++q) {
+        const f32x2 w2 = weight_h(i, q), v2 = weight_y(i, q);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float a = d.v[e] * w.v[e], vy = v.v[e] * y.v[e];
-        s_a = __builtin_fmaf(a, h.v[e], s_a);
-        s_b = __builtin_fmaf(__builtin_fmaf(r.rstd_pre, a, dh.v[e]), vy, s_b);
-        s_c = __builtin_fmaf(h.v[e], vy, s_c);
+        for (int e = 0; e < 2; ++e) {
+          const float h = half_of(r.h[i][q], e);
+          const float a = half_of(r.dn[i][q], e) * w2[e];
+          float vy = v2[e] * half_of(r.y[i][q], e);
+          if constexpr (FULL) vy *= half_of(r.g[i][q], e);
+          s_a = __builtin_fmaf(a, h, s_a);
+          s_b = __builtin_fmaf(__builtin_fmaf(r.rstd_pre, a, half_of(r.dh[i][q], e)), vy, s_b);
+          s_c = __builtin_fmaf(h, vy, s_c);
+        }
+        if constexpr (IN_LDS) __builtin_amdgcn_sched_barrier(0);
       }
     }
     s_a = wave_sum(s_a);
@@ -299,35 +326,43 @@ __global__ __launch_bounds__(MAX_THREADS) void block_norm_bwd_kernel(NormBwdArgs
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = column(i);
-      const F8 d = unpack8(r.dn[i]), h = unpack8(r.h[i]), dh = unpack8(r.dh[i]), y = unpack8(r.y[i]);
-      const F8 w = VPT == 1 ? keep_h : to_h(c);
-      const F8 v = VPT == 1 ? keep_y : to_y(c);
-      F8 dx, dy, dg;
+      u32x4 dx, dy, dg;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float dr = d.v[e] * r.rstd_pre;
-        const float dres = __builtin_fmaf(to_dres, h.v[e], __builtin_fmaf(dr, w.v[e], dh.v[e]));
-        dpre[i].v[e] = __builtin_fmaf(dr, h.v[e], dpre[i].v[e]);
-        dx.v[e] = p.residual_scale * dres;
-        float gated = dres, to = dres * v.v[e];
-        if constexpr (FULL) {
-          const float g = __builtin_bit_cast(float, e & 1 ? r.g[i][e / 2] & 0xFFFF0000u : r.g[i][e / 2] << 16);
-          dg.v[e] = to * (y.v[e] * r.rstd_post);
-          gated *= g;
-          to *= g;
+      for (int q = 0; q < 4; ++q) {
+        const f32x2 w2 = weight_h(i, q), v2 = weight_y(i, q);
+        f32x2 dx2, dy2, dg2;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float h = half_of(r.h[i][q], e), y = half_of(r.y[i][q], e);
+          const float dr = half_of(r.dn[i][q], e) * r.rstd_pre;
+          const float dres = __builtin_fmaf(to_dres, h, __builtin_fmaf(dr, w2[e], half_of(r.dh[i][q], e)));
+          dpre[i].v[2 * q + e] = __builtin_fmaf(dr, h, dpre[i].v[2 * q + e]);
+          dx2[e] = p.residual_scale * dres;
+          float gated = dres, to = dres * v2[e];
+          if constexpr (FULL) {
+            const float g = half_of(r.g[i][q], e);
+            dg2[e] = to * (y * r.rstd_post);
+            gated *= g;
+            to *= g;
+          }
+          dpost[i].v[2 * q + e] = __builtin_fmaf(gated, y * out, dpost[i].v[2 * q + e]);
+          dy2[e] = __builtin_fmaf(out, to, to_dy * y);
         }
-        dpost[i].v[e] = __builtin_fmaf(gated, y.v[e] * out, dpost[i].v[e]);
-        dy.v[e] = __builtin_fmaf(out, to, to_dy * y.v[e]);
+        dx[q] = pack2(dx2);
+        dy[q] = pack2(dy2);
+        if constexpr (FULL) dg[q] = pack2(dg2);
+        if constexpr (IN_LDS) __builtin_amdgcn_sched_barrier(0);  // as few registers at once as can be
       }
       if (live && c < H) {
-        store_stream(static_cast<uint16_t*>(p.dx) + (size_t)t * H + c, pack8(dx));
-        if (p.y) store_stream(static_cast<uint16_t*>(p.dy) + (size_t)t * H + c, pack8(dy));
-        if (FULL && p.dgate) store_stream(static_cast<uint16_t*>(p.dgate) + (size_t)t * H + c, pack8(dg));
+        store_stream(static_cast<uint16_t*>(p.dx) + (size_t)t * H + c, dx);
+        if (p.y) store_stream(static_cast<uint16_t*>(p.dy) + (size_t)t * H + c, dy);
+        if (FULL && p.dgate) store_stream(static_cast<uint16_t*>(p.dgate) + (size_t)t * H + c, dg);
       }
     }
   }
 
   float* out = static_cast<float*>(p.workspace) + (size_t)blockIdx.x * 2 * H;
+  if (IN_LDS && tm.teams > 1) __syncthreads();
   for (int turn = 0; turn < tm.teams; ++turn) {
     if (turn > 0) __syncthreads();
     if (turn != tm.team) continue;
@@ -339,11 +374,11 @@ __global__ __launch_bounds__(MAX_THREADS) void block_norm_bwd_kernel(NormBwdArgs
       for (int k = 0; k < 2; ++k) {
         F8 v = k == 0 ? dpost[i] : dpre[i];
         if (turn > 0) {
-          const F8 before = load_f8(column_sums + k * H + c);
+          const F8 before = load_f8(columns + k * H + c);
 #pragma unroll
           for (int e = 0; e < 8; ++e) v.v[e] += before.v[e];
         }
-        if (turn + 1 < tm.teams) store_f8(column_sums + k * H + c, v);
+        if (turn + 1 < tm.teams) store_f8(columns + k * H + c, v);
         else store_f8(out + k * H + c, v);
       }
     }
@@ -383,13 +418,6 @@ __global__ __launch_bounds__(256) void column_sums_kernel(NormBwdArgs p, int par
   }
 }
 
-template <class F>
-void with_vpt(int vpt, F&& f) {
-  if (vpt == 1) f(std::integral_constant<int, 1>{});
-  else if (vpt == 2) f(std::integral_constant<int, 2>{});
-  else f(std::integral_constant<int, 4>{});
-}
-
 constexpr int CUS = 256;
 
 // One workgroup a CU: 2 and 4 were slower at every size (8192 rows of 7168 in 87
@@ -404,9 +432,8 @@ int norm_bwd_grid(int tokens) { return row_grid(tokens); }
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t stream) {
   const TeamShape s = team_shape(a.hidden);
   const int grid = row_grid(a.tokens);
-  with_vpt(s.vpt, [&](auto v) {
-    hipLaunchKernelGGL(block_norm_kernel<decltype(v)::value>, dim3(grid), dim3(s.threads()), 0, stream, a, s.waves);
-  });
+  auto* kernel = s.vpt == 1 ? block_norm_kernel<1> : block_norm_kernel<2>;
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(s.threads()), 0, stream, a, s.waves);
   return hipGetLastError();
 }
 
@@ -414,13 +441,10 @@ hipError_t launch_block_norm_bwd(const NormBwdArgs& a, hipStream_t stream) {
   const TeamShape s = team_shape(a.hidden);
   const int grid = row_grid(a.tokens);
   if (grid > 0) {
-    const size_t lds = s.teams > 1 ? (size_t)2 * a.hidden * sizeof(float) : 0;
-    with_vpt(s.vpt, [&](auto v) {
-      constexpr int VPT = decltype(v)::value;
-      auto* kernel = a.gate_kind == DG_MOE_GATE_FULL ? block_norm_bwd_kernel<VPT, true>
-                                                     : block_norm_bwd_kernel<VPT, false>;
-      hipLaunchKernelGGL(kernel, dim3(grid), dim3(s.threads()), lds, stream, a, s.waves);
-    });
+    const bool full = a.gate_kind == DG_MOE_GATE_FULL;
+    auto* kernel = s.vpt == 1 ? (full ? block_norm_bwd_kernel<1, true> : block_norm_bwd_kernel<1, false>)
+                              : (full ? block_norm_bwd_kernel<2, true> : block_norm_bwd_kernel<2, false>);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(s.threads()), 0, stream, a, s.waves);
     if (hipError_t e = hipGetLastError()) return e;
   }
   hipLaunchKernelGGL(column_sums_kernel, dim3((a.hidden + 63) / 64, 2), dim3(256), 0, stream, a, grid);

@@ -150,7 +150,7 @@ def test_block_norm_refusals():
     assert _norm(post=None) == NULL                            # rstd_post without post_weight
     assert _norm(gate=None) == NULL and _norm(kind=0) == NULL
     assert _norm(kind=4) == SHAPE and _norm(kind=-1) == SHAPE
-    assert _norm(hidden=0) == SHAPE and _norm(hidden=12) == SHAPE and _norm(hidden=32776) == UNSUPPORTED
+    assert _norm(hidden=0) == SHAPE and _norm(hidden=12) == SHAPE and _norm(hidden=16392) == UNSUPPORTED
     assert _norm(tokens=-1) == SHAPE and _norm(tokens=(1 << 21) + 1) == UNSUPPORTED
     assert _norm(eps=-1.0) == SHAPE and _norm(eps=float("nan")) == SHAPE
     assert _norm(x=A + 2) == ALIGN and _norm(gate=D + 4) == ALIGN and _norm(kind=2, gate=D + 2) == ALIGN
@@ -168,7 +168,7 @@ def test_block_norm_bwd_refusals():
     assert _norm_bwd(dn=None) == NULL and _norm_bwd(y=None) == NULL and _norm_bwd(post=None) == NULL
     assert _norm_bwd(kind=0) == NULL and _norm_bwd(kind=5) == SHAPE
     assert _norm_bwd(kind=0, gate=None) == NULL                # dgate without a gate
-    assert _norm_bwd(hidden=20) == SHAPE and _norm_bwd(hidden=32776) == UNSUPPORTED and _norm_bwd(tokens=-2) == SHAPE
+    assert _norm_bwd(hidden=20) == SHAPE and _norm_bwd(hidden=16392) == UNSUPPORTED and _norm_bwd(tokens=-2) == SHAPE
     assert _norm_bwd(dx=D + 8) == ALIGN and _norm_bwd(ws=C + 4) == ALIGN and _norm_bwd(dpre=B + 1) == ALIGN
     need = moe.lib().dg_moe_block_norm_workspace_bytes(4, 64)
     assert need > 0 and _norm_bwd(ws_bytes=need - 1) == SHAPE
