@@ -27,52 +27,52 @@ __device__ __forceinline__ int nopad_rows(const GluArgs& p) {
   return (int)min(n, (long long)p.m);
 }
 
-// How workgroups share rows.
-//   ROWS_ONE   one row a workgroup. Whether it holds a token is the same in all
-//              lanes, asked before anything is stored, and so comes by scalar
-//              loads, soonest: 57 us against 65 with a loop over rows around it
-//              (32000 rows of 2048, contiguous layout).
-//   ROWS_LOOP  as many workgroups as fill the device a few times, each going on
-//              to later rows of its group: for the masked layout where G * max_m
-//              rows, most of them empty in decoding, would each cost a workgroup:
-//              2 rows in each of 256 groups of 256 take 10.4 us, a row a
-//              workgroup 16.8 (and full groups 114 against 109).
-//   ROWS_MANY  several rows a workgroup, 16 lanes a block, for an inner of at
-//              most 1024: 29416 rows of 256 take 10 us, a row a workgroup 25.
-enum { ROWS_ONE, ROWS_LOOP, ROWS_MANY };
+// Row of the i-th turn of a group's workgroups, a permutation of each 8 << chunk
+// rows: workgroups go round the 8 XCDs, and this gives an XCD 1 << chunk rows
+// in succession, whose scales of a block are (part of) one line of sfa and fill it
+// in one L2. Without it 32000 rows of 2048 wrote 79 MB where 66 are needed, and
+// took 57 us against 51. Which XCD comes first goes by the group: in the masked
+// layout the first rows of every group hold tokens, the last ones none.
+__device__ __forceinline__ int turn_row(int i, int g, int chunk) {
+  const int low = (8 << chunk) - 1;
+  return (i & ~low) + (((i + g) & 7) << chunk) + ((i & low) >> 3);
+}
 
 // Calls f(row of the buffer, group, row in the group, block) for every 128-value
-// block of every row that holds a token.
-template <int MODE, class F>
-__device__ __forceinline__ void for_held_blocks(const GluArgs& p, int row_step, F&& f) {
+// block of every row that holds a token, 16 lanes a block. A workgroup takes one
+// row, or with MANY the `row_step` rows that 16 lanes a block leave it room for
+// (an inner of at most 1024: 29416 rows of 256 take 9 us, a row a workgroup 26).
+// With one row, whether it holds a token is the same in all lanes, asked before
+// anything is stored, and so comes by scalar loads, soonest: with a loop over
+// rows around it, 65 us for 32000 rows of 2048 in place of 57. A row without a
+// token costs its workgroup's launch: 16 us for 256 groups of 256 rows of which
+// 2 hold tokens (13 with fewer workgroups that loop, but 111 against 99 with all
+// rows held).
+template <bool MANY, class F>
+__device__ __forceinline__ void for_held_blocks(const GluArgs& p, int row_step, int chunk, F&& f) {
   const int blocks = p.inner / QBLOCK, at = threadIdx.x >> 4;
   const int g = blockIdx.y;
   int rows = p.m;  // rows below this hold tokens (contiguous: as their ids say)
   if (p.layout == DG_MOE_MASKED) rows = min(p.rows[g], p.m);
   if (p.layout == DG_MOE_NOPAD) rows = nopad_rows(p);
-  auto row_blocks = [&](int r) {
-    for (int b = at; b < blocks; b += blockDim.x >> 4) f((size_t)g * p.m + r, g, r, b);
-  };
-  if constexpr (MODE == ROWS_ONE) {
-    const int r = blockIdx.x;
-    if (r < rows && (p.layout != DG_MOE_CONTIGUOUS || p.rows[r] >= 0)) row_blocks(r);
-  } else if constexpr (MODE == ROWS_LOOP) {
-    for (int r = blockIdx.x; r < rows; r += gridDim.x) row_blocks(r);
+  if constexpr (MANY) {
+    const int sub = at / blocks, r = blockIdx.x * row_step + sub;
+    if (sub < row_step && r < rows && (p.layout != DG_MOE_CONTIGUOUS || p.rows[r] >= 0))
+      f((size_t)g * p.m + r, g, r, at - sub * blocks);
   } else {
-    const int sub = at / blocks, b = at - sub * blocks;
-    if (sub >= row_step) return;
-    for (int r = blockIdx.x * row_step + sub; r < rows; r += gridDim.x * row_step)
-      if (p.layout != DG_MOE_CONTIGUOUS || p.rows[r] >= 0) f((size_t)g * p.m + r, g, r, b);
+    const int r = turn_row(blockIdx.x, g, chunk);
+    if (r < rows && (p.layout != DG_MOE_CONTIGUOUS || p.rows[r] >= 0))
+      for (int b = at; b < blocks; b += blockDim.x >> 4) f((size_t)g * p.m + r, g, r, b);
   }
 }
 
 // Bound by memory: 4 bytes read and 1 + 4/128 written a value, about 20
 // instructions each between.
-template <bool E8, int MODE>
-__global__ __launch_bounds__(GLU_THREADS) void swiglu_fp8_kernel(GluArgs p, int row_step) {
+template <bool E8, bool MANY>
+__global__ __launch_bounds__(GLU_THREADS) void swiglu_fp8_kernel(GluArgs p, int row_step, int chunk) {
   const size_t I = p.inner;
   const int blocks = p.inner / QBLOCK, ld = align4(p.m), l16 = threadIdx.x & 15;
-  for_held_blocks<MODE>(p, row_step, [&](size_t row, int g, int r, int b) {
+  for_held_blocks<MANY>(p, row_step, chunk, [&](size_t row, int g, int r, int b) {
     const uint16_t* src = p.gu + row * 2 * I + b * QBLOCK + l16 * 8;
     const u32x4 gate_raw = load_stream16(src), up_raw = load_stream16(src + I);
     const F8 gate = unpack8(gate_raw), up = unpack8(up_raw);
@@ -86,11 +86,11 @@ __global__ __launch_bounds__(GLU_THREADS) void swiglu_fp8_kernel(GluArgs p, int 
 }
 
 // Bound by memory: 6 bytes read and 4 written a value.
-template <int MODE>
-__global__ __launch_bounds__(GLU_THREADS) void swiglu_bwd_kernel(GluArgs p, int row_step) {
+template <bool MANY>
+__global__ __launch_bounds__(GLU_THREADS) void swiglu_bwd_kernel(GluArgs p, int row_step, int chunk) {
   const size_t I = p.inner;
   const int l16 = threadIdx.x & 15;
-  for_held_blocks<MODE>(p, row_step, [&](size_t row, int, int, int b) {
+  for_held_blocks<MANY>(p, row_step, chunk, [&](size_t row, int, int, int b) {
     const size_t c = b * QBLOCK + l16 * 8;
     const u32x4 gate_raw = load_stream16(p.gu + row * 2 * I + c), up_raw = load_stream16(p.gu + row * 2 * I + I + c);
     const u32x4 da_raw = load_stream16(p.da + row * I + c);
@@ -107,51 +107,40 @@ __global__ __launch_bounds__(GLU_THREADS) void swiglu_bwd_kernel(GluArgs p, int 
   });
 }
 
-// Most workgroups of the masked layout.
-constexpr int MASKED_WORKGROUPS = 16384;
-
 struct GluShape {
   dim3 grid;
-  int threads, row_step, mode;
+  int threads, row_step, chunk;
 };
 GluShape glu_shape(const GluArgs& a) {
-  const int pieces = a.inner / 8;
-  GluShape s;
+  const int pieces = a.inner / 8, groups = a.layout == DG_MOE_MASKED ? a.num_groups : 1;
+  GluShape s{};
   s.row_step = std::max(1, 256 / pieces);
-  s.mode = s.row_step > 1 ? ROWS_MANY : ROWS_ONE;
-  s.threads = s.row_step > 1 ? 256 : even_threads(pieces, GLU_THREADS);
-  const int steps = (a.m + s.row_step - 1) / s.row_step;
-  s.grid = dim3(steps);
-  if (a.layout == DG_MOE_MASKED) {
-    const int most = std::max(1, MASKED_WORKGROUPS / a.num_groups);
-    if (steps > most && s.mode == ROWS_ONE) s.mode = ROWS_LOOP;
-    s.grid = dim3(std::min(steps, most), a.num_groups);
+  if (s.row_step > 1) {
+    s.threads = 256;
+    s.grid = dim3((a.m + s.row_step - 1) / s.row_step, groups);
+    return s;
   }
+  s.threads = even_threads(pieces, GLU_THREADS);
+  for (s.chunk = 5; s.chunk > 0 && a.m < 8 << s.chunk;) --s.chunk;  // up to a line of sfa, 32 rows
+  s.grid = dim3((a.m + (8 << s.chunk) - 1) / (8 << s.chunk) * (8 << s.chunk), groups);
   return s;
-}
-
-template <int MODE>
-void launch_fp8(const GluArgs& a, const GluShape& s, bool ue8m0, hipStream_t stream) {
-  hipLaunchKernelGGL((ue8m0 ? swiglu_fp8_kernel<true, MODE> : swiglu_fp8_kernel<false, MODE>), s.grid, dim3(s.threads),
-                     0, stream, a, s.row_step);
 }
 
 }  // namespace
 
 hipError_t launch_swiglu_fp8(const GluArgs& a, bool ue8m0, hipStream_t stream) {
   const GluShape s = glu_shape(a);
-  if (s.mode == ROWS_ONE) launch_fp8<ROWS_ONE>(a, s, ue8m0, stream);
-  else if (s.mode == ROWS_LOOP) launch_fp8<ROWS_LOOP>(a, s, ue8m0, stream);
-  else launch_fp8<ROWS_MANY>(a, s, ue8m0, stream);
+  const bool many = s.row_step > 1;
+  auto* kernel = ue8m0 ? (many ? swiglu_fp8_kernel<true, true> : swiglu_fp8_kernel<true, false>)
+                       : (many ? swiglu_fp8_kernel<false, true> : swiglu_fp8_kernel<false, false>);
+  hipLaunchKernelGGL(kernel, s.grid, dim3(s.threads), 0, stream, a, s.row_step, s.chunk);
   return hipGetLastError();
 }
 
 hipError_t launch_swiglu_bwd(const GluArgs& a, hipStream_t stream) {
   const GluShape s = glu_shape(a);
-  auto* kernel = s.mode == ROWS_ONE    ? swiglu_bwd_kernel<ROWS_ONE>
-                 : s.mode == ROWS_LOOP ? swiglu_bwd_kernel<ROWS_LOOP>
-                                       : swiglu_bwd_kernel<ROWS_MANY>;
-  hipLaunchKernelGGL(kernel, s.grid, dim3(s.threads), 0, stream, a, s.row_step);
+  auto* kernel = s.row_step > 1 ? swiglu_bwd_kernel<true> : swiglu_bwd_kernel<false>;
+  hipLaunchKernelGGL(kernel, s.grid, dim3(s.threads), 0, stream, a, s.row_step, s.chunk);
   return hipGetLastError();
 }
 
