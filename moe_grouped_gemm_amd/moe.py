@@ -171,10 +171,14 @@ class Plan:
             raise ValueError(f"a plan lives on a GPU, got {device}")
         self.device = device if device.index is not None else torch.device("cuda", torch.cuda.current_device())
         self._index = self.device.index
-        self.row_of = torch.full((self.max_tokens, self.top_k), -1, dtype=_I32, device=device)
-        self.group_rows = torch.zeros(self.num_groups, dtype=_I32, device=device)
-        self.grouped_layout = (torch.full((self.rows,), -1, dtype=_I32, device=device)
-                               if layout == "contiguous" else None)
+        # one allocation, each part 16-byte aligned; -1: no slot has a row yet, no group has rows
+        slots, rows_of_layout = self.max_tokens * self.top_k, self.rows if layout == "contiguous" else 0
+        at_rows = (slots + 3) // 4 * 4
+        at_layout = at_rows + (self.num_groups + 3) // 4 * 4
+        ints = torch.full((at_layout + rows_of_layout,), -1, dtype=_I32, device=device)
+        self.row_of = ints[:slots].view(self.max_tokens, self.top_k)
+        self.group_rows = ints[at_rows:at_rows + self.num_groups]
+        self.grouped_layout = ints[at_layout:] if layout == "contiguous" else None
         self.workspace = torch.empty(size, dtype=torch.uint8, device=device)
         s = self._struct
         s.row_of, s.group_rows, s.grouped_layout = (self.row_of.data_ptr(), self.group_rows.data_ptr(),
