@@ -54,7 +54,7 @@ long long plan_workspace(const dg_moe_plan* p) {
 dg_status plan_checks(const dg_moe_plan* p, int tokens, RouteArgs& a) {
   if (dg_status s = plan_sizes(p)) return s;
   if (tokens < 0 || tokens > p->max_tokens) return DG_ERR_SHAPE;
-  if (!p->row_of || !p->group_rows || !p->workspace) return DG_ERR_NULL;
+  if ((!p->row_of && p->max_tokens > 0) || !p->group_rows || !p->workspace) return DG_ERR_NULL;
   if (p->layout == DG_MOE_CONTIGUOUS && p->rows > 0 && !p->grouped_layout) return DG_ERR_NULL;
   if (!aligned4b(p->row_of) || !aligned4b(p->group_rows) || !aligned4b(p->grouped_layout) || !aligned16(p->workspace))
     return DG_ERR_ALIGN;

@@ -1,5 +1,5 @@
 // Device code shared by the steps around the GEMMs: BF16 vectors, sums over
-// a wave or workgroup, and the quantisation of a 128-value block.
+// a wave, and the quantisation of a 128-value block.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -93,18 +93,6 @@ __device__ __forceinline__ float wave_sum(float v) {
   for (int i = 0; i < 4; ++i)
     row[i] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 16 * i));
   return (row[0] + row[1]) + (row[2] + row[3]);
-}
-
-// Sum over the workgroup's waves, in every lane. `scratch` holds a float a
-// wave and may be written again once every wave has passed a later barrier.
-__device__ __forceinline__ float block_sum(float v, float* scratch, int waves) {
-  v = wave_sum(v);
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  if (lane == 0) scratch[wave] = v;
-  __syncthreads();
-  float s = 0.f;
-  for (int w = 0; w < waves; ++w) s += scratch[w];
-  return s;
 }
 
 // v rotated by N lanes within each row of 16 lanes (DPP row_ror).

@@ -317,10 +317,13 @@ __global__ __launch_bounds__(SMALL_THREADS) void small_kernel(RouteArgs p, MoveA
   }
   if (wave == 0 && lane < k) p.row_of[t * k + lane] = row;
   if constexpr (MODE != MOVE_NONE) {
+    // Spread to every 16 lanes here, with all lanes active: below, some of a
+    // wave's blocks may be past the token's end, the ones with rows 16.. first.
+    const int low = __shfl(row, l16), high = k > 16 ? __shfl(row, 16 + l16) : -1;
     for (int b = tid >> 4; b < blocks; b += SMALL_THREADS / 16) {
       if (b >= SMALL_THREADS / 16) raw = load16(m.x + (size_t)t * p.hidden + b * QBLOCK + l16 * 8);
-      for (int j0 = 0; j0 < k; j0 += 16)
-        put_block<MODE>(p, m, raw, b, l16, __shfl(row, j0 + l16), min(k - j0, 16));
+      for (int j0 = 0; j0 < k; j0 += 16)  // (a loop: one copy of the code, which a cold launch has to fetch)
+        put_block<MODE>(p, m, raw, b, l16, j0 ? high : low, min(k - j0, 16));
     }
   }
 }

@@ -153,6 +153,18 @@ def test_sort_extreme_ids(dev, layout, t):
         _check_sorted(plan, ids)
 
 
+def test_empty_plan(dev):
+    _say("a plan for no tokens")
+    for layout, rows in (("nopad", 0), ("contiguous", 0), ("masked", 4)):
+        plan = moe.Plan(0, 2, 4, layout, rows, 128, dev)
+        moe.sort(plan, torch.empty(0, 2, dtype=torch.int32, device=dev))
+        assert plan.group_rows.tolist() == [0, 0, 0, 0]
+        none = torch.empty(0, 128, dtype=torch.bfloat16, device=dev)
+        xp = torch.zeros(plan.rows_shape, dtype=torch.bfloat16, device=dev)
+        moe.dispatch(plan, none, xp, topk_ids=torch.empty(0, 2, dtype=torch.int32, device=dev))
+        moe.combine(plan, xp, none)
+
+
 def test_plan_serves_fewer_tokens_and_none(dev):
     _say("plan with fewer tokens")
     for layout in ("contiguous", "nopad", "masked"):
@@ -186,6 +198,8 @@ MOVES = [
     ("nopad", 3, 2, 4, 128, None), ("nopad", 130, 4, 8, 1920, None), ("nopad", 601, 8, 32, 384, 3000),
     ("contiguous", 17, 3, 5, 256, None), ("contiguous", 333, 4, 8, 2048, 1024), ("contiguous", 1500, 3, 40, 128, None),
     ("nopad", 2100, 4, 16, 512, None),
+    # more than 16 slots a token, with blocks that leave part of a wave idle
+    ("masked", 9, 32, 40, 128, 16), ("contiguous", 30, 17, 64, 4224, None), ("nopad", 200, 24, 32, 640, None),
 ]
 
 
@@ -686,6 +700,32 @@ def test_offsets_past_32_bits(dev):
     vals, scales = M.quantize(_f64(x).astype(np.float32), False)
     assert np.array_equal(q[rows - 1].float().cpu().numpy(), vals[0]) and np.array_equal(_f64(sfa[:, rows - 1]), scales[0])
     assert np.array_equal(q[rows - 300].float().cpu().numpy(), vals[2])
+
+
+def test_norm_offsets_past_32_bits(dev):
+    """The last of 300000 rows of 7168 (2.15e9 elements) as when normalised alone."""
+    _say("norm offsets past 32 bits")
+    t, h, last = 300_000, 7168, 5
+    d = _norm_inputs(last, h, "channel")
+    x, y = torch.zeros(t, h, dtype=torch.bfloat16, device=dev), torch.zeros(t, h, dtype=torch.bfloat16, device=dev)
+    x[-last:], y[-last:] = d["x"], d["y"]
+    r1, r2 = torch.zeros(t, device=dev), torch.zeros(t, device=dev)
+    small = [torch.zeros(last, h, dtype=torch.bfloat16, device=dev) for _ in range(4)]
+    s1, s2 = torch.zeros(last, device=dev), torch.zeros(last, device=dev)
+    moe.block_norm(d["x"], d["y"], d["post"], d["gate"], d["pre"], small[0], small[1], s1, s2)
+    moe.block_norm(x, y, d["post"], d["gate"], d["pre"], x, y, r1, r2)               # in place
+    assert torch.equal(x[-last:], small[0]) and torch.equal(y[-last:], small[1])
+    assert torch.equal(r1[-last:], s1) and torch.equal(r2[-last:], s2)
+    # and the gradient, dh = h and dn = n standing in
+    cols = [torch.zeros(h, device=dev) for _ in range(3)]
+    moe.block_norm_bwd(small[0], small[1], small[0], d["y"], d["post"], d["gate"], d["pre"], s1, s2, small[2], small[3],
+                       *cols, moe.block_norm_workspace(last, h, dev))
+    yin = torch.zeros(t, h, dtype=torch.bfloat16, device=dev)
+    yin[-last:] = d["y"]
+    dx, dy = torch.zeros_like(x), torch.zeros_like(x)
+    moe.block_norm_bwd(x, y, x, yin, d["post"], d["gate"], d["pre"], r1, r2, dx, dy, None, None, None,
+                       moe.block_norm_workspace(t, h, dev))
+    assert torch.equal(dx[-last:], small[2]) and torch.equal(dy[-last:], small[3]) and not dx[:-last].any()
 
 
 def test_glu_offsets_past_32_bits(dev):
