@@ -67,7 +67,7 @@ __device__ __forceinline__ void for_held_blocks(const GluArgs& p, int row_step, 
 }
 
 // Bound by memory: 4 bytes read and 1 + 4/128 written a value, about 20
-// instructions each between.
+// instructions each between. 32000 rows of 2048: 50 us (6.6 TB/s).
 template <bool E8, bool MANY>
 __global__ __launch_bounds__(GLU_THREADS) void swiglu_fp8_kernel(GluArgs p, int row_step, int chunk) {
   const size_t I = p.inner;
@@ -85,7 +85,8 @@ __global__ __launch_bounds__(GLU_THREADS) void swiglu_fp8_kernel(GluArgs p, int 
   });
 }
 
-// Bound by memory: 6 bytes read and 4 written a value.
+// Bound by memory: 6 bytes read and 4 written a value. 29416 rows of 2048: 92 us
+// (6.4 TB/s).
 template <bool MANY>
 __global__ __launch_bounds__(GLU_THREADS) void swiglu_bwd_kernel(GluArgs p, int row_step, int chunk) {
   const size_t I = p.inner;
