@@ -33,11 +33,6 @@ constexpr int SORT_THREADS = 1024;
 constexpr int SORT_WAVES = SORT_THREADS / 64;
 constexpr int MAX_CHUNKS = 256;
 
-// Up to here every workgroup of the second pass counts all the ids itself, which
-// saves the first pass: 7.9 us against 9.7 for sort and dispatch of 4096 slots
-// (32 groups, rows of 256), 8.5 against 9.6 at 8192, 10.5 against 10.0 at 16384.
-constexpr int COUNT_SLOTS = 8192;
-
 __host__ __device__ inline int chunk_slots(int slots) {
   const int per = (slots + MAX_CHUNKS - 1) / MAX_CHUNKS;
   return per <= SORT_THREADS ? SORT_THREADS : (per + SORT_THREADS - 1) / SORT_THREADS * SORT_THREADS;
@@ -104,7 +99,6 @@ __global__ __launch_bounds__(SORT_THREADS) void count_kernel(RouteArgs p, int ch
   for (int g = tid; g < G; g += SORT_THREADS) out[g] = count[g];
 }
 
-template <bool COUNT>
 __global__ __launch_bounds__(SORT_THREADS) void rank_kernel(RouteArgs p, int chunk, int chunks) {
   __shared__ int next[MAX_GROUPS];   // rows of the group before this chunk, then its next free row
   __shared__ int total[MAX_GROUPS];  // rows of the group
@@ -116,31 +110,22 @@ __global__ __launch_bounds__(SORT_THREADS) void rank_kernel(RouteArgs p, int chu
   for (int g = tid; g < G; g += SORT_THREADS) next[g] = total[g] = 0;
   __syncthreads();
   const int begin = blockIdx.x * chunk, end = min(begin + chunk, N);
-  if constexpr (COUNT) {
-    for (int i = tid; i < N; i += SORT_THREADS) {
-      const int e = p.ids[i];
-      if (e < 0 || e >= G) continue;
-      atomicAdd(&total[e], 1);
-      if (i < begin) atomicAdd(&next[e], 1);
-    }
-  } else {
-    // The table of counts, summed over chunks: as many chunks at once as there
-    // are threads for.
-    int width = 1;
-    while (width < G && width < SORT_THREADS) width <<= 1;
-    const int slices = SORT_THREADS / width, slice = tid / width;
-    for (int g = tid & (width - 1); g < G; g += width) {
-      int before = 0, all = 0;
+  // The table of counts, summed over chunks: as many chunks at once as there
+  // are threads for.
+  int width = 1;
+  while (width < G && width < SORT_THREADS) width <<= 1;
+  const int slices = SORT_THREADS / width, slice = tid / width;
+  for (int g = tid & (width - 1); g < G; g += width) {
+    int before = 0, all = 0;
 #pragma unroll 4
-      for (int c = slice; c < chunks; c += slices) {
-        const int v = counts[(size_t)c * G + g];
-        all += v;
-        before += c < (int)blockIdx.x ? v : 0;
-      }
-      if (all) {
-        atomicAdd(&total[g], all);
-        atomicAdd(&next[g], before);
-      }
+    for (int c = slice; c < chunks; c += slices) {
+      const int v = counts[(size_t)c * G + g];
+      all += v;
+      before += c < (int)blockIdx.x ? v : 0;
+    }
+    if (all) {
+      atomicAdd(&total[g], all);
+      atomicAdd(&next[g], before);
     }
   }
   __syncthreads();
@@ -244,89 +229,88 @@ __global__ __launch_bounds__(DISPATCH_THREADS) void dispatch_kernel(RouteArgs p,
   }
 }
 
-// Few slots: one launch sorts and moves. A workgroup a token finds the rows of
-// its slots by itself, by comparing them with all the ids, 64 at a time in a
-// ballot: the rank of a slot is the number of equal ids before it, and its
-// group starts after the smaller ids (no-padding) or after their groups'
-// segments (contiguous, from counts in LDS). Its first piece of the token is
-// on the way meanwhile. The workgroups after the tokens' write the groups'
-// rows and the layout.
-constexpr int SMALL_THREADS = 512;
-constexpr int SMALL_WAVES = SMALL_THREADS / 64;
-// The comparisons grow with the square of the slots: measured (masked, FP8, 7168
-// values) 5.6 us against 9.0 of sort and dispatch at 512 slots, 9.8 against
-// 11.4 at 2048, 18.9 against 15.2 at 4096.
-constexpr int SMALL_SLOTS = 2048;
-constexpr int FILL_ROWS = 2048;  // rows of grouped_layout a workgroup writes
+// Few slots: one launch sorts and moves. A workgroup takes a few tokens, counts
+// all the ids itself -- those of the slots before its own, and all of them --
+// finds the groups' starts from the counts, ranks its own slots as rank_kernel
+// does and moves its tokens; in the contiguous layout every workgroup writes a
+// share of the rows' groups, and there may be workgroups without tokens for that.
+// Bound by latency: a launch costs more than the counting, which is the same in
+// every workgroup, LDS atomics on whole numbers (their order does not matter)
+// that grow with the slots. Against sort and dispatch as launches of their own
+// (no-padding, 32 groups, FP8): 512 slots of 256 values 4.3 us and 8.5, 4096 5.9 and
+// 9.7, 8192 7.4 and 9.6, 16384 10.6 and 10.0; of 7168 values, 4096 slots 12.1 us
+// and 15.0, 16384 43.6 and 40.2. Ranking by comparing each slot with all ids took as
+// long at 40 slots and 14 us at 4096.
+constexpr int FEW_SLOTS = 8192;
+constexpr int FEW_THREADS = 512;
+constexpr int FEW_WORKGROUPS = 512;  // 256: slower with long rows, 1024: with many slots
+constexpr int FILL_ROWS = 2048;      // rows of grouped_layout that are worth a workgroup
+// A workgroup's slots are at most its share of them and one token's more.
+static_assert(FEW_SLOTS / FEW_WORKGROUPS + MAX_TOP_K <= 64, "a wave ranks a workgroup's slots");
 
 template <int MODE>
-__global__ __launch_bounds__(SMALL_THREADS) void small_kernel(RouteArgs p, MoveArgs m) {
-  __shared__ int count[MAX_GROUPS];
-  __shared__ int first[MAX_GROUPS];
-  __shared__ int part[SMALL_WAVES][MAX_TOP_K];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = tid & 15;
+__global__ __launch_bounds__(FEW_THREADS) void few_kernel(RouteArgs p, MoveArgs m, int tokens_each) {
+  __shared__ int next[MAX_GROUPS];   // rows of the group before these tokens, then its next free row
+  __shared__ int total[MAX_GROUPS];  // rows of the group
+  __shared__ int first[MAX_GROUPS];  // first row of the group
+  __shared__ int rows[64];           // of this workgroup's slots
+  const int tid = threadIdx.x, l16 = tid & 15;
   const int G = p.num_groups, N = p.tokens * p.top_k, k = p.top_k;
-  const bool fill = (int)blockIdx.x >= p.tokens;
-  const bool counted = fill || p.layout == DG_MOE_CONTIGUOUS;
-  const int t = fill ? 0 : blockIdx.x, blocks = p.hidden / QBLOCK;
+  const int t0 = blockIdx.x * tokens_each, tokens = max(min(tokens_each, p.tokens - t0), 0);
+  const int begin = t0 * k, slots = tokens * k;
 
+  // On their way while the ids are counted: the first piece of the tokens, the
+  // workgroup's own ids.
+  const int blocks = p.hidden / QBLOCK, first_item = tid >> 4;
   u32x4 raw = {};
-  if (MODE != MOVE_NONE && !fill && (tid >> 4) < blocks) raw = load16(m.x + (size_t)t * p.hidden + tid * 8);
-  const int own = !fill && lane < k ? p.ids[t * k + lane] : -1;
-  if (counted) {
-    for (int g = tid; g < G; g += SMALL_THREADS) count[g] = 0;
-    __syncthreads();
-  }
-  int before = 0;  // lane j: ids that come before slot j
-  for (int n0 = wave * 64; n0 < N; n0 += SMALL_THREADS) {
-    const int n = n0 + lane;
-    const int e = n < N ? p.ids[n] : -1;
-    const bool valid = e >= 0 && e < G;
-    if (counted && valid) atomicAdd(&count[e], 1);
-    if (fill) continue;
-    for (int j = 0; j < k; ++j) {
-      const int ej = __builtin_amdgcn_readlane(own, j);
-      const bool hit = valid && ((e == ej && n < t * k + j) || (p.layout == DG_MOE_NOPAD && e < ej));
-      const int c = __popcll(__ballot(hit));
-      if (lane == j) before += c;
-    }
-  }
-  if (lane < MAX_TOP_K) part[wave][lane] = before;
+  if (MODE != MOVE_NONE && first_item < tokens * blocks)
+    raw = load16(m.x + (size_t)t0 * p.hidden + first_item * QBLOCK + l16 * 8);
+  const int e = tid < slots ? p.ids[begin + tid] : -1;
+
+  for (int g = tid; g < G; g += FEW_THREADS) next[g] = total[g] = 0;
   __syncthreads();
-  if (fill) {
-    const int f = blockIdx.x - p.tokens, fills = gridDim.x - p.tokens;
-    group_starts<SMALL_THREADS>(p, count, first, f == 0);
-    if (p.layout == DG_MOE_CONTIGUOUS) fill_layout(p, count, first, f * SMALL_THREADS + tid, fills * SMALL_THREADS);
-    return;
+#pragma unroll 4
+  for (int i = tid; i < N; i += FEW_THREADS) {
+    const int id = p.ids[i];
+    if (id < 0 || id >= G) continue;
+    atomicAdd(&total[id], 1);
+    if (i < begin) atomicAdd(&next[id], 1);
   }
-  if (p.layout == DG_MOE_CONTIGUOUS) {
-    for (int j = wave; j < k; j += SMALL_WAVES) {
-      const int ej = min(__builtin_amdgcn_readlane(own, j), G);
-      int s = 0;
-      for (int g = lane; g < ej; g += 64) s += (count[g] + SEGMENT - 1) / SEGMENT * SEGMENT;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
-      if (lane == 0) first[j] = s;
+  __syncthreads();
+  if (p.layout == DG_MOE_MASKED) {
+    for (int g = tid; g < G; g += FEW_THREADS) {
+      next[g] += g * p.rows;
+      if (blockIdx.x == 0) p.group_rows[g] = min(total[g], p.rows);
     }
-    __syncthreads();
+  } else {
+    group_starts<FEW_THREADS>(p, total, first, blockIdx.x == 0);
+    for (int g = tid; g < G; g += FEW_THREADS) next[g] += first[g];
   }
-  int row = -1;
-  if (lane < k && own >= 0 && own < G) {
-    int rank = 0;
-#pragma unroll
-    for (int w = 0; w < SMALL_WAVES; ++w) rank += part[w][lane];
-    const int start = p.layout == DG_MOE_MASKED ? own * p.rows : p.layout == DG_MOE_CONTIGUOUS ? first[lane] : 0;
-    if ((p.layout == DG_MOE_MASKED ? rank : start + rank) < p.rows) row = start + rank;
+
+  __syncthreads();
+
+  if (tid < 64) {
+    const bool valid = e >= 0 && e < G;
+    const uint64_t peers = same_key(e, valid, 32 - __builtin_clz(G));
+    int row = -1;
+    if (valid) {
+      row = next[e] + __popcll(peers & ((1ull << tid) - 1));
+      if (row >= (p.layout == DG_MOE_MASKED ? (e + 1) * p.rows : p.rows)) row = -1;
+    }
+    rows[tid] = row;
+    if (tid < slots) p.row_of[begin + tid] = row;
   }
-  if (wave == 0 && lane < k) p.row_of[t * k + lane] = row;
+  if (p.layout == DG_MOE_CONTIGUOUS)
+    fill_layout(p, total, first, blockIdx.x * FEW_THREADS + tid, gridDim.x * FEW_THREADS);
   if constexpr (MODE != MOVE_NONE) {
-    // Spread to every 16 lanes here, with all lanes active: below, some of a
-    // wave's blocks may be past the token's end, the ones with rows 16.. first.
-    const int low = __shfl(row, l16), high = k > 16 ? __shfl(row, 16 + l16) : -1;
-    for (int b = tid >> 4; b < blocks; b += SMALL_THREADS / 16) {
-      if (b >= SMALL_THREADS / 16) raw = load16(m.x + (size_t)t * p.hidden + b * QBLOCK + l16 * 8);
-      for (int j0 = 0; j0 < k; j0 += 16)  // (a loop: one copy of the code, which a cold launch has to fetch)
-        put_block<MODE>(p, m, raw, b, l16, j0 ? high : low, min(k - j0, 16));
+    __syncthreads();
+    for (int i = first_item; i < tokens * blocks; i += FEW_THREADS / 16) {
+      const int t = i / blocks, b = i - t * blocks;  // the tokens' blocks follow one another
+      if (i >= FEW_THREADS / 16) raw = load16(m.x + (size_t)t0 * p.hidden + (size_t)i * QBLOCK + l16 * 8);
+      for (int j0 = 0; j0 < k; j0 += 16) {
+        const int here = min(k - j0, 16);
+        put_block<MODE>(p, m, raw, b, l16, l16 < here ? rows[t * k + j0 + l16] : -1, here);
+      }
     }
   }
 }
@@ -440,20 +424,22 @@ long long sort_workspace(int slots, int num_groups) {
 
 namespace {
 
-// Where sorting (and moving) in one launch beats the passes over chunks.
-bool few_slots(const RouteArgs& a) { return a.tokens * a.top_k <= SMALL_SLOTS; }
+// Sorting (and moving) in one launch, where that beats the passes over chunks.
+bool one_launch(const RouteArgs& a) { return a.tokens * a.top_k <= FEW_SLOTS; }
 
 template <int MODE>
-hipError_t launch_small(const RouteArgs& a, const MoveArgs& m, hipStream_t stream) {
-  const int fills = a.layout == DG_MOE_CONTIGUOUS ? std::max(1, std::min((a.rows + FILL_ROWS - 1) / FILL_ROWS, 64)) : 1;
-  hipLaunchKernelGGL(small_kernel<MODE>, dim3(a.tokens + fills), dim3(SMALL_THREADS), 0, stream, a, m);
+hipError_t launch_one(const RouteArgs& a, const MoveArgs& m, hipStream_t stream) {
+  const int each = std::max((a.tokens + FEW_WORKGROUPS - 1) / FEW_WORKGROUPS, 1);
+  const int fills = a.layout == DG_MOE_CONTIGUOUS ? std::min((a.rows + FILL_ROWS - 1) / FILL_ROWS, 64) : 1;
+  const int grid = std::max({(a.tokens + each - 1) / each, fills, 1});
+  hipLaunchKernelGGL(few_kernel<MODE>, dim3(grid), dim3(FEW_THREADS), 0, stream, a, m, each);
   return hipGetLastError();
 }
 
 template <int MODE>
 hipError_t launch_move(const RouteArgs& a, const MoveArgs& m, hipStream_t stream) {
   if (a.ids) {
-    if (few_slots(a)) return launch_small<MODE>(a, m, stream);
+    if (one_launch(a)) return launch_one<MODE>(a, m, stream);
     if (hipError_t e = launch_sort(a, stream)) return e;
   }
   const long long groups = (long long)((a.tokens + 7) / 8) * (a.hidden / QBLOCK);
@@ -465,15 +451,11 @@ hipError_t launch_move(const RouteArgs& a, const MoveArgs& m, hipStream_t stream
 }  // namespace
 
 hipError_t launch_sort(const RouteArgs& a, hipStream_t stream) {
-  if (few_slots(a)) return launch_small<MOVE_NONE>(a, MoveArgs{}, stream);
+  if (one_launch(a)) return launch_one<MOVE_NONE>(a, MoveArgs{}, stream);
   const int slots = a.tokens * a.top_k, chunk = chunk_slots(slots), chunks = (slots + chunk - 1) / chunk;
-  if (slots <= COUNT_SLOTS) {
-    hipLaunchKernelGGL(rank_kernel<true>, dim3(chunks), dim3(SORT_THREADS), 0, stream, a, chunk, chunks);
-    return hipGetLastError();
-  }
   hipLaunchKernelGGL(count_kernel, dim3(chunks), dim3(SORT_THREADS), 0, stream, a, chunk);
   if (hipError_t e = hipGetLastError()) return e;
-  hipLaunchKernelGGL(rank_kernel<false>, dim3(chunks), dim3(SORT_THREADS), 0, stream, a, chunk, chunks);
+  hipLaunchKernelGGL(rank_kernel, dim3(chunks), dim3(SORT_THREADS), 0, stream, a, chunk, chunks);
   return hipGetLastError();
 }
 
