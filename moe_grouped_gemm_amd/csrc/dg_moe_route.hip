@@ -236,12 +236,13 @@ __global__ __launch_bounds__(DISPATCH_THREADS) void dispatch_kernel(RouteArgs p,
 // share of the rows' groups, and there may be workgroups without tokens for that.
 // Bound by latency: a launch costs more than the counting, which is the same in
 // every workgroup, LDS atomics on whole numbers (their order does not matter)
-// that grow with the slots. Against sort and dispatch as launches of their own
-// (no-padding, 32 groups, FP8): 512 slots of 256 values 4.3 us and 8.5, 4096 5.9 and
-// 9.7, 8192 7.4 and 9.6, 16384 10.6 and 10.0; of 7168 values, 4096 slots 12.1 us
-// and 15.0, 16384 43.6 and 40.2. Ranking by comparing each slot with all ids took as
-// long at 40 slots and 14 us at 4096.
-constexpr int FEW_SLOTS = 8192;
+// that grow with the slots. An XCD takes successive tokens, for their rows' scales
+// as in dispatch_kernel (8192 slots of 7168 values: 19.0 us, without 22.1). Against
+// sort and dispatch as launches of their own (no-padding, 32 groups, FP8): 512
+// slots of 256 values 4.3 us and 8.5, 4096 5.8 and 9.7, 16384 10.7 and 10.1; of 7168
+// values, 512 slots 5.6 us and 9.0, 4096 10.7 and 15.0, 16384 34.8 and 40.2. Ranking by
+// comparing each slot with all ids took as long at 40 slots and 14 us at 4096.
+constexpr int FEW_SLOTS = 16384;
 constexpr int FEW_THREADS = 512;
 constexpr int FEW_WORKGROUPS = 512;  // 256: slower with long rows, 1024: with many slots
 constexpr int FILL_ROWS = 2048;      // rows of grouped_layout that are worth a workgroup
@@ -256,7 +257,8 @@ __global__ __launch_bounds__(FEW_THREADS) void few_kernel(RouteArgs p, MoveArgs 
   __shared__ int rows[64];           // of this workgroup's slots
   const int tid = threadIdx.x, l16 = tid & 15;
   const int G = p.num_groups, N = p.tokens * p.top_k, k = p.top_k;
-  const int t0 = blockIdx.x * tokens_each, tokens = max(min(tokens_each, p.tokens - t0), 0);
+  const int chunk = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+  const int t0 = chunk * tokens_each, tokens = max(min(tokens_each, p.tokens - t0), 0);
   const int begin = t0 * k, slots = tokens * k;
 
   // On their way while the ids are counted: the first piece of the tokens, the
@@ -431,7 +433,7 @@ template <int MODE>
 hipError_t launch_one(const RouteArgs& a, const MoveArgs& m, hipStream_t stream) {
   const int each = std::max((a.tokens + FEW_WORKGROUPS - 1) / FEW_WORKGROUPS, 1);
   const int fills = a.layout == DG_MOE_CONTIGUOUS ? std::min((a.rows + FILL_ROWS - 1) / FILL_ROWS, 64) : 1;
-  const int grid = std::max({(a.tokens + each - 1) / each, fills, 1});
+  const int grid = (std::max({(a.tokens + each - 1) / each, fills, 1}) + 7) / 8 * 8;
   hipLaunchKernelGGL(few_kernel<MODE>, dim3(grid), dim3(FEW_THREADS), 0, stream, a, m, each);
   return hipGetLastError();
 }

@@ -115,7 +115,7 @@ SORTS = [
     # tokens, top_k, groups, rows (None: as many as can be needed)
     (1, 1, 1, None), (1, 8, 16, None), (5, 8, 16, None), (64, 4, 8, None), (259, 8, 16, None), (1023, 1, 3, None),
     (700, 7, 129, None), (1025, 8, 64, None), (3001, 5, 33, None), (8192, 8, 32, None), (20000, 3, 257, None),
-    (300, 2, 4, 128), (2500, 4, 8, 1280), (40, 32, 2, None),
+    (300, 2, 4, 128), (2500, 4, 8, 1280), (40, 32, 2, None), (512, 32, 40, None), (2048, 8, 8, None), (2049, 8, 8, None),
 ]
 
 
@@ -197,7 +197,7 @@ MOVES = [
     ("masked", 1, 1, 1, 128, 4), ("masked", 5, 8, 16, 7168, 256), ("masked", 64, 6, 8, 640, 9),
     ("nopad", 3, 2, 4, 128, None), ("nopad", 130, 4, 8, 1920, None), ("nopad", 601, 8, 32, 384, 3000),
     ("contiguous", 17, 3, 5, 256, None), ("contiguous", 333, 4, 8, 2048, 1024), ("contiguous", 1500, 3, 40, 128, None),
-    ("nopad", 2100, 4, 16, 512, None),
+    ("nopad", 2100, 4, 16, 512, None), ("masked", 2048, 8, 16, 256, 1000), ("contiguous", 2049, 8, 16, 128, None),
     # more than 16 slots a token, with blocks that leave part of a wave idle
     ("masked", 9, 32, 40, 128, 16), ("contiguous", 30, 17, 64, 4224, None), ("nopad", 200, 24, 32, 640, None),
 ]
