@@ -173,14 +173,11 @@ __device__ __forceinline__ u32x2 quantize_row(const F8& x, float& scale) {
   return quantize8(x, top, scale, 1.0f / scale);
 }
 
-// Threads (a multiple of 64 up to `most`) that share `pieces` of work evenly:
-// the fewest idle ones, and of those the most threads.
-inline int even_threads(int pieces, int most) {
-  int best = 64;
-  auto idle = [&](int n) { return (pieces + n - 1) / n * n - pieces; };
-  for (int n = 128; n <= most; n += 64)
-    if (idle(n) <= idle(best)) best = n;
-  return best;
+// Threads (a multiple of 64 up to `most`) of a workgroup that goes over `pieces`
+// of work by itself: the fewest passes, and the fewest threads for those.
+inline int pass_threads(int pieces, int most) {
+  const int passes = (pieces + most - 1) / most;
+  return ((pieces + passes - 1) / passes + 63) / 64 * 64;
 }
 
 }  // namespace moe

@@ -121,7 +121,7 @@ GluShape glu_shape(const GluArgs& a) {
     s.grid = dim3((a.m + s.row_step - 1) / s.row_step, groups);
     return s;
   }
-  s.threads = even_threads(pieces, GLU_THREADS);
+  s.threads = pass_threads(pieces, GLU_THREADS);
   for (s.chunk = 5; s.chunk > 0 && a.m < 8 << s.chunk;) --s.chunk;  // up to a line of sfa, 32 rows
   s.grid = dim3((a.m + (8 << s.chunk) - 1) / (8 << s.chunk) * (8 << s.chunk), groups);
   return s;

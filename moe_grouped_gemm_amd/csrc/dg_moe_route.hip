@@ -472,6 +472,20 @@ hipError_t launch_dispatch_fp8(const RouteArgs& a, const void* x, void* q, float
   return ue8m0 ? launch_move<MOVE_FP8_E8>(a, m, stream) : launch_move<MOVE_FP8>(a, m, stream);
 }
 
+namespace {
+
+// Threads (a multiple of 64 up to `most`) of workgroups that share `pieces`
+// of work: the fewest idle ones, and of those the most threads.
+int even_threads(int pieces, int most) {
+  int best = 64;
+  auto idle = [&](int n) { return (pieces + n - 1) / n * n - pieces; };
+  for (int n = 128; n <= most; n += 64)
+    if (idle(n) <= idle(best)) best = n;
+  return best;
+}
+
+}  // namespace
+
 hipError_t launch_combine(const RouteArgs& a, const void* yp, const float* w, void* y, hipStream_t stream) {
   const int threads = even_threads(a.hidden / 8, COMBINE_THREADS);
   const uint32_t parts = (a.hidden / 8 + threads - 1) / threads;
@@ -483,7 +497,7 @@ hipError_t launch_combine(const RouteArgs& a, const void* yp, const float* w, vo
 
 hipError_t launch_combine_bwd(const RouteArgs& a, const void* dy, const void* yp, const float* w, void* dyp,
                               float* dw, hipStream_t stream) {
-  hipLaunchKernelGGL(combine_bwd_kernel, dim3(a.tokens), dim3(even_threads(a.hidden / 8, BWD_THREADS)), 0, stream, a,
+  hipLaunchKernelGGL(combine_bwd_kernel, dim3(a.tokens), dim3(pass_threads(a.hidden / 8, BWD_THREADS)), 0, stream, a,
                      static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(yp), w,
                      static_cast<uint16_t*>(dyp), dw);
   return hipGetLastError();
