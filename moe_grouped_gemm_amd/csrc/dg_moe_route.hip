@@ -249,6 +249,22 @@ constexpr int FILL_ROWS = 2048;      // rows of grouped_layout that are worth a 
 // A workgroup's slots are at most its share of them and one token's more.
 static_assert(FEW_SLOTS / FEW_WORKGROUPS + MAX_TOP_K <= 64, "a wave ranks a workgroup's slots");
 
+// Counters in LDS for few groups come in several copies, a lane's one by its number, so
+// that lanes with the same id seldom meet in one atomic: 16080 ids over 5 groups took
+// 17 us with one copy (rows of 256), with sixteen 11. Many groups spread by
+// themselves, and few ids are not worth clearing and adding up more counters.
+__device__ __forceinline__ int counter_copies(int ids, int groups) {
+  int copies = 1;
+  while (copies * groups < 64 && copies * 1024 < ids) copies <<= 1;
+  return copies;  // copies * groups < 128, or 1
+}
+// The copies' sum for group g, left in its first counter.
+__device__ __forceinline__ void sum_copies(int* counters, int copies, int groups, int g) {
+  int s = 0;
+  for (int c = 0; c < copies; ++c) s += counters[c * groups + g];
+  counters[g] = s;
+}
+
 template <int MODE>
 __global__ __launch_bounds__(FEW_THREADS) void few_kernel(RouteArgs p, MoveArgs m, int tokens_each) {
   __shared__ int next[MAX_GROUPS];   // rows of the group before these tokens, then its next free row
@@ -269,16 +285,24 @@ __global__ __launch_bounds__(FEW_THREADS) void few_kernel(RouteArgs p, MoveArgs 
     raw = load16(m.x + (size_t)t0 * p.hidden + first_item * QBLOCK + l16 * 8);
   const int e = tid < slots ? p.ids[begin + tid] : -1;
 
-  for (int g = tid; g < G; g += FEW_THREADS) next[g] = total[g] = 0;
+  const int copies = counter_copies(N, G), mine = (tid & (copies - 1)) * G;
+  for (int g = tid; g < copies * G; g += FEW_THREADS) next[g] = total[g] = 0;
   __syncthreads();
 #pragma unroll 4
   for (int i = tid; i < N; i += FEW_THREADS) {
     const int id = p.ids[i];
     if (id < 0 || id >= G) continue;
-    atomicAdd(&total[id], 1);
-    if (i < begin) atomicAdd(&next[id], 1);
+    atomicAdd(&total[mine + id], 1);
+    if (i < begin) atomicAdd(&next[mine + id], 1);
   }
   __syncthreads();
+  if (copies > 1) {
+    for (int g = tid; g < G; g += FEW_THREADS) {
+      sum_copies(total, copies, G, g);
+      sum_copies(next, copies, G, g);
+    }
+    __syncthreads();
+  }
   if (p.layout == DG_MOE_MASKED) {
     for (int g = tid; g < G; g += FEW_THREADS) {
       next[g] += g * p.rows;
@@ -288,7 +312,6 @@ __global__ __launch_bounds__(FEW_THREADS) void few_kernel(RouteArgs p, MoveArgs 
     group_starts<FEW_THREADS>(p, total, first, blockIdx.x == 0);
     for (int g = tid; g < G; g += FEW_THREADS) next[g] += first[g];
   }
-
   __syncthreads();
 
   if (tid < 64) {
@@ -368,7 +391,12 @@ __global__ __launch_bounds__(BWD_THREADS) void combine_bwd_kernel(RouteArgs p, c
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const int32_t mine = lane < p.top_k ? p.row_of[t * p.top_k + lane] : -1;
   const float weight = mine >= 0 ? w[t * p.top_k + lane] : 0.0f;
+  int turn = 0;
   for (int j0 = 0; j0 < p.top_k; j0 += AHEAD) {
+    if (!__ballot(lane >= j0 && lane < j0 + AHEAD && mine >= 0)) {  // no row among these slots
+      if (dw && threadIdx.x < AHEAD && j0 + (int)threadIdx.x < p.top_k) dw[t * p.top_k + j0 + threadIdx.x] = 0.0f;
+      continue;
+    }
     float dot[AHEAD] = {};
     int r[AHEAD];
     float wj[AHEAD];
@@ -400,10 +428,11 @@ __global__ __launch_bounds__(BWD_THREADS) void combine_bwd_kernel(RouteArgs p, c
       }
     }
     if (!dw) continue;
-    float(*s)[AHEAD] = scratch[(j0 / AHEAD) & 1];
+    float(*s)[AHEAD] = scratch[turn];
+    turn ^= 1;  // (blocks of slots that were skipped had no barrier, so they take no turn)
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j) {
-      const float sum = wave_sum(dot[j]);
+      const float sum = r[j] >= 0 ? wave_sum(dot[j]) : 0.0f;
       if (lane == j) s[wave][j] = sum;
     }
     __syncthreads();

@@ -349,6 +349,50 @@ def test_combine_bwd(dev, case, with_dw):
         check_f32(dw, want_dw, (_depth(hidden) + 2) * U * mag, str(case))
 
 
+@pytest.mark.parametrize("t,hidden", [(300, 1024), (65, 4224)])
+def test_combine_bwd_blocks_without_rows(dev, t, hidden):
+    """Tokens whose slots have rows only in some stretches of the top_k."""
+    _say(f"combine_bwd {t} tokens of {hidden} with stretches of dropped slots")
+    k, g = 32, 40
+    plan = _make_plan(t, k, g, "nopad", None, hidden)
+    ids = _ids(t, k, g, t, 0.1)
+    for i in range(t):
+        for b in range(4):
+            if (i * 7 + i // 16) >> b & 1:
+                ids[i, 8 * b:8 * b + 8] = -1
+    moe.sort(plan, torch.from_numpy(ids).to(dev))
+    row_of = _check_sorted(plan, ids)
+    yp, dy = _randn(*plan.rows_shape, seed=17), _randn(t, hidden, seed=18)
+    w = _randn(t, k, seed=19, dtype=torch.float32)
+    dyp, dw = _unwritten(plan.rows_shape), _unwritten((t, k), torch.float32)
+    moe.combine_bwd(plan, dy, yp, w, dyp, dw)
+    src, d, wn = _f64(yp).reshape(-1, hidden), _f64(dy), _f64(w)
+    want, want_dw = M.combine_bwd(d, src, row_of, wn, np.full_like(src, np.nan))
+    held = ~np.isnan(want[:, 0])
+    got = dyp.view(-1, hidden)
+    assert (_bits(got)[~held] == SENTINEL).all()
+    check_bf16(got[torch.from_numpy(held).to(dev)], want[held], 2 * U * np.abs(want[held]))
+    mag = M.combine_bwd(np.abs(d), np.abs(src), row_of, wn, np.zeros_like(src))[1]
+    check_f32(dw, want_dw, (_depth(hidden) + 2) * U * mag)
+    assert not _f64(dw)[row_of < 0].any()
+
+
+@pytest.mark.parametrize("layout", ["contiguous", "nopad", "masked"])
+@pytest.mark.parametrize("t,k,g", [(1025, 1, 1), (3000, 5, 5), (8192, 2, 2), (700, 6, 63), (1100, 4, 64)])
+def test_dispatch_few_groups(dev, layout, t, k, g):
+    """Many slots over few groups, with most of them in one group."""
+    _say(f"dispatch {layout} {t}x{k} over {g}")
+    plan = _make_plan(t, k, g, layout, None, 128)
+    ids = _ids(t, k, g, t + g)
+    if g >= k + 1:
+        ids[: t // 2, 0] = np.where((ids[: t // 2, 1:] == g - 1).any(1), -1, g - 1)
+    x, xp = _randn(t, 128, seed=21), _unwritten(plan.rows_shape)
+    moe.dispatch(plan, x, xp, topk_ids=torch.from_numpy(ids).to(dev))
+    row_of = _check_sorted(plan, ids)
+    want = M.dispatch(_bits(x), row_of, np.full((xp.numel() // 128, 128), SENTINEL, np.int16))
+    np.testing.assert_array_equal(_bits(xp).reshape(want.shape), want)
+
+
 # ---------------------------------------------------------------------------
 # Norms
 # ---------------------------------------------------------------------------
