@@ -36,7 +36,8 @@ extern "C" {
  *   top_k       slots of a token, 1..32
  *   num_groups  groups (local experts) G, 1..4096 (no-padding: 1..2048)
  *   rows        contiguous and no-padding: rows M of the permuted buffers
- *               (contiguous: a multiple of 128); masked: max_m, rows a group (G * max_m < 2^30)
+ *               (contiguous: a multiple of 128); masked: max_m, rows a group;
+ *               M and G * max_m below 2^30
  *   hidden      values of a token, a multiple of 128
  *   row_of      [max_tokens][top_k] int32: row of each slot in the permuted
  *               buffer (masked: group * max_m + row), -1 for a dropped slot

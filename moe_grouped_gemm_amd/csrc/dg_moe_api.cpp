@@ -14,6 +14,7 @@ using namespace dg::moe;
 constexpr long long kMaxBytes = 1LL << 40;
 constexpr long long kMaxSlots = 1LL << 22;  // this and the next two keep workgroups * threads of every grid below 2^32
 constexpr int kMaxGluRows = 1 << 22;
+constexpr long long kMaxRows = 1LL << 30;
 constexpr int kMaxNormTokens = 1 << 21;
 constexpr int kMaxDim = 1 << 20;
 
@@ -31,7 +32,8 @@ dg_status layout_checks(int layout, int m, int num_groups) {
   if (layout == DG_MOE_MASKED && m == 0) return DG_ERR_SHAPE;
   if (layout == DG_MOE_CONTIGUOUS && m % SEGMENT != 0) return DG_ERR_SHAPE;
   if (num_groups > (layout == DG_MOE_NOPAD ? MAX_NOPAD : MAX_GROUPS)) return DG_ERR_UNSUPPORTED;
-  if (layout == DG_MOE_MASKED && (long long)m * num_groups >= (1LL << 30)) return DG_ERR_UNSUPPORTED;
+  // Row numbers are ints, and a kernel's loop over rows steps past the last one.
+  if ((long long)m * (layout == DG_MOE_MASKED ? num_groups : 1) >= kMaxRows) return DG_ERR_UNSUPPORTED;
   return DG_OK;
 }
 

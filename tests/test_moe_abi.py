@@ -61,6 +61,17 @@ def test_bad_plan_sizes(change, status):
         assert call() == status, name
 
 
+@pytest.mark.parametrize("layout,rows", [(1, 2 ** 31 - 128), (3, 2 ** 31 - 1), (1, 2 ** 30), (3, 2 ** 30)])
+def test_rows_past_the_kernels_indices(layout, rows):
+    """Row numbers are int32 and the kernels step past the last one: 2^30 rows
+    and more are refused, whatever the row length."""
+    plan = _plan(layout=layout, rows=rows, hidden=128)
+    assert moe.lib().dg_moe_workspace_bytes(ctypes.addressof(plan)) == -1
+    for name, call in _calls(plan).items():
+        assert call() == UNSUPPORTED, name
+    assert moe.lib().dg_moe_workspace_bytes(ctypes.addressof(_plan(layout=layout, rows=2 ** 30 - 128, hidden=128))) > 0
+
+
 def test_bad_plan_pointers():
     for name, call in _calls(None).items():
         assert call() == NULL, name
