@@ -6,8 +6,9 @@
  * and residual scale, and the gradients of all of these. Same library
  * (libdg.so), status codes and conventions as dg.h: every pointer is
  * caller-owned device memory, nothing is allocated, arguments are checked
- * before anything is enqueued, calls enqueue on `stream` and return without
- * synchronising, and all of them are safe to capture in a HIP graph.
+ * before anything is enqueued, calls enqueue on `stream` (of the current
+ * device, where the buffers lie too) and return without synchronising, and
+ * all of them are safe to capture in a HIP graph.
  * Activations are BF16, FP8 is OCP E4M3, sums and statistics are float32, and
  * every result is rounded once, to nearest even. Results do not depend on
  * timing: the same inputs give the same bits.

@@ -91,6 +91,21 @@ def _stream(index: int) -> int:
     return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _call(name: str, index: int, *args) -> None:
+    """Calls an entry point on device `index`'s current stream, with that device
+    current: the handle of a default stream is 0 on every device."""
+    if _current_device() == index:
+        status = getattr(lib(), name)(*args, _stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = getattr(lib(), name)(*args, _stream(index))
+    if status:
+        _check(status, name)
+
+
 def _want(t: torch.Tensor, name: str, dtype, shape, index: int) -> None:
     """As dg._need, with the whole shape and the device by its index (the
     cheapest way to ask: get_device() is -1 on the host)."""
@@ -212,7 +227,7 @@ def sort(plan: Plan, topk_ids: torch.Tensor) -> Plan:
     """Sorts the slots of topk_ids [tokens, top_k] int32 by group, stably, into
     the plan; ids outside [0, num_groups) drop their slot."""
     n = plan._tokens(topk_ids, "topk_ids", _I32, plan.top_k)
-    _check(lib().dg_moe_sort(plan._ref, topk_ids.data_ptr(), n, _stream(plan._index)), "dg_moe_sort")
+    _call("dg_moe_sort", plan._index, plan._ref, topk_ids.data_ptr(), n)
     return plan
 
 
@@ -222,8 +237,7 @@ def dispatch(plan: Plan, x, xp, topk_ids=None) -> torch.Tensor:
     are not written. topk_ids: sorts first. Gradient: combine(plan, dxp, dx)."""
     n = plan._tokens(x, "x", _BF16, plan.hidden)
     _want(xp, "xp", _BF16, plan.rows_shape, plan._index)
-    _check(lib().dg_moe_dispatch(plan._ref, plan._ids(topk_ids, n), x.data_ptr(), xp.data_ptr(), n, _stream(plan._index)),
-           "dg_moe_dispatch")
+    _call("dg_moe_dispatch", plan._index, plan._ref, plan._ids(topk_ids, n), x.data_ptr(), xp.data_ptr(), n)
     return xp
 
 
@@ -234,8 +248,8 @@ def dispatch_fp8(plan: Plan, x, q, sfa, topk_ids=None, ue8m0: bool = False):
     n = plan._tokens(x, "x", _BF16, plan.hidden)
     _want(q, "q", _FP8, plan.rows_shape, plan._index)
     _want(sfa, "sfa", _F32, plan.scale_shape, plan._index)
-    _check(lib().dg_moe_dispatch_fp8(plan._ref, plan._ids(topk_ids, n), x.data_ptr(), q.data_ptr(), sfa.data_ptr(),
-                                     n, ue8m0, _stream(plan._index)), "dg_moe_dispatch_fp8")
+    _call("dg_moe_dispatch_fp8", plan._index, plan._ref, plan._ids(topk_ids, n), x.data_ptr(), q.data_ptr(),
+          sfa.data_ptr(), n, ue8m0)
     return q, sfa
 
 
@@ -247,8 +261,7 @@ def combine(plan: Plan, yp, y, weights=None) -> torch.Tensor:
     _want(yp, "yp", _BF16, plan.rows_shape, plan._index)
     if weights is not None:
         _want(weights, "weights", _F32, (n, plan.top_k), plan._index)
-    _check(lib().dg_moe_combine(plan._ref, yp.data_ptr(), _ptr(weights), y.data_ptr(), n, _stream(plan._index)),
-           "dg_moe_combine")
+    _call("dg_moe_combine", plan._index, plan._ref, yp.data_ptr(), _ptr(weights), y.data_ptr(), n)
     return y
 
 
@@ -263,8 +276,8 @@ def combine_bwd(plan: Plan, dy, yp, weights, dyp, dweights=None):
         _want(dweights, "dweights", _F32, (n, plan.top_k), plan._index)
     if dweights is not None or yp is not None:
         _want(yp, "yp", _BF16, plan.rows_shape, plan._index)
-    _check(lib().dg_moe_combine_bwd(plan._ref, dy.data_ptr(), _ptr(yp), weights.data_ptr(), dyp.data_ptr(),
-                                    _ptr(dweights), n, _stream(plan._index)), "dg_moe_combine_bwd")
+    _call("dg_moe_combine_bwd", plan._index, plan._ref, dy.data_ptr(), _ptr(yp), weights.data_ptr(), dyp.data_ptr(),
+          _ptr(dweights), n)
     return dyp, dweights
 
 
@@ -307,8 +320,8 @@ def swiglu_fp8(gu, q, sfa, rows=None, layout: str = "dense", ue8m0: bool = False
     lead = gu.shape[:-2]
     _want(q, "q", _FP8, (*lead, m, inner), index)
     _want(sfa, "sfa", _F32, (*lead, inner // 128, (m + 3) // 4 * 4), index)
-    _check(lib().dg_moe_swiglu_fp8(gu.data_ptr(), q.data_ptr(), sfa.data_ptr(), _ptr(rows), kind, m, groups, inner,
-                                   ue8m0, _stream(index)), "dg_moe_swiglu_fp8")
+    _call("dg_moe_swiglu_fp8", index, gu.data_ptr(), q.data_ptr(), sfa.data_ptr(), _ptr(rows), kind, m, groups, inner,
+          ue8m0)
     return q, sfa
 
 
@@ -318,8 +331,7 @@ def swiglu_bwd(da, gu, dgu, rows=None, layout: str = "dense") -> torch.Tensor:
     kind, m, groups, inner, index = _glu(gu, rows, layout)
     _want(da, "da", _BF16, (*gu.shape[:-1], inner), index)
     _want(dgu, "dgu", _BF16, gu.shape, index)
-    _check(lib().dg_moe_swiglu_bwd(da.data_ptr(), gu.data_ptr(), dgu.data_ptr(), _ptr(rows), kind, m, groups, inner,
-                                   _stream(index)), "dg_moe_swiglu_bwd")
+    _call("dg_moe_swiglu_bwd", index, da.data_ptr(), gu.data_ptr(), dgu.data_ptr(), _ptr(rows), kind, m, groups, inner)
     return dgu
 
 
@@ -365,7 +377,7 @@ def block_norm(x, y, post_weight, gate, pre_weight, h, n, rstd_post=None, rstd_p
     kind = _gate_kind(gate, t, hidden, index)
     args = _NORM.pack(x.data_ptr(), _ptr(y), _ptr(post_weight), _ptr(gate), _ptr(pre_weight), _ptr(h), _ptr(n),
                       _ptr(rstd_post), _ptr(rstd_pre), residual_scale, eps, kind, t, hidden)
-    _check(lib().dg_moe_block_norm(args, _stream(index)), "dg_moe_block_norm")
+    _call("dg_moe_block_norm", index, args)
     return h, n
 
 
@@ -398,5 +410,5 @@ def block_norm_bwd(dh, dn, h, y, post_weight, gate, pre_weight, rstd_post, rstd_
     args = _NORM_BWD.pack(_ptr(dh), _ptr(dn), _ptr(h), _ptr(y), _ptr(post_weight), _ptr(gate), _ptr(pre_weight),
                           _ptr(rstd_post), _ptr(rstd_pre), dx.data_ptr(), _ptr(dy), _ptr(dpost_weight), _ptr(dgate),
                           _ptr(dpre_weight), workspace.data_ptr(), workspace.numel(), residual_scale, kind, t, hidden)
-    _check(lib().dg_moe_block_norm_bwd(args, _stream(index)), "dg_moe_block_norm_bwd")
+    _call("dg_moe_block_norm_bwd", index, args)
     return dx, dy
