@@ -77,6 +77,12 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+def _int32(v: int) -> int:
+    """A size as the library's int takes it; -1, which every call refuses, where it
+    does not fit (ctypes would take it modulo 2^32)."""
+    return v if -2 ** 31 <= v < 2 ** 31 else -1
+
+
 def _ptr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
@@ -175,8 +181,8 @@ class Plan:
         self.layout = layout
         self.max_tokens, self.top_k, self.num_groups = int(max_tokens), int(top_k), int(num_groups)
         self.rows, self.hidden = int(rows), int(hidden)
-        self._struct = _PlanStruct(_LAYOUTS[layout], self.max_tokens, self.top_k, self.num_groups, self.rows,
-                                   self.hidden)
+        self._struct = _PlanStruct(_LAYOUTS[layout], _int32(self.max_tokens), _int32(self.top_k),
+                                   _int32(self.num_groups), _int32(self.rows), _int32(self.hidden))
         self._ref = ctypes.addressof(self._struct)
         size = lib().dg_moe_workspace_bytes(self._ref)
         if size < 0:
@@ -305,7 +311,7 @@ def _glu(gu, rows, layout: str):
         return 1, m, 1, width // 2, index
     if layout == "masked" and rows.shape[0] != gu.shape[0]:
         raise ValueError("rows must be masked_m, one int32 a group of gu")
-    return _LAYOUTS[layout], m, rows.shape[0], width // 2, index
+    return _LAYOUTS[layout], m, _int32(rows.shape[0]), width // 2, index
 
 
 def swiglu_fp8(gu, q, sfa, rows=None, layout: str = "dense", ue8m0: bool = False):
@@ -383,7 +389,7 @@ def block_norm(x, y, post_weight, gate, pre_weight, h, n, rstd_post=None, rstd_p
 
 def block_norm_workspace(tokens: int, hidden: int, device) -> torch.Tensor:
     """A workspace for block_norm_bwd, to be kept from call to call."""
-    size = lib().dg_moe_block_norm_workspace_bytes(int(tokens), int(hidden))
+    size = lib().dg_moe_block_norm_workspace_bytes(_int32(int(tokens)), _int32(int(hidden)))
     if size < 0:
         raise ValueError(f"sizes out of range: tokens={tokens}, hidden={hidden}")
     return torch.empty(size, dtype=torch.uint8, device=device)

@@ -94,3 +94,20 @@ def test_calls_run_on_their_tensors_device(monkeypatch, name):
     machine.current = 1
     _calls()[name]()
     assert machine.calls[1:] == [(name, 1, 1000)] and machine.current == 1
+
+
+@pytest.mark.parametrize("field", ["max_tokens", "top_k", "num_groups", "rows", "hidden"])
+@pytest.mark.parametrize("past", [2 ** 32, -2 ** 32, 2 ** 31])
+def test_plan_sizes_past_32_bits(field, past):
+    """Sizes that the library's int32 fields would take modulo 2^32 are refused."""
+    sizes = {"max_tokens": 4, "top_k": 2, "num_groups": 3, "rows": 8, "hidden": 128}
+    sizes[field] += past
+    with pytest.raises(ValueError, match="out of range"):
+        moe.Plan(sizes["max_tokens"], sizes["top_k"], sizes["num_groups"], "nopad", sizes["rows"], sizes["hidden"],
+                 "cpu")
+
+
+@pytest.mark.parametrize("tokens,hidden", [(2 ** 32 + 4, 256), (4, 2 ** 32 + 256), (-2 ** 32 + 4, 256)])
+def test_norm_workspace_sizes_past_32_bits(tokens, hidden):
+    with pytest.raises(ValueError, match="out of range"):
+        moe.block_norm_workspace(tokens, hidden, "cpu")
