@@ -11,7 +11,10 @@
  * all of them are safe to capture in a HIP graph.
  * Activations are BF16, FP8 is OCP E4M3, sums and statistics are float32, and
  * every result is rounded once, to nearest even. Results do not depend on
- * timing: the same inputs give the same bits.
+ * timing: the same inputs give the same bits. The norms and their gradient
+ * spread over dg_get_num_cus() compute units (the order of the gradient's
+ * column sums goes by their number), the other calls over as many workgroups
+ * as they have work for.
  */
 #ifndef DG_MOE_H
 #define DG_MOE_H

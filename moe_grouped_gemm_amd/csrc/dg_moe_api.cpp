@@ -225,8 +225,9 @@ dg_status dg_moe_block_norm(const dg_moe_norm* args, void* stream) {
                         (const void*)a.n})
     if (!aligned16(p)) return DG_ERR_ALIGN;
   if (!gate_aligned(a.gate, a.gate_kind) || !aligned4b(a.rstd_post) || !aligned4b(a.rstd_pre)) return DG_ERR_ALIGN;
-  if (dg_status s = device_check()) return s;
-  return status_of(launch_block_norm(a, as_stream(stream)));
+  const int cus = dg_get_num_cus();
+  if (cus <= 0) return DG_ERR_DEVICE;
+  return status_of(launch_block_norm(a, cus, as_stream(stream)));
 }
 
 long long dg_moe_block_norm_workspace_bytes(int tokens, int hidden) {
@@ -255,8 +256,9 @@ dg_status dg_moe_block_norm_bwd(const dg_moe_norm_bwd* args, void* stream) {
   if (!aligned4b(a.rstd_post) || !aligned4b(a.rstd_pre) || !aligned4b(a.dpost_weight) || !aligned4b(a.dpre_weight))
     return DG_ERR_ALIGN;
   if (a.workspace_bytes < dg_moe_block_norm_workspace_bytes(a.tokens, a.hidden)) return DG_ERR_SHAPE;
-  if (dg_status s = device_check()) return s;
-  return status_of(launch_block_norm_bwd(a, as_stream(stream)));
+  const int cus = dg_get_num_cus();
+  if (cus <= 0) return DG_ERR_DEVICE;
+  return status_of(launch_block_norm_bwd(a, cus, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -51,10 +51,10 @@ hipError_t launch_swiglu_fp8(const GluArgs& a, bool ue8m0, hipStream_t stream);
 hipError_t launch_swiglu_bwd(const GluArgs& a, hipStream_t stream);
 
 // Norms around the block (dg_moe_norm.hip).
-// Workgroups of the gradient's row loop (and rows of its partial sums).
+// Most workgroups of the gradient's row loop (and rows of its partial sums).
 int norm_bwd_grid(int tokens);
-hipError_t launch_block_norm(const dg_moe_norm& a, hipStream_t stream);
-hipError_t launch_block_norm_bwd(const dg_moe_norm_bwd& a, hipStream_t stream);
+hipError_t launch_block_norm(const dg_moe_norm& a, int cus, hipStream_t stream);
+hipError_t launch_block_norm_bwd(const dg_moe_norm_bwd& a, int cus, hipStream_t stream);
 
 }  // namespace moe
 }  // namespace dg

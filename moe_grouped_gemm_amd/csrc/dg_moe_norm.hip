@@ -420,38 +420,39 @@ __global__ __launch_bounds__(256) void column_sums_kernel(NormBwdArgs p, int par
   }
 }
 
-constexpr int CUS = 256;
+constexpr int MOST_WORKGROUPS = 256;  // the device's CUs
 
 // As many teams as a workgroup has room and rows for: waves without rows make
 // every launch longer, and each team is a turn at the gradient's end (512 rows of
 // 512: 3.0 us forward and 8.0 back, with 16 teams 4.1 and 12.2).
-TeamShape team_shape(int tokens, int hidden) {
+TeamShape team_shape(int tokens, int hidden, int grid) {
   const int pieces = hidden / 8, vpt = pieces <= MAX_THREADS ? 1 : 2;
   const int waves = ((pieces + vpt - 1) / vpt + 63) / 64;
-  return {waves, std::min(MAX_WAVES / waves, (tokens + CUS - 1) / CUS), vpt};
+  return {waves, std::min(MAX_WAVES / waves, (tokens + grid - 1) / grid), vpt};
 }
 
-// One workgroup a CU: 2 and 4 were slower at every size (8192 rows of 7168 in 87
-// us against 92 and 97). Fewer where they need no more rounds of rows are no
-// faster: a round takes what a CU takes for its rows.
-int row_grid(int tokens) { return std::min(tokens, CUS); }
+// One workgroup a CU of the `cus` that the caller leaves the kernels: 2 and 4 were
+// slower at every size (8192 rows of 7168 in 87 us against 92 and 97). Fewer where
+// they need no more rounds of rows are no faster: a round takes what a CU takes for
+// its rows.
+int row_grid(int tokens, int cus) { return std::min({tokens, cus, MOST_WORKGROUPS}); }
 
 }  // namespace
 
-int norm_bwd_grid(int tokens) { return row_grid(tokens); }
+int norm_bwd_grid(int tokens) { return row_grid(tokens, MOST_WORKGROUPS); }
 
-hipError_t launch_block_norm(const NormArgs& a, hipStream_t stream) {
-  const TeamShape s = team_shape(a.tokens, a.hidden);
-  const int grid = row_grid(a.tokens);
+hipError_t launch_block_norm(const NormArgs& a, int cus, hipStream_t stream) {
+  const int grid = row_grid(a.tokens, cus);
+  const TeamShape s = team_shape(a.tokens, a.hidden, grid);
   auto* kernel = s.vpt == 1 ? block_norm_kernel<1> : block_norm_kernel<2>;
   hipLaunchKernelGGL(kernel, dim3(grid), dim3(s.threads()), 0, stream, a, s.waves);
   return hipGetLastError();
 }
 
-hipError_t launch_block_norm_bwd(const NormBwdArgs& a, hipStream_t stream) {
-  const TeamShape s = team_shape(a.tokens, a.hidden);
-  const int grid = row_grid(a.tokens);
+hipError_t launch_block_norm_bwd(const NormBwdArgs& a, int cus, hipStream_t stream) {
+  const int grid = row_grid(a.tokens, cus);
   if (grid > 0) {
+    const TeamShape s = team_shape(a.tokens, a.hidden, grid);
     const bool full = a.gate_kind == DG_MOE_GATE_FULL;
     auto* kernel = s.vpt == 1 ? (full ? block_norm_bwd_kernel<1, true> : block_norm_bwd_kernel<1, false>)
                               : (full ? block_norm_bwd_kernel<2, true> : block_norm_bwd_kernel<2, false>);

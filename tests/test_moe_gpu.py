@@ -595,6 +595,35 @@ def test_block_norm_no_tokens(dev):
     assert not any(v.any().item() for v in out)
 
 
+@pytest.mark.parametrize("cus", [1, 5, 100])
+@pytest.mark.parametrize("t,h", [(300, 384), (70, 7168), (9, 8200)])
+def test_norms_keep_to_the_compute_units_set(dev, t, h, cus):
+    """With dg.set_num_cus(n) a row comes out as before and the gradient leaves at
+    most n workgroups' partial column sums; its workspace serves any setting."""
+    _say(f"norms on {cus} compute units, {t}x{h}")
+    d = _norm_inputs(t, h, "channel")
+    res, dh, dn = _randn(t, h, seed=31, scale=2.0), _randn(t, h, seed=32), _randn(t, h, seed=33)
+    r1, r2 = _rstds(d, res)
+    full = _bwd(d, dh, dn, res, r1, r2, 0.5)
+    fwd = [_unwritten((t, h)) for _ in range(4)]
+    moe.block_norm(d["x"], d["y"], d["post"], d["gate"], d["pre"], fwd[0], fwd[1])
+    out = {k: torch.empty_like(v) for k, v in full.items()}
+    try:
+        dg.set_num_cus(cus)
+        moe.block_norm(d["x"], d["y"], d["post"], d["gate"], d["pre"], fwd[2], fwd[3])
+        ws = moe.block_norm_workspace(t, h, dev)
+        ws.fill_(0xAB)
+        moe.block_norm_bwd(dh, dn, res, d["y"], d["post"], d["gate"], d["pre"], r1, r2, out["dx"], out["dy"], out["dpost"],
+                           out["dgate"], out["dpre"], ws, residual_scale=0.5)
+    finally:
+        dg.set_num_cus(0)
+    assert torch.equal(fwd[0], fwd[2]) and torch.equal(fwd[1], fwd[3])
+    assert torch.equal(out["dx"], full["dx"]) and torch.equal(out["dy"], full["dy"])
+    _check_bwd(out, d, dh, dn, res, r1, r2, 0.5, f"{cus} compute units")
+    assert ws.numel() >= min(t, 256) * 2 * h * 4
+    assert bool((ws[min(t, cus) * 2 * h * 4:] == 0xAB).all())
+
+
 # ---------------------------------------------------------------------------
 # Gated activation
 # ---------------------------------------------------------------------------
