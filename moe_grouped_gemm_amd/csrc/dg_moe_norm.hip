@@ -158,12 +158,14 @@ __global__ __launch_bounds__(MAX_THREADS) void block_norm_kernel(NormArgs p, int
       }
     }
     if (!p.n) continue;
+    // Pieces past the row were loaded as zeros, but an infinite gate or factor makes NaN of them.
     float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
+    for (int i = 0; i < VPT; ++i) {
+      if ((i * waves * 64 + tm.lane_in_team) * 8 >= H) continue;
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(h[i].v[e], h[i].v[e], ss);
-    // (lanes past the row hold zeros: their pieces were loaded as zeros)
+    }
     const float rstd = rsqrtf(team_sum(ss, tm, s0 + MAX_WAVES) * inv_hidden + p.eps);
     if (p.rstd_pre && live && tm.lane_in_team == 0) p.rstd_pre[t] = rstd;
 #pragma unroll

@@ -484,6 +484,34 @@ def test_block_norm_zero_and_special_rows(dev):
     assert np.isfinite(_f64(h)[[1, 3, 5]]).all() and np.isfinite(_f64(n)[[1, 3, 5]]).all()
 
 
+@pytest.mark.parametrize("h", [8, 520, 7168, 8200])
+@pytest.mark.parametrize("by", ["gate", "residual_scale"])
+def test_block_norm_infinite_rows(dev, h, by):
+    """A row that an infinite gate or factor makes infinite in every column has
+    1 / sqrt(infinity) = 0 for its second rstd, whatever part of a wave its columns
+    leave idle, and the other rows are not touched by it."""
+    _say(f"block_norm infinite {by}, {h} columns")
+    d = _norm_inputs(3, h, "token")
+    for name in ("x", "y"):
+        d[name][d[name] == 0] = 1.0
+    rs = 0.5
+    if by == "gate":
+        d["gate"][1] = float("inf")
+    else:
+        d["x"][:] = d["x"].abs()
+        rs = float("inf")
+    out_h, out_n = _unwritten((3, h)), _unwritten((3, h))
+    r1, r2 = _unwritten((3,), torch.float32), _unwritten((3,), torch.float32)
+    moe.block_norm(d["x"], d["y"], d["post"], d["gate"], d["pre"], out_h, out_n, r1, r2, residual_scale=rs)
+    rows = [1] if by == "gate" else [0, 1, 2]
+    assert np.isinf(_f64(out_h)[rows]).all() and np.isnan(_f64(out_n)[rows]).all()
+    assert np.isfinite(_f64(r1)).all() and not _f64(r2)[rows].any()
+    if by == "gate":
+        rest = {k: v[[0, 2]] if k in ("x", "y", "gate") else v for k, v in d.items()}
+        _check_norm([v[[0, 2]] for v in (out_h, out_n, r1, r2)], rest, _f64(rest["y"]), _f64(d["post"]), _f64(d["pre"]),
+                    rs, 1e-6, "rows beside it")
+
+
 def _bwd(d, dh, dn, h, r1, r2, rs, parts=("dpost", "dgate", "dpre")):
     t, hid = (dh if dh is not None else dn).shape
     out = {"dx": _unwritten((t, hid)), "dy": None if d["y"] is None else _unwritten((t, hid))}
