@@ -188,6 +188,31 @@ def test_plan_serves_fewer_tokens_and_none(dev):
                            8 * U * M.combine_mag(np.nan_to_num(_f64(xp)).reshape(-1, 256), row_of), f"{layout} {t}")
 
 
+@pytest.mark.parametrize("layout", ["contiguous", "nopad", "masked"])
+def test_sort_extreme_ids_many_slots(dev, layout):
+    test_sort_extreme_ids(dev, layout, 10000)
+
+
+@pytest.mark.parametrize("layout", ["contiguous", "nopad", "masked"])
+def test_plan_across_the_limit_of_one_launch(dev, layout):
+    """One plan with more and fewer than 16384 slots in turn, by sort and by
+    dispatch: nothing of a call is left for the next."""
+    _say(f"a plan across the limit of one launch, {layout}")
+    k, g = 4, 8
+    plan = _make_plan(6000, k, g, layout, None)
+    for t in (6000, 5, 4097, 4096, 0, 6000, 257, 4099):
+        ids = _ids(t, k, g, t)
+        x, xp = _randn(t, 256, seed=t), _unwritten(plan.rows_shape)
+        if t % 2:
+            moe.sort(plan, torch.from_numpy(ids).to(dev))
+            moe.dispatch(plan, x, xp)
+        else:
+            moe.dispatch(plan, x, xp, topk_ids=torch.from_numpy(ids).to(dev))
+        row_of = _check_sorted(plan, ids, f"{t}")
+        want = M.dispatch(_bits(x), row_of, np.full((xp.numel() // 256, 256), SENTINEL, np.int16))
+        np.testing.assert_array_equal(_bits(xp).reshape(want.shape), want)
+
+
 # ---------------------------------------------------------------------------
 # Dispatch
 # ---------------------------------------------------------------------------
@@ -269,6 +294,55 @@ def test_dispatch_fp8(dev, case, ue8m0, special):
     q, sfa = _unwritten(plan.rows_shape, torch.float8_e4m3fn), _unwritten(plan.scale_shape, torch.float32)
     moe.dispatch_fp8(plan, x, q, sfa, topk_ids=ids_d, ue8m0=ue8m0)
     _check_codes(q, sfa, _f64(x).astype(np.float32), _check_sorted(plan, ids), ue8m0, plan)
+
+
+# more slots than one launch sorts and moves (16384)
+LARGE_MOVES = [
+    ("masked", 2500, 8, 16, 384, 1001), ("masked", 1100, 17, 64, 1152, 301), ("nopad", 900, 24, 40, 640, 15000),
+    ("nopad", 2060, 8, 256, 1920, None), ("contiguous", 700, 32, 33, 256, None), ("contiguous", 4100, 5, 9, 512, 12800),
+]
+
+
+@pytest.mark.parametrize("special", [False, True])
+@pytest.mark.parametrize("ue8m0", [False, True])
+@pytest.mark.parametrize("with_sort", [True, False])
+@pytest.mark.parametrize("case", LARGE_MOVES)
+def test_dispatch_fp8_many_slots(dev, case, with_sort, ue8m0, special):
+    _say(f"dispatch_fp8 {case} sort={with_sort} ue8m0={ue8m0} special={special}")
+    _dispatch_fp8(dev, case, with_sort, ue8m0, special)
+
+
+@pytest.mark.parametrize("special", [False, True])
+@pytest.mark.parametrize("ue8m0", [False, True])
+@pytest.mark.parametrize("case", MOVES)
+def test_dispatch_fp8_after_sort(dev, case, ue8m0, special):
+    _say(f"dispatch_fp8 {case} after sort, ue8m0={ue8m0} special={special}")
+    _dispatch_fp8(dev, case, False, ue8m0, special)
+
+
+def _dispatch_fp8(dev, case, with_sort, ue8m0, special):
+    layout, t, k, g, hidden, rows = case
+    plan, ids, ids_d = _moved(*case, dev)
+    x = _randn(t, hidden, seed=2, scale=3.0)
+    if special:
+        x = _special(x)
+    q, sfa = _unwritten(plan.rows_shape, torch.float8_e4m3fn), _unwritten(plan.scale_shape, torch.float32)
+    if not with_sort:
+        moe.sort(plan, ids_d)
+    moe.dispatch_fp8(plan, x, q, sfa, topk_ids=ids_d if with_sort else None, ue8m0=ue8m0)
+    _check_codes(q, sfa, _f64(x).astype(np.float32), _check_sorted(plan, ids), ue8m0, plan)
+
+
+@pytest.mark.parametrize("with_sort", [True, False])
+@pytest.mark.parametrize("case", LARGE_MOVES)
+def test_dispatch_bf16_many_slots(dev, case, with_sort):
+    test_dispatch_bf16(dev, case, with_sort)
+
+
+@pytest.mark.parametrize("case", LARGE_MOVES)
+def test_combine_and_gradient_many_slots(dev, case):
+    test_combine(dev, case, True)
+    test_combine_bwd(dev, case, True)
 
 
 def test_dispatch_fp8_feeds_the_gemm(dev):
@@ -928,6 +1002,33 @@ def test_streams(dev):
     torch.cuda.synchronize()
     alone = [_snap(outs) for _, _, outs in sets]
     for _, _, outs in sets:
+        for o in outs:
+            o.zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(3):
+        for s, (_, run, _) in zip(streams, sets):
+            with torch.cuda.stream(s):
+                run()
+    torch.cuda.synchronize()
+    for want, (_, _, outs) in zip(alone, sets):
+        assert all(np.array_equal(a, b) for a, b in zip(want, _snap(outs)))
+
+
+def test_graph_replay_and_repeatability_many_slots(dev):
+    test_graph_replay_and_repeatability(dev, 4200)
+
+
+def test_streams_many_slots(dev):
+    """As test_streams, with more slots than one launch sorts."""
+    _say("two streams, many slots")
+    sets = [_block_calls(dev, t=t, seed=s) for t, s in ((4200, 500), (4500, 600))]
+    torch.cuda.synchronize()
+    alone = []
+    for _, run, outs in sets:
+        run()
+        torch.cuda.synchronize()
+        alone.append(_snap(outs))
         for o in outs:
             o.zero_()
     torch.cuda.synchronize()
