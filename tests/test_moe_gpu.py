@@ -823,6 +823,26 @@ def test_swiglu_fp8_special_values(dev):
     assert np.array_equal(s[:, 4], (np.abs(a).reshape(2, 128).max(1).astype(np.float32) / np.float32(448)))
 
 
+def test_swiglu_smallest_sigmoids(dev):
+    """Gates from -87.5 to -88.5, whose sigmoids are below 2^-126: with a u as large
+    as BF16's, what they make is no less exact than elsewhere."""
+    _say("swiglu, sigmoids below 2^-126")
+    inner = 256
+    gate = torch.tensor([-87.0, -87.5, -88.0, -88.5]).repeat_interleave(inner).view(4, inner)
+    up = torch.linspace(1.0, 3.0, inner).repeat(4, 1) * 2.0 ** 126
+    gu = torch.cat([gate, up], 1).to(dev).to(torch.bfloat16)
+    rows, held = None, np.ones(4, bool)
+    q, sfa = _unwritten((4, inner), torch.float8_e4m3fn), _unwritten((inner // 128, 4), torch.float32)
+    moe.swiglu_fp8(gu, q, sfa, rows=rows)
+    _check_glu_codes(q, sfa, gu, held, False, "smallest sigmoids")
+    da, dgu = _randn(4, inner, seed=44), _unwritten((4, 2 * inner))
+    moe.swiglu_bwd(da, gu, dgu)
+    x, d = _f64(gu), _f64(da)
+    s, rel = M.sigmoid(x[:, :inner]), (np.abs(x[:, :inner]) + 16) * 2.0 ** -23
+    mag = np.concatenate([np.abs(d * x[:, inner:]) * s * (1 + np.abs(x[:, :inner])), np.abs(d * x[:, :inner]) * s], -1)
+    check_bf16(dgu, M.swiglu_bwd(d, x), mag * np.concatenate([rel, rel], -1), "smallest sigmoids")
+
+
 @pytest.mark.parametrize("case", GLUS)
 def test_swiglu_bwd(dev, case):
     _say(f"swiglu_bwd {case}")
