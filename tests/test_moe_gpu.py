@@ -657,6 +657,64 @@ def test_block_norm_bwd_parts(dev, t, h, part):
     _check_bwd(out, d, dh, dn, res, r1, r2, rs, part)
 
 
+# Several rounds of rows a workgroup (256 workgroups, as many teams as fit them): one
+# team of 9 and of 14 waves, 8 teams of 2, 16 teams of one wave, which has no barrier.
+NORM_ROUNDS = [(600, 4104), (1100, 7168), (2100, 1024), (9000, 384)]
+
+
+@pytest.mark.parametrize("gate", GATES)
+@pytest.mark.parametrize("t,h", NORM_ROUNDS)
+def test_block_norm_rounds(dev, t, h, gate):
+    test_block_norm(dev, t, h, gate)
+
+
+@pytest.mark.parametrize("gate", GATES)
+@pytest.mark.parametrize("t,h", NORM_ROUNDS)
+def test_block_norm_bwd_rounds(dev, t, h, gate):
+    test_block_norm_bwd(dev, t, h, gate)
+
+
+@pytest.mark.parametrize("part", ["no_pre", "no_post", "only_pre", "in_place"])
+@pytest.mark.parametrize("t,h", [(1100, 4104), (9000, 384)])
+def test_block_norm_parts_rounds(dev, t, h, part):
+    test_block_norm_parts(dev, t, h, part)
+
+
+@pytest.mark.parametrize("part", ["no_dh", "no_dn", "no_post", "only_pre", "in_place"])
+@pytest.mark.parametrize("t,h", [(1100, 4104), (9000, 384)])
+def test_block_norm_bwd_parts_rounds(dev, t, h, part):
+    test_block_norm_bwd_parts(dev, t, h, part)
+
+
+@pytest.mark.parametrize("t,h", [(1100, 7168), (9000, 384), (1100, 8200)])
+def test_block_norm_bwd_every_row_counts(dev, t, h):
+    """Column sums in which each row shows: dH yn and dn hn of row r are a power of
+    two that is its own for 20 successive rows, so a row that is left out or taken
+    twice changes the exact sums."""
+    _say(f"block_norm_bwd row by row, {t}x{h}")
+    for first in (0, t // 2, t - 20):
+        dh = torch.zeros(t, h, dtype=torch.bfloat16, device=dev)
+        dn = torch.zeros_like(dh)
+        dh[first:first + 20] = (2.0 ** torch.arange(20, device=dev))[:, None].to(torch.bfloat16)
+        one = torch.ones(t, h, dtype=torch.bfloat16, device=dev)
+        w, r = torch.ones(h, device=dev), torch.ones(t, device=dev)
+        dx, dy = torch.empty_like(dh), torch.empty_like(dh)
+        dpost, dgate = torch.empty(h, device=dev), torch.empty(h, device=dev)
+        moe.block_norm_bwd(dh, None, None, one, w, w, None, r, None, dx, dy, dpost, dgate, None,
+                           moe.block_norm_workspace(t, h, dev))
+        # dy is zero but for the mean, a sum of h equal terms times 1 / h: two roundings
+        assert torch.equal(dx, dh) and bool((dy.abs() <= dh * 2.0 ** -22).all())
+        assert bool((dpost == 2.0 ** 20 - 1).all()) and bool((dgate == 2.0 ** 20 - 1).all())
+        # dn alternating in sign by column pairs: its mean with hn is zero, dH = dn
+        dn[first:first + 20] = dh[first:first + 20]
+        dn[:, 1::2] *= -1
+        dpre = torch.empty(h, device=dev)
+        moe.block_norm_bwd(None, dn, one, None, None, None, w, None, r, dx, None, None, None, dpre,
+                           moe.block_norm_workspace(t, h, dev))
+        assert torch.equal(dx, dn)
+        assert bool((dpre[::2] == 2.0 ** 20 - 1).all()) and bool((dpre[1::2] == 1 - 2.0 ** 20).all())
+
+
 def test_block_norm_bwd_against_differences(dev):
     """Central differences of the forward kernel's float64 definition at the
     kernel's own inputs: dx, dy and the weights along random directions."""
@@ -715,8 +773,8 @@ def test_norms_keep_to_the_compute_units_set(dev, t, h, cus):
         moe.block_norm(d["x"], d["y"], d["post"], d["gate"], d["pre"], fwd[2], fwd[3])
         ws = moe.block_norm_workspace(t, h, dev)
         ws.fill_(0xAB)
-        moe.block_norm_bwd(dh, dn, res, d["y"], d["post"], d["gate"], d["pre"], r1, r2, out["dx"], out["dy"], out["dpost"],
-                           out["dgate"], out["dpre"], ws, residual_scale=0.5)
+        moe.block_norm_bwd(dh, dn, res, d["y"], d["post"], d["gate"], d["pre"], r1, r2, out["dx"], out["dy"],
+                           out["dpost"], out["dgate"], out["dpre"], ws, residual_scale=0.5)
     finally:
         dg.set_num_cus(0)
     assert torch.equal(fwd[0], fwd[2]) and torch.equal(fwd[1], fwd[3])
