@@ -861,6 +861,26 @@ def test_swiglu_fp8(dev, case, ue8m0):
     _check_glu_codes(q, sfa, gu, held, ue8m0, str(case))
 
 
+# a row a workgroup (an inner above 1024) in every layout, and more than one pass
+# over a row (above 4096)
+LONG_GLUS = [
+    ("masked", 5, 70, 2048), ("masked", 11, 300, 1152), ("masked", 9, 9, 4480), ("masked", 3, 1, 2048),
+    ("nopad", 7, 45, 1280), ("nopad", 3, 120, 4224), ("contiguous", 4, 100, 2048), ("contiguous", 3, 150, 5248),
+    ("dense", 1, 70, 8320), ("dense", 1, 3, 1152),
+]
+
+
+@pytest.mark.parametrize("ue8m0", [False, True])
+@pytest.mark.parametrize("case", LONG_GLUS)
+def test_swiglu_fp8_long_rows(dev, case, ue8m0):
+    test_swiglu_fp8(dev, case, ue8m0)
+
+
+@pytest.mark.parametrize("case", LONG_GLUS)
+def test_swiglu_bwd_long_rows(dev, case):
+    test_swiglu_bwd(dev, case)
+
+
 def test_swiglu_fp8_special_values(dev):
     _say("swiglu_fp8 special values")
     gu = _randn(6, 512, seed=50)
