@@ -16,10 +16,10 @@ import numpy as np
 import pytest
 import torch
 
-from moe_grouped_gemm_amd import dg, moe
+from moe_grouped_gemm_amd import dg, moe, synth
 from oracle import dg_oracle as O
 from oracle import moe_oracle as M
-from parity import bf16_ulp
+from parity import bf16_ulp, element_bound
 
 pytestmark = pytest.mark.gpu
 
@@ -368,6 +368,75 @@ def test_dispatch_fp8_feeds_the_gemm(dev):
         ref = w[ids[i, j]] @ deq[i]
         mag = np.abs(w[ids[i, j]]) @ np.abs(deq[i])
         assert np.all(np.abs(out[row_of[i, j]] - ref) <= bf16_ulp(np.abs(ref) + mag * 2 ** -14) + mag * 2 ** -14)
+
+
+def _masked_gemm_inputs(layout, t, k, g, hidden, max_m, dev, ue8m0):
+    plan, ids, ids_d = _moved(layout, t, k, g, hidden, max_m, dev)
+    x = _randn(t, hidden, seed=3)
+    x *= torch.linspace(0.3, 3.0, t, device=dev)[:, None].to(torch.bfloat16)     # scales of many mantissas
+    q = torch.zeros(plan.rows_shape, dtype=torch.float8_e4m3fn, device=dev)
+    sfa = torch.zeros(plan.scale_shape, device=dev)
+    moe.dispatch_fp8(plan, x, q, sfa, topk_ids=ids_d, ue8m0=ue8m0)
+    vals, scales = M.quantize(_f64(x).astype(np.float32), ue8m0)
+    return plan, ids, q, sfa, vals * np.repeat(scales.astype(np.float64), 128, 1)
+
+
+def _check_product(d, ids, deq, w, max_m, g, k):
+    """Rows of a masked product against the tokens' dequantised values times the
+    groups' weights w [G, N, K]: the GEMM's own bound."""
+    out = _f64(d).reshape(-1, w.shape[1])
+    row_of = M.sort(ids, g, "masked", max_m)[0]
+    for i, j in np.argwhere(row_of >= 0)[::5]:
+        ref, mag = w[ids[i, j]] @ deq[i], np.abs(w[ids[i, j]]) @ np.abs(deq[i])
+        got = out[row_of[i, j]]
+        assert np.all(np.abs(got - ref) <= bf16_ulp(np.maximum(np.abs(got), np.abs(ref))) + element_bound(mag, k))
+
+
+def test_dispatch_fp8_feeds_the_ue8m0_gemm(dev):
+    """Power-of-two scales into the calls that read a scale's exponent only."""
+    _say("dispatch_fp8 into the masked UE8M0 GEMM")
+    t, k, g, hidden, n, max_m = 50, 4, 6, 512, 256, 64
+    plan, ids, q, sfa, deq = _masked_gemm_inputs("masked", t, k, g, hidden, max_m, dev, True)
+    b = _randn(g, n, hidden, seed=4).to(torch.float8_e4m3fn)
+    sfb = 2.0 ** torch.randint(-3, 4, (g, n // 128, hidden // 128), generator=_gen(5), device=dev).float()
+    d = _unwritten((g, max_m, n))
+    dg.m_grouped_fp8_gemm_nt_masked(q, sfa, b, sfb, d, plan.group_rows, ue8m0=True)
+    w = b.float().cpu().numpy().astype(np.float64) * np.repeat(np.repeat(_f64(sfb), 128, 1), 128, 2)
+    _check_product(d, ids, deq, w, max_m, g, hidden)
+
+
+def test_dispatch_and_activation_feed_the_w4a8_gemm(dev):
+    """ue8m0=True operands of dispatch_fp8 and of swiglu_fp8 in the FP8 x FP4 product,
+    which reads every scale's exponent only."""
+    _say("dispatch_fp8 and swiglu_fp8 into the masked W4A8 GEMM")
+    t, k, g, hidden, n, max_m = 50, 4, 6, 512, 512, 64
+    plan, ids, q, sfa, deq = _masked_gemm_inputs("masked", t, k, g, hidden, max_m, dev, True)
+    parts = [synth.quantize_rhs_e2m1(torch.randn(n, hidden, generator=_gen(6 + e), device=dev)) for e in range(g)]
+    b, sfb = torch.stack([p[0] for p in parts]), torch.stack([p[1] for p in parts])
+    d = _unwritten((g, max_m, n))
+    dg.m_grouped_fp8_fp4_gemm_nt_masked(q, sfa, b, sfb, d, plan.group_rows)
+    w = np.stack([O.dequant_rhs_e2m1(e.cpu().numpy(), f.cpu().numpy()) for e, f in zip(b, sfb)])
+    _check_product(d, ids, deq, w, max_m, g, hidden)
+    # the product's rows through the activation into a second one, of the first n / 2 inputs
+    inner = n // 2
+    aq, asf = _unwritten((g, max_m, inner), torch.float8_e4m3fn), _unwritten((g, inner // 128, max_m), torch.float32)
+    moe.swiglu_fp8(d, aq, asf, rows=plan.group_rows, layout="masked", ue8m0=True)
+    parts = [synth.quantize_rhs_e2m1(torch.randn(hidden, inner, generator=_gen(20 + e), device=dev)) for e in range(g)]
+    b2, sfb2 = torch.stack([p[0] for p in parts]), torch.stack([p[1] for p in parts])
+    yp = _unwritten((g, max_m, hidden))
+    dg.m_grouped_fp8_fp4_gemm_nt_masked(aq, asf, b2, sfb2, yp, plan.group_rows)
+    counts = plan.group_rows.tolist()
+    gu, out = _f64(d), _f64(yp)
+    for e in range(g):
+        w2 = O.dequant_rhs_e2m1(b2[e].cpu().numpy(), sfb2[e].cpu().numpy())
+        act = M.swiglu(gu[e, :counts[e]])
+        ref, mag = act @ w2.T, np.abs(act) @ np.abs(w2).T
+        # each code is within 2^-4 of its value, or 2^-10 of the block's scale, which power-of-two
+        # rounding takes up to twice amax / 448; a scale taken for another one would double or halve a block
+        top = np.repeat(np.abs(act).reshape(counts[e], -1, 128).max(-1), 128, -1)
+        off = (np.abs(act) * 2.0 ** -4 + top * 2.0 ** -9 / 448) @ np.abs(w2).T
+        bound = off * 1.01 + np.abs(ref) * 2.0 ** -8 + element_bound(mag, inner) * 2
+        assert np.all(np.abs(out[e, :counts[e]] - ref) <= bound)
 
 
 # ---------------------------------------------------------------------------
