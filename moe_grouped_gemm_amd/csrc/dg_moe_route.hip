@@ -237,12 +237,10 @@ __global__ __launch_bounds__(DISPATCH_THREADS) void dispatch_kernel(RouteArgs p,
 // Bound by latency: a launch costs more than the counting, which is the same in
 // every workgroup, LDS atomics on whole numbers (their order does not matter)
 // that grow with the slots. An XCD takes successive tokens, for their rows' scales
-// as in dispatch_kernel (8192 slots of 7168 values: 19.0 us, without 22.1). Against
-// sort and dispatch as launches of their own (no-padding, 32 groups, FP8): 512
-// slots of 256 values 4.3 us and 8.5, 4096 5.8 and 9.7, 16384 10.7 and 10.1; of 7168
-// values, 512 slots 5.6 us and 9.0, 4096 10.7 and 15.0, 16384 34.8 and 40.2. Ranking by
+// as in dispatch_kernel (8192 slots of 7168 values: 19.9 us, without 22.1). Ranking by
 // comparing each slot with all ids took as long at 40 slots and 14 us at 4096.
-constexpr int FEW_SLOTS = 16384;
+// Where it is used: one_launch.
+constexpr int FEW_SLOTS = 16384;  // at most
 constexpr int FEW_THREADS = 512;
 constexpr int FEW_WORKGROUPS = 512;  // 256: slower with long rows, 1024: with many slots
 constexpr int FILL_ROWS = 2048;      // rows of grouped_layout that are worth a workgroup
@@ -455,8 +453,20 @@ long long sort_workspace(int slots, int num_groups) {
 
 namespace {
 
-// Sorting (and moving) in one launch, where that beats the passes over chunks.
-bool one_launch(const RouteArgs& a) { return a.tokens * a.top_k <= FEW_SLOTS; }
+// Whether one launch sorts (and moves), where that beats the passes over chunks.
+// Times in us, 64 groups, FP8, first the one launch: ids spread evenly / by a Zipf
+// law of exponent 1.2, whose counting meets on few counters.
+//   sort alone       4096 slots   4.7 / 7.2 against 6.9 / 7.0; 8192  6.2 / 11.3 against 7.1 / 7.2
+//   rows of 256      8192 (4096 tokens)  7.3 / 11.4 against 9.9 / 9.9; 16384  10.0 / 16.2 against 10.4 / 10.5
+//   rows of 4096     16384 (4096 tokens)  28.6 / 28.9 against 30.0 / 29.9
+//   rows of 7168     8192 (1024 tokens)  19.9 / 19.6 against 24.9 / 25.0; 16384 (4096 tokens)  41.0 / 41.5 against 45.8 / 45.5
+// More tokens than that are too many for each workgroup, which moves its own in
+// turn: 8192 slots of 8192 tokens of 7168  55.4 / 58.0 against 46.8 / 46.2.
+bool one_launch(const RouteArgs& a, bool moves) {
+  const int slots = a.tokens * a.top_k;
+  if (!moves) return slots <= 4096;
+  return a.tokens <= 4096 && slots <= (a.hidden >= 4096 ? FEW_SLOTS : 8192);
+}
 
 template <int MODE>
 hipError_t launch_one(const RouteArgs& a, const MoveArgs& m, hipStream_t stream) {
@@ -467,11 +477,19 @@ hipError_t launch_one(const RouteArgs& a, const MoveArgs& m, hipStream_t stream)
   return hipGetLastError();
 }
 
+hipError_t launch_passes(const RouteArgs& a, hipStream_t stream) {
+  const int slots = a.tokens * a.top_k, chunk = chunk_slots(slots), chunks = (slots + chunk - 1) / chunk;
+  hipLaunchKernelGGL(count_kernel, dim3(chunks), dim3(SORT_THREADS), 0, stream, a, chunk);
+  if (hipError_t e = hipGetLastError()) return e;
+  hipLaunchKernelGGL(rank_kernel, dim3(chunks), dim3(SORT_THREADS), 0, stream, a, chunk, chunks);
+  return hipGetLastError();
+}
+
 template <int MODE>
 hipError_t launch_move(const RouteArgs& a, const MoveArgs& m, hipStream_t stream) {
   if (a.ids) {
-    if (one_launch(a)) return launch_one<MODE>(a, m, stream);
-    if (hipError_t e = launch_sort(a, stream)) return e;
+    if (one_launch(a, true)) return launch_one<MODE>(a, m, stream);
+    if (hipError_t e = launch_passes(a, stream)) return e;
   }
   const long long groups = (long long)((a.tokens + 7) / 8) * (a.hidden / QBLOCK);
   const int per_xcd = (int)std::min<long long>((groups + DISPATCH_THREADS / 16 - 1) / (DISPATCH_THREADS / 16), 1 << 19);
@@ -482,12 +500,7 @@ hipError_t launch_move(const RouteArgs& a, const MoveArgs& m, hipStream_t stream
 }  // namespace
 
 hipError_t launch_sort(const RouteArgs& a, hipStream_t stream) {
-  if (one_launch(a)) return launch_one<MOVE_NONE>(a, MoveArgs{}, stream);
-  const int slots = a.tokens * a.top_k, chunk = chunk_slots(slots), chunks = (slots + chunk - 1) / chunk;
-  hipLaunchKernelGGL(count_kernel, dim3(chunks), dim3(SORT_THREADS), 0, stream, a, chunk);
-  if (hipError_t e = hipGetLastError()) return e;
-  hipLaunchKernelGGL(rank_kernel, dim3(chunks), dim3(SORT_THREADS), 0, stream, a, chunk, chunks);
-  return hipGetLastError();
+  return one_launch(a, false) ? launch_one<MOVE_NONE>(a, MoveArgs{}, stream) : launch_passes(a, stream);
 }
 
 hipError_t launch_dispatch(const RouteArgs& a, const void* x, void* xp, hipStream_t stream) {

@@ -439,6 +439,30 @@ def test_dispatch_and_activation_feed_the_w4a8_gemm(dev):
         assert np.all(np.abs(out[e, :counts[e]] - ref) <= bound)
 
 
+@pytest.mark.parametrize("call,t,k,hidden,passes", [
+    ("sort", 4096, 1, 128, False), ("sort", 4100, 1, 128, True), ("sort", 2048, 8, 7168, True),
+    ("dispatch", 1024, 8, 128, False), ("dispatch", 1025, 8, 128, True), ("dispatch", 4096, 2, 7168, False),
+    ("dispatch", 4097, 1, 7168, True), ("dispatch", 2048, 8, 4096, False), ("dispatch", 2049, 8, 4096, True),
+])
+def test_few_slots_take_one_launch(dev, call, t, k, hidden, passes):
+    """Which of the two ways a call takes, by whether its workspace is written: only
+    the passes over chunks leave their counts there."""
+    _say(f"{call} of {t}x{k}, rows of {hidden}")
+    plan = _make_plan(t, k, 64, "nopad", None, hidden)
+    plan.workspace.fill_(0xAB)
+    ids = _ids(t, k, 64, t)
+    if call == "sort":
+        moe.sort(plan, torch.from_numpy(ids).to(dev))
+    else:
+        x, xp = _randn(t, hidden, seed=t), _unwritten(plan.rows_shape)
+        moe.dispatch(plan, x, xp, topk_ids=torch.from_numpy(ids).to(dev))
+    row_of = _check_sorted(plan, ids)
+    if call == "dispatch":
+        for i, j in np.argwhere(row_of >= 0)[::997]:
+            assert torch.equal(xp[row_of[i, j]], x[i])
+    assert passes != bool((plan.workspace == 0xAB).all())
+
+
 # ---------------------------------------------------------------------------
 # Combine
 # ---------------------------------------------------------------------------
