@@ -95,6 +95,10 @@ dg_status dg_moe_dispatch(const dg_moe_plan* plan, const int32_t* topk_ids, cons
  *   q   [M][hidden] E4M3 (masked [G][max_m][hidden])
  *   sfa [hidden/128][dg_get_tma_aligned_size(M, 4)] float32
  *       (masked [G][hidden/128][dg_get_tma_aligned_size(max_m, 4)])
+ * The *_ue8m0 GEMMs and the FP8 x FP4 GEMMs read only a scale's exponent:
+ * operands for them need ue8m0 != 0 (a float32 scale's mantissa would be
+ * dropped, and the block come out up to a factor of two too small, without an
+ * error). Power-of-two scales are right for the other GEMMs too.
  * A NaN in a block makes its scale and codes NaN; an infinity makes the scale
  * infinite, its own code NaN and the others zero.
  */
@@ -131,6 +135,7 @@ dg_status dg_moe_combine_bwd(const dg_moe_plan* plan, const void* dy, const void
  *        masked_m [num_groups]; dense: NULL, every row does. Counts are
  *        clamped as by the GEMMs. Other rows do not influence the result and
  *        are not written.
+ * ue8m0 by the GEMM that reads the operand, as for dg_moe_dispatch_fp8.
  * inner % 128 == 0; m % 128 == 0 for the contiguous layout, m <= 2^22;
  * num_groups as in a plan (not read for the dense and contiguous layouts).
  */

@@ -16,6 +16,8 @@ A block in FP8, masked layout (b1 [G, 2I, H], b2 [G, H, I] and their scales):
     dg.m_grouped_fp8_gemm_nt_masked(a, sfa2, b2, sfb2, yp, plan.group_rows)
     moe.combine(plan, yp, y, weights=w)
     moe.block_norm(x, y, post_weight, gate, pre_weight, h, n)
+
+With the UE8M0 or the FP8 x FP4 GEMMs dispatch_fp8 and swiglu_fp8 need ue8m0=True.
 """
 
 from __future__ import annotations
@@ -250,7 +252,10 @@ def dispatch(plan: Plan, x, xp, topk_ids=None) -> torch.Tensor:
 def dispatch_fp8(plan: Plan, x, q, sfa, topk_ids=None, ue8m0: bool = False):
     """dispatch() into the GEMMs' LHS operand: q like xp in float8_e4m3fn and
     sfa [hidden/128, tma_aligned(rows)] float32 (masked: [G, ...]), one scale
-    max(amax, 1e-4) / 448 per 128 values (ue8m0: rounded up to a power of two)."""
+    max(amax, 1e-4) / 448 per 128 values (ue8m0: rounded up to a power of two).
+    GEMMs called with ue8m0=True and the FP8 x FP4 GEMMs read only a scale's
+    exponent: their operands need ue8m0=True here too, or blocks come out up to a
+    factor of two too small."""
     n = plan._tokens(x, "x", _BF16, plan.hidden)
     _want(q, "q", _FP8, plan.rows_shape, plan._index)
     _want(sfa, "sfa", _F32, plan.scale_shape, plan._index)
@@ -321,7 +326,8 @@ def swiglu_fp8(gu, q, sfa, rows=None, layout: str = "dense", ue8m0: bool = False
 
     rows says which rows hold tokens, as the GEMM of that layout takes it:
     grouped_layout [M] (contiguous; a negative id holds none), group_rows [G]
-    (nopad), masked_m [G] (masked), None (dense: all). Others are not written."""
+    (nopad), masked_m [G] (masked), None (dense: all). Others are not written.
+    ue8m0 by the GEMM that reads q, as for dispatch_fp8."""
     kind, m, groups, inner, index = _glu(gu, rows, layout)
     lead = gu.shape[:-2]
     _want(q, "q", _FP8, (*lead, m, inner), index)
