@@ -36,7 +36,7 @@ __device__ __forceinline__ int nopad_rows(const GluArgs& p) {
 // rows: workgroups go round the 8 XCDs, and this gives an XCD 1 << chunk rows
 // in succession, whose scales of a block are (part of) one line of sfa and fill it
 // in one L2. Without it 32000 rows of 2048 wrote 79 MB where 66 are needed, and
-// took 57 us against 51. Which XCD comes first goes by the group: in the masked
+// took a tenth more time. Which XCD comes first goes by the group: in the masked
 // layout the first rows of every group hold tokens, the last ones none.
 __device__ __forceinline__ int turn_row(int i, int g, int chunk) {
   const int low = (8 << chunk) - 1;
@@ -49,10 +49,10 @@ __device__ __forceinline__ int turn_row(int i, int g, int chunk) {
 // (an inner of at most 1024: 29416 rows of 256 take 9 us, a row a workgroup 26).
 // With one row, whether it holds a token is the same in all lanes, asked before
 // anything is stored, and so comes by scalar loads, soonest: with a loop over
-// rows around it, 65 us for 32000 rows of 2048 in place of 57. A row without a
-// token costs its workgroup's launch: 16 us for 256 groups of 256 rows of which
-// 2 hold tokens (13 with fewer workgroups that loop, but 111 against 99 with all
-// rows held).
+// rows around it, 32000 rows of 2048 took a seventh more time. A row without a
+// token costs its workgroup's launch: 16 us for 256 groups of 256 rows of 2048 of
+// which 2 hold tokens (a fifth less with fewer workgroups that loop, but an eighth
+// more with all rows held).
 template <bool MANY, class F>
 __device__ __forceinline__ void for_held_blocks(const GluArgs& p, int row_step, int chunk, F&& f) {
   const int blocks = p.inner / QBLOCK, at = threadIdx.x >> 4;
@@ -72,7 +72,7 @@ __device__ __forceinline__ void for_held_blocks(const GluArgs& p, int row_step, 
 }
 
 // Bound by memory: 4 bytes read and 1 + 4/128 written a value, about 20
-// instructions each between. 32000 rows of 2048: 50 us (6.6 TB/s).
+// instructions each between. 32000 rows of 2048: 50 us (333 MB counted, 6.6 TB/s).
 template <bool E8, bool MANY>
 __global__ __launch_bounds__(GLU_THREADS) void swiglu_fp8_kernel(GluArgs p, int row_step, int chunk) {
   const size_t I = p.inner;
@@ -90,8 +90,8 @@ __global__ __launch_bounds__(GLU_THREADS) void swiglu_fp8_kernel(GluArgs p, int 
   });
 }
 
-// Bound by memory: 6 bytes read and 4 written a value. 29416 rows of 2048: 92 us
-// (6.4 TB/s).
+// Bound by memory: 6 bytes read and 4 written a value. 29416 rows of 2048: 93 us
+// (591 MB counted, 6.4 TB/s).
 template <bool MANY>
 __global__ __launch_bounds__(GLU_THREADS) void swiglu_bwd_kernel(GluArgs p, int row_step, int chunk) {
   const size_t I = p.inner;

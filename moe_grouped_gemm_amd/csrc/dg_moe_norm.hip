@@ -11,6 +11,7 @@
 // where the team has more waves) run under them. Bound by memory: every
 // activation is read once and written once. 8192 rows of 7168: 82 us forward (470
 // MB, 5.7 TB/s); the gradient of 4099 rows: 72 us with its column sums (353 MB).
+// Other figures here are ratios, or of other sizes.
 
 #include <algorithm>
 
@@ -148,7 +149,7 @@ __global__ __launch_bounds__(MAX_THREADS) void block_norm_kernel(NormArgs p, int
       for (int i = 0; i < VPT; ++i) h[i] = unpack8(x[i]);
     }
     // The next row is asked for once this one has been read out; asked for
-    // earlier it would come before this row's own waits (84 us against 96).
+    // earlier it would come before this row's own waits (a seventh slower).
     load(t + step);
     if (p.y) {
 #pragma unroll
@@ -263,7 +264,7 @@ __global__ __launch_bounds__(MAX_THREADS) void block_norm_bwd_kernel(NormBwdArgs
     if constexpr (FULL) load_row<VPT>(r.g, p.gate, row, H, tm, live);
   };
   // Two rows on their way where the registers allow, else one or none: 4099 rows of
-  // 7168 in 72 us, with one 75.
+  // 7168 take 4% less time with two than with one.
   constexpr int LEAD = VPT > 1 ? 0 : FULL ? 1 : 2;
   Row ahead[2];
   if constexpr (LEAD > 0) load(ahead[0], t);
@@ -433,10 +434,10 @@ TeamShape team_shape(int tokens, int hidden, int grid) {
   return {waves, std::min(MAX_WAVES / waves, (tokens + grid - 1) / grid), vpt};
 }
 
-// One workgroup a CU of the `cus` that the caller leaves the kernels: 2 and 4 were
-// slower at every size (8192 rows of 7168 in 87 us against 92 and 97). Fewer where
-// they need no more rounds of rows are no faster: a round takes what a CU takes for
-// its rows.
+// One workgroup a CU of the `cus` that the caller leaves the kernels: 2 and 4 are
+// slower (8192 rows of 7168 by 3 and 7%, the gradient of 4099 rows by 12 and 36%).
+// Fewer where they need no more rounds of rows are no faster: a round takes what a
+// CU takes for its rows.
 int row_grid(int tokens, int cus) { return std::min({tokens, cus, MOST_WORKGROUPS}); }
 
 }  // namespace

@@ -28,7 +28,7 @@ __device__ __forceinline__ uint64_t same_key(int key, bool valid, int bits) {
 // order. Bound by latency: 2 N reads and N writes of 4 bytes are nothing, so
 // chunks are as small as keeps the table of counts small (MAX_CHUNKS rows,
 // read by every workgroup of the second pass). 65536 slots over 32 groups take
-// 4.8 and 6.8 us, in one workgroup they took 174.
+// 5 and 7 us, in one workgroup they took 174.
 constexpr int SORT_THREADS = 1024;
 constexpr int SORT_WAVES = SORT_THREADS / 64;
 constexpr int MAX_CHUNKS = 256;
@@ -159,7 +159,7 @@ __global__ __launch_bounds__(SORT_THREADS) void rank_kernel(RouteArgs p, int chu
     fill_layout(p, total, first, blockIdx.x * SORT_THREADS + tid, chunks * SORT_THREADS);
 }
 
-constexpr int DISPATCH_THREADS = 512;  // 65536 rows of 7168 in FP8: 127 us with the sort, 133 with 256 threads
+constexpr int DISPATCH_THREADS = 512;  // 256: 65536 rows of 7168 in FP8 take 4% more time, BF16 rows the same
 
 // How a token's values arrive in its rows: copied, or quantised with float32
 // or power-of-two scales (or not at all, where only the sort is wanted).
@@ -237,7 +237,7 @@ __global__ __launch_bounds__(DISPATCH_THREADS) void dispatch_kernel(RouteArgs p,
 // Bound by latency: a launch costs more than the counting, which is the same in
 // every workgroup, LDS atomics on whole numbers (their order does not matter)
 // that grow with the slots. An XCD takes successive tokens, for their rows' scales
-// as in dispatch_kernel (8192 slots of 7168 values: 19.9 us, without 22.1). Ranking by
+// as in dispatch_kernel (without that 8192 slots of 7168 values took a seventh more). Ranking by
 // comparing each slot with all ids took as long at 40 slots and 14 us at 4096.
 // Where it is used: one_launch.
 constexpr int FEW_SLOTS = 16384;  // at most
@@ -248,9 +248,10 @@ constexpr int FILL_ROWS = 2048;      // rows of grouped_layout that are worth a 
 static_assert(FEW_SLOTS / FEW_WORKGROUPS + MAX_TOP_K <= 64, "a wave ranks a workgroup's slots");
 
 // Counters in LDS for few groups come in several copies, a lane's one by its number, so
-// that lanes with the same id seldom meet in one atomic: 16080 ids over 5 groups took
-// 17 us with one copy (rows of 256), with sixteen 11. Many groups spread by
-// themselves, and few ids are not worth clearing and adding up more counters.
+// that lanes with the same id seldom meet in one atomic: 8192 ids over 2 groups (rows
+// of 256) take 7.7 us, with one copy 17.2, over 4 groups 7.5 and 10.9; 4096 ids over
+// 32 groups 6.2 and 5.7. Many groups spread by themselves if the ids do, and few ids are
+// not worth clearing and adding up more counters.
 __device__ __forceinline__ int counter_copies(int ids, int groups) {
   int copies = 1;
   while (copies * groups < 64 && copies * 1024 < ids) copies <<= 1;
@@ -342,7 +343,7 @@ __global__ __launch_bounds__(FEW_THREADS) void few_kernel(RouteArgs p, MoveArgs 
 // rows of 8 slots on their way at once. Bound by memory: every row is read
 // once. A row of values is spread over workgroups too (`parts` of them), so
 // that a few hundred tokens fill the device. 8192 tokens of 8 rows of 7168: 171
-// us (6.2 TB/s); 259 tokens: 7.5 us (4.4 TB/s; one row's loads after the other
+// us (6.2 TB/s); 259 tokens: 7.2 us (4.6 TB/s; one row's loads after the other
 // and a workgroup a token took 20).
 constexpr int COMBINE_THREADS = 256;
 constexpr int AHEAD = 8;
@@ -456,10 +457,13 @@ namespace {
 // Whether one launch sorts (and moves), where that beats the passes over chunks.
 // Times in us, 64 groups, FP8, first the one launch: ids spread evenly / by a Zipf
 // law of exponent 1.2, whose counting meets on few counters.
-//   sort alone       4096 slots   4.7 / 7.2 against 6.9 / 7.0; 8192  6.2 / 11.3 against 7.1 / 7.2
-//   rows of 256      8192 (4096 tokens)  7.3 / 11.4 against 9.9 / 9.9; 16384  10.0 / 16.2 against 10.4 / 10.5
-//   rows of 4096     16384 (4096 tokens)  28.6 / 28.9 against 30.0 / 29.9
-//   rows of 7168     8192 (1024 tokens)  19.9 / 19.6 against 24.9 / 25.0; 16384 (4096 tokens)  41.0 / 41.5 against 45.8 / 45.5
+//   sort alone     4096 slots                4.7 /  7.2 against  6.9 /  7.0
+//                  8192                      6.2 / 11.3 against  7.1 /  7.2
+//   rows of 256    8192 of 4096 tokens       7.3 / 11.4 against  9.9 /  9.9
+//                  16384 of 4096            10.0 / 16.2 against 10.4 / 10.5
+//   rows of 4096   16384 of 4096            28.6 / 28.9 against 30.0 / 29.9
+//   rows of 7168   8192 of 1024             19.9 / 19.6 against 24.9 / 25.0
+//                  16384 of 4096            41.0 / 41.5 against 45.8 / 45.5
 // More tokens than that are too many for each workgroup, which moves its own in
 // turn: 8192 slots of 8192 tokens of 7168  55.4 / 58.0 against 46.8 / 46.2.
 bool one_launch(const RouteArgs& a, bool moves) {
