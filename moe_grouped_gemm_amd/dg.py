@@ -9,6 +9,7 @@ library's gfx950 kernels. There is no fallback: a missing library raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -84,6 +85,22 @@ def _stream(t: torch.Tensor) -> int:
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _on_its_device(gemm):
+    """Calls `gemm` with its first operand's device current: the handle of a default
+    stream is 0 on every device, and the library launches on the current one."""
+    @functools.wraps(gemm)
+    def call(a, *args, **kwargs):
+        index = a.get_device() if isinstance(a, torch.Tensor) else -1
+        if index < 0 or index == _current_device():
+            return gemm(a, *args, **kwargs)
+        with torch.cuda.device(index):
+            return gemm(a, *args, **kwargs)
+    return call
+
+
 def _need(t: torch.Tensor, name: str, dtype, ndim: int, device) -> None:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -146,6 +163,7 @@ get_col_major_tma_aligned_tensor = get_mn_major_tma_aligned_tensor
 # The GEMMs
 # ---------------------------------------------------------------------------
 
+@_on_its_device
 def fp8_gemm_nt(a, sfa, b, sfb, d, ue8m0: bool = False) -> torch.Tensor:
     """d[m, n] = bf16(sum_k a[m,k] sfa[k/128][m] * b[n,k] sfb[n/128][k/128]).
 
@@ -174,6 +192,7 @@ def fp8_gemm_nt(a, sfa, b, sfb, d, ue8m0: bool = False) -> torch.Tensor:
     return d
 
 
+@_on_its_device
 def m_grouped_fp8_gemm_nt_contiguous(a, sfa, b, sfb, d, grouped_layout, ue8m0: bool = False) -> torch.Tensor:
     """Contiguous-layout grouped GEMM; grouped_layout [M] int32 holds each
     row's group (-1 for padding). b [G, N, K], sfb [G, N/128, K/128]."""
@@ -196,6 +215,7 @@ def m_grouped_fp8_gemm_nt_contiguous(a, sfa, b, sfb, d, grouped_layout, ue8m0: b
     return d
 
 
+@_on_its_device
 def m_grouped_fp8_gemm_nt_masked(a, sfa, b, sfb, d, masked_m, ue8m0: bool = False) -> torch.Tensor:
     """Masked-layout grouped GEMM; masked_m [G] int32 (device) holds each
     group's valid rows. a [G, max_m, K], sfa [G, K/128, tma_aligned(max_m)],
@@ -220,6 +240,7 @@ def m_grouped_fp8_gemm_nt_masked(a, sfa, b, sfb, d, masked_m, ue8m0: bool = Fals
     return d
 
 
+@_on_its_device
 def m_grouped_fp8_gemm_nt_nopad(a, sfa, b, sfb, d, group_rows, ue8m0: bool = False) -> torch.Tensor:
     """No-padding grouped GEMM; group_rows [G] int32 (device) holds each
     group's row count, the groups' rows following one another from row 0 of
@@ -244,6 +265,7 @@ def m_grouped_fp8_gemm_nt_nopad(a, sfa, b, sfb, d, group_rows, ue8m0: bool = Fal
     return d
 
 
+@_on_its_device
 def m_grouped_fp8_fp4_gemm_nt_contiguous(a, sfa, b, sfb, d, grouped_layout) -> torch.Tensor:
     """FP8 x FP4 (W4A8) contiguous-layout grouped GEMM: as the FP8 call, with
     b [G, N, K/2] uint8 (packed E2M1, element 2j in the low nibble of byte j)
@@ -268,6 +290,7 @@ def m_grouped_fp8_fp4_gemm_nt_contiguous(a, sfa, b, sfb, d, grouped_layout) -> t
     return d
 
 
+@_on_its_device
 def m_grouped_fp8_fp4_gemm_nt_masked(a, sfa, b, sfb, d, masked_m) -> torch.Tensor:
     """FP8 x FP4 (W4A8) masked-layout grouped GEMM: a [G, max_m, K],
     sfa [G, K/128, tma_aligned(max_m)], b [G, N, K/2] uint8 (packed E2M1),
@@ -292,6 +315,7 @@ def m_grouped_fp8_fp4_gemm_nt_masked(a, sfa, b, sfb, d, masked_m) -> torch.Tenso
     return d
 
 
+@_on_its_device
 def k_grouped_fp8_gemm_nt_contiguous(a, sfa, b, sfb, d, ks, c=None, ue8m0: bool = False) -> torch.Tensor:
     """K-grouped GEMM (weight-gradient shape): for each group g,
     d[g] = (c[g] or 0) + A[:, K_g] . B[:, K_g]^T with per-row, per-128-K

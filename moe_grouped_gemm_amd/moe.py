@@ -29,7 +29,7 @@ from typing import Optional
 import torch
 
 from . import dg
-from .dg import DGError, _check, _need  # noqa: F401  (DGError: what a failed call raises)
+from .dg import DGError, _check, _current_device, _need  # noqa: F401  (DGError: what a failed call raises)
 
 _LAYOUTS = {"dense": 0, "contiguous": 1, "masked": 2, "nopad": 3}
 _BF16, _F32, _I32, _FP8 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
@@ -97,9 +97,6 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _stream(index: int) -> int:
     return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
-
-
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(name: str, index: int, *args) -> None:
