@@ -195,8 +195,8 @@ def test_sort_extreme_ids_many_slots(dev, layout):
 
 @pytest.mark.parametrize("layout", ["contiguous", "nopad", "masked"])
 def test_plan_across_the_limit_of_one_launch(dev, layout):
-    """One plan with more and fewer than 16384 slots in turn, by sort and by
-    dispatch: nothing of a call is left for the next."""
+    """One plan with more and fewer slots in turn than one launch takes, by sort and
+    by dispatch: nothing of a call is left for the next."""
     _say(f"a plan across the limit of one launch, {layout}")
     k, g = 4, 8
     plan = _make_plan(6000, k, g, layout, None)
@@ -296,7 +296,7 @@ def test_dispatch_fp8(dev, case, ue8m0, special):
     _check_codes(q, sfa, _f64(x).astype(np.float32), _check_sorted(plan, ids), ue8m0, plan)
 
 
-# more slots than one launch sorts and moves (16384)
+# more slots than one launch ever sorts and moves (16384)
 LARGE_MOVES = [
     ("masked", 2500, 8, 16, 384, 1001), ("masked", 1100, 17, 64, 1152, 301), ("nopad", 900, 24, 40, 640, 15000),
     ("nopad", 2060, 8, 256, 1920, None), ("contiguous", 700, 32, 33, 256, None), ("contiguous", 4100, 5, 9, 512, 12800),
@@ -310,6 +310,15 @@ LARGE_MOVES = [
 def test_dispatch_fp8_many_slots(dev, case, with_sort, ue8m0, special):
     _say(f"dispatch_fp8 {case} sort={with_sort} ue8m0={ue8m0} special={special}")
     _dispatch_fp8(dev, case, with_sort, ue8m0, special)
+
+
+@pytest.mark.parametrize("ue8m0", [False, True])
+@pytest.mark.parametrize("case", [("masked", 1500, 8, 16, 4224, 901), ("contiguous", 600, 25, 40, 4096, None),
+                                  ("nopad", 4000, 4, 7, 4096, 14000)])
+def test_dispatch_fp8_long_rows_in_one_launch(dev, case, ue8m0):
+    """As many slots as one launch takes with long rows; several tokens a workgroup."""
+    _say(f"dispatch_fp8 {case} ue8m0={ue8m0}")
+    _dispatch_fp8(dev, case, True, ue8m0, True)
 
 
 @pytest.mark.parametrize("special", [False, True])
