@@ -1,7 +1,9 @@
 // C ABI of the FP8 NT GEMM library: argument validation, CU-count setting and
-// dispatch to the gfx950 kernels. The contract is documented in include/dg.h.
+// dispatch to the gfx950 kernels. The contract is documented in include/dg.h
+// and include/fp4/dg_fp4.h.
 
 #include "../../include/dg.h"
+#include "../../include/fp4/dg_fp4.h"
 
 #include <hip/hip_runtime.h>
 
@@ -57,6 +59,9 @@ int effective_cus() {
 
 constexpr long long kMaxDim = 1 << 20;
 constexpr long long kMaxBytes = 1LL << 40;
+// FP4: rows, and 128 x 128 tiles, which the kernels count in ints with room to step past the last.
+constexpr long long kMaxFp4Rows = 1LL << 30;
+constexpr long long kMaxFp4Tiles = 1LL << 29;
 constexpr int kMaxMaskedGroups = dg::MAX_MASKED_GROUPS;
 constexpr int kMaxNopadGroups = dg::MAX_NOPAD_GROUPS;
 
@@ -282,6 +287,103 @@ dg_status dg_m_grouped_fp8_fp4_gemm_nt_masked(const void* a, const float* sfa, c
   const int cus = effective_cus();
   if (cus <= 0) return DG_ERR_DEVICE;
   return dg::launch_fp8_fp4(dg::KIND_MASKED, args, cus, reinterpret_cast<hipStream_t>(stream)) == hipSuccess
+             ? DG_OK
+             : DG_ERR_LAUNCH;
+}
+
+}  // extern "C"
+
+namespace {
+
+// The FP4 products: rows of k / 2 bytes, scale words [k/128][align4] for either
+// operand. `rows` is what the layout says about them (dense: null).
+dg_status fp4(int kind, const void* a, const uint32_t* sfa, const void* b, const uint32_t* sfb, void* d,
+              const int32_t* rows, int num_groups, int m, int n, int k, void* stream) {
+  if (dg_status s = common_checks(a, reinterpret_cast<const float*>(sfa), b, reinterpret_cast<const float*>(sfb), d, n,
+                                  k))
+    return s;
+  if (kind != dg::KIND_DENSE && !rows) return DG_ERR_NULL;
+  if (num_groups < 0 || (kind == dg::KIND_MASKED ? m <= 0 : m < 0)) return DG_ERR_SHAPE;
+  if (kind == dg::KIND_CONTIGUOUS && m % 128 != 0) return DG_ERR_SHAPE;
+  if (kind == dg::KIND_MASKED && num_groups > kMaxMaskedGroups) return DG_ERR_UNSUPPORTED;
+  if (kind == dg::KIND_NOPAD && num_groups > kMaxNopadGroups) return DG_ERR_UNSUPPORTED;
+  const long long all = (kind == dg::KIND_MASKED ? (long long)num_groups : 1LL) * m;
+  // The kernel's row and tile numbers are ints.
+  if (all >= kMaxFp4Rows || (all / 128 + num_groups + 1) * (n / 128) >= kMaxFp4Tiles) return DG_ERR_UNSUPPORTED;
+  if (all * (k / 2) >= kMaxBytes || all * n * 2 >= kMaxBytes || (long long)num_groups * n * (k / 2) >= kMaxBytes)
+    return DG_ERR_UNSUPPORTED;
+  if (m == 0 || num_groups == 0) return DG_OK;
+  dg::GemmArgs args{};
+  args.a = static_cast<const uint8_t*>(a);
+  args.sfa = reinterpret_cast<const float*>(sfa);
+  args.b = static_cast<const uint8_t*>(b);
+  args.sfb = reinterpret_cast<const float*>(sfb);
+  args.d = static_cast<uint16_t*>(d);
+  args.aux = rows;
+  args.m = m;
+  args.n = n;
+  args.k = k;
+  args.num_groups = num_groups;
+  args.ld_sfa = tma_aligned(m, 4);
+  args.ld_sfb = tma_aligned(n, 4);
+  const int cus = effective_cus();
+  if (cus <= 0) return DG_ERR_DEVICE;
+  return dg::launch_fp4(kind, args, cus, reinterpret_cast<hipStream_t>(stream)) == hipSuccess ? DG_OK : DG_ERR_LAUNCH;
+}
+
+dg_status quantize_checks(const void* x, const void* q, const uint32_t* sf, int groups, int rows, int k) {
+  if (groups < 0 || rows < 0 || k <= 0 || k % 128 != 0) return DG_ERR_SHAPE;
+  if (k > kMaxDim || (long long)groups * rows >= kMaxFp4Rows || (long long)groups * rows * k * 4 >= kMaxBytes)
+    return DG_ERR_UNSUPPORTED;
+  if (groups > 0 && rows > 0 && (!x || !q || !sf)) return DG_ERR_NULL;
+  if (!aligned16(x) || !aligned16(q) || !aligned16(sf)) return DG_ERR_ALIGN;
+  return DG_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+dg_status dg_fp4_gemm_nt(const void* a, const uint32_t* sfa, const void* b, const uint32_t* sfb, void* d, int m, int n,
+                         int k, void* stream) {
+  return fp4(dg::KIND_DENSE, a, sfa, b, sfb, d, nullptr, 1, m, n, k, stream);
+}
+
+dg_status dg_m_grouped_fp4_gemm_nt_contiguous(const void* a, const uint32_t* sfa, const void* b, const uint32_t* sfb,
+                                              void* d, const int32_t* grouped_layout, int m, int n, int k,
+                                              int num_groups, void* stream) {
+  return fp4(dg::KIND_CONTIGUOUS, a, sfa, b, sfb, d, grouped_layout, num_groups, m, n, k, stream);
+}
+
+dg_status dg_m_grouped_fp4_gemm_nt_masked(const void* a, const uint32_t* sfa, const void* b, const uint32_t* sfb,
+                                          void* d, const int32_t* masked_m, int num_groups, int max_m, int n, int k,
+                                          void* stream) {
+  return fp4(dg::KIND_MASKED, a, sfa, b, sfb, d, masked_m, num_groups, max_m, n, k, stream);
+}
+
+dg_status dg_m_grouped_fp4_gemm_nt_nopad(const void* a, const uint32_t* sfa, const void* b, const uint32_t* sfb,
+                                         void* d, const int32_t* group_rows, int m, int n, int k, int num_groups,
+                                         void* stream) {
+  return fp4(dg::KIND_NOPAD, a, sfa, b, sfb, d, group_rows, num_groups, m, n, k, stream);
+}
+
+dg_status dg_quantize_fp4(const void* x, int x_type, void* q, uint32_t* sf, int groups, int rows, int k,
+                          void* stream) {
+  if (x_type != DG_BF16 && x_type != DG_FLOAT32) return DG_ERR_SHAPE;
+  if (dg_status s = quantize_checks(x, q, sf, groups, rows, k)) return s;
+  if (groups == 0 || rows == 0) return DG_OK;
+  if (effective_cus() <= 0) return DG_ERR_DEVICE;
+  const dg::QuantizeArgs args{x, static_cast<uint8_t*>(q), sf, x_type == DG_FLOAT32, groups, rows, k,
+                              tma_aligned(rows, 4)};
+  return dg::launch_quantize_fp4(args, reinterpret_cast<hipStream_t>(stream)) == hipSuccess ? DG_OK : DG_ERR_LAUNCH;
+}
+
+dg_status dg_dequantize_fp4(const void* q, const uint32_t* sf, void* x, int groups, int rows, int k, void* stream) {
+  if (dg_status s = quantize_checks(x, q, sf, groups, rows, k)) return s;
+  if (groups == 0 || rows == 0) return DG_OK;
+  if (effective_cus() <= 0) return DG_ERR_DEVICE;
+  return dg::launch_dequantize_fp4(static_cast<const uint8_t*>(q), sf, x, groups, rows, k, tma_aligned(rows, 4),
+                                   reinterpret_cast<hipStream_t>(stream)) == hipSuccess
              ? DG_OK
              : DG_ERR_LAUNCH;
 }

@@ -1,6 +1,6 @@
 // Device code shared by the GEMM kernels (the two FP8 K-loop pipelines
 // dg_kernel.hip and dg_kernel_deep.hip, the K-grouped kernel and the FP8 x FP4
-// kernel): vector types, the LDS swizzle, waits and barriers, buffer
+// and FP4 kernels): vector types, the LDS swizzle, waits and barriers, buffer
 // descriptors, E8M0 scale codes, the tile scheduler of the M-grouped layouts
 // with its on-device group table, and the contiguous layout's row masks.
 #pragma once
@@ -103,6 +103,10 @@ __device__ __forceinline__ f32x4 mfma_fp8_scaled(const i32x8& a, const i32x8& b,
 __device__ __forceinline__ int e8m0_code(float s) {
   return (int)((__builtin_bit_cast(uint32_t, s) >> 23) & 0xFFu);
 }
+
+// log2 of a kernel configuration's LHS values per byte: 1 where A is packed FP4.
+template <class C>
+constexpr int A_PACK_SHIFT = 0;
 
 // Where one output tile's operands live, and which of its rows are valid.
 struct TileRef {
@@ -247,13 +251,13 @@ __device__ __forceinline__ TileRef resolve_tile(const GemmArgs& p, int t, int nu
       // The group's rows: a row range of the shared A, sfa and D.
       const int first = s_prefix[p.num_groups + 1 + g];
       v = s_prefix[p.num_groups + 2 + g] - first;
-      tr.a = p.a + (size_t)first * K;
+      tr.a = p.a + (size_t)first * (K >> A_PACK_SHIFT<C>);
       tr.sfa = p.sfa + first;
       tr.d = p.d + (size_t)first * p.n;
     } else {
       // The group's own [max_m] slice of A, sfa and D.
       v = min(max(aux_scalar(p.aux, g), 0), p.m);
-      tr.a = p.a + (size_t)g * p.m * K;
+      tr.a = p.a + (size_t)g * p.m * (K >> A_PACK_SHIFT<C>);
       tr.sfa = p.sfa + (size_t)g * k_blocks * p.ld_sfa;
       tr.d = p.d + (size_t)g * p.m * p.n;
     }

@@ -42,6 +42,23 @@ struct GemmArgs {
 // masked) on `stream` (dg_kernel_fp4.hip); arguments already validated.
 hipError_t launch_fp8_fp4(int kind, GemmArgs args, int num_cus, hipStream_t stream);
 
+// Enqueues the FP4 GEMM of layout `kind` on `stream` (dg_kernel_mx.hip): sfa and
+// sfb hold words of four E8M0 codes; arguments already validated.
+hipError_t launch_fp4(int kind, GemmArgs args, int num_cus, hipStream_t stream);
+
+// Rows quantised to FP4 and back (dg_quantize_fp4.hip): `groups` times `rows`
+// rows of k values, the scale words of a group [k/128][ld].
+struct QuantizeArgs {
+  const void* x;
+  uint8_t* q;
+  uint32_t* sf;
+  int wide;            // nonzero: x is float32, else BF16
+  int groups, rows, k, ld;
+};
+hipError_t launch_quantize_fp4(const QuantizeArgs& args, hipStream_t stream);
+hipError_t launch_dequantize_fp4(const uint8_t* q, const uint32_t* sf, void* x, int groups, int rows, int k, int ld,
+                                 hipStream_t stream);
+
 // Largest group count of the K-grouped GEMM (its group offsets travel in the
 // kernel arguments).
 constexpr int MAX_KGROUPED_GROUPS = 512;

@@ -1,5 +1,5 @@
 // Device code shared by the steps around the GEMMs: BF16 vectors, sums over
-// a wave, and the quantisation of a 128-value block.
+// a wave, and the quantisation of 128-value blocks.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -175,6 +175,63 @@ __device__ __forceinline__ u32x2 quantize_row(const F8& x, float& scale) {
   const uint32_t top = max16(abs_top(x));
   scale = block_scale<E8>(top);
   return quantize8(x, top, scale, 1.0f / scale);
+}
+
+// FP4 (E2M1) with one power-of-two scale per 32 values, a team of 4 lanes with 8
+// values each; the scales of the 128 values of 16 lanes are the bytes of a word.
+
+// Largest over the 4 lanes of a team, in each of them (DPP quad_perm).
+template <int PERM>
+__device__ __forceinline__ uint32_t quad(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, PERM, 0xF, 0xF, false);
+}
+__device__ __forceinline__ uint32_t max4(uint32_t v) {
+  v = max(v, quad<0xB1>(v));   // lanes 1, 0, 3, 2
+  return max(v, quad<0x4E>(v));  // lanes 2, 3, 0, 1
+}
+
+constexpr uint32_t FP4_NAN_SCALE = 255;
+
+// The E8M0 code of a block's scale from the largest bit pattern of its |x|: the
+// smallest power of two that is not below amax / 6. With amax = 1.m 2^e and 6 =
+// 1.5 2^2 that is 2^(e - 2), or twice that where 1.m > 1.5, which adding
+// 0x3FFFFF carries into the exponent. At least 2^-127, code 0, at which what is
+// smaller rounds towards zero. An infinity or NaN gives the code that makes all 32
+// values NaN.
+__device__ __forceinline__ uint32_t fp4_scale(uint32_t top) {
+  if (top >= 0x7F800000u) return FP4_NAN_SCALE;
+  return (uint32_t)max((int)((top + 0x3FFFFFu) >> 23) - 2, 0);
+}
+
+// A scale code as the float whose exponent field it is, which the conversions
+// read as 2^(code - 127) (code 0 too; NaN for 255).
+__device__ __forceinline__ float fp4_scale_value(uint32_t code) { return __builtin_bit_cast(float, code << 23); }
+
+// The four codes of a word from those of its four teams.
+__device__ __forceinline__ uint32_t fp4_scale_word(uint32_t code) {
+  return (uint32_t)bcast16<0>((int)code) | (uint32_t)bcast16<4>((int)code) << 8 |
+         (uint32_t)bcast16<8>((int)code) << 16 | (uint32_t)bcast16<12>((int)code) << 24;
+}
+
+// E2M1 codes of 8 values over their block's scale, the first in the low nibble of
+// the low byte: rounded to the nearest, ties to the even code, by the conversion
+// itself (|x| / scale is at most 6). Zeros under a NaN scale.
+__device__ __forceinline__ uint32_t fp4_codes(const F8& x, uint32_t code) {
+  const float s = fp4_scale_value(code);
+  uint32_t q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, x.v[0], x.v[1], s, 0);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, x.v[2], x.v[3], s, 1);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, x.v[4], x.v[5], s, 2);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, x.v[6], x.v[7], s, 3);
+  return code == FP4_NAN_SCALE ? 0u : q;
+}
+
+// What 8 codes stand for, in BF16 (exact but where it overflows).
+__device__ __forceinline__ u32x4 fp4_values(uint32_t q, uint32_t code) {
+  const float s = fp4_scale_value(code);
+  return (u32x4){__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 0)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 1)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 2)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 3))};
 }
 
 // Threads (a multiple of 64 up to `most`) of a workgroup that goes over `pieces`

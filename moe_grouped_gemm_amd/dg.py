@@ -1,8 +1,9 @@
-"""Python binding of libdg.so: the FP8 NT GEMM and its M-grouped variants.
+"""Python binding of libdg.so: the FP8 NT GEMM and its M-grouped variants, and the
+FP4 products with their quantiser.
 
 Argument marshalling only: each function checks tensor dtypes, shapes,
 devices and contiguity, then passes raw device pointers and the current HIP
-stream to the C ABI declared in include/dg.h. All arithmetic runs in the
+stream to the C ABI declared in include/dg.h and include/fp4/dg_fp4.h. All arithmetic runs in the
 library's gfx950 kernels. There is no fallback: a missing library raises.
 """
 
@@ -46,6 +47,16 @@ SIGNATURES = [
     ("dg_mfma_fp8_ceiling", [_vp, _vp, _i, _i, ctypes.POINTER(ctypes.c_longlong), _vp], _i),
 ]
 
+# ... and of every symbol include/fp4/dg_fp4.h declares.
+FP4_SIGNATURES = [
+    ("dg_fp4_gemm_nt", [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp], _i),
+    ("dg_m_grouped_fp4_gemm_nt_contiguous", [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp], _i),
+    ("dg_m_grouped_fp4_gemm_nt_masked", [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp], _i),
+    ("dg_m_grouped_fp4_gemm_nt_nopad", [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp], _i),
+    ("dg_quantize_fp4", [_vp, _i, _vp, _vp, _i, _i, _i, _vp], _i),
+    ("dg_dequantize_fp4", [_vp, _vp, _vp, _i, _i, _i, _vp], _i),
+]
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -63,7 +74,7 @@ def lib() -> ctypes.CDLL:
         if not os.path.exists(LIB_PATH):
             raise ImportError(f"{LIB_PATH} is missing: build it with `python -m moe_grouped_gemm_amd.build`")
         handle = ctypes.CDLL(LIB_PATH)
-        for name, argtypes, restype in SIGNATURES:
+        for name, argtypes, restype in SIGNATURES + FP4_SIGNATURES:
             fn = getattr(handle, name)
             fn.argtypes = argtypes
             fn.restype = restype
@@ -348,6 +359,135 @@ def k_grouped_fp8_gemm_nt_contiguous(a, sfa, b, sfb, d, ks, c=None, ue8m0: bool 
         a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), None if c is None else c.data_ptr(),
         d.data_ptr(), ks_arr, g, m, n, _stream(a)), "dg_k_grouped_fp8_gemm_nt_contiguous")
     return d
+
+
+# ---------------------------------------------------------------------------
+# FP4: E2M1 values with one power-of-two scale per 32 (MXFP4)
+# ---------------------------------------------------------------------------
+
+def _fp4_operand(q, sf, name: str, ndim: int, dev):
+    """(rows, k) of packed codes [..., rows, k/2] uint8 with their scale words
+    [..., k/128, tma_aligned(rows)] int32."""
+    _need(q, name, torch.uint8, ndim, dev)
+    _need(sf, "sf" + name, torch.int32, ndim, dev)
+    *lead, rows, half = q.shape
+    k = 2 * half
+    if k % 128:
+        raise ValueError(f"{name}: k must be a multiple of 128")
+    if any(size >= 2 ** 31 for size in q.shape):  # (the library's sizes are ints)
+        raise ValueError(f"{name}: sizes past 32 bits")
+    want = (*lead, k // 128, get_tma_aligned_size(rows, 4))
+    if tuple(sf.shape) != want:
+        raise ValueError(f"sf{name} must have shape {want}, got {tuple(sf.shape)}")
+    return rows, k
+
+
+def _fp4_gemm(name, a, sfa, b, sfb, d, rows=None, masked=False):
+    dev = a.device
+    m, k = _fp4_operand(a, sfa, "a", 3 if masked else 2, dev)
+    n, kb = _fp4_operand(b, sfb, "b", 2 if rows is None else 3, dev)
+    _need(d, "d", torch.bfloat16, a.dim(), dev)
+    if kb != k or tuple(d.shape) != (*a.shape[:-1], n):
+        raise ValueError("shape mismatch between a, b and d")
+    if n % 128:
+        raise ValueError("n must be a multiple of 128")
+    args = [a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), d.data_ptr()]
+    if rows is None:
+        sizes = (m, n, k)
+    else:
+        _need(rows, "the layout's rows", torch.int32, 1, dev)
+        g = b.shape[0]
+        if masked and a.shape[0] != g:
+            raise ValueError("a and b differ in groups")
+        if rows.shape[0] != (m if name.endswith("contiguous") else g):
+            raise ValueError("the layout's rows have the wrong length")
+        args.append(rows.data_ptr())
+        sizes = (g, m, n, k) if masked else (m, n, k, g)
+    if not d.numel():  # nothing to compute, and empty tensors have no address
+        return d
+    _check(getattr(lib(), name)(*args, *sizes, _stream(a)), name)
+    return d
+
+
+@_on_its_device
+def fp4_gemm_nt(a, sfa, b, sfb, d) -> torch.Tensor:
+    """d[m, n] = bf16(sum_k a[m,k] sfa[m,k/32] * b[n,k] sfb[n,k/32]) of FP4 values.
+
+    a [M, K/2], b [N, K/2] uint8 (packed E2M1, element 2j in the low nibble of
+    byte j), sfa [K/128, tma_aligned(M)], sfb [K/128, tma_aligned(N)] int32 (the
+    E8M0 codes of a row's four 32-value blocks, the first in the lowest byte),
+    d [M, N] bfloat16. quantize_fp4 makes both operands."""
+    return _fp4_gemm("dg_fp4_gemm_nt", a, sfa, b, sfb, d)
+
+
+@_on_its_device
+def m_grouped_fp4_gemm_nt_contiguous(a, sfa, b, sfb, d, grouped_layout) -> torch.Tensor:
+    """Contiguous-layout grouped FP4 GEMM; grouped_layout [M] int32 holds each
+    row's group (-1 for padding). b [G, N, K/2], sfb [G, K/128, tma_aligned(N)]."""
+    return _fp4_gemm("dg_m_grouped_fp4_gemm_nt_contiguous", a, sfa, b, sfb, d, grouped_layout)
+
+
+@_on_its_device
+def m_grouped_fp4_gemm_nt_masked(a, sfa, b, sfb, d, masked_m) -> torch.Tensor:
+    """Masked-layout grouped FP4 GEMM; masked_m [G] int32 (device) holds each
+    group's valid rows. a [G, max_m, K/2], sfa [G, K/128, tma_aligned(max_m)],
+    b [G, N, K/2], sfb [G, K/128, tma_aligned(N)], d [G, max_m, N]."""
+    return _fp4_gemm("dg_m_grouped_fp4_gemm_nt_masked", a, sfa, b, sfb, d, masked_m, masked=True)
+
+
+@_on_its_device
+def m_grouped_fp4_gemm_nt_nopad(a, sfa, b, sfb, d, group_rows) -> torch.Tensor:
+    """No-padding grouped FP4 GEMM; group_rows [G] int32 (device) holds each
+    group's row count, the groups' rows following one another from row 0 of a.
+    b [G, N, K/2], sfb [G, K/128, tma_aligned(N)]."""
+    return _fp4_gemm("dg_m_grouped_fp4_gemm_nt_nopad", a, sfa, b, sfb, d, group_rows)
+
+
+def _fp4_rows(x, q, sf, types, first):
+    """(groups, rows, k) of rows x [rows, k] or [groups, rows, k] and their FP4
+    operand, on the device of the call's first tensor."""
+    if not isinstance(x, torch.Tensor) or not isinstance(q, torch.Tensor):
+        raise TypeError("x and q must be torch.Tensors")
+    if x.dtype not in types:
+        raise TypeError(f"x must be {' or '.join(map(str, types))}, got {x.dtype}")
+    if first.dim() not in (2, 3):
+        raise ValueError(f"rows have 2 or 3 dims, got shape {tuple(first.shape)}")
+    _need(x, "x", x.dtype, first.dim(), first.device)
+    rows, k = _fp4_operand(q, sf, "q", first.dim(), first.device)
+    if tuple(x.shape) != (*q.shape[:-1], k):
+        raise ValueError("shape mismatch between x and q")
+    return (x.shape[0] if x.dim() == 3 else 1), rows, k
+
+
+def quantize_fp4(x, q, sf):
+    """Rows x [M, K] (or [G, M, K]) bfloat16 or float32 to an FP4 GEMM operand:
+    q [M, K/2] uint8 and sf [K/128, tma_aligned(M)] int32 (or with the leading G).
+    Per 32 values one scale, the smallest power of two not below amax / 6; codes
+    round to the nearest value, ties to the even code. An infinity or NaN makes its
+    32 values NaN. Words of sf past the last row are not written."""
+    return _quantize_fp4(x, q, sf)
+
+
+def dequantize_fp4(q, sf, x) -> torch.Tensor:
+    """The values that an FP4 operand (q, sf as quantize_fp4 makes them) stands
+    for, into x [M, K] (or [G, M, K]) bfloat16."""
+    return _dequantize_fp4(q, sf, x)
+
+
+@_on_its_device
+def _quantize_fp4(x, q, sf):
+    groups, rows, k = _fp4_rows(x, q, sf, (torch.bfloat16, torch.float32), x)
+    _check(lib().dg_quantize_fp4(x.data_ptr(), int(x.dtype is torch.float32), q.data_ptr(), sf.data_ptr(), groups,
+                                 rows, k, _stream(x)), "dg_quantize_fp4")
+    return q, sf
+
+
+@_on_its_device
+def _dequantize_fp4(q, sf, x):
+    groups, rows, k = _fp4_rows(x, q, sf, (torch.bfloat16,), q)
+    _check(lib().dg_dequantize_fp4(q.data_ptr(), sf.data_ptr(), x.data_ptr(), groups, rows, k, _stream(q)),
+           "dg_dequantize_fp4")
+    return x
 
 
 def run_workload(w, d: torch.Tensor) -> torch.Tensor:
