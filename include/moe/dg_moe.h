@@ -106,6 +106,16 @@ dg_status dg_moe_dispatch_fp8(const dg_moe_plan* plan, const int32_t* topk_ids, 
                               int tokens, int ue8m0, void* stream);
 
 /*
+ * The same with the token quantised into the FP4 GEMMs' LHS operand
+ * (../fp4/dg_fp4.h), as by dg_quantize_fp4.
+ *   q  [M][hidden/2] bytes (masked [G][max_m][hidden/2])
+ *   sf [hidden/128][dg_get_tma_aligned_size(M, 4)] words
+ *      (masked [G][hidden/128][dg_get_tma_aligned_size(max_m, 4)])
+ */
+dg_status dg_moe_dispatch_fp4(const dg_moe_plan* plan, const int32_t* topk_ids, const void* x, void* q, uint32_t* sf,
+                              int tokens, void* stream);
+
+/*
  * Sums a token's rows: y[t] = sum_j weights[t][j] * yp[row_of[t][j]], in
  * slot order in float32. Dropped slots add nothing, whatever their weight; a
  * token without rows gets zeros. weights [tokens][top_k] float32 or NULL for
@@ -141,6 +151,17 @@ dg_status dg_moe_combine_bwd(const dg_moe_plan* plan, const void* dy, const void
  */
 dg_status dg_moe_swiglu_fp8(const void* gu, void* q, float* sfa, const int32_t* rows, int layout, int m,
                             int num_groups, int inner, int ue8m0, void* stream);
+
+/*
+ * The same quantised into the FP4 GEMMs' LHS operand, as by dg_quantize_fp4:
+ *   q [m][inner/2] bytes; sf [inner/128][dg_get_tma_aligned_size(m, 4)] words
+ *     (masked: each with the leading num_groups)
+ * Codes and scales are those of the formula (not of float32 terms that may lie
+ * on the other side of a border); a product that float32 rounds to infinity counts
+ * as one.
+ */
+dg_status dg_moe_swiglu_fp4(const void* gu, void* q, uint32_t* sf, const int32_t* rows, int layout, int m,
+                            int num_groups, int inner, void* stream);
 
 /* Gradient of the activation: with s = 1 / (1 + exp(-g)),
  *   dgu[:, :inner] = da * u * s * (1 + g * (1 - s)),  dgu[:, inner:] = da * g * s.

@@ -145,6 +145,19 @@ dg_status dg_moe_dispatch_fp8(const dg_moe_plan* plan, const int32_t* topk_ids, 
   return status_of(launch_dispatch_fp8(a, x, q, sfa, ue8m0 != 0, as_stream(stream)));
 }
 
+dg_status dg_moe_dispatch_fp4(const dg_moe_plan* plan, const int32_t* topk_ids, const void* x, void* q, uint32_t* sf,
+                              int tokens, void* stream) {
+  RouteArgs a;
+  if (dg_status s = plan_checks(plan, tokens, a)) return s;
+  if (missing(x, tokens) || missing(q, (long long)tokens * a.rows) || missing(sf, (long long)tokens * a.rows))
+    return DG_ERR_NULL;
+  if (!aligned16(x) || !aligned16(q) || !aligned16(sf) || !aligned4b(topk_ids)) return DG_ERR_ALIGN;
+  a.ids = topk_ids;
+  if (tokens == 0 && !topk_ids) return DG_OK;
+  if (dg_status s = device_check()) return s;
+  return status_of(launch_dispatch_fp4(a, x, q, sf, as_stream(stream)));
+}
+
 dg_status dg_moe_combine(const dg_moe_plan* plan, const void* yp, const float* weights, void* y, int tokens,
                          void* stream) {
   RouteArgs a;
@@ -187,6 +200,25 @@ dg_status dg_moe_swiglu_fp8(const void* gu, void* q, float* sfa, const int32_t* 
   a.inner = inner;
   if (dg_status s = device_check()) return s;
   return status_of(launch_swiglu_fp8(a, ue8m0 != 0, as_stream(stream)));
+}
+
+dg_status dg_moe_swiglu_fp4(const void* gu, void* q, uint32_t* sf, const int32_t* rows, int layout, int m,
+                            int num_groups, int inner, void* stream) {
+  if (dg_status s = glu_checks(rows, layout, m, num_groups, inner)) return s;
+  if (missing(gu, m) || missing(q, m) || missing(sf, m)) return DG_ERR_NULL;
+  if (!aligned16(gu) || !aligned16(q) || !aligned16(sf)) return DG_ERR_ALIGN;
+  if (m == 0) return DG_OK;
+  GluArgs a{};
+  a.gu = static_cast<const uint16_t*>(gu);
+  a.q = static_cast<uint8_t*>(q);
+  a.sfa = sf;
+  a.rows = rows;
+  a.layout = layout;
+  a.m = m;
+  a.num_groups = num_groups;
+  a.inner = inner;
+  if (dg_status s = device_check()) return s;
+  return status_of(launch_swiglu_fp4(a, as_stream(stream)));
 }
 
 dg_status dg_moe_swiglu_bwd(const void* da, const void* gu, void* dgu, const int32_t* rows, int layout, int m,

@@ -1,5 +1,5 @@
 // The gated activation between the two grouped GEMMs, quantised into the
-// second one's FP8 operand, and its gradient.
+// second one's FP8 or FP4 operand, and its gradient.
 
 #include <algorithm>
 
@@ -86,7 +86,94 @@ __global__ __launch_bounds__(GLU_THREADS) void swiglu_fp8_kernel(GluArgs p, int 
     for (int i = 0; i < 8; ++i) a.v[i] = gate.v[i] * sigmoid(gate.v[i]) * up.v[i];
     float scale;
     store_stream(p.q + row * I + b * QBLOCK + l16 * 8, quantize_row<E8>(a, scale));
-    if (l16 == 0) p.sfa[((size_t)g * blocks + b) * ld + r] = scale;
+    if (l16 == 0) static_cast<float*>(p.sfa)[((size_t)g * blocks + b) * ld + r] = scale;
+  });
+}
+
+// To FP4, one step of which is a quarter to a half of a value: the codes are those of
+// the formula itself, whatever the last places of its float32 terms. These are
+// good to well below SLACK (the exponential's argument rounds by |g| 2^-24, |g| < 89,
+// the rest by a few 2^-24), so a code or scale that comes out the same for values
+// that much smaller and larger is the formula's. The others, one value in 10^5, are
+// computed again in 64 bits, a wave at a time, and so are blocks so small and gates so
+// far below zero that float32 terms lose their precision.
+constexpr float SLACK = 0x1p-17f;
+constexpr uint32_t TINY = 0x0D800000u;  // 2^-100
+constexpr float LOW_GATE = -87.0f;
+
+__device__ __forceinline__ uint32_t swiglu_fp4_exact(u32x4 gate_raw, u32x4 up_raw, uint32_t* scale) {
+  double a[8], top = 0.0;
+  bool finite = true;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const double g = half_of(gate_raw[i / 2], i & 1), u = half_of(up_raw[i / 2], i & 1);
+    a[i] = g / (1.0 + exp(-g)) * u;
+    const double m = fabs(a[i]);
+    finite &= m < 0x1.ffffffp127;  // what float32 rounds to infinity counts as that
+    top = m > top ? m : top;
+  }
+  uint64_t bits = __builtin_bit_cast(uint64_t, top);
+#pragma unroll
+  for (int d = 1; d < 4; d <<= 1) {
+    const uint64_t other = __shfl_xor(bits, d);
+    bits = bits > other ? bits : other;
+  }
+  uint32_t all = finite ? 1u : 0u;
+  all = all & quad<0xB1>(all);
+  all = all & quad<0x4E>(all);
+  // As fp4_scale(), of a float64's exponent and mantissa (the exponent's offset is 1023).
+  const int e = (int)((bits + 0x7FFFFFFFFFFFFull) >> 52) - (1023 - 127) - 2;
+  const int code = bits == 0 ? 0 : max(e, 0);
+  *scale = all ? (uint32_t)code : FP4_NAN_SCALE;
+  if (!all) return 0;
+  uint32_t q = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const double v = ldexp(fabs(a[i]), 127 - code);
+    const uint32_t c = (v > 0.25) + (v >= 0.75) + (v > 1.25) + (v >= 1.75) + (v > 2.5) + (v >= 3.5) + (v > 5.0);
+    q |= (c | (signbit(a[i]) ? 8u : 0u)) << (4 * i);
+  }
+  return q;
+}
+
+__device__ __forceinline__ F8 scaled(const F8& a, float by) {
+  F8 r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r.v[i] = a.v[i] * by;
+  return r;
+}
+
+// Bound by memory: 4 bytes read and 1/2 + 1/32 written a value.
+template <bool MANY>
+__global__ __launch_bounds__(GLU_THREADS) void swiglu_fp4_kernel(GluArgs p, int row_step, int chunk) {
+  const size_t I = p.inner;
+  const int blocks = p.inner / QBLOCK, ld = align4(p.m), l16 = threadIdx.x & 15;
+  for_held_blocks<MANY>(p, row_step, chunk, [&](size_t row, int g, int r, int b) {
+    const uint16_t* src = p.gu + row * 2 * I + b * QBLOCK + l16 * 8;
+    const u32x4 gate_raw = load_stream16(src), up_raw = load_stream16(src + I);
+    const F8 gate = unpack8(gate_raw), up = unpack8(up_raw);
+    F8 a;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a.v[i] = gate.v[i] * sigmoid(gate.v[i]) * up.v[i];
+    const uint32_t top = max4(abs_top(a));
+    uint32_t code = fp4_scale(top);
+    uint32_t q = fp4_codes(scaled(a, 1.0f - SLACK), code);
+    const float amax = __builtin_bit_cast(float, top);
+    bool near = q != fp4_codes(scaled(a, 1.0f + SLACK), code);
+    near |= fp4_scale(abs_bits(amax * (1.0f - SLACK))) != fp4_scale(abs_bits(amax * (1.0f + SLACK)));
+    float low = gate.v[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) low = fminf(low, gate.v[i]);
+    if (__any(low < LOW_GATE || top < TINY)) {  // but a block of zeros is exact
+      bool zero = true;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) zero &= gate.v[i] == 0.0f || up.v[i] == 0.0f;
+      near |= (low < LOW_GATE || top < TINY) && !zero;
+    }
+    if (__any(near)) q = swiglu_fp4_exact(gate_raw, up_raw, &code);
+    __builtin_nontemporal_store(q, reinterpret_cast<uint32_t*>(p.q + (row * I + b * QBLOCK + l16 * 8) / 2));
+    const uint32_t word = fp4_scale_word(code);
+    if (l16 == 0) static_cast<uint32_t*>(p.sfa)[((size_t)g * blocks + b) * ld + r] = word;
   });
 }
 
@@ -139,6 +226,13 @@ hipError_t launch_swiglu_fp8(const GluArgs& a, bool ue8m0, hipStream_t stream) {
   const bool many = s.row_step > 1;
   auto* kernel = ue8m0 ? (many ? swiglu_fp8_kernel<true, true> : swiglu_fp8_kernel<true, false>)
                        : (many ? swiglu_fp8_kernel<false, true> : swiglu_fp8_kernel<false, false>);
+  hipLaunchKernelGGL(kernel, s.grid, dim3(s.threads), 0, stream, a, s.row_step, s.chunk);
+  return hipGetLastError();
+}
+
+hipError_t launch_swiglu_fp4(const GluArgs& a, hipStream_t stream) {
+  const GluShape s = glu_shape(a);
+  auto* kernel = s.row_step > 1 ? swiglu_fp4_kernel<true> : swiglu_fp4_kernel<false>;
   hipLaunchKernelGGL(kernel, s.grid, dim3(s.threads), 0, stream, a, s.row_step, s.chunk);
   return hipGetLastError();
 }

@@ -33,6 +33,7 @@ long long sort_workspace(int slots, int num_groups);
 hipError_t launch_sort(const RouteArgs& a, hipStream_t stream);
 hipError_t launch_dispatch(const RouteArgs& a, const void* x, void* xp, hipStream_t stream);
 hipError_t launch_dispatch_fp8(const RouteArgs& a, const void* x, void* q, float* sfa, bool ue8m0, hipStream_t stream);
+hipError_t launch_dispatch_fp4(const RouteArgs& a, const void* x, void* q, uint32_t* sf, hipStream_t stream);
 hipError_t launch_combine(const RouteArgs& a, const void* yp, const float* w, void* y, hipStream_t stream);
 hipError_t launch_combine_bwd(const RouteArgs& a, const void* dy, const void* yp, const float* w, void* dyp,
                               float* dw, hipStream_t stream);
@@ -42,12 +43,13 @@ struct GluArgs {
   const uint16_t* gu;
   const uint16_t* da;   // gradient only
   uint8_t* q;           // forward only
-  float* sfa;           // forward only
+  void* sfa;            // forward only: float, or words of four codes where q is FP4
   uint16_t* dgu;        // gradient only
   const int32_t* rows;
   int layout, m, num_groups, inner;
 };
 hipError_t launch_swiglu_fp8(const GluArgs& a, bool ue8m0, hipStream_t stream);
+hipError_t launch_swiglu_fp4(const GluArgs& a, hipStream_t stream);
 hipError_t launch_swiglu_bwd(const GluArgs& a, hipStream_t stream);
 
 // Norms around the block (dg_moe_norm.hip).

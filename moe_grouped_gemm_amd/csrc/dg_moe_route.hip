@@ -1,5 +1,5 @@
 // Tokens sorted by expert into the GEMMs' row layouts, moved there (BF16, or
-// quantised to the FP8 operand) and back with weights, and the gradients.
+// quantised to the FP8 or FP4 operand) and back with weights, and the gradients.
 
 #include <algorithm>
 
@@ -162,13 +162,13 @@ __global__ __launch_bounds__(SORT_THREADS) void rank_kernel(RouteArgs p, int chu
 constexpr int DISPATCH_THREADS = 512;  // 256: 65536 rows of 7168 in FP8 take 4% more time, BF16 rows the same
 
 // How a token's values arrive in its rows: copied, or quantised with float32
-// or power-of-two scales (or not at all, where only the sort is wanted).
-enum { MOVE_BF16 = 0, MOVE_FP8 = 1, MOVE_FP8_E8 = 2, MOVE_NONE = 3 };
+// or power-of-two scales, or to FP4 (or not at all, where only the sort is wanted).
+enum { MOVE_BF16 = 0, MOVE_FP8 = 1, MOVE_FP8_E8 = 2, MOVE_NONE = 3, MOVE_FP4 = 4 };
 
 struct MoveArgs {
   const uint16_t* x;
-  uint8_t* out;  // rows of BF16 or E4M3
-  float* sfa;    // quantised only
+  uint8_t* out;  // rows of BF16, E4M3 or packed E2M1
+  void* sfa;     // quantised only: a float or (FP4) a word of four codes for 128 values
 };
 
 // Block b (128 values) of token t to the rows of up to 16 slots: 16 lanes, 8
@@ -176,17 +176,24 @@ struct MoveArgs {
 template <int MODE>
 __device__ __forceinline__ void put_block(const RouteArgs& p, const MoveArgs& m, u32x4 raw, int b, int l16, int row,
                                           int slots) {
-  constexpr int BYTES = MODE == MOVE_BF16 ? 2 : 1;
-  const size_t offset = ((size_t)b * QBLOCK + l16 * 8) * BYTES, stride = (size_t)p.hidden * BYTES;
-  u32x2 codes;
+  constexpr int HALF_BYTES = MODE == MOVE_BF16 ? 4 : MODE == MOVE_FP4 ? 1 : 2;
+  const size_t offset = ((size_t)b * QBLOCK + l16 * 8) * HALF_BYTES / 2, stride = (size_t)p.hidden * HALF_BYTES / 2;
+  std::conditional_t<MODE == MOVE_FP4, uint32_t, u32x2> codes;
   if constexpr (MODE != MOVE_BF16) {
-    float scale;
-    codes = quantize_row<MODE == MOVE_FP8_E8>(unpack8(raw), scale);
+    std::conditional_t<MODE == MOVE_FP4, uint32_t, float> scale;
+    const F8 x = unpack8(raw);
+    if constexpr (MODE == MOVE_FP4) {
+      const uint32_t code = fp4_scale(max4(abs_top(x)));
+      codes = fp4_codes(x, code);
+      scale = fp4_scale_word(code);
+    } else {
+      codes = quantize_row<MODE == MOVE_FP8_E8>(x, scale);
+    }
     // Lane l16 leaves the scale of slot l16.
     if (row >= 0) {
       const int blocks = p.hidden / QBLOCK, ld = align4(p.rows);
       const int g = p.layout == DG_MOE_MASKED ? row / p.rows : 0;
-      m.sfa[((size_t)g * blocks + b) * ld + (row - g * p.rows)] = scale;
+      static_cast<decltype(scale)*>(m.sfa)[((size_t)g * blocks + b) * ld + (row - g * p.rows)] = scale;
     }
   }
   static_for<0, 16>([&](auto J) {
@@ -516,6 +523,11 @@ hipError_t launch_dispatch_fp8(const RouteArgs& a, const void* x, void* q, float
                                hipStream_t stream) {
   const MoveArgs m{static_cast<const uint16_t*>(x), static_cast<uint8_t*>(q), sfa};
   return ue8m0 ? launch_move<MOVE_FP8_E8>(a, m, stream) : launch_move<MOVE_FP8>(a, m, stream);
+}
+
+hipError_t launch_dispatch_fp4(const RouteArgs& a, const void* x, void* q, uint32_t* sf, hipStream_t stream) {
+  const MoveArgs m{static_cast<const uint16_t*>(x), static_cast<uint8_t*>(q), sf};
+  return launch_move<MOVE_FP4>(a, m, stream);
 }
 
 namespace {

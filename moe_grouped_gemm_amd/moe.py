@@ -18,6 +18,8 @@ A block in FP8, masked layout (b1 [G, 2I, H], b2 [G, H, I] and their scales):
     moe.block_norm(x, y, post_weight, gate, pre_weight, h, n)
 
 With the UE8M0 or the FP8 x FP4 GEMMs dispatch_fp8 and swiglu_fp8 need ue8m0=True.
+With weights in FP4 (dg.quantize_fp4) dispatch_fp4 and swiglu_fp4 take their
+places, and the FP4 GEMMs the products'.
 """
 
 from __future__ import annotations
@@ -49,9 +51,11 @@ SIGNATURES = [
     ("dg_moe_sort", [_vp, _vp, _i, _vp], _i),
     ("dg_moe_dispatch", [_vp, _vp, _vp, _vp, _i, _vp], _i),
     ("dg_moe_dispatch_fp8", [_vp, _vp, _vp, _vp, _vp, _i, _i, _vp], _i),
+    ("dg_moe_dispatch_fp4", [_vp, _vp, _vp, _vp, _vp, _i, _vp], _i),
     ("dg_moe_combine", [_vp, _vp, _vp, _vp, _i, _vp], _i),
     ("dg_moe_combine_bwd", [_vp, _vp, _vp, _vp, _vp, _vp, _i, _vp], _i),
     ("dg_moe_swiglu_fp8", [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp], _i),
+    ("dg_moe_swiglu_fp4", [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp], _i),
     ("dg_moe_swiglu_bwd", [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp], _i),
     ("dg_moe_block_norm", [ctypes.c_char_p, _vp], _i),
     ("dg_moe_block_norm_workspace_bytes", [_i, _i], _ll),
@@ -207,6 +211,7 @@ class Plan:
         # shapes of the permuted buffers
         lead = (self.num_groups,) if layout == "masked" else ()
         self.rows_shape = torch.Size((*lead, self.rows, self.hidden))
+        self.codes_shape = torch.Size((*lead, self.rows, self.hidden // 2))  # FP4
         self.scale_shape = torch.Size((*lead, self.hidden // 128, dg.get_tma_aligned_size(self.rows, 4)))
 
     def _tokens(self, t: torch.Tensor, name: str, dtype, width: int) -> int:
@@ -259,6 +264,18 @@ def dispatch_fp8(plan: Plan, x, q, sfa, topk_ids=None, ue8m0: bool = False):
     _call("dg_moe_dispatch_fp8", plan._index, plan._ref, plan._ids(topk_ids, n), x.data_ptr(), q.data_ptr(),
           sfa.data_ptr(), n, ue8m0)
     return q, sfa
+
+
+def dispatch_fp4(plan: Plan, x, q, sf, topk_ids=None):
+    """dispatch() into the FP4 GEMMs' LHS operand, quantised as by dg.quantize_fp4:
+    q [rows, hidden/2] uint8 (masked [G, rows, hidden/2]) and sf [hidden/128,
+    tma_aligned(rows)] int32 (masked: [G, ...])."""
+    n = plan._tokens(x, "x", _BF16, plan.hidden)
+    _want(q, "q", torch.uint8, plan.codes_shape, plan._index)
+    _want(sf, "sf", _I32, plan.scale_shape, plan._index)
+    _call("dg_moe_dispatch_fp4", plan._index, plan._ref, plan._ids(topk_ids, n), x.data_ptr(), q.data_ptr(),
+          sf.data_ptr(), n)
+    return q, sf
 
 
 def combine(plan: Plan, yp, y, weights=None) -> torch.Tensor:
@@ -332,6 +349,18 @@ def swiglu_fp8(gu, q, sfa, rows=None, layout: str = "dense", ue8m0: bool = False
     _call("dg_moe_swiglu_fp8", index, gu.data_ptr(), q.data_ptr(), sfa.data_ptr(), _ptr(rows), kind, m, groups, inner,
           ue8m0)
     return q, sfa
+
+
+def swiglu_fp4(gu, q, sf, rows=None, layout: str = "dense"):
+    """silu(g) * u of gu, as swiglu_fp8 takes it, quantised into the next FP4 GEMM's
+    LHS operand: q [M, I/2] uint8 and sf [I/128, tma_aligned(M)] int32 (masked:
+    [G, ...]). Codes and scales are those of the formula."""
+    kind, m, groups, inner, index = _glu(gu, rows, layout)
+    lead = gu.shape[:-2]
+    _want(q, "q", torch.uint8, (*lead, m, inner // 2), index)
+    _want(sf, "sf", _I32, (*lead, inner // 128, (m + 3) // 4 * 4), index)
+    _call("dg_moe_swiglu_fp4", index, gu.data_ptr(), q.data_ptr(), sf.data_ptr(), _ptr(rows), kind, m, groups, inner)
+    return q, sf
 
 
 def swiglu_bwd(da, gu, dgu, rows=None, layout: str = "dense") -> torch.Tensor:

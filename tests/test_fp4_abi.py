@@ -1,13 +1,14 @@
 """Refusals of the FP4 calls that need no GPU: nothing is enqueued (the pointers
 below are never dereferenced)."""
 
+import ctypes
 import os
 import re
 
 import pytest
 import torch
 
-from moe_grouped_gemm_amd import dg
+from moe_grouped_gemm_amd import dg, moe
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "fp4", "dg_fp4.h")
 A, B, C, D, E, F = (0x10000 * i for i in range(1, 7))
@@ -84,6 +85,42 @@ def test_quantizer_refuses(call):
     assert call(groups=1 << 15, rows=1 << 15) == UNSUPPORTED and call(groups=1 << 10, rows=1 << 15, k=1 << 20) == UNSUPPORTED
     assert call(rows=0, x=None, q=None, sf=None) == 0 and call(groups=0, x=None, q=None, sf=None) == 0
     assert _quantize(kind=2) == SHAPE
+
+
+def _dispatch(ids=D, x=A, q=B, sf=C, tokens=16, **change):
+    sizes = {"layout": 2, "max_tokens": 64, "top_k": 4, "num_groups": 8, "rows": 128, "hidden": 256, "row_of": E,
+             "group_rows": F, "grouped_layout": A, "workspace": B, "workspace_bytes": 1 << 30, **change}
+    plan = moe._PlanStruct(*sizes.values())
+    return moe.lib().dg_moe_dispatch_fp4(ctypes.byref(plan), ids, x, q, sf, tokens, None)
+
+
+def test_dispatch_refuses():
+    assert _dispatch(hidden=192) == SHAPE and _dispatch(layout=0) == SHAPE and _dispatch(workspace_bytes=0) == SHAPE
+    assert _dispatch(tokens=-1) == SHAPE and _dispatch(tokens=65) == SHAPE
+    assert _dispatch(rows=1 << 30, layout=3) == UNSUPPORTED and _dispatch(row_of=None) == NULL
+    for p in ("x", "q", "sf"):
+        assert _dispatch(**{p: None}) == NULL and _dispatch(**{p: A + 8}) == ALIGN
+    assert _dispatch(ids=D + 2) == ALIGN
+    assert _dispatch(tokens=0, ids=None, x=None, q=None, sf=None) == 0
+
+
+def _glu(gu=A, q=B, sf=C, rows=D, layout=2, m=128, groups=8, inner=256):
+    return moe.lib().dg_moe_swiglu_fp4(gu, q, sf, rows, layout, m, groups, inner, None)
+
+
+def test_glu_refuses():
+    for p in ("gu", "q", "sf"):
+        assert _glu(**{p: None}) == NULL and _glu(**{p: A + 8}) == ALIGN
+    assert _glu(rows=None) == NULL and _glu(rows=D + 2) == ALIGN
+    assert _glu(inner=0) == SHAPE and _glu(inner=200) == SHAPE and _glu(inner=1 << 21) == UNSUPPORTED
+    assert _glu(m=-1) == SHAPE and _glu(layout=7) == SHAPE and _glu(groups=0) == SHAPE and _glu(layout=1, m=100) == SHAPE
+    assert _glu(groups=4097) == UNSUPPORTED and _glu(layout=0, rows=None, m=1 << 24) == UNSUPPORTED
+    assert _glu(layout=0, m=0, rows=None, gu=None, q=None, sf=None) == 0
+
+
+@no_gpu
+def test_valid_steps_need_a_device():
+    assert _dispatch() == DEVICE and _glu() == DEVICE
 
 
 def test_binding_refuses():
