@@ -247,6 +247,51 @@ typedef struct dg_moe_norm_bwd {
 } dg_moe_norm_bwd;
 dg_status dg_moe_block_norm_bwd(const dg_moe_norm_bwd* args, void* stream);
 
+/*
+ * A whole expert layer for a few tokens, in two launches:
+ *   y[t] = sum_j weights[t][j] * B2[e] (silu(g) * u),  [g | u] = B1[e] x[t],
+ * with e = topk_ids[t][j] and silu(v) = v / (1 + exp(-v)).
+ *   x, y     [tokens][hidden] BF16
+ *   topk_ids [tokens][top_k] int32; an id outside [0, num_groups) adds
+ *            nothing, whatever its weight; a token without experts gets zeros
+ *   weights  [tokens][top_k] float32, or NULL for ones
+ *   b1, b2   [num_groups][2 * inner][hidden] (g's rows first) and
+ *            [num_groups][hidden][inner], by weight_type E4M3 or packed E2M1, with
+ *            their scales as the products take them as b and sfb:
+ *            DG_MOE_WEIGHTS_FP8: float32 per 128 x 128 (dg.h);
+ *            DG_MOE_WEIGHTS_FP4: words of E8M0 codes (../fp4/dg_fp4.h)
+ *   workspace  16-byte aligned, dg_moe_experts_workspace_bytes() bytes;
+ *            contents need not be kept between calls; calls that use one must be
+ *            ordered (one stream, or events)
+ * The weights of the experts that have tokens are read once. Neither x nor the
+ * weights are quantised on the way: weights stand for their exact values (of FP4
+ * in BF16's range), products sum in float32 and silu(g) * u is rounded once to
+ * BF16. (The order of a token's sums goes by how many experts the call's tokens
+ * name.)
+ * tokens <= 128, top_k <= 32, tokens * top_k <= 1024, num_groups <= 4096,
+ * hidden and inner multiples of 128 up to 2^16. tokens == 0 is a no-op.
+ */
+#define DG_MOE_WEIGHTS_FP8 0
+#define DG_MOE_WEIGHTS_FP4 1
+typedef struct dg_moe_experts_args {
+  const void* x;
+  const int32_t* topk_ids;
+  const float* weights;
+  const void* b1;
+  const void* sfb1;
+  const void* b2;
+  const void* sfb2;
+  void* y;
+  void* workspace;
+  long long workspace_bytes;
+  int weight_type, tokens, top_k, num_groups, hidden, inner;
+} dg_moe_experts_args;
+
+/* Bytes of the workspace for up to so many tokens, or -1 if the sizes are not valid. */
+long long dg_moe_experts_workspace_bytes(int tokens, int top_k, int num_groups, int inner);
+
+dg_status dg_moe_experts(const dg_moe_experts_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -14,7 +14,8 @@ LIB = os.path.join(PKG, "libdg.so")
 
 SOURCES = ["dg_kernel.hip", "dg_kernel_deep.hip", "dg_kernel_kgrouped.hip", "dg_kernel_fp4.hip", "dg_kernel_mx.hip",
            "dg_quantize_fp4.hip", "dg_ceiling.hip",
-           "dg_moe_route.hip", "dg_moe_glu.hip", "dg_moe_norm.hip", "dg_api.cpp", "dg_moe_api.cpp"]
+           "dg_moe_route.hip", "dg_moe_glu.hip", "dg_moe_norm.hip",
+           "dg_moe_experts.hip", "dg_api.cpp", "dg_moe_api.cpp"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

@@ -17,6 +17,7 @@ constexpr int kMaxGluRows = 1 << 22;
 constexpr long long kMaxRows = 1LL << 30;
 constexpr int kMaxNormTokens = 1 << 21;
 constexpr int kMaxDim = 1 << 20;
+constexpr int kMaxFewDim = 1 << 16;  // hidden and inner of a layer for a few tokens
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4b(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -98,6 +99,18 @@ dg_status norm_sizes(int tokens, int hidden, int gate_kind) {
   if (gate_kind < DG_MOE_GATE_NONE || gate_kind > DG_MOE_GATE_FULL) return DG_ERR_SHAPE;
   if (hidden > MAX_NORM_HIDDEN || tokens > kMaxNormTokens) return DG_ERR_UNSUPPORTED;
   return DG_OK;
+}
+
+dg_status experts_sizes(int tokens, int top_k, int num_groups, int inner) {
+  if (tokens < 0 || top_k <= 0 || num_groups <= 0 || inner <= 0 || inner % QBLOCK != 0) return DG_ERR_SHAPE;
+  if (tokens > MAX_FEW_TOKENS || top_k > MAX_TOP_K || tokens * top_k > MAX_FEW_PAIRS || num_groups > MAX_GROUPS ||
+      inner > kMaxFewDim)
+    return DG_ERR_UNSUPPORTED;
+  return DG_OK;
+}
+
+long long experts_workspace(int tokens, int top_k, int inner) {
+  return EXPERT_PLAN_BYTES + (long long)tokens * top_k * inner * 2;
 }
 
 bool gate_aligned(const void* gate, int kind) { return kind == DG_MOE_GATE_TOKEN ? aligned4b(gate) : aligned16(gate); }
@@ -238,6 +251,45 @@ dg_status dg_moe_swiglu_bwd(const void* da, const void* gu, void* dgu, const int
   a.inner = inner;
   if (dg_status s = device_check()) return s;
   return status_of(launch_swiglu_bwd(a, as_stream(stream)));
+}
+
+long long dg_moe_experts_workspace_bytes(int tokens, int top_k, int num_groups, int inner) {
+  return experts_sizes(tokens, top_k, num_groups, inner) == DG_OK ? experts_workspace(tokens, top_k, inner) : -1;
+}
+
+dg_status dg_moe_experts(const dg_moe_experts_args* args, void* stream) {
+  if (!args) return DG_ERR_NULL;
+  const dg_moe_experts_args& a = *args;
+  if (dg_status s = experts_sizes(a.tokens, a.top_k, a.num_groups, a.inner)) return s;
+  if (a.hidden <= 0 || a.hidden % QBLOCK != 0) return DG_ERR_SHAPE;
+  if (a.weight_type != DG_MOE_WEIGHTS_FP8 && a.weight_type != DG_MOE_WEIGHTS_FP4) return DG_ERR_SHAPE;
+  if (a.hidden > kMaxFewDim || (long long)a.num_groups * 2 * a.inner * a.hidden >= kMaxBytes)
+    return DG_ERR_UNSUPPORTED;
+  if (a.tokens == 0) return DG_OK;
+  if (!a.x || !a.topk_ids || !a.b1 || !a.sfb1 || !a.b2 || !a.sfb2 || !a.y || !a.workspace) return DG_ERR_NULL;
+  for (const void* p : {a.x, a.b1, a.sfb1, a.b2, a.sfb2, (const void*)a.y, (const void*)a.workspace})
+    if (!aligned16(p)) return DG_ERR_ALIGN;
+  if (!aligned4b(a.topk_ids) || !aligned4b(a.weights)) return DG_ERR_ALIGN;
+  if (a.workspace_bytes < experts_workspace(a.tokens, a.top_k, a.inner)) return DG_ERR_SHAPE;
+  if (dg_status s = device_check()) return s;
+  ExpertsArgs e{};
+  e.x = static_cast<const uint16_t*>(a.x);
+  e.ids = a.topk_ids;
+  e.weights = a.weights;
+  e.b1 = a.b1;
+  e.sfb1 = a.sfb1;
+  e.b2 = a.b2;
+  e.sfb2 = a.sfb2;
+  e.y = static_cast<uint16_t*>(a.y);
+  e.plan = a.workspace;
+  e.act = reinterpret_cast<uint16_t*>(static_cast<char*>(a.workspace) + EXPERT_PLAN_BYTES);
+  e.fp4 = a.weight_type == DG_MOE_WEIGHTS_FP4;
+  e.tokens = a.tokens;
+  e.top_k = a.top_k;
+  e.num_groups = a.num_groups;
+  e.hidden = a.hidden;
+  e.inner = a.inner;
+  return status_of(launch_experts(e, as_stream(stream)));
 }
 
 dg_status dg_moe_block_norm(const dg_moe_norm* args, void* stream) {

@@ -177,6 +177,17 @@ __device__ __forceinline__ u32x2 quantize_row(const F8& x, float& scale) {
   return quantize8(x, top, scale, 1.0f / scale);
 }
 
+// 1 / (1 + exp(-g)) with the hardware's exponential and reciprocal, each good to
+// an ulp or so (the exponential's argument rounds once, |g| 2^-24 more): far
+// below the rounding of what is made of it, and a third of the instructions
+// of the correctly rounded division. The reciprocal's result must not be below
+// 2^-126, which it makes zero (from g = -87.4 on): a quarter of the sum is
+// inverted, and a quarter of that taken. Below g = -88.7, where the exponential
+// is infinite, the sigmoid is zero, as in the formula's float32 terms.
+__device__ __forceinline__ float sigmoid(float g) {
+  return 0.25f * __builtin_amdgcn_rcpf(__builtin_fmaf(0.25f, __expf(-g), 0.25f));
+}
+
 // FP4 (E2M1) with one power-of-two scale per 32 values, a team of 4 lanes with 8
 // values each; the scales of the 128 values of 16 lanes are the bytes of a word.
 

@@ -11,17 +11,6 @@ namespace {
 
 constexpr int GLU_THREADS = 512;  // at most
 
-// 1 / (1 + exp(-g)) with the hardware's exponential and reciprocal, each good to
-// an ulp or so (the exponential's argument rounds once, |g| 2^-24 more): far
-// below the rounding of what is made of it, and a third of the instructions
-// of the correctly rounded division. The reciprocal's result must not be below
-// 2^-126, which it makes zero (from g = -87.4 on): a quarter of the sum is
-// inverted, and a quarter of that taken. Below g = -88.7, where the exponential
-// is infinite, the sigmoid is zero, as in the formula's float32 terms.
-__device__ __forceinline__ float sigmoid(float g) {
-  return 0.25f * __builtin_amdgcn_rcpf(__builtin_fmaf(0.25f, __expf(-g), 0.25f));
-}
-
 // Rows of the no-padding layout that hold tokens: the counts' sum, negative
 // counts as zero, cut at m. Computed by each wave for itself.
 __device__ __forceinline__ int nopad_rows(const GluArgs& p) {

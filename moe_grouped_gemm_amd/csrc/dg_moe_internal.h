@@ -52,6 +52,25 @@ hipError_t launch_swiglu_fp8(const GluArgs& a, bool ue8m0, hipStream_t stream);
 hipError_t launch_swiglu_fp4(const GluArgs& a, hipStream_t stream);
 hipError_t launch_swiglu_bwd(const GluArgs& a, hipStream_t stream);
 
+// A whole expert layer for a few tokens (dg_moe_experts.hip).
+constexpr int MAX_FEW_TOKENS = 128;
+constexpr int MAX_FEW_PAIRS = 1024;                            // tokens * top_k
+constexpr int EXPERT_PLAN_BYTES = 16 + MAX_FEW_PAIRS * 24;     // the workspace's head; a multiple of 16
+struct ExpertsArgs {
+  const uint16_t* x;
+  const int32_t* ids;
+  const float* weights;  // or null: ones
+  const void* b1;
+  const void* sfb1;
+  const void* b2;
+  const void* sfb2;
+  uint16_t* y;
+  void* plan;            // EXPERT_PLAN_BYTES
+  uint16_t* act;         // [tokens * top_k][inner]
+  int fp4, tokens, top_k, num_groups, hidden, inner;
+};
+hipError_t launch_experts(const ExpertsArgs& a, hipStream_t stream);
+
 // Norms around the block (dg_moe_norm.hip).
 // Most workgroups of the gradient's row loop (and rows of its partial sums).
 int norm_bwd_grid(int tokens);

@@ -57,15 +57,18 @@ SIGNATURES = [
     ("dg_moe_swiglu_fp8", [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp], _i),
     ("dg_moe_swiglu_fp4", [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp], _i),
     ("dg_moe_swiglu_bwd", [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp], _i),
+    ("dg_moe_experts_workspace_bytes", [_i, _i, _i, _i], _ll),
+    ("dg_moe_experts", [ctypes.c_char_p, _vp], _i),
     ("dg_moe_block_norm", [ctypes.c_char_p, _vp], _i),
     ("dg_moe_block_norm_workspace_bytes", [_i, _i], _ll),
     ("dg_moe_block_norm_bwd", [ctypes.c_char_p, _vp], _i),
 ]
 
-# The argument structs dg_moe_norm and dg_moe_norm_bwd, packed in one go (a
+# The argument structs dg_moe_norm, dg_moe_norm_bwd and dg_moe_experts_args, packed in one go (a
 # ctypes call converts its arguments one by one, 0.1 us each).
 _NORM = struct.Struct("9P2f3i4x")
 _NORM_BWD = struct.Struct("15Pqf3i")
+_EXPERTS = struct.Struct("9Pq6i")
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -371,6 +374,57 @@ def swiglu_bwd(da, gu, dgu, rows=None, layout: str = "dense") -> torch.Tensor:
     _want(dgu, "dgu", _BF16, gu.shape, index)
     _call("dg_moe_swiglu_bwd", index, da.data_ptr(), gu.data_ptr(), dgu.data_ptr(), _ptr(rows), kind, m, groups, inner)
     return dgu
+
+
+# ---------------------------------------------------------------------------
+# A whole layer for a few tokens
+# ---------------------------------------------------------------------------
+
+def experts_workspace(tokens: int, top_k: int, num_groups: int, inner: int, device) -> torch.Tensor:
+    """A workspace for experts() calls of up to `tokens` tokens, to be kept from call to call."""
+    size = lib().dg_moe_experts_workspace_bytes(*(_int32(int(v)) for v in (tokens, top_k, num_groups, inner)))
+    if size < 0:
+        raise ValueError(f"sizes out of range: tokens={tokens}, top_k={top_k}, num_groups={num_groups}, inner={inner}")
+    return torch.empty(size, dtype=torch.uint8, device=device)
+
+
+def experts(x, topk_ids, weights, b1, sfb1, b2, sfb2, y, workspace) -> torch.Tensor:
+    """An expert layer for up to 128 tokens (tokens * top_k up to 1024) in two launches:
+
+        y[t] = sum_j weights[t, j] * b2[e] (silu(g) * u),  [g | u] = b1[e] x[t],  e = topk_ids[t, j]
+
+    x, y [tokens, H] bfloat16; topk_ids [tokens, top_k] int32 (an id outside
+    [0, G) adds nothing); weights [tokens, top_k] float32 or None for ones.
+    b1 [G, 2I, H], b2 [G, H, I] and their scales as the grouped GEMMs take them:
+    float8_e4m3fn with float32 sfb [G, N/128, K/128], or uint8 (packed FP4, half as
+    many columns) with int32 sfb [G, K/128, N]. What decode steps call in place of
+    dispatch, two products, the activation and combine: nothing is quantised on the
+    way."""
+    index = _first(x, "x", _BF16, 2)
+    t, hidden = shape = x.shape
+    fp4 = isinstance(b1, torch.Tensor) and b1.dtype is torch.uint8
+    wtype, stype = (torch.uint8, _I32) if fp4 else (_FP8, _F32)
+    _first(b1, "b1", wtype, 3)
+    g, rows = b1.shape[:2]
+    inner, top_k = rows // 2, topk_ids.shape[-1] if isinstance(topk_ids, torch.Tensor) and topk_ids.dim() == 2 else 0
+    if hidden % 128 or rows % 256 or not rows:
+        raise ValueError("hidden and inner must be multiples of 128")
+    _want(y, "y", _BF16, shape, index)
+    _want(topk_ids, "topk_ids", _I32, (t, top_k), index)
+    if weights is not None:
+        _want(weights, "weights", _F32, (t, top_k), index)
+    pack = 2 if fp4 else 1
+    _want(b1, "b1", wtype, (g, rows, hidden // pack), index)
+    _want(b2, "b2", wtype, (g, hidden, inner // pack), index)
+    _want(sfb1, "sfb1", stype, (g, hidden // 128, rows) if fp4 else (g, rows // 128, hidden // 128), index)
+    _want(sfb2, "sfb2", stype, (g, inner // 128, hidden) if fp4 else (g, hidden // 128, inner // 128), index)
+    if _first(workspace, "workspace", torch.uint8, 1) != index:
+        raise ValueError(f"workspace must be on {x.device}")
+    args = _EXPERTS.pack(x.data_ptr(), topk_ids.data_ptr(), _ptr(weights), b1.data_ptr(), sfb1.data_ptr(), b2.data_ptr(),
+                         sfb2.data_ptr(), y.data_ptr(), workspace.data_ptr(), workspace.numel(), fp4, t, top_k,
+                         _int32(g), hidden, inner)
+    _call("dg_moe_experts", index, args)
+    return y
 
 
 # ---------------------------------------------------------------------------

@@ -77,11 +77,13 @@ def gemm(a, sfa, b, sfb):
 
 
 def experts(x, ids, w, w1, w2):
-    """(y, mag) of y[t] = sum_j w[t, j] W2[e] (silu(g) u), [g | u] = W1[e] x[t], e =
-    ids[t, j]; ids outside [0, G) add nothing. mag: every sum with the magnitudes of its
-    terms, the gated activation by |g| s(g) |u| with the products' magnitudes."""
-    inner = w1.shape[1] // 2
-    y, mag = np.zeros((x.shape[0], w2.shape[1])), np.zeros((x.shape[0], w2.shape[1]))
+    """(y, act_mag, mag, top) of y[t] = sum_j w[t, j] W2[e] (silu(g) u), [g | u] =
+    W1[e] x[t], e = ids[t, j]; ids outside [0, G) add nothing. act_mag: the second sum
+    with the magnitudes of its terms; mag: the same with each activation's first-order
+    dependence on its two sums, their terms by magnitude (|d silu / dg| is at most
+    1.1); top: the largest |g|."""
+    inner, top = w1.shape[1] // 2, 0.0
+    y, act_mag, mag = (np.zeros((x.shape[0], w2.shape[1])) for _ in range(3))
     for t in range(x.shape[0]):
         for j in range(ids.shape[1]):
             e = int(ids[t, j])
@@ -89,9 +91,9 @@ def experts(x, ids, w, w1, w2):
                 continue
             gu, gm = w1[e] @ x[t], np.abs(w1[e]) @ np.abs(x[t])
             g, u = gu[:inner], gu[inner:]
-            s = M.sigmoid(g)
-            y[t] += float(w[t, j]) * (w2[e] @ (g * s * u))
-            # |d silu / dg| is at most 1.1
-            terms = np.abs(g * s) * gm[inner:] + 1.1 * gm[:inner] * np.abs(u)
-            mag[t] += abs(float(w[t, j])) * (np.abs(w2[e]) @ terms)
-    return y, mag
+            s = g * M.sigmoid(g)
+            top = max(top, np.abs(g).max())
+            y[t] += float(w[t, j]) * (w2[e] @ (s * u))
+            act_mag[t] += abs(float(w[t, j])) * (np.abs(w2[e]) @ np.abs(s * u))
+            mag[t] += abs(float(w[t, j])) * (np.abs(w2[e]) @ (np.abs(s) * gm[inner:] + 1.1 * gm[:inner] * np.abs(u)))
+    return y, act_mag, mag, top

@@ -78,11 +78,11 @@ def test_experts_by_hand():
     w2 = np.array([[[3.0], [-1.0]], [[0.5], [2.0]]])
     ids, w = np.array([[0, 5], [1, -1]]), np.array([[0.25, 9.0], [4.0, 9.0]])
     silu = lambda v: v / (1 + np.exp(-v))  # noqa: E731
-    y, mag = F.experts(x, ids, w, w1, w2)
+    y, act_mag, mag, top = F.experts(x, ids, w, w1, w2)
     a0 = silu(1.5) * -2.0
     np.testing.assert_allclose(y[0], 0.25 * a0 * np.array([3.0, -1.0]), rtol=1e-15)
     np.testing.assert_allclose(y[1], 4.0 * silu(3.0) * 0.0 * np.array([0.5, 2.0]), atol=0)
-    assert (mag >= np.abs(y)).all()
+    assert (act_mag >= np.abs(y)).all() and (mag >= act_mag).all() and top == 3.0
 
 
 @pytest.mark.parametrize("mistake", ["floor", "nibbles", "words", "ties"])
