@@ -14,9 +14,15 @@
 //
 // v_mfma_f32_16x16x32_bf16: the first operand's lane (r, g) = (lane % 16, lane /
 // 16) holds 8 values of K of weight row r, the second's of token r, and result i of
-// the lane is weight row 4g + i for token r. Lane group g takes K positions 32g ..
-// 32g + 31 of 128 in four such steps, so that a lane's weights are 32 successive
-// bytes (FP8) or 16 (FP4), one scale block.
+// the lane is weight row 4g + i for token r. Lane group g takes a quarter of a
+// 128-value block in four such instructions: of FP4 K positions 32g .. 32g + 31, one
+// scale's; of FP8 16g .. 16g + 15 and 64 more, so that the four groups' loads are 64
+// bytes of a row in either case. (Which positions those are is free, as long as the
+// tokens' values are the same ones.)
+//
+// The weights are read by plain loads: half a line at a time of 16 rows, streaming
+// ones reach 5.6 TB/s in a kernel that only reads, plain ones 6.3 (long rows read
+// through 6.8, 6.2).
 
 #include <algorithm>
 
@@ -48,62 +54,61 @@ static_assert(sizeof(ExpertPlan) == EXPERT_PLAN_BYTES, "room for the plan");
 // Weights
 // ---------------------------------------------------------------------------
 
-// A chunk is 128 bytes of a weight row: 128 values of FP8, 256 of FP4.
-template <bool FP4>
-constexpr int CHUNK_BLOCKS = FP4 ? 2 : 1;
-
 // One expert's matrix [rows][k] and its scales.
 struct Matrix {
   const uint8_t* w;
-  const void* sf;  // FP8: float [rows/128][k/128]; FP4: words [k/128][ld]
-  int k, ld;
+  const uint32_t* sf;  // FP8: floats [rows/128][k/128]; FP4: words [k/128][rows]
 };
 
-// A 16-row tile's chunk as loaded: lane (r, g) of row r.
+// What is the same for every expert and step: sizes, and the lane's places.
 template <bool FP4>
-struct Chunk {
-  u32x4 w[2];       // FP8: bytes 32g .. + 31; FP4: bytes 16g .. + 15 of either block
-  uint32_t sf[FP4 ? 2 : 1];
-};
+struct Shape {
+  int rows, k;
+  size_t row_bytes;
+  uint32_t w_at, sf_at;  // of lane (r, g) in a tile's block: bytes; words
 
-template <bool FP4>
-__device__ __forceinline__ void load_chunk(Chunk<FP4>& c, const Matrix& m, int row0, int block, int lane) {
-  const int r = lane & 15, g = lane >> 4, blocks = m.k / QBLOCK;
-  if constexpr (FP4) {
-    const uint8_t* src = m.w + (size_t)(row0 + r) * (m.k / 2) + block * 64 + g * 16;
-    const uint32_t* sf = static_cast<const uint32_t*>(m.sf) + (size_t)block * m.ld + row0 + r;
-    c.w[0] = load_stream16(src);
-    c.sf[0] = sf[0];
-    c.w[1] = (u32x4){0, 0, 0, 0};
-    c.sf[1] = 0;
-    if (block + 1 < blocks) {
-      c.w[1] = load_stream16(src + 64);
-      c.sf[1] = sf[m.ld];
-    }
-  } else {
-    const uint8_t* src = m.w + (size_t)(row0 + r) * m.k + block * 128 + g * 32;
-    c.w[0] = load_stream16(src);
-    c.w[1] = load_stream16(src + 16);
-    c.sf[0] = static_cast<const uint32_t*>(m.sf)[(size_t)(row0 / 128) * blocks + block];
+  __device__ Shape(int rows_, int k_, int lane)
+      : rows(rows_), k(k_), row_bytes(FP4 ? k_ / 2 : k_),
+        w_at((uint32_t)(lane & 15) * (uint32_t)row_bytes + (lane >> 4) * 16), sf_at(FP4 ? lane & 15 : 0) {}
+  __device__ Matrix expert(const void* b, const void* sf, int e) const {
+    const size_t values = (size_t)rows * k;
+    return Matrix{static_cast<const uint8_t*>(b) + (size_t)e * (FP4 ? values / 2 : values),
+                  static_cast<const uint32_t*>(sf) + (size_t)e * (FP4 ? values / QBLOCK : values / QBLOCK / 128)};
   }
+};
+
+// One 128-value block of a 16-row tile as loaded: lane (r, g) of row r.
+template <bool FP4>
+struct Tile {
+  u32x4 w[FP4 ? 1 : 2];  // bytes 16g .. 16g + 15 and, FP8, 64 + 16g .. + 15
+  uint32_t sf;
+};
+
+template <bool FP4>
+__device__ __forceinline__ void load_tile(Tile<FP4>& t, const Shape<FP4>& sh, const Matrix& m, int row0, int block) {
+  const uint8_t* src = m.w + (size_t)row0 * sh.row_bytes + (size_t)block * (FP4 ? 64 : 128);
+  t.w[0] = load16(src + sh.w_at);
+  if constexpr (!FP4) t.w[1] = load16(src + sh.w_at + 64);
+  const uint32_t* sf = FP4 ? m.sf + (size_t)block * sh.rows + row0 : m.sf + (size_t)(row0 / 128) * (sh.k / QBLOCK) + block;
+  t.sf = sf[sh.sf_at];
 }
 
 __device__ __forceinline__ bf16x8 as_operand(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
-// The four operands of one 128-value block.
+// The four operands of the block.
 template <bool FP4>
-__device__ __forceinline__ void operands(const Chunk<FP4>& c, int b, int g, bf16x8 (&out)[4]) {
+__device__ __forceinline__ void operands(const Tile<FP4>& t, int g, bf16x8 (&out)[4]) {
   if constexpr (FP4) {
-    const uint32_t code = (c.sf[b] >> (8 * g)) & 0xFF;
+    const uint32_t code = (t.sf >> (8 * g)) & 0xFF;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t dword = c.w[b][j];
+      const uint32_t dword = t.w[0][j];
       out[j] = as_operand(fp4_values(dword, code));
     }
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t lo = c.w[j / 2][2 * (j & 1)], hi = c.w[j / 2][2 * (j & 1) + 1];
+      const uint32_t lo = t.w[j / 2][2 * (j & 1)], hi = t.w[j / 2][2 * (j & 1) + 1];
       const u32x4 v = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false)),
                        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true)),
                        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false)),
@@ -113,100 +118,71 @@ __device__ __forceinline__ void operands(const Chunk<FP4>& c, int b, int g, bf16
   }
 }
 
-// Tokens' values of the same chunk: lane (r, g) of token r.
-template <bool FP4, int NT>
-struct Tokens {
-  u32x4 v[NT][4 * CHUNK_BLOCKS<FP4>];
+// A step: one 128-value block of K of TILES 16-row tiles and of 16 NT tokens, lane
+// (r, g) of row or token r.
+template <bool FP4, int TILES, int NT>
+struct Step {
+  Tile<FP4> w[TILES];
+  u32x4 t[NT][4];
 };
 
 template <bool FP4, int NT>
-__device__ __forceinline__ void load_tokens(Tokens<FP4, NT>& t, const uint16_t* const (&row)[NT], int block,
-                                            int blocks, int lane) {
+__device__ __forceinline__ void load_tokens(u32x4 (&t)[NT][4], const uint16_t* const (&row)[NT], int block, int lane) {
   const int g = lane >> 4;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int b = 0; b < CHUNK_BLOCKS<FP4>; ++b)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        t.v[nt][4 * b + j] = (u32x4){0, 0, 0, 0};
-        if (b == 0 || block + b < blocks) t.v[nt][4 * b + j] = load16(row[nt] + (block + b) * QBLOCK + 32 * g + 8 * j);
-      }
+    for (int j = 0; j < 4; ++j)
+      t[nt][j] = load16(row[nt] + block * QBLOCK + (FP4 ? 32 * g + 8 * j : 64 * (j >> 1) + 16 * g + 8 * (j & 1)));
 }
 
-// acc += the chunk's weights times the tokens.
-template <bool FP4, int NT>
-__device__ __forceinline__ void multiply(f32x4 (&acc)[NT], const Chunk<FP4>& c, const Tokens<FP4, NT>& t, int lane) {
-  bf16x8 w[4];
-  if constexpr (FP4) {
+template <bool FP4, int TILES, int NT>
+__device__ __forceinline__ void multiply(f32x4 (&acc)[TILES][NT], const Step<FP4, TILES, NT>& s, int lane) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      operands<FP4>(c, b, lane >> 4, w);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          acc[nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j], as_operand(t.v[nt][4 * b + j]), acc[nt], 0, 0, 0);
-    }
-  } else {
-    operands<FP4>(c, 0, lane >> 4, w);
-    const float s = __builtin_bit_cast(float, c.sf[0]);
+  for (int i = 0; i < TILES; ++i) {
+    bf16x8 w[4];
+    operands<FP4>(s.w[i], lane >> 4, w);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      f32x4 part = {0.f, 0.f, 0.f, 0.f};
+      if constexpr (FP4) {  // the scales are in the operands
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j], as_operand(t.v[nt][j]), part, 0, 0, 0);
+        for (int j = 0; j < 4; ++j)
+          acc[i][nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j], as_operand(s.t[nt][j]), acc[i][nt], 0, 0, 0);
+      } else {
+        const float scale = __builtin_bit_cast(float, s.w[i].sf);
+        f32x4 part = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[nt][i] = __builtin_fmaf(part[i], s, acc[nt][i]);
+        for (int j = 0; j < 4; ++j)
+          part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j], as_operand(s.t[nt][j]), part, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[i][nt][k] = __builtin_fmaf(part[k], scale, acc[i][nt][k]);
+      }
     }
   }
 }
 
-// Sums of TILES 16-row tiles, tile i from matrix row row0[i], over the chunks
-// first, first + step, ... below `end` (counted in chunks): the next chunk's
-// loads are on their way while one is multiplied.
-template <bool FP4, int TILES, int NT>
-__device__ __forceinline__ void stream_rows(f32x4 (&acc)[TILES][NT], const Matrix& m, const int (&row0)[TILES],
-                                            const uint16_t* const (&row)[NT], int first, int step, int end,
-                                            int lane) {
-  constexpr int CB = CHUNK_BLOCKS<FP4>;
-  const int blocks = m.k / QBLOCK;
-  Chunk<FP4> c[2][TILES];
-  Tokens<FP4, NT> t[2];
-  auto load = [&](auto S, int chunk) {
-    constexpr int s = decltype(S)::value;
-#pragma unroll
-    for (int i = 0; i < TILES; ++i) load_chunk<FP4>(c[s][i], m, row0[i], chunk * CB, lane);
-    load_tokens<FP4, NT>(t[s], row, chunk * CB, blocks, lane);
-  };
-  auto multiply_all = [&](auto S) {
-    constexpr int s = decltype(S)::value;
-#pragma unroll
-    for (int i = 0; i < TILES; ++i) multiply<FP4, NT>(acc[i], c[s][i], t[s], lane);
-  };
-  using S0 = std::integral_constant<int, 0>;
-  using S1 = std::integral_constant<int, 1>;
-  if (first >= end) return;
-  load(S0{}, first);
-  for (int chunk = first; chunk < end; chunk += 2 * step) {
-    if (chunk + step < end) load(S1{}, chunk + step);
-    multiply_all(S0{});
-    if (chunk + step >= end) break;
-    if (chunk + 2 * step < end) load(S0{}, chunk + 2 * step);
-    multiply_all(S1{});
+// Runs steps 0 .. n-1 with DEPTH of them in registers: load(buffer, i) is called
+// DEPTH - 1 steps ahead of use(buffer, i), in order, without a condition around it
+// (past the last step it is asked for the last one again), in rounds that are left
+// at their end only: on every path to a use the compiler then knows how many loads
+// follow the ones that it waits for.
+template <int DEPTH, class BUFFER, class LOAD, class USE>
+__device__ __forceinline__ void pipeline(int n, LOAD&& load, USE&& use) {
+  BUFFER buf[DEPTH];
+  if (n <= 0) return;
+  static_for<0, DEPTH - 1>([&](auto I) { load(buf[decltype(I)::value], min((int)decltype(I)::value, n - 1)); });
+  const int rounds = n / DEPTH * DEPTH;
+  for (int i0 = 0; i0 < rounds; i0 += DEPTH) {
+    static_for<0, DEPTH>([&](auto I) {
+      constexpr int j = decltype(I)::value;
+      load(buf[(j + DEPTH - 1) % DEPTH], min(i0 + j + DEPTH - 1, n - 1));
+      use(buf[j], i0 + j);
+    });
   }
-}
-
-template <bool FP4>
-__device__ __forceinline__ Matrix expert_matrix(const void* b, const void* sf, int e, int rows, int k) {
-  Matrix m;
-  m.k = k;
-  m.ld = rows;  // a multiple of 128, and so aligned
-  const size_t values = (size_t)rows * k;
-  m.w = static_cast<const uint8_t*>(b) + (size_t)e * (FP4 ? values / 2 : values);
-  m.sf = static_cast<const uint32_t*>(sf) + (size_t)e * (FP4 ? values / QBLOCK : values / QBLOCK / 128);
-  return m;
+  static_for<0, DEPTH - 1>([&](auto I) {
+    constexpr int j = decltype(I)::value;
+    if (rounds + j < n) use(buf[j], rounds + j);
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -214,6 +190,19 @@ __device__ __forceinline__ Matrix expert_matrix(const void* b, const void* sf, i
 // ---------------------------------------------------------------------------
 
 constexpr int UP_WAVES = 4, UP_THREADS = UP_WAVES * 64;
+
+// The i-th block of K that a wave takes, and how many there are: turn by turn, for
+// FP4 two successive ones, which share a 128-byte line of a row.
+template <bool FP4>
+__device__ __forceinline__ int wave_block(int wave, int i) {
+  return FP4 ? (i >> 1) * 2 * UP_WAVES + 2 * wave + (i & 1) : i * UP_WAVES + wave;
+}
+template <bool FP4>
+__device__ __forceinline__ int wave_blocks(int wave, int blocks) {
+  if (!FP4) return (blocks - wave + UP_WAVES - 1) / UP_WAVES;
+  const int rounds = blocks / (2 * UP_WAVES);
+  return 2 * rounds + min(max(blocks - rounds * 2 * UP_WAVES - 2 * wave, 0), 2);
+}
 
 // Whether slot i is the first of its token with its expert.
 __device__ __forceinline__ bool first_of_token(const int* ids, int i, int top_k) {
@@ -272,11 +261,17 @@ __device__ void build_plan(const ExpertsArgs& p, ExpertPlan* plan, const int* id
   }
 }
 
+// Steps in registers.
+template <bool FP4, int NT>
+constexpr int UP_DEPTH = FP4 && NT == 1 ? 3 : 2;
+
 // One pass of an expert's workgroup over its rows with up to 16 NT tokens: the
 // waves share K and their sums meet in LDS.
 template <bool FP4, int RT, int NT>
-__device__ void up_pass(const ExpertsArgs& p, const Matrix& m, int f0, const int* slots, int count, f32x4* red) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+__device__ __forceinline__ void up_pass(const ExpertsArgs& p, const Shape<FP4>& shape, const Matrix& m, int f0,
+                                        const int* slots, int count, f32x4* red) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
   const uint16_t* row[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -292,8 +287,16 @@ __device__ void up_pass(const ExpertsArgs& p, const Matrix& m, int f0, const int
   for (int i = 0; i < 2 * RT; ++i)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) acc[i][nt] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  const int chunks = (m.k / QBLOCK + CHUNK_BLOCKS<FP4> - 1) / CHUNK_BLOCKS<FP4>;
-  stream_rows<FP4, 2 * RT, NT>(acc, m, row0, row, wave, UP_WAVES, chunks, lane);
+  using Buffer = Step<FP4, 2 * RT, NT>;
+  pipeline<UP_DEPTH<FP4, NT>, Buffer>(
+      wave_blocks<FP4>(wave, p.hidden / QBLOCK),
+      [&](Buffer& s, int i) {
+        const int block = wave_block<FP4>(wave, i);
+#pragma unroll
+        for (int k = 0; k < 2 * RT; ++k) load_tile<FP4>(s.w[k], shape, m, row0[k], block);
+        load_tokens<FP4, NT>(s.t, row, block, lane);
+      },
+      [&](const Buffer& s, int) { multiply<FP4, 2 * RT, NT>(acc, s, lane); });
 
   constexpr int UNITS = 2 * RT * NT;
   __syncthreads();  // of an earlier pass: its sums have been read
@@ -361,12 +364,12 @@ __global__ __launch_bounds__(UP_THREADS) void experts_up_kernel(ExpertsArgs p) {
   }
   if (__syncthreads_or(earlier) || count == 0) return;
 
-  const Matrix m = expert_matrix<FP4>(p.b1, p.sfb1, e, 2 * p.inner, p.hidden);
+  const Shape<FP4> shape(2 * p.inner, p.hidden, lane);
+  const Matrix m = shape.expert(p.b1, p.sfb1, __builtin_amdgcn_readfirstlane(e));
   for (int t0 = 0; t0 < count; t0 += 16 * NT) {
     const int here = min(count - t0, 16 * NT);
-    if (NT == 1 || here <= 16) up_pass<FP4, RT, 1>(p, m, f0, list + t0, here, red);
-    else if (NT == 2 || here <= 32) up_pass<FP4, RT, std::min(NT, 2)>(p, m, f0, list + t0, here, red);
-    else up_pass<FP4, RT, NT>(p, m, f0, list + t0, here, red);
+    if (NT == 1 || here <= 16) up_pass<FP4, RT, 1>(p, shape, m, f0, list + t0, here, red);
+    else up_pass<FP4, RT, NT>(p, shape, m, f0, list + t0, here, red);
   }
 }
 
@@ -376,72 +379,139 @@ __global__ __launch_bounds__(UP_THREADS) void experts_up_kernel(ExpertsArgs p) {
 
 constexpr int DOWN_WAVES = 8, DOWN_THREADS = DOWN_WAVES * 64;
 
-// A workgroup takes 16 RT columns of y for all tokens. Its waves share the experts
-// and, where these do not come out even, each expert's K in parts; each wave keeps
-// sums of its own in LDS, which are added in order at the end.
-template <bool FP4, int RT, int NT>
-__device__ __forceinline__ void down_pass(const ExpertsArgs& p, const Matrix& m, int c0, const int* slots,
-                                          const float* weights, int count, int first, int end, float* sums,
-                                          int stride) {
-  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-  const uint16_t* row[NT];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) row[nt] = p.act + (size_t)slots[min(nt * 16 + r, count - 1)] * p.inner;
-  int row0[RT];
-#pragma unroll
-  for (int i = 0; i < RT; ++i) row0[i] = c0 + 16 * i;
-  f32x4 acc[RT][NT];
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) acc[i][nt] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  stream_rows<FP4, RT, NT>(acc, m, row0, row, first, 1, end, lane);
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int t = nt * 16 + r;
-    if (t < count) {  // the tile's tokens differ from one another
-      const float w = weights[t];
-      float* at = sums + (slots[t] / p.top_k) * stride + 4 * g;
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        f32x4 s = *reinterpret_cast<f32x4*>(at + 16 * i);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) s[k] = __builtin_fmaf(w, acc[i][nt][k], s[k]);
-        *reinterpret_cast<f32x4*>(at + 16 * i) = s;
-      }
-    }
-  }
-}
+// A workgroup takes 16 RT columns of y for all tokens. Its waves share the experts,
+// 16 tokens of one at a time, and, where these do not come out even, their K in
+// parts; each wave keeps sums of its own in LDS, which are added in order at the end.
+// A wave's items follow one another in one pipeline of steps.
+template <bool FP4>
+constexpr int DOWN_DEPTH = FP4 ? 4 : 3;
+
+struct DownItem {
+  int expert, begin, count;  // pairs of the plan, at most 16
+};
 
 template <bool FP4, int RT, int TOKENS>
 __global__ __launch_bounds__(DOWN_THREADS) void experts_down_kernel(ExpertsArgs p) {
-  constexpr int STRIDE = 16 * RT + 4;  // floats; 4 past a power of two, for the banks
+  constexpr int STRIDE = 16 * RT + (TOKENS > 64 ? 0 : 4);  // floats; 4 past a power of two where there is room
   __shared__ float sums[DOWN_WAVES * TOKENS * STRIDE];
+  __shared__ DownItem items[MAX_FEW_PAIRS];
+  __shared__ int items_of[DOWN_THREADS / 64];
+  // Of the pairs; read from memory in the loop, they would be waited for with all the
+  // weights that are on their way.
+  __shared__ int slots[MAX_FEW_PAIRS];
+  __shared__ uint16_t sums_at[MAX_FEW_PAIRS];  // of the pair's token, in 16 bytes
+  __shared__ float weights[MAX_FEW_PAIRS];
   const ExpertPlan* plan = reinterpret_cast<const ExpertPlan*>(p.plan);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c0 = blockIdx.x * 16 * RT;
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), c0 = blockIdx.x * 16 * RT;
   float* mine = sums + wave * TOKENS * STRIDE;
-  for (int i = threadIdx.x & 63; i < p.tokens * STRIDE; i += 64) mine[i] = 0.0f;
+  for (int i = lane; i < p.tokens * STRIDE; i += 64) mine[i] = 0.0f;
 
-  const int experts = plan->experts, chunks = (p.inner / QBLOCK + CHUNK_BLOCKS<FP4> - 1) / CHUNK_BLOCKS<FP4>;
-  // Parts of an expert's K: so many that the waves have the same number of them, or eight rounds.
-  int parts = 1;
-  while (parts < DOWN_WAVES && parts * 2 <= chunks && experts * parts % DOWN_WAVES && experts * parts < 8 * DOWN_WAVES)
-    parts *= 2;
-  for (int item = wave; item < experts * parts; item += DOWN_WAVES) {
-    const ExpertEntry entry = plan->entry[item / parts];
-    const int part = item % parts, first = chunks * part / parts, end = chunks * (part + 1) / parts;
-    const Matrix m = expert_matrix<FP4>(p.b2, p.sfb2, entry.expert, p.hidden, p.inner);
-    for (int t0 = 0; t0 < entry.count; t0 += 64) {
-      const int here = min(entry.count - t0, 64);
-      const int* slots = plan->slot + entry.begin + t0;
-      const float* weights = plan->weight + entry.begin + t0;
-      if (TOKENS <= 16 || here <= 16) down_pass<FP4, RT, 1>(p, m, c0, slots, weights, here, first, end, mine, STRIDE);
-      else if (here <= 32) down_pass<FP4, RT, 2>(p, m, c0, slots, weights, here, first, end, mine, STRIDE);
-      else down_pass<FP4, RT, 4>(p, m, c0, slots, weights, here, first, end, mine, STRIDE);
-    }
+  const int experts = plan->experts, pairs = plan->pairs;
+  for (int i = tid; i < pairs; i += DOWN_THREADS) {
+    const int slot = plan->slot[i];
+    slots[i] = slot;
+    sums_at[i] = (uint16_t)(slot / p.top_k * (STRIDE / 4));
+    weights[i] = plan->weight[i];
   }
+  // The items: an expert's pairs 16 at a time, in order.
+  int total = 0;
+  for (int r0 = 0; r0 < experts; r0 += DOWN_THREADS) {
+    const int at = r0 + tid;
+    ExpertEntry entry{0, 0, 0, 0};
+    if (at < experts) entry = plan->entry[at];
+    const int has = (entry.count + 15) / 16;
+    int upto = has;
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(upto, d);
+      if (lane >= d) upto += v;
+    }
+    if (lane == 63) items_of[wave] = upto;
+    __syncthreads();
+    int before = total + upto - has;
+    for (int w = 0; w < DOWN_THREADS / 64; ++w) {
+      if (w < wave) before += items_of[w];
+      total += items_of[w];
+    }
+    for (int i = 0; i < has; ++i)
+      items[before + i] = DownItem{entry.expert, entry.begin + 16 * i, min(entry.count - 16 * i, 16)};
+    __syncthreads();
+  }
+
+  // Parts of K (of pairs of blocks, see wave_block): so many that the waves have the
+  // same number of items, or that they have eight each.
+  const int blocks = p.inner / QBLOCK, unit = FP4 ? 2 : 1, units = (blocks + unit - 1) / unit;
+  int parts = 1;
+  while (parts < DOWN_WAVES && parts * 2 <= units && total * parts % DOWN_WAVES && total * parts < 8 * DOWN_WAVES)
+    parts *= 2;
+  const int all = total * parts, turns = wave < all ? (all - wave + DOWN_WAVES - 1) / DOWN_WAVES : 0;
+
+  const Shape<FP4> shape(p.hidden, p.inner, lane);
+  // Where the loads and the products are: the turn, its item and its blocks.
+  struct Cursor {
+    int turn, block, end, begin, count;
+    Matrix m;
+  };
+  auto start = [&](Cursor& c) {
+    const int item = wave + c.turn * DOWN_WAVES, part = item % parts;
+    const DownItem at = items[item / parts];
+    c.begin = __builtin_amdgcn_readfirstlane(at.begin);
+    c.count = __builtin_amdgcn_readfirstlane(at.count);
+    c.m = shape.expert(p.b2, p.sfb2, __builtin_amdgcn_readfirstlane(at.expert));
+    c.block = units * part / parts * unit;
+    c.end = min(units * (part + 1) / parts * unit, blocks);
+  };
+  int steps = 0;
+  for (int turn = 0; turn < turns; ++turn) {
+    const int part = (wave + turn * DOWN_WAVES) % parts;
+    steps += min(units * (part + 1) / parts * unit, blocks) - units * part / parts * unit;
+  }
+
+  using Buffer = Step<FP4, RT, 1>;
+  Cursor ahead{}, now{};
+  const uint16_t* row[1] = {p.act};
+  f32x4 acc[RT][1] = {};
+  int loaded = 0;
+  if (steps > 0) {
+    start(ahead);
+    start(now);
+    row[0] = p.act + (size_t)slots[ahead.begin + min(r, ahead.count - 1)] * p.inner;
+  }
+  pipeline<DOWN_DEPTH<FP4>, Buffer>(
+      steps,
+      [&](Buffer& s, int) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i) load_tile<FP4>(s.w[i], shape, ahead.m, c0 + 16 * i, ahead.block);
+        load_tokens<FP4, 1>(s.t, row, ahead.block, lane);
+        if (++loaded < steps && ++ahead.block == ahead.end) {
+          ++ahead.turn;
+          start(ahead);
+          row[0] = p.act + (size_t)slots[ahead.begin + min(r, ahead.count - 1)] * p.inner;
+        }
+      },
+      [&](const Buffer& s, int i) {
+        multiply<FP4, RT, 1>(acc, s, lane);
+        if (++now.block < now.end) return;
+        if (r < now.count) {  // the item's tokens differ from one another
+          const float w = weights[now.begin + r];
+          float* at = mine + 4 * (sums_at[now.begin + r] + g);
+#pragma unroll
+          for (int k = 0; k < RT; ++k) {
+            f32x4 sum = *reinterpret_cast<f32x4*>(at + 16 * k);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) sum[v] = __builtin_fmaf(w, acc[k][0][v], sum[v]);
+            *reinterpret_cast<f32x4*>(at + 16 * k) = sum;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < RT; ++k) acc[k][0] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        if (i + 1 < steps) {
+          ++now.turn;
+          start(now);
+        }
+      });
   __syncthreads();
-  for (int i = threadIdx.x; i < p.tokens * 8 * RT; i += DOWN_THREADS) {
+  for (int i = tid; i < p.tokens * 8 * RT; i += DOWN_THREADS) {
     const int t = i / (8 * RT), c = i % (8 * RT) * 2;
     f32x2 s = {0.f, 0.f};
 #pragma unroll
@@ -456,8 +526,7 @@ template <bool FP4, int RT>
 hipError_t launch_typed(const ExpertsArgs& a, hipStream_t stream) {
   const int n = a.tokens * a.top_k;
   const int ups = 1 + std::min(n, a.num_groups) * (a.inner / (16 * RT));
-  auto* up = a.tokens <= 16 ? experts_up_kernel<FP4, RT, 1>
-                            : a.tokens <= 32 ? experts_up_kernel<FP4, RT, 2> : experts_up_kernel<FP4, RT, 4>;
+  auto* up = a.tokens <= 16 ? experts_up_kernel<FP4, RT, 1> : experts_up_kernel<FP4, RT, 2>;
   hipLaunchKernelGGL(up, dim3(ups), dim3(UP_THREADS), 0, stream, a);
   if (hipError_t e = hipGetLastError()) return e;
   auto* down = a.tokens <= 16 ? experts_down_kernel<FP4, RT, 16>
@@ -470,7 +539,7 @@ hipError_t launch_typed(const ExpertsArgs& a, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_experts(const ExpertsArgs& a, hipStream_t stream) {
-  return a.fp4 ? launch_typed<true, 1>(a, stream) : launch_typed<false, 1>(a, stream);
+  return a.fp4 ? launch_typed<true, 2>(a, stream) : launch_typed<false, 2>(a, stream);
 }
 
 }  // namespace moe
