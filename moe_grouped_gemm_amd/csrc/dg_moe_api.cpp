@@ -109,8 +109,8 @@ dg_status experts_sizes(int tokens, int top_k, int num_groups, int inner) {
   return DG_OK;
 }
 
-long long experts_workspace(int tokens, int top_k, int inner) {
-  return EXPERT_PLAN_BYTES + (long long)tokens * top_k * inner * 2;
+long long experts_workspace(int tokens, int top_k, int num_groups, int inner) {
+  return EXPERT_PLAN_BYTES + experts_act_bytes(tokens, top_k, num_groups, inner);
 }
 
 bool gate_aligned(const void* gate, int kind) { return kind == DG_MOE_GATE_TOKEN ? aligned4b(gate) : aligned16(gate); }
@@ -254,7 +254,7 @@ dg_status dg_moe_swiglu_bwd(const void* da, const void* gu, void* dgu, const int
 }
 
 long long dg_moe_experts_workspace_bytes(int tokens, int top_k, int num_groups, int inner) {
-  return experts_sizes(tokens, top_k, num_groups, inner) == DG_OK ? experts_workspace(tokens, top_k, inner) : -1;
+  return experts_sizes(tokens, top_k, num_groups, inner) == DG_OK ? experts_workspace(tokens, top_k, num_groups, inner) : -1;
 }
 
 dg_status dg_moe_experts(const dg_moe_experts_args* args, void* stream) {
@@ -270,7 +270,7 @@ dg_status dg_moe_experts(const dg_moe_experts_args* args, void* stream) {
   for (const void* p : {a.x, a.b1, a.sfb1, a.b2, a.sfb2, (const void*)a.y, (const void*)a.workspace})
     if (!aligned16(p)) return DG_ERR_ALIGN;
   if (!aligned4b(a.topk_ids) || !aligned4b(a.weights)) return DG_ERR_ALIGN;
-  if (a.workspace_bytes < experts_workspace(a.tokens, a.top_k, a.inner)) return DG_ERR_SHAPE;
+  if (a.workspace_bytes < experts_workspace(a.tokens, a.top_k, a.num_groups, a.inner)) return DG_ERR_SHAPE;
   if (dg_status s = device_check()) return s;
   ExpertsArgs e{};
   e.x = static_cast<const uint16_t*>(a.x);

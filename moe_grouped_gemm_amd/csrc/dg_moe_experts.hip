@@ -1,31 +1,33 @@
 // A whole expert layer for a few tokens in two launches:
 //
-//   a[t, e] = silu(g) * u,  [g | u] = B1[e] x[t]        (up)
+//   a[t, e] = silu(g) * u,  [g | u] = B1[e] x[t]             (up)
 //   y[t]    = sum_j w[t, j] * B2[e] a[t, e], e = ids[t, j]   (down)
 //
 // with the experts' weights in FP8 (one float32 scale per 128 x 128) or FP4 (one
 // power-of-two scale per 32 values of a row) and everything else as it comes: x in
 // BF16, sums in float32, a rounded once to BF16 (the rounding of y itself is as
 // large; a grouped product's path rounds g, u and then a to FP8). The weights of
-// the experts that have tokens are read once, and that bounds both launches:
-// every wave streams weights from memory straight into registers, converts them to
-// BF16 (exact: E4M3 has 4 significant bits, E2M1 2) and multiplies them on the
-// matrix cores with up to 16 tokens a tile, whose rows come from L2.
+// the experts that have tokens are read once, and that bounds both launches.
+//
+// Every wave streams weights of its own through a ring in LDS, without a barrier:
+// direct-to-LDS loads whose successive lanes read a row's successive 16 bytes, some
+// steps ahead; each step it waits for its own oldest ones, reads them as the matrix
+// cores want them, converts them to BF16 (exact: E4M3 has 4 significant bits, E2M1 2)
+// and multiplies them with up to 16 tokens a tile. Loads straight into the matrix
+// cores' registers, lane by lane a row, take the L1 four times the accesses: one
+// 16-byte piece each, 3.4 TB/s where tokens' rows come the same way.
 //
 // v_mfma_f32_16x16x32_bf16: the first operand's lane (r, g) = (lane % 16, lane /
 // 16) holds 8 values of K of weight row r, the second's of token r, and result i of
 // the lane is weight row 4g + i for token r. Lane group g takes a quarter of a
-// 128-value block in four such instructions: of FP4 K positions 32g .. 32g + 31, one
-// scale's; of FP8 16g .. 16g + 15 and 64 more, so that the four groups' loads are 64
-// bytes of a row in either case. (Which positions those are is free, as long as the
-// tokens' values are the same ones.)
-//
-// The weights are read by plain loads: half a line at a time of 16 rows, streaming
-// ones reach 5.6 TB/s in a kernel that only reads, plain ones 6.3 (long rows read
-// through 6.8, 6.2).
+// 128-value block in four such instructions j: of FP4 K positions 32g + 8j .. + 7,
+// one scale's; of FP8 64 (j / 2) + 16g + 8 (j % 2) .. + 7, which are 16-byte pieces g
+// and g + 4 of the row. (Which positions those are is free, as long as the tokens'
+// values are the same ones.)
 
 #include <algorithm>
 
+#include "dg_device.h"
 #include "dg_moe_device.h"
 
 namespace dg {
@@ -33,12 +35,11 @@ namespace moe {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 // What the first launch leaves for the second, before the activations: the experts
 // that have tokens, in order of their first slot, and their (token, expert) pairs.
-// A pair is known by its first slot, and its activation lies in that slot's row; a
-// token that names an expert twice is one pair with the weights' sum.
+// A pair is known by its first slot; a token that names an expert twice is one pair
+// with the weights' sum.
 struct ExpertEntry {
   int expert, begin, count, pad;
 };
@@ -51,158 +52,161 @@ struct ExpertPlan {
 static_assert(sizeof(ExpertPlan) == EXPERT_PLAN_BYTES, "room for the plan");
 
 // ---------------------------------------------------------------------------
+// Activations between the launches
+// ---------------------------------------------------------------------------
+
+// They lie in tiles of one expert's up to 16 tokens, in the order in which the second
+// launch's lanes load them, 16 bytes each: block b of 128 values, instruction j, lane
+// group g, row. `rows` is 4 where the call has no more tokens (the lanes of other rows
+// repeat them), else 16. With no more slots than experts a tile is known by its first
+// pair's slot, else by the expert and its number.
+__device__ __forceinline__ int act_tile(const ExpertsArgs& p, int expert, int number, int first_slot) {
+  const bool by_slot = p.tokens * p.top_k <= p.num_groups;
+  return by_slot ? first_slot : expert * ((p.tokens + 15) / 16) + number;
+}
+// Of value k of a tile's row, in values.
+template <bool FP4, int ROWS>
+__device__ __forceinline__ int act_at(int k, int row) {
+  const int b = k / QBLOCK, in = k % QBLOCK;
+  const int g = FP4 ? in / 32 : in / 16 % 4, j = FP4 ? in / 8 % 4 : in / 64 * 2 + in / 8 % 2;
+  return b * QBLOCK * ROWS + ((j * 4 + g) * ROWS + row) * 8 + in % 8;
+}
+
+// ---------------------------------------------------------------------------
 // Weights
 // ---------------------------------------------------------------------------
 
-// One expert's matrix [rows][k] and its scales.
-struct Matrix {
-  const uint8_t* w;
-  const uint32_t* sf;  // FP8: floats [rows/128][k/128]; FP4: words [k/128][rows]
-};
-
-// What is the same for every expert and step: sizes, and the lane's places.
-template <bool FP4>
-struct Shape {
-  int rows, k;
-  size_t row_bytes;
-  uint32_t w_at, sf_at;  // of lane (r, g) in a tile's block: bytes; words
-
-  __device__ Shape(int rows_, int k_, int lane)
-      : rows(rows_), k(k_), row_bytes(FP4 ? k_ / 2 : k_),
-        w_at((uint32_t)(lane & 15) * (uint32_t)row_bytes + (lane >> 4) * 16), sf_at(FP4 ? lane & 15 : 0) {}
-  __device__ Matrix expert(const void* b, const void* sf, int e) const {
-    const size_t values = (size_t)rows * k;
-    return Matrix{static_cast<const uint8_t*>(b) + (size_t)e * (FP4 ? values / 2 : values),
-                  static_cast<const uint32_t*>(sf) + (size_t)e * (FP4 ? values / QBLOCK : values / QBLOCK / 128)};
-  }
-};
-
-// One 128-value block of a 16-row tile as loaded: lane (r, g) of row r.
-template <bool FP4>
-struct Tile {
-  u32x4 w[FP4 ? 1 : 2];  // bytes 16g .. 16g + 15 and, FP8, 64 + 16g .. + 15
-  uint32_t sf;
-};
-
-template <bool FP4>
-__device__ __forceinline__ void load_tile(Tile<FP4>& t, const Shape<FP4>& sh, const Matrix& m, int row0, int block) {
-  const uint8_t* src = m.w + (size_t)row0 * sh.row_bytes + (size_t)block * (FP4 ? 64 : 128);
-  t.w[0] = load16(src + sh.w_at);
-  if constexpr (!FP4) t.w[1] = load16(src + sh.w_at + 64);
-  const uint32_t* sf = FP4 ? m.sf + (size_t)block * sh.rows + row0 : m.sf + (size_t)(row0 / 128) * (sh.k / QBLOCK) + block;
-  t.sf = sf[sh.sf_at];
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint32_t lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds_dest(lds), 16, voff, soff, 0, 0);
+}
+__device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint32_t lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds_dest(lds), 4, voff, soff, 0, 0);
 }
 
-__device__ __forceinline__ bf16x8 as_operand(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
+// Neither the loads' waits nor their LDS writes are seen by the compiler: no access to
+// LDS moves past these.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  wait_vmcnt<N>();
+  asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ void before_loads() {
+  wait_lgkmcnt_0();  // what a slot held has been read
+  asm volatile("" ::: "memory");
+}
 
-// The four operands of the block.
-template <bool FP4>
-__device__ __forceinline__ void operands(const Tile<FP4>& t, int g, bf16x8 (&out)[4]) {
-  if constexpr (FP4) {
-    const uint32_t code = (t.sf >> (8 * g)) & 0xFF;
+// One step of the weights: a 128-value block of K of TILES 16-row tiles, GROUPS
+// (1 or 2) runs of successive rows, with their scales.
+template <bool FP4, int TILES_, int GROUPS>
+struct Weights {
+  static constexpr int TILES = TILES_, PER_GROUP = TILES / GROUPS;
+  static constexpr int TILE_BYTES = FP4 ? 1024 : 2048, BLOCK_BYTES = FP4 ? 64 : 128;
+  static constexpr int SCALE_LOADS = FP4 ? (TILES + 3) / 4 : 1;
+  static constexpr int BYTES = TILES * TILE_BYTES + SCALE_LOADS * 256;  // of a step in LDS
+  static constexpr int LOADS = TILES * (TILE_BYTES / 1024) + SCALE_LOADS;
+
+  __amdgpu_buffer_rsrc_t rows[GROUPS], scales;
+  uint32_t row_bytes, scale_step;                // bytes between rows; between a block's scales and the next's
+  uint32_t w_at[TILE_BYTES / 1024], sf_at[SCALE_LOADS];  // the lane's offsets, fixed
+  uint32_t read_at, read_sf;                     // and in LDS
+
+  // Rows row0[.] of expert e's matrix [n][k].
+  __device__ Weights(const void* b, const void* sf, int e, int n, int k, const int (&row0)[GROUPS], int lane) {
+    const int r = lane & 15, g = lane >> 4;
+    const size_t values = (size_t)n * k;
+    row_bytes = FP4 ? k / 2 : k;
+    const uint8_t* w = static_cast<const uint8_t*>(b) + (size_t)e * (FP4 ? values / 2 : values);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t dword = t.w[0][j];
-      out[j] = as_operand(fp4_values(dword, code));
+    for (int i = 0; i < GROUPS; ++i) rows[i] = buffer_rsrc(w + (size_t)row0[i] * row_bytes, 0xFFFFFFFFu);
+    scales = buffer_rsrc(static_cast<const uint32_t*>(sf) + (size_t)e * (FP4 ? values / QBLOCK : values / QBLOCK / 128),
+                         0xFFFFFFFFu);
+    scale_step = FP4 ? n * 4 : 4;
+    if constexpr (FP4) {
+      // A load is 16 rows of 64 bytes; pieces of 16 are swizzled so that a fragment
+      // read's 16 lanes of a pass (see lds_offset()) lie on 16 different slots.
+      const int row = lane >> 2, piece = (lane & 3) ^ (-(row >> 2) & 3);
+      w_at[0] = row * row_bytes + piece * 16;
+      read_at = r * 64 + ((g ^ (-(r >> 2) & 3)) << 4);
+#pragma unroll
+      for (int q = 0; q < SCALE_LOADS; ++q) {
+        const int tile = min(4 * q + g, TILES - 1), group = tile / PER_GROUP;
+        sf_at[q] = (GROUPS == 2 && group ? row0[GROUPS - 1] : row0[0]) * 4 + ((tile - group * PER_GROUP) * 16 + r) * 4;
+      }
+      read_sf = r * 4;
+    } else {
+      // A load is 8 rows of 128 bytes.
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = 8 * h + (lane >> 3), piece = (lane & 7) ^ ((row >> 1) & 7);
+        w_at[h] = row * row_bytes + piece * 16;
+      }
+      read_at = lds_offset(r, g);  // and, with bit 6 flipped, lds_offset(r, g + 4)
+      sf_at[0] = (GROUPS == 2 && (lane & 1) ? row0[GROUPS - 1] : row0[0]) / 128 * (k / QBLOCK) * 4;
+      read_sf = 0;
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t lo = t.w[j / 2][2 * (j & 1)], hi = t.w[j / 2][2 * (j & 1) + 1];
-      const u32x4 v = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false)),
-                       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true)),
-                       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false)),
-                       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true))};
-      out[j] = as_operand(v);
-    }
   }
-}
 
-// A step: one 128-value block of K of TILES 16-row tiles and of 16 NT tokens, lane
-// (r, g) of row or token r.
-template <bool FP4, int TILES, int NT>
-struct Step {
-  Tile<FP4> w[TILES];
-  u32x4 t[NT][4];
-};
+  __device__ __forceinline__ void load(int block, uint32_t lds) const {
+#pragma unroll
+    for (int i = 0; i < TILES; ++i)
+#pragma unroll
+      for (int h = 0; h < TILE_BYTES / 1024; ++h)
+        dma16(rows[i / PER_GROUP], w_at[h], (uint32_t)(i % PER_GROUP) * 16 * row_bytes + (uint32_t)block * BLOCK_BYTES,
+              lds + i * TILE_BYTES + h * 1024);
+#pragma unroll
+    for (int q = 0; q < SCALE_LOADS; ++q)
+      dma4(scales, sf_at[q], (uint32_t)block * scale_step, lds + TILES * TILE_BYTES + q * 256);
+  }
 
-template <bool FP4, int NT>
-__device__ __forceinline__ void load_tokens(u32x4 (&t)[NT][4], const uint16_t* const (&row)[NT], int block, int lane) {
-  const int g = lane >> 4;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      t[nt][j] = load16(row[nt] + block * QBLOCK + (FP4 ? 32 * g + 8 * j : 64 * (j >> 1) + 16 * g + 8 * (j & 1)));
-}
-
-template <bool FP4, int TILES, int NT>
-__device__ __forceinline__ void multiply(f32x4 (&acc)[TILES][NT], const Step<FP4, TILES, NT>& s, int lane) {
-#pragma unroll
-  for (int i = 0; i < TILES; ++i) {
+  // acc += tile i of the step at `st` times the tokens' operands.
+  template <int NT>
+  __device__ __forceinline__ void multiply(f32x4 (&acc)[NT], const uint8_t* st, int i, const u32x4 (&t)[NT][4],
+                                           int lane) const {
+    const uint8_t* tile = st + i * TILE_BYTES;
+    const uint8_t* sf = st + TILES * TILE_BYTES;
     bf16x8 w[4];
-    operands<FP4>(s.w[i], lane >> 4, w);
+    if constexpr (FP4) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(tile + read_at);
+      const uint32_t code = (*reinterpret_cast<const uint32_t*>(sf + i * 64 + read_sf) >> (8 * (lane >> 4))) & 0xFF;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if constexpr (FP4) {  // the scales are in the operands
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t dword = v[j];
+        w[j] = __builtin_bit_cast(bf16x8, fp4_values(dword, code));
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          acc[i][nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j], as_operand(s.t[nt][j]), acc[i][nt], 0, 0, 0);
-      } else {
-        const float scale = __builtin_bit_cast(float, s.w[i].sf);
+          acc[nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j], __builtin_bit_cast(bf16x8, t[nt][j]), acc[nt], 0, 0, 0);
+    } else {
+      const u32x4 v[2] = {*reinterpret_cast<const u32x4*>(tile + read_at),
+                          *reinterpret_cast<const u32x4*>(tile + (read_at ^ 64))};
+      const float scale = *reinterpret_cast<const float*>(sf + i / PER_GROUP * 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = v[j / 2][2 * (j & 1)], hi = v[j / 2][2 * (j & 1) + 1];
+        const u32x4 o = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false)),
+                         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true)),
+                         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false)),
+                         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true))};
+        w[j] = __builtin_bit_cast(bf16x8, o);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
         f32x4 part = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j], as_operand(s.t[nt][j]), part, 0, 0, 0);
+          part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j], __builtin_bit_cast(bf16x8, t[nt][j]), part, 0, 0, 0);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc[i][nt][k] = __builtin_fmaf(part[k], scale, acc[i][nt][k]);
+        for (int k = 0; k < 4; ++k) acc[nt][k] = __builtin_fmaf(part[k], scale, acc[nt][k]);
       }
     }
   }
-}
-
-// Runs steps 0 .. n-1 with DEPTH of them in registers: load(buffer, i) is called
-// DEPTH - 1 steps ahead of use(buffer, i), in order, without a condition around it
-// (past the last step it is asked for the last one again), in rounds that are left
-// at their end only: on every path to a use the compiler then knows how many loads
-// follow the ones that it waits for.
-template <int DEPTH, class BUFFER, class LOAD, class USE>
-__device__ __forceinline__ void pipeline(int n, LOAD&& load, USE&& use) {
-  BUFFER buf[DEPTH];
-  if (n <= 0) return;
-  static_for<0, DEPTH - 1>([&](auto I) { load(buf[decltype(I)::value], min((int)decltype(I)::value, n - 1)); });
-  const int rounds = n / DEPTH * DEPTH;
-  for (int i0 = 0; i0 < rounds; i0 += DEPTH) {
-    static_for<0, DEPTH>([&](auto I) {
-      constexpr int j = decltype(I)::value;
-      load(buf[(j + DEPTH - 1) % DEPTH], min(i0 + j + DEPTH - 1, n - 1));
-      use(buf[j], i0 + j);
-    });
-  }
-  static_for<0, DEPTH - 1>([&](auto I) {
-    constexpr int j = decltype(I)::value;
-    if (rounds + j < n) use(buf[j], rounds + j);
-  });
-}
+};
 
 // ---------------------------------------------------------------------------
-// Up
+// The plan
 // ---------------------------------------------------------------------------
-
-constexpr int UP_WAVES = 4, UP_THREADS = UP_WAVES * 64;
-
-// The i-th block of K that a wave takes, and how many there are: turn by turn, for
-// FP4 two successive ones, which share a 128-byte line of a row.
-template <bool FP4>
-__device__ __forceinline__ int wave_block(int wave, int i) {
-  return FP4 ? (i >> 1) * 2 * UP_WAVES + 2 * wave + (i & 1) : i * UP_WAVES + wave;
-}
-template <bool FP4>
-__device__ __forceinline__ int wave_blocks(int wave, int blocks) {
-  if (!FP4) return (blocks - wave + UP_WAVES - 1) / UP_WAVES;
-  const int rounds = blocks / (2 * UP_WAVES);
-  return 2 * rounds + min(max(blocks - rounds * 2 * UP_WAVES - 2 * wave, 0), 2);
-}
 
 // Whether slot i is the first of its token with its expert.
 __device__ __forceinline__ bool first_of_token(const int* ids, int i, int top_k) {
@@ -212,12 +216,13 @@ __device__ __forceinline__ bool first_of_token(const int* ids, int i, int top_k)
   return true;
 }
 
-// The plan, by one workgroup: every slot looks at all others (LDS, all lanes at
-// the same one), at most 1024 of them.
+// By one workgroup: every slot looks at all others (in LDS, all lanes at the same
+// one), at most 1024 of them.
+template <int THREADS>
 __device__ void build_plan(const ExpertsArgs& p, ExpertPlan* plan, const int* ids, int* owner) {
   const int n = p.tokens * p.top_k;
   // owner[i]: the first slot of i's expert, where i is its pair's first slot; else n.
-  for (int i = threadIdx.x; i < n; i += UP_THREADS) {
+  for (int i = threadIdx.x; i < n; i += THREADS) {
     const int e = ids[i];
     int own = n;
     if (e >= 0 && e < p.num_groups && first_of_token(ids, i, p.top_k)) {
@@ -231,7 +236,7 @@ __device__ void build_plan(const ExpertsArgs& p, ExpertPlan* plan, const int* id
     owner[i] = own;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += UP_THREADS) {
+  for (int i = threadIdx.x; i < n; i += THREADS) {
     const int own = owner[i];
     if (own == n) continue;
     int at = 0, rank = 0, begin = 0, count = 0;
@@ -250,61 +255,138 @@ __device__ void build_plan(const ExpertsArgs& p, ExpertPlan* plan, const int* id
     plan->weight[at] = w;
     if (own == i) plan->entry[rank] = ExpertEntry{ids[i], begin, count, 0};
   }
-  if (threadIdx.x == 0) {
+  if (threadIdx.x < 64) {
     int experts = 0, pairs = 0;
-    for (int j = 0; j < n; ++j) {
+    for (int j = threadIdx.x; j < n; j += 64) {
       pairs += owner[j] != n;
       experts += owner[j] == j;
     }
-    plan->experts = experts;
-    plan->pairs = pairs;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      pairs += __shfl_xor(pairs, d);
+      experts += __shfl_xor(experts, d);
+    }
+    if (threadIdx.x == 0) {
+      plan->experts = experts;
+      plan->pairs = pairs;
+    }
   }
+  __syncthreads();
 }
 
-// Steps in registers.
-template <bool FP4, int NT>
-constexpr int UP_DEPTH = FP4 && NT == 1 ? 3 : 2;
+// ---------------------------------------------------------------------------
+// Up
+// ---------------------------------------------------------------------------
 
-// One pass of an expert's workgroup over its rows with up to 16 NT tokens: the
-// waves share K and their sums meet in LDS.
-template <bool FP4, int RT, int NT>
-__device__ __forceinline__ void up_pass(const ExpertsArgs& p, const Shape<FP4>& shape, const Matrix& m, int f0,
-                                        const int* slots, int count, f32x4* red) {
+constexpr int UP_WAVES = 4, UP_THREADS = UP_WAVES * 64;
+constexpr int UP_W_SLOTS = 3, UP_T_SLOTS = 2;  // steps of weights and of tokens in a wave's ring
+
+// Tokens' rows of a block come in loads of 4 rows of 256 bytes; their 16-byte pieces
+// are swizzled for the fragment reads, as the weights' are.
+__device__ __forceinline__ int token_swizzle(int row) { return (row & 3) | ((-(row >> 2) & 3) << 2); }
+
+// The i-th block of K that a wave takes, and how many there are: turn by turn, for
+// FP4 two successive ones, which share a 128-byte line of a row.
+template <bool FP4>
+__device__ __forceinline__ int wave_block(int wave, int i) {
+  return FP4 ? (i >> 1) * 2 * UP_WAVES + 2 * wave + (i & 1) : i * UP_WAVES + wave;
+}
+template <bool FP4>
+__device__ __forceinline__ int wave_blocks(int wave, int blocks) {
+  if (!FP4) return max((blocks - wave + UP_WAVES - 1) / UP_WAVES, 0);
+  const int rounds = blocks / (2 * UP_WAVES);
+  return 2 * rounds + min(max(blocks - rounds * 2 * UP_WAVES - 2 * wave, 0), 2);
+}
+
+template <bool FP4, int RT>
+using UpWeights = Weights<FP4, 2 * RT, 2>;
+
+// Most tokens of a pass, in fours: what leaves the rings room.
+constexpr int UP_MOST_FOURS = 6;
+template <bool FP4, int RT>
+constexpr int UP_RING = UP_W_SLOTS * UpWeights<FP4, RT>::BYTES + UP_T_SLOTS * UP_MOST_FOURS * 1024;
+
+// One pass of an expert's workgroup over its rows with up to 4 FOURS tokens: the
+// waves share K and their sums meet in LDS. The first two steps' weights are already
+// on their way.
+template <bool FP4, int RT, int FOURS, int ROWS>
+__device__ __forceinline__ void up_pass(const ExpertsArgs& p, const UpWeights<FP4, RT>& weights, int f0, int expert,
+                                        int number, const int* slots, int count, uint8_t* lds) {
+  constexpr int NT = (FOURS + 3) / 4, W = UpWeights<FP4, RT>::LOADS, T = FOURS, TILES = 2 * RT;
+  constexpr int STEP = UpWeights<FP4, RT>::BYTES, TOKENS = FOURS * 1024;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const uint16_t* row[NT];
+  uint8_t* const ring = lds + wave * UP_RING<FP4, RT>;
+  const uint32_t base = (uint32_t)(uintptr_t)(lds_void*)ring, token_base = base + UP_W_SLOTS * STEP;
+  const __amdgpu_buffer_rsrc_t x = buffer_rsrc(p.x, 0xFFFFFFFFu);
+  uint32_t x_at[FOURS];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-    row[nt] = p.x + (size_t)(slots[min(nt * 16 + r, count - 1)] / p.top_k) * p.hidden;
-  int row0[2 * RT];
-#pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    row0[i] = f0 + 16 * i;
-    row0[RT + i] = p.inner + f0 + 16 * i;
+  for (int q = 0; q < FOURS; ++q) {
+    const int row = 4 * q + g;
+    x_at[q] = (uint32_t)(slots[min(row, count - 1)] / p.top_k) * (uint32_t)(p.hidden * 2) +
+              (uint32_t)((r ^ token_swizzle(row & 15)) << 4);
   }
-  f32x4 acc[2 * RT][NT];
+  uint32_t read_at[NT];  // of the lane's token, piece 0
+  uint32_t swizzle[NT];
 #pragma unroll
-  for (int i = 0; i < 2 * RT; ++i)
+  for (int nt = 0; nt < NT; ++nt) {
+    const int rows = min(FOURS * 4 - nt * 16, 16), row = nt * 16 + (r & (rows - 1));  // 4, 8 or 16 rows: others repeat
+    read_at[nt] = row * 256;
+    swizzle[nt] = token_swizzle(row & 15);
+  }
+  auto load_tokens = [&](int block, int slot) {
+#pragma unroll
+    for (int q = 0; q < FOURS; ++q) dma16(x, x_at[q], (uint32_t)block * 256, token_base + slot * TOKENS + q * 1024);
+  };
+
+  f32x4 acc[TILES][NT];
+#pragma unroll
+  for (int i = 0; i < TILES; ++i)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) acc[i][nt] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  using Buffer = Step<FP4, 2 * RT, NT>;
-  pipeline<UP_DEPTH<FP4, NT>, Buffer>(
-      wave_blocks<FP4>(wave, p.hidden / QBLOCK),
-      [&](Buffer& s, int i) {
-        const int block = wave_block<FP4>(wave, i);
-#pragma unroll
-        for (int k = 0; k < 2 * RT; ++k) load_tile<FP4>(s.w[k], shape, m, row0[k], block);
-        load_tokens<FP4, NT>(s.t, row, block, lane);
-      },
-      [&](const Buffer& s, int) { multiply<FP4, 2 * RT, NT>(acc, s, lane); });
 
-  constexpr int UNITS = 2 * RT * NT;
-  __syncthreads();  // of an earlier pass: its sums have been read
+  const int steps = wave_blocks<FP4>(wave, p.hidden / QBLOCK), last = max(steps - 1, 0);
+  auto block = [&](int i) { return wave_block<FP4>(wave, min(i, last)); };
+  if (steps > 0) {
+    load_tokens(block(0), 0);
+    int w_slot = 0, w_next = 2;
+    for (int i = 0; i < steps; ++i) {
+      before_loads();
+      load_tokens(block(i + 1), (i + 1) & 1);
+      weights.load(block(i + 2), base + w_next * STEP);
+      // What follows this step's loads: one step's tokens and two steps' weights (first:
+      // its tokens came after the second step's weights).
+      if (i == 0) wait_loads<T + W>();
+      else wait_loads<T + 2 * W>();
+      const uint8_t* const st = ring + w_slot * STEP;
+      const uint8_t* const tok = ring + UP_W_SLOTS * STEP + (i & 1) * TOKENS;
+      u32x4 t[NT][4];
 #pragma unroll
-  for (int i = 0; i < 2 * RT; ++i)
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t piece = FP4 ? 4 * g + j : 8 * (j >> 1) + 2 * g + (j & 1);
+          t[nt][j] = *reinterpret_cast<const u32x4*>(tok + read_at[nt] + ((piece ^ swizzle[nt]) << 4));
+        }
+#pragma unroll
+      for (int k = 0; k < TILES; ++k) weights.template multiply<NT>(acc[k], st, k, t, lane);
+      w_slot = w_slot == UP_W_SLOTS - 1 ? 0 : w_slot + 1;
+      w_next = w_next == UP_W_SLOTS - 1 ? 0 : w_next + 1;
+    }
+  }
+
+  // The waves' sums, in the rings' place.
+  constexpr int UNITS = TILES * NT;
+  static_assert(UP_WAVES * UNITS * 1024 <= UP_WAVES * UP_RING<FP4, RT>, "sums in the rings' place");
+  f32x4* const red = reinterpret_cast<f32x4*>(lds);
+  wait_loads<0>();
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < TILES; ++i)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) red[(wave * UNITS + i * NT + nt) * 64 + lane] = acc[i][nt];
   __syncthreads();
+  const int tile = act_tile(p, expert, number, slots[0]), tile2 = NT > 1 && count > 16 ? act_tile(p, expert, number + 1, slots[16]) : 0;
   for (int unit = wave; unit < RT * NT; unit += UP_WAVES) {
     f32x4 gate = red[unit * 64 + lane], up = red[(RT * NT + unit) * 64 + lane];
 #pragma unroll
@@ -315,34 +397,46 @@ __device__ __forceinline__ void up_pass(const ExpertsArgs& p, const Shape<FP4>& 
     f32x4 a;
 #pragma unroll
     for (int i = 0; i < 4; ++i) a[i] = gate[i] * sigmoid(gate[i]) * up[i];
-    const int i = unit / NT, t = (unit % NT) * 16 + r;
-    if (t < count) {
+    const int i = unit / NT, nt = unit % NT;
+    if (nt * 16 + r < count) {
       const u32x2 packed = {pack2((f32x2){a[0], a[1]}), pack2((f32x2){a[2], a[3]})};
-      *reinterpret_cast<u32x2*>(p.act + (size_t)slots[t] * p.inner + f0 + 16 * i + 4 * g) = packed;
+      uint16_t* const at = p.act + (size_t)(nt ? tile2 : tile) * ROWS * p.inner;
+      *reinterpret_cast<u32x2*>(at + act_at<FP4, ROWS>(f0 + 16 * i + 4 * g, r)) = packed;
     }
   }
+  __syncthreads();  // the sums have been read: the rings are free
 }
 
-// Workgroup 0 makes the plan; the others take 16 RT gate rows and as many up rows
-// of one expert each: an expert by its number, or with more experts than slots the
-// expert of a slot that is the first to name it.
-template <bool FP4, int RT, int NT>
-__global__ __launch_bounds__(UP_THREADS) void experts_up_kernel(ExpertsArgs p) {
+// A workgroup takes 16 RT gate rows and as many up rows of one expert: an expert by its
+// number, or with no more slots than experts the expert of a slot that is the first to
+// name it. The first one makes the plan as well.
+template <bool FP4, int RT, int ROWS>
+__global__ __launch_bounds__(UP_THREADS, 1) void experts_up_kernel(ExpertsArgs p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[UP_WAVES * UP_RING<FP4, RT>];
   __shared__ int ids[MAX_FEW_PAIRS];
-  __shared__ int list[MAX_FEW_PAIRS];  // the plan's owners; else the expert's slots
-  __shared__ int waves_before[UP_WAVES + 1];
-  __shared__ f32x4 red[UP_WAVES * 2 * RT * NT * 64];
-  const int n = p.tokens * p.top_k, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ int list[MAX_FEW_PAIRS];  // the plan's owners; then the expert's slots
+  __shared__ int waves_before[UP_WAVES];
+  const int n = p.tokens * p.top_k, tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tiles = p.inner / (16 * RT), item = blockIdx.x / tiles, f0 = blockIdx.x % tiles * 16 * RT;
+  const bool by_slot = n <= p.num_groups;
+  const int e = __builtin_amdgcn_readfirstlane(by_slot ? p.ids[item] : item);
+  const bool named = e >= 0 && e < p.num_groups;
+  const int row0[2] = {f0, p.inner + f0};
+  const UpWeights<FP4, RT> weights(p.b1, p.sfb1, named ? e : 0, 2 * p.inner, p.hidden, row0, lane);
+  const int steps = wave_blocks<FP4>(wave, p.hidden / QBLOCK), last = max(steps - 1, 0);
+  const uint32_t base = (uint32_t)(uintptr_t)(lds_void*)(lds + wave * UP_RING<FP4, RT>);
+  auto first_weights = [&]() {  // (a wave without steps loads blocks that nobody reads)
+    if (steps == 0) return;
+    weights.load(wave_block<FP4>(wave, 0), base);
+    weights.load(wave_block<FP4>(wave, min(1, last)), base + UpWeights<FP4, RT>::BYTES);
+  };
+  if (named) first_weights();
+
   for (int i = tid; i < n; i += UP_THREADS) ids[i] = p.ids[i];
   __syncthreads();
-  if (blockIdx.x == 0) {
-    build_plan(p, reinterpret_cast<ExpertPlan*>(p.plan), ids, list);
-    return;
-  }
-  const int tiles = p.inner / (16 * RT), item = (blockIdx.x - 1) / tiles, f0 = (blockIdx.x - 1) % tiles * 16 * RT;
-  const bool by_slot = n <= p.num_groups;
-  const int e = by_slot ? ids[item] : item;
-  if (e < 0 || e >= p.num_groups) return;
+  if (blockIdx.x == 0) build_plan<UP_THREADS>(p, reinterpret_cast<ExpertPlan*>(p.plan), ids, list);
+  if (!named) return;
   // The expert's slots in order, counted 256 at a time.
   int count = 0;
   bool earlier = false;
@@ -362,57 +456,66 @@ __global__ __launch_bounds__(UP_THREADS) void experts_up_kernel(ExpertsArgs p) {
     if (take) list[before + __popcll(votes & ((1ull << lane) - 1))] = i;
     __syncthreads();
   }
-  if (__syncthreads_or(earlier) || count == 0) return;
-
-  const Shape<FP4> shape(2 * p.inner, p.hidden, lane);
-  const Matrix m = shape.expert(p.b1, p.sfb1, __builtin_amdgcn_readfirstlane(e));
-  for (int t0 = 0; t0 < count; t0 += 16 * NT) {
-    const int here = min(count - t0, 16 * NT);
-    if (NT == 1 || here <= 16) up_pass<FP4, RT, 1>(p, shape, m, f0, list + t0, here, red);
-    else up_pass<FP4, RT, NT>(p, shape, m, f0, list + t0, here, red);
+  const bool none = __syncthreads_or(earlier) || count == 0;
+  // The tokens 16 at a time, the last 17 to 24 at once.
+  for (int t0 = 0; !none && t0 < count;) {
+    const int left = count - t0, here = left <= 4 * UP_MOST_FOURS ? left : 16;
+    if (t0 > 0) first_weights();
+    if constexpr (ROWS == 4) {
+      up_pass<FP4, RT, 1, ROWS>(p, weights, f0, e, t0 / 16, list + t0, here, lds);
+    } else {
+      if (here <= 4) up_pass<FP4, RT, 1, ROWS>(p, weights, f0, e, t0 / 16, list + t0, here, lds);
+      else if (here <= 8) up_pass<FP4, RT, 2, ROWS>(p, weights, f0, e, t0 / 16, list + t0, here, lds);
+      else if (here <= 16) up_pass<FP4, RT, 4, ROWS>(p, weights, f0, e, t0 / 16, list + t0, here, lds);
+      else up_pass<FP4, RT, 6, ROWS>(p, weights, f0, e, t0 / 16, list + t0, here, lds);
+    }
+    t0 += here;
   }
+  wait_loads<0>();  // no wave may end while a load can still write its LDS
 }
 
 // ---------------------------------------------------------------------------
 // Down
 // ---------------------------------------------------------------------------
 
-constexpr int DOWN_WAVES = 8, DOWN_THREADS = DOWN_WAVES * 64;
+constexpr int DOWN_WAVES = 4, DOWN_THREADS = DOWN_WAVES * 64, DOWN_RT = 2;
 
-// A workgroup takes 16 RT columns of y for all tokens. Its waves share the experts,
-// 16 tokens of one at a time, and, where these do not come out even, their K in
-// parts; each wave keeps sums of its own in LDS, which are added in order at the end.
-// A wave's items follow one another in one pipeline of steps.
+// Steps on their way and in use: of 4 KB (FP8) or 2, as many as leave the sums room.
+template <bool FP4, int TOKENS>
+constexpr int DOWN_DEPTH = FP4 ? 8 : TOKENS > 64 ? 4 : 5;
 template <bool FP4>
-constexpr int DOWN_DEPTH = FP4 ? 4 : 3;
+using DownWeights = Weights<FP4, DOWN_RT, 1>;
 
 struct DownItem {
-  int expert, begin, count;  // pairs of the plan, at most 16
+  int expert, begin, count, tile;  // pairs of the plan, at most 16, and their activations
 };
 
-template <bool FP4, int RT, int TOKENS>
-__global__ __launch_bounds__(DOWN_THREADS) void experts_down_kernel(ExpertsArgs p) {
-  constexpr int STRIDE = 16 * RT + (TOKENS > 64 ? 0 : 4);  // floats; 4 past a power of two where there is room
-  __shared__ float sums[DOWN_WAVES * TOKENS * STRIDE];
-  __shared__ DownItem items[MAX_FEW_PAIRS];
-  __shared__ int items_of[DOWN_THREADS / 64];
+// A workgroup takes 32 columns of y for all tokens. Its waves share the experts, 16
+// tokens of one at a time, and, where these do not come out even, their K in parts;
+// each wave keeps sums of its own in LDS, which are added in order at the end. A wave's
+// items follow one another in one pipeline of steps.
+template <bool FP4, int ROWS, int TOKENS>
+__global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsArgs p) {
+  constexpr int STRIDE = 16 * DOWN_RT + (TOKENS > 64 ? 0 : 4);  // floats; 4 past a power of two where there is room
+  constexpr int DEPTH = DOWN_DEPTH<FP4, TOKENS>, W = DownWeights<FP4>::LOADS, STEP = DownWeights<FP4>::BYTES;
+  __shared__ __attribute__((aligned(1024))) uint8_t rings[DOWN_WAVES * DEPTH * STEP];
+  __shared__ __attribute__((aligned(16))) float sums[DOWN_WAVES * TOKENS * STRIDE];
   // Of the pairs; read from memory in the loop, they would be waited for with all the
   // weights that are on their way.
-  __shared__ int slots[MAX_FEW_PAIRS];
+  __shared__ DownItem items[MAX_FEW_PAIRS];
   __shared__ uint16_t sums_at[MAX_FEW_PAIRS];  // of the pair's token, in 16 bytes
-  __shared__ float weights[MAX_FEW_PAIRS];
+  __shared__ float pair_weights[MAX_FEW_PAIRS];
+  __shared__ int items_of[DOWN_WAVES];
   const ExpertPlan* plan = reinterpret_cast<const ExpertPlan*>(p.plan);
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), c0 = blockIdx.x * 16 * RT;
-  float* mine = sums + wave * TOKENS * STRIDE;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), c0 = blockIdx.x * 16 * DOWN_RT;
+  float* const mine = sums + wave * TOKENS * STRIDE;
   for (int i = lane; i < p.tokens * STRIDE; i += 64) mine[i] = 0.0f;
 
   const int experts = plan->experts, pairs = plan->pairs;
   for (int i = tid; i < pairs; i += DOWN_THREADS) {
-    const int slot = plan->slot[i];
-    slots[i] = slot;
-    sums_at[i] = (uint16_t)(slot / p.top_k * (STRIDE / 4));
-    weights[i] = plan->weight[i];
+    sums_at[i] = (uint16_t)(plan->slot[i] / p.top_k * (STRIDE / 4));
+    pair_weights[i] = plan->weight[i];
   }
   // The items: an expert's pairs 16 at a time, in order.
   int total = 0;
@@ -429,37 +532,37 @@ __global__ __launch_bounds__(DOWN_THREADS) void experts_down_kernel(ExpertsArgs 
     if (lane == 63) items_of[wave] = upto;
     __syncthreads();
     int before = total + upto - has;
-    for (int w = 0; w < DOWN_THREADS / 64; ++w) {
+    for (int w = 0; w < DOWN_WAVES; ++w) {
       if (w < wave) before += items_of[w];
       total += items_of[w];
     }
     for (int i = 0; i < has; ++i)
-      items[before + i] = DownItem{entry.expert, entry.begin + 16 * i, min(entry.count - 16 * i, 16)};
+      items[before + i] = DownItem{entry.expert, entry.begin + 16 * i, min(entry.count - 16 * i, 16),
+                                   act_tile(p, entry.expert, i, plan->slot[entry.begin + 16 * i])};
     __syncthreads();
   }
+  total = __builtin_amdgcn_readfirstlane(total);
 
   // Parts of K (of pairs of blocks, see wave_block): so many that the waves have the
   // same number of items, or that they have eight each.
   const int blocks = p.inner / QBLOCK, unit = FP4 ? 2 : 1, units = (blocks + unit - 1) / unit;
   int parts = 1;
-  while (parts < DOWN_WAVES && parts * 2 <= units && total * parts % DOWN_WAVES && total * parts < 8 * DOWN_WAVES)
-    parts *= 2;
+  while (parts < 8 && parts * 2 <= units && total * parts % DOWN_WAVES && total * parts < 8 * DOWN_WAVES) parts *= 2;
   const int all = total * parts, turns = wave < all ? (all - wave + DOWN_WAVES - 1) / DOWN_WAVES : 0;
 
-  const Shape<FP4> shape(p.hidden, p.inner, lane);
   // Where the loads and the products are: the turn, its item and its blocks.
   struct Cursor {
-    int turn, block, end, begin, count;
-    Matrix m;
+    int turn, block, end, begin, count, tile;
   };
   auto start = [&](Cursor& c) {
     const int item = wave + c.turn * DOWN_WAVES, part = item % parts;
     const DownItem at = items[item / parts];
     c.begin = __builtin_amdgcn_readfirstlane(at.begin);
     c.count = __builtin_amdgcn_readfirstlane(at.count);
-    c.m = shape.expert(p.b2, p.sfb2, __builtin_amdgcn_readfirstlane(at.expert));
+    c.tile = __builtin_amdgcn_readfirstlane(at.tile);
     c.block = units * part / parts * unit;
     c.end = min(units * (part + 1) / parts * unit, blocks);
+    return __builtin_amdgcn_readfirstlane(at.expert);
   };
   int steps = 0;
   for (int turn = 0; turn < turns; ++turn) {
@@ -467,52 +570,73 @@ __global__ __launch_bounds__(DOWN_THREADS) void experts_down_kernel(ExpertsArgs 
     steps += min(units * (part + 1) / parts * unit, blocks) - units * part / parts * unit;
   }
 
-  using Buffer = Step<FP4, RT, 1>;
-  Cursor ahead{}, now{};
-  const uint16_t* row[1] = {p.act};
-  f32x4 acc[RT][1] = {};
-  int loaded = 0;
   if (steps > 0) {
-    start(ahead);
+    const uint8_t* const ring = rings + wave * DEPTH * STEP;
+    const uint32_t base = (uint32_t)(uintptr_t)(lds_void*)ring;
+    const int row0[1] = {c0};
+    Cursor ahead{}, now{};
     start(now);
-    row[0] = p.act + (size_t)slots[ahead.begin + min(r, ahead.count - 1)] * p.inner;
-  }
-  pipeline<DOWN_DEPTH<FP4>, Buffer>(
-      steps,
-      [&](Buffer& s, int) {
+    const int first = start(ahead);
+    DownWeights<FP4> weights(p.b2, p.sfb2, first, p.hidden, p.inner, row0, lane);
+    const uint16_t* act = p.act + (size_t)ahead.tile * ROWS * p.inner;
+    const uint32_t act_lane = (uint32_t)(g * ROWS + (r & (ROWS - 1))) * 8;
+    f32x4 acc[DOWN_RT][1] = {};
+    int loaded = 0, w_next = 0, w_slot = 0;
+    u32x4 t[DEPTH][1][4];
+    auto load = [&](u32x4 (&to)[1][4]) {
 #pragma unroll
-        for (int i = 0; i < RT; ++i) load_tile<FP4>(s.w[i], shape, ahead.m, c0 + 16 * i, ahead.block);
-        load_tokens<FP4, 1>(s.t, row, ahead.block, lane);
-        if (++loaded < steps && ++ahead.block == ahead.end) {
-          ++ahead.turn;
-          start(ahead);
-          row[0] = p.act + (size_t)slots[ahead.begin + min(r, ahead.count - 1)] * p.inner;
+      for (int j = 0; j < 4; ++j) to[0][j] = load16(act + (ahead.block * QBLOCK * ROWS + j * 4 * ROWS * 8) + act_lane);
+      weights.load(ahead.block, base + w_next * STEP);
+      w_next = w_next == DEPTH - 1 ? 0 : w_next + 1;
+      if (++loaded < steps && ++ahead.block == ahead.end) {  // (past the last step it is loaded again)
+        ++ahead.turn;
+        const int e = start(ahead);
+        weights = DownWeights<FP4>(p.b2, p.sfb2, e, p.hidden, p.inner, row0, lane);
+        act = p.act + (size_t)ahead.tile * ROWS * p.inner;
+      }
+    };
+    auto use = [&](const u32x4 (&from)[1][4]) {
+      const uint8_t* const st = ring + w_slot * STEP;
+      w_slot = w_slot == DEPTH - 1 ? 0 : w_slot + 1;
+#pragma unroll
+      for (int k = 0; k < DOWN_RT; ++k) weights.template multiply<1>(acc[k], st, k, from, lane);
+      if (++now.block < now.end) return;
+      if (r < now.count) {  // the item's tokens differ from one another
+        const float w = pair_weights[now.begin + r];
+        float* const at = mine + 4 * (sums_at[now.begin + r] + g);
+#pragma unroll
+        for (int k = 0; k < DOWN_RT; ++k) {
+          f32x4 sum = *reinterpret_cast<f32x4*>(at + 16 * k);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) sum[v] = __builtin_fmaf(w, acc[k][0][v], sum[v]);
+          *reinterpret_cast<f32x4*>(at + 16 * k) = sum;
         }
-      },
-      [&](const Buffer& s, int i) {
-        multiply<FP4, RT, 1>(acc, s, lane);
-        if (++now.block < now.end) return;
-        if (r < now.count) {  // the item's tokens differ from one another
-          const float w = weights[now.begin + r];
-          float* at = mine + 4 * (sums_at[now.begin + r] + g);
+      }
 #pragma unroll
-          for (int k = 0; k < RT; ++k) {
-            f32x4 sum = *reinterpret_cast<f32x4*>(at + 16 * k);
-#pragma unroll
-            for (int v = 0; v < 4; ++v) sum[v] = __builtin_fmaf(w, acc[k][0][v], sum[v]);
-            *reinterpret_cast<f32x4*>(at + 16 * k) = sum;
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < RT; ++k) acc[k][0] = (f32x4){0.f, 0.f, 0.f, 0.f};
-        if (i + 1 < steps) {
-          ++now.turn;
-          start(now);
-        }
+      for (int k = 0; k < DOWN_RT; ++k) acc[k][0] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      if (++now.turn < turns) start(now);
+    };
+    // Rounds that are left at their end only, so that on every path to a use the compiler
+    // knows how many loads follow the ones that it waits for.
+    static_for<0, DEPTH - 1>([&](auto I) { load(t[decltype(I)::value]); });
+    const int rounds = steps / DEPTH * DEPTH;
+    for (int i0 = 0; i0 < rounds; i0 += DEPTH) {
+      static_for<0, DEPTH>([&](auto I) {
+        constexpr int j = decltype(I)::value;
+        before_loads();
+        load(t[(j + DEPTH - 1) % DEPTH]);
+        wait_loads<(DEPTH - 1) * (4 + W)>();
+        use(t[j]);
       });
+    }
+    wait_loads<0>();
+    static_for<0, DEPTH - 1>([&](auto I) {
+      if (rounds + decltype(I)::value < steps) use(t[decltype(I)::value]);
+    });
+  }
   __syncthreads();
-  for (int i = tid; i < p.tokens * 8 * RT; i += DOWN_THREADS) {
-    const int t = i / (8 * RT), c = i % (8 * RT) * 2;
+  for (int i = tid; i < p.tokens * 8 * DOWN_RT; i += DOWN_THREADS) {
+    const int t = i / (8 * DOWN_RT), c = i % (8 * DOWN_RT) * 2;
     f32x2 s = {0.f, 0.f};
 #pragma unroll
     for (int w = 0; w < DOWN_WAVES; ++w)
@@ -522,24 +646,37 @@ __global__ __launch_bounds__(DOWN_THREADS) void experts_down_kernel(ExpertsArgs 
   }
 }
 
-template <bool FP4, int RT>
-hipError_t launch_typed(const ExpertsArgs& a, hipStream_t stream) {
-  const int n = a.tokens * a.top_k;
-  const int ups = 1 + std::min(n, a.num_groups) * (a.inner / (16 * RT));
-  auto* up = a.tokens <= 16 ? experts_up_kernel<FP4, RT, 1> : experts_up_kernel<FP4, RT, 2>;
-  hipLaunchKernelGGL(up, dim3(ups), dim3(UP_THREADS), 0, stream, a);
-  if (hipError_t e = hipGetLastError()) return e;
-  auto* down = a.tokens <= 16 ? experts_down_kernel<FP4, RT, 16>
-                              : a.tokens <= 64 ? experts_down_kernel<FP4, RT, 64>
-                                               : experts_down_kernel<FP4, RT, MAX_FEW_TOKENS>;
-  hipLaunchKernelGGL(down, dim3(a.hidden / (16 * RT)), dim3(DOWN_THREADS), 0, stream, a);
+template <bool FP4, int RT, int ROWS>
+hipError_t launch_up(const ExpertsArgs& a, hipStream_t stream) {
+  const int workgroups = std::min(a.tokens * a.top_k, a.num_groups) * (a.inner / (16 * RT));
+  hipLaunchKernelGGL((experts_up_kernel<FP4, RT, ROWS>), dim3(workgroups), dim3(UP_THREADS), 0, stream, a);
+  return hipGetLastError();
+}
+
+// ROWS: 4 for up to 4 tokens, else 16.
+template <bool FP4, int ROWS>
+hipError_t launch_both(const ExpertsArgs& a, hipStream_t stream) {
+  constexpr int RT = FP4 ? 4 : 2;
+  // Half as many rows a workgroup where there would not be one for every compute unit.
+  const bool few = std::min(a.tokens * a.top_k, a.num_groups) * (a.inner / (16 * RT)) < 256;
+  if (hipError_t e = few ? launch_up<FP4, RT / 2, ROWS>(a, stream) : launch_up<FP4, RT, ROWS>(a, stream)) return e;
+  void (*down)(ExpertsArgs);
+  if constexpr (ROWS == 4) down = experts_down_kernel<FP4, ROWS, 4>;
+  else down = a.tokens <= 64 ? experts_down_kernel<FP4, ROWS, 64> : experts_down_kernel<FP4, ROWS, MAX_FEW_TOKENS>;
+  hipLaunchKernelGGL(down, dim3(a.hidden / (16 * DOWN_RT)), dim3(DOWN_THREADS), 0, stream, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
+long long experts_act_bytes(int tokens, int top_k, int num_groups, int inner) {
+  const int n = tokens * top_k, tiles = n <= num_groups ? n : num_groups * ((tokens + 15) / 16);
+  return (long long)tiles * (tokens <= 4 ? 4 : 16) * inner * 2;
+}
+
 hipError_t launch_experts(const ExpertsArgs& a, hipStream_t stream) {
-  return a.fp4 ? launch_typed<true, 2>(a, stream) : launch_typed<false, 2>(a, stream);
+  if (a.tokens <= 4) return a.fp4 ? launch_both<true, 4>(a, stream) : launch_both<false, 4>(a, stream);
+  return a.fp4 ? launch_both<true, 16>(a, stream) : launch_both<false, 16>(a, stream);
 }
 
 }  // namespace moe

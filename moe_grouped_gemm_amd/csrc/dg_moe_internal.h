@@ -66,9 +66,11 @@ struct ExpertsArgs {
   const void* sfb2;
   uint16_t* y;
   void* plan;            // EXPERT_PLAN_BYTES
-  uint16_t* act;         // [tokens * top_k][inner]
+  uint16_t* act;         // experts_act_bytes()
   int fp4, tokens, top_k, num_groups, hidden, inner;
 };
+// Grows with tokens.
+long long experts_act_bytes(int tokens, int top_k, int num_groups, int inner);
 hipError_t launch_experts(const ExpertsArgs& a, hipStream_t stream);
 
 // Norms around the block (dg_moe_norm.hip).
