@@ -271,7 +271,8 @@ dg_status dg_moe_experts(const dg_moe_experts_args* args, void* stream) {
     if (!aligned16(p)) return DG_ERR_ALIGN;
   if (!aligned4b(a.topk_ids) || !aligned4b(a.weights)) return DG_ERR_ALIGN;
   if (a.workspace_bytes < experts_workspace(a.tokens, a.top_k, a.num_groups, a.inner)) return DG_ERR_SHAPE;
-  if (dg_status s = device_check()) return s;
+  const int cus = dg_get_num_cus();
+  if (cus <= 0) return DG_ERR_DEVICE;
   ExpertsArgs e{};
   e.x = static_cast<const uint16_t*>(a.x);
   e.ids = a.topk_ids;
@@ -289,6 +290,7 @@ dg_status dg_moe_experts(const dg_moe_experts_args* args, void* stream) {
   e.num_groups = a.num_groups;
   e.hidden = a.hidden;
   e.inner = a.inner;
+  e.cus = cus;
   return status_of(launch_experts(e, as_stream(stream)));
 }
 

@@ -105,21 +105,19 @@ struct Weights {
   static constexpr int BYTES = TILES * TILE_BYTES + SCALE_LOADS * 256;  // of a step in LDS
   static constexpr int LOADS = TILES * (TILE_BYTES / 1024) + SCALE_LOADS;
 
-  __amdgpu_buffer_rsrc_t rows[GROUPS], scales;
+  const uint8_t* b;
+  const uint32_t* sf;
+  int n, k;                                      // the matrix is [n][k]
   uint32_t row_bytes, scale_step;                // bytes between rows; between a block's scales and the next's
-  uint32_t w_at[TILE_BYTES / 1024], sf_at[SCALE_LOADS];  // the lane's offsets, fixed
+  uint32_t w_at[TILE_BYTES / 1024];              // the lane's offsets,
   uint32_t read_at, read_sf;                     // and in LDS
+  __amdgpu_buffer_rsrc_t rows[GROUPS], scales;   // of the place at hand
+  uint32_t sf_at[SCALE_LOADS];
 
-  // Rows row0[.] of expert e's matrix [n][k].
-  __device__ Weights(const void* b, const void* sf, int e, int n, int k, const int (&row0)[GROUPS], int lane) {
+  __device__ __forceinline__ Weights(const void* b_, const void* sf_, int n_, int k_, int lane)
+      : b(static_cast<const uint8_t*>(b_)), sf(static_cast<const uint32_t*>(sf_)), n(n_), k(k_) {
     const int r = lane & 15, g = lane >> 4;
-    const size_t values = (size_t)n * k;
     row_bytes = FP4 ? k / 2 : k;
-    const uint8_t* w = static_cast<const uint8_t*>(b) + (size_t)e * (FP4 ? values / 2 : values);
-#pragma unroll
-    for (int i = 0; i < GROUPS; ++i) rows[i] = buffer_rsrc(w + (size_t)row0[i] * row_bytes, 0xFFFFFFFFu);
-    scales = buffer_rsrc(static_cast<const uint32_t*>(sf) + (size_t)e * (FP4 ? values / QBLOCK : values / QBLOCK / 128),
-                         0xFFFFFFFFu);
     scale_step = FP4 ? n * 4 : 4;
     if constexpr (FP4) {
       // A load is 16 rows of 64 bytes; pieces of 16 are swizzled so that a fragment
@@ -127,11 +125,6 @@ struct Weights {
       const int row = lane >> 2, piece = (lane & 3) ^ (-(row >> 2) & 3);
       w_at[0] = row * row_bytes + piece * 16;
       read_at = r * 64 + ((g ^ (-(r >> 2) & 3)) << 4);
-#pragma unroll
-      for (int q = 0; q < SCALE_LOADS; ++q) {
-        const int tile = min(4 * q + g, TILES - 1), group = tile / PER_GROUP;
-        sf_at[q] = (GROUPS == 2 && group ? row0[GROUPS - 1] : row0[0]) * 4 + ((tile - group * PER_GROUP) * 16 + r) * 4;
-      }
       read_sf = r * 4;
     } else {
       // A load is 8 rows of 128 bytes.
@@ -141,8 +134,25 @@ struct Weights {
         w_at[h] = row * row_bytes + piece * 16;
       }
       read_at = lds_offset(r, g);  // and, with bit 6 flipped, lds_offset(r, g + 4)
-      sf_at[0] = (GROUPS == 2 && (lane & 1) ? row0[GROUPS - 1] : row0[0]) / 128 * (k / QBLOCK) * 4;
       read_sf = 0;
+    }
+  }
+
+  // Turns to the runs of rows from row0[.] of expert e's matrix.
+  __device__ __forceinline__ void place(int e, const int (&row0)[GROUPS], int lane) {
+    const size_t values = (size_t)n * k;
+    const uint8_t* w = b + (size_t)e * (FP4 ? values / 2 : values);
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i) rows[i] = buffer_rsrc(w + (size_t)row0[i] * row_bytes, 0xFFFFFFFFu);
+    scales = buffer_rsrc(sf + (size_t)e * (FP4 ? values / QBLOCK : values / QBLOCK / 128), 0xFFFFFFFFu);
+    if constexpr (FP4) {
+#pragma unroll
+      for (int q = 0; q < SCALE_LOADS; ++q) {
+        const int tile = min(4 * q + (lane >> 4), TILES - 1), group = tile / PER_GROUP;
+        sf_at[q] = ((GROUPS == 2 && group ? row0[GROUPS - 1] : row0[0]) + (tile - group * PER_GROUP) * 16 + (lane & 15)) * 4;
+      }
+    } else {
+      sf_at[0] = (GROUPS == 2 && (lane & 1) ? row0[GROUPS - 1] : row0[0]) / 128 * (k / QBLOCK) * 4;
     }
   }
 
@@ -205,81 +215,13 @@ struct Weights {
 };
 
 // ---------------------------------------------------------------------------
-// The plan
-// ---------------------------------------------------------------------------
-
-// Whether slot i is the first of its token with its expert.
-__device__ __forceinline__ bool first_of_token(const int* ids, int i, int top_k) {
-  const int e = ids[i];
-  for (int j = i - i % top_k; j < i; ++j)
-    if (ids[j] == e) return false;
-  return true;
-}
-
-// By one workgroup: every slot looks at all others (in LDS, all lanes at the same
-// one), at most 1024 of them.
-template <int THREADS>
-__device__ void build_plan(const ExpertsArgs& p, ExpertPlan* plan, const int* ids, int* owner) {
-  const int n = p.tokens * p.top_k;
-  // owner[i]: the first slot of i's expert, where i is its pair's first slot; else n.
-  for (int i = threadIdx.x; i < n; i += THREADS) {
-    const int e = ids[i];
-    int own = n;
-    if (e >= 0 && e < p.num_groups && first_of_token(ids, i, p.top_k)) {
-      own = i;
-      for (int j = 0; j < i; ++j)
-        if (ids[j] == e) {
-          own = j;
-          break;
-        }
-    }
-    owner[i] = own;
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += THREADS) {
-    const int own = owner[i];
-    if (own == n) continue;
-    int at = 0, rank = 0, begin = 0, count = 0;
-    for (int j = 0; j < n; ++j) {
-      const int other = owner[j];
-      at += other < own || (other == own && j < i);
-      begin += other < own;
-      count += other == own;
-      rank += other == j && j < own;
-    }
-    float w = 0.0f;
-    const int t0 = i - i % p.top_k;
-    for (int j = t0; j < t0 + p.top_k; ++j)
-      if (ids[j] == ids[i]) w += p.weights ? p.weights[j] : 1.0f;
-    plan->slot[at] = i;
-    plan->weight[at] = w;
-    if (own == i) plan->entry[rank] = ExpertEntry{ids[i], begin, count, 0};
-  }
-  if (threadIdx.x < 64) {
-    int experts = 0, pairs = 0;
-    for (int j = threadIdx.x; j < n; j += 64) {
-      pairs += owner[j] != n;
-      experts += owner[j] == j;
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      pairs += __shfl_xor(pairs, d);
-      experts += __shfl_xor(experts, d);
-    }
-    if (threadIdx.x == 0) {
-      plan->experts = experts;
-      plan->pairs = pairs;
-    }
-  }
-  __syncthreads();
-}
-
-// ---------------------------------------------------------------------------
 // Up
 // ---------------------------------------------------------------------------
 
 constexpr int UP_WAVES = 4, UP_THREADS = UP_WAVES * 64;
-constexpr int UP_W_SLOTS = 3, UP_T_SLOTS = 2;  // steps of weights and of tokens in a wave's ring
+constexpr int UP_W_SLOTS = 3;   // steps of weights in a wave's ring
+constexpr int UP_T_BYTES = 12288;  // and bytes of tokens: two steps of 24, three of up to 16
+constexpr int UP_MOST_FOURS = 6;   // most tokens of a pass, in fours
 
 // Tokens' rows of a block come in loads of 4 rows of 256 bytes; their 16-byte pieces
 // are swizzled for the fragment reads, as the weights' are.
@@ -300,25 +242,151 @@ __device__ __forceinline__ int wave_blocks(int wave, int blocks) {
 
 template <bool FP4, int RT>
 using UpWeights = Weights<FP4, 2 * RT, 2>;
-
-// Most tokens of a pass, in fours: what leaves the rings room.
-constexpr int UP_MOST_FOURS = 6;
 template <bool FP4, int RT>
-constexpr int UP_RING = UP_W_SLOTS * UpWeights<FP4, RT>::BYTES + UP_T_SLOTS * UP_MOST_FOURS * 1024;
+constexpr int UP_RING = UP_W_SLOTS * UpWeights<FP4, RT>::BYTES + UP_T_BYTES;
 
-// One pass of an expert's workgroup over its rows with up to 4 FOURS tokens: the
-// waves share K and their sums meet in LDS. The first two steps' weights are already
-// on their way.
+// A barrier that leaves loads on their way: LDS accesses before it are done after it.
+__device__ __forceinline__ void meet() {
+  wait_lgkmcnt_0();
+  barrier();
+}
+
+// Who is where, in LDS.
+struct UpLists {
+  short ids[MAX_FEW_PAIRS];        // each slot's expert, -1: none
+  uint16_t active[MAX_FEW_PAIRS];  // the experts that have slots, in order of their first ones
+  uint16_t list[MAX_FEW_PAIRS];    // the pairs of the expert at hand (and of the plan on its way)
+  int waves_before[UP_WAVES];
+};
+
+// Whether slot i is the first of its token with its expert.
+__device__ __forceinline__ bool first_of_token(const short* ids, int i, int top_k) {
+  const int e = ids[i];
+  for (int j = i - i % top_k; j < i; ++j)
+    if (ids[j] == e) return false;
+  return true;
+}
+
+// Calls put(i, place) for the slots with take(i), in order; returns their number. By the
+// whole workgroup.
+template <class TAKE, class PUT>
+__device__ __forceinline__ int gather(UpLists& l, int n, TAKE&& take, PUT&& put) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int count = 0;
+  for (int i0 = 0; i0 < n; i0 += UP_THREADS) {
+    const bool mine = i0 + tid < n && take(i0 + tid);
+    const uint64_t votes = __ballot(mine);
+    if (lane == 0) l.waves_before[wave] = __popcll(votes);
+    meet();
+    int before = count;
+    for (int w = 0; w < UP_WAVES; ++w) {
+      if (w < wave) before += l.waves_before[w];
+      count += l.waves_before[w];
+    }
+    if (mine) put(i0 + tid, before + __popcll(votes & ((1ull << lane) - 1)));
+    meet();
+  }
+  return __builtin_amdgcn_readfirstlane(count);
+}
+
+// Writes the plan, by one wave: `order` takes each expert's place among the active ones,
+// `next` counts its pairs, both of num_groups ints.
+__device__ void write_plan(const ExpertsArgs& p, const UpLists& l, int experts, int* order, int* next) {
+  ExpertPlan* const plan = reinterpret_cast<ExpertPlan*>(p.plan);
+  const int n = p.tokens * p.top_k, lane = threadIdx.x;
+  for (int r = lane; r < experts; r += 64) {
+    order[l.active[r]] = r;
+    next[l.active[r]] = 0;
+  }
+  wait_lgkmcnt_0();
+  // Each expert's pairs, counted; then where they begin.
+  const int bits = 32 - __builtin_clz(p.num_groups);
+  auto for_pairs = [&](auto&& f) {
+    for (int i0 = 0; i0 < n; i0 += 64) {
+      const int i = i0 + lane, e = i < n ? l.ids[i] : -1;
+      const bool pair = e >= 0 && first_of_token(l.ids, i, p.top_k);
+      uint64_t peers = __ballot(pair);
+      for (int b = 0; b < bits; ++b) {
+        const uint64_t ones = __ballot((e >> b) & 1);
+        peers &= ((e >> b) & 1) ? ones : ~ones;
+      }
+      const int before = pair ? next[e] : 0, rank = __popcll(peers & ((1ull << lane) - 1));
+      wait_lgkmcnt_0();
+      if (pair && rank == 0) next[e] = before + __popcll(peers);
+      wait_lgkmcnt_0();
+      if (pair) f(i, e, before + rank);
+    }
+  };
+  for_pairs([](int, int, int) {});
+  int pairs = 0;
+  for (int r0 = 0; r0 < experts; r0 += 64) {
+    const int r = r0 + lane, e = r < experts ? l.active[r] : 0, has = r < experts ? next[e] : 0;
+    int upto = has;
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(upto, d);
+      if (lane >= d) upto += v;
+    }
+    if (r < experts) {
+      plan->entry[r] = ExpertEntry{e, pairs + upto - has, has, 0};
+      next[e] = pairs + upto - has;
+    }
+    pairs += __shfl(upto, 63);
+  }
+  wait_lgkmcnt_0();
+  for_pairs([&](int i, int e, int at) {
+    float w = 0.0f;
+    const int t0 = i - i % p.top_k;
+    for (int j = t0; j < t0 + p.top_k; ++j)
+      if (l.ids[j] == e) w += p.weights ? p.weights[j] : 1.0f;
+    plan->slot[at] = i;
+    plan->weight[at] = w;
+  });
+  if (lane == 0) {
+    plan->experts = experts;
+    plan->pairs = pairs;
+  }
+}
+
+// The tiles [tile, tile_end) of 16 RT gate rows and as many up rows of one expert, with up
+// to 4 FOURS of its tokens: the waves share K and their sums meet in LDS at a tile's end.
+// The weights go on from one tile to the next; tokens' rows are fetched again, from L2.
 template <bool FP4, int RT, int FOURS, int ROWS>
-__device__ __forceinline__ void up_pass(const ExpertsArgs& p, const UpWeights<FP4, RT>& weights, int f0, int expert,
-                                        int number, const int* slots, int count, uint8_t* lds) {
+__device__ __forceinline__ void up_tiles(const ExpertsArgs& p, UpWeights<FP4, RT>& weights, int tile, int tile_end,
+                                         int expert, int number, const uint16_t* slots, int count, uint8_t* lds) {
   constexpr int NT = (FOURS + 3) / 4, W = UpWeights<FP4, RT>::LOADS, T = FOURS, TILES = 2 * RT;
   constexpr int STEP = UpWeights<FP4, RT>::BYTES, TOKENS = FOURS * 1024;
+  constexpr int T_AHEAD = FOURS <= 4 ? 2 : 1, T_SLOTS = T_AHEAD + 1;
+  static_assert(T_SLOTS * TOKENS <= UP_T_BYTES && TILES * 1024 <= UP_T_BYTES, "tokens, and sums in their place");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   uint8_t* const ring = lds + wave * UP_RING<FP4, RT>;
   const uint32_t base = (uint32_t)(uintptr_t)(lds_void*)ring, token_base = base + UP_W_SLOTS * STEP;
   const __amdgpu_buffer_rsrc_t x = buffer_rsrc(p.x, 0xFFFFFFFFu);
+  const int steps = wave_blocks<FP4>(wave, p.hidden / QBLOCK);
+
+  // The weights' loads: where they are, two steps ahead of the products.
+  int w_tile = tile, w_i = 0, w_next = 0;
+  auto place = [&]() {
+    const int row0[2] = {w_tile * 16 * RT, p.inner + w_tile * 16 * RT};
+    weights.place(expert, row0, lane);
+  };
+  auto load_weights = [&]() {  // (past the last step it is loaded again)
+    weights.load(wave_block<FP4>(wave, w_i), base + w_next * STEP);
+    w_next = w_next == UP_W_SLOTS - 1 ? 0 : w_next + 1;
+    if (w_i + 1 < steps) {
+      ++w_i;
+    } else if (w_tile + 1 < tile_end) {
+      ++w_tile;
+      w_i = 0;
+      place();
+    }
+  };
+  place();
+  if (steps > 0) {
+    load_weights();
+    load_weights();
+  }
+
   uint32_t x_at[FOURS];
 #pragma unroll
   for (int q = 0; q < FOURS; ++q) {
@@ -326,40 +394,55 @@ __device__ __forceinline__ void up_pass(const ExpertsArgs& p, const UpWeights<FP
     x_at[q] = (uint32_t)(slots[min(row, count - 1)] / p.top_k) * (uint32_t)(p.hidden * 2) +
               (uint32_t)((r ^ token_swizzle(row & 15)) << 4);
   }
-  uint32_t read_at[NT];  // of the lane's token, piece 0
-  uint32_t swizzle[NT];
+  uint32_t read_at[NT], swizzle[NT];  // of the lane's token
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int rows = min(FOURS * 4 - nt * 16, 16), row = nt * 16 + (r & (rows - 1));  // 4, 8 or 16 rows: others repeat
     read_at[nt] = row * 256;
     swizzle[nt] = token_swizzle(row & 15);
   }
-  auto load_tokens = [&](int block, int slot) {
+  const int act_tiles[2] = {act_tile(p, expert, number, slots[0]),
+                            NT > 1 && count > 16 ? act_tile(p, expert, number + 1, slots[16]) : 0};
+  int t_next = 0;
+  auto load_tokens = [&](int i) {
+    const int block = wave_block<FP4>(wave, i);
 #pragma unroll
-    for (int q = 0; q < FOURS; ++q) dma16(x, x_at[q], (uint32_t)block * 256, token_base + slot * TOKENS + q * 1024);
+    for (int q = 0; q < FOURS; ++q) dma16(x, x_at[q], (uint32_t)block * 256, token_base + t_next * TOKENS + q * 1024);
+    t_next = t_next == T_SLOTS - 1 ? 0 : t_next + 1;
   };
 
-  f32x4 acc[TILES][NT];
+  int w_slot = 0;
+  for (; tile < tile_end; ++tile) {
+    f32x4 acc[TILES][NT];
 #pragma unroll
-  for (int i = 0; i < TILES; ++i)
+    for (int i = 0; i < TILES; ++i)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) acc[i][nt] = (f32x4){0.f, 0.f, 0.f, 0.f};
-
-  const int steps = wave_blocks<FP4>(wave, p.hidden / QBLOCK), last = max(steps - 1, 0);
-  auto block = [&](int i) { return wave_block<FP4>(wave, min(i, last)); };
-  if (steps > 0) {
-    load_tokens(block(0), 0);
-    int w_slot = 0, w_next = 2;
+      for (int nt = 0; nt < NT; ++nt) acc[i][nt] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    int t_slot = 0;
+    t_next = 0;
+#pragma unroll
+    for (int i = 0; i < T_AHEAD; ++i)
+      if (i < steps) load_tokens(i);
     for (int i = 0; i < steps; ++i) {
       before_loads();
-      load_tokens(block(i + 1), (i + 1) & 1);
-      weights.load(block(i + 2), base + w_next * STEP);
-      // What follows this step's loads: one step's tokens and two steps' weights (first:
-      // its tokens came after the second step's weights).
-      if (i == 0) wait_loads<T + W>();
-      else wait_loads<T + 2 * W>();
+      const bool more = i + T_AHEAD < steps;
+      if (more) load_tokens(i + T_AHEAD);
+      load_weights();
+      // What may still be on its way: the next two steps' weights (at a tile's first step,
+      // whose tokens came after the second one's weights, one step's), and the tokens of the
+      // steps after this.
+      const int tokens_after = more ? T_AHEAD : steps - 1 - i;
+      if (i == 0) {
+        if (tokens_after == 0) wait_loads<W>();
+        else if (tokens_after == 1) wait_loads<W + T>();
+        else wait_loads<W + T_AHEAD * T>();
+      } else {
+        if (tokens_after == 0) wait_loads<2 * W>();
+        else if (tokens_after == 1) wait_loads<2 * W + T>();
+        else wait_loads<2 * W + T_AHEAD * T>();
+      }
       const uint8_t* const st = ring + w_slot * STEP;
-      const uint8_t* const tok = ring + UP_W_SLOTS * STEP + (i & 1) * TOKENS;
+      const uint8_t* const tok = ring + UP_W_SLOTS * STEP + t_slot * TOKENS;
       u32x4 t[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -371,107 +454,91 @@ __device__ __forceinline__ void up_pass(const ExpertsArgs& p, const UpWeights<FP
 #pragma unroll
       for (int k = 0; k < TILES; ++k) weights.template multiply<NT>(acc[k], st, k, t, lane);
       w_slot = w_slot == UP_W_SLOTS - 1 ? 0 : w_slot + 1;
-      w_next = w_next == UP_W_SLOTS - 1 ? 0 : w_next + 1;
+      t_slot = t_slot == T_SLOTS - 1 ? 0 : t_slot + 1;
     }
-  }
 
-  // The waves' sums, in the rings' place.
-  constexpr int UNITS = TILES * NT;
-  static_assert(UP_WAVES * UNITS * 1024 <= UP_WAVES * UP_RING<FP4, RT>, "sums in the rings' place");
-  f32x4* const red = reinterpret_cast<f32x4*>(lds);
-  wait_loads<0>();
-  __syncthreads();
+    // The waves' sums, in the tokens' place, 16 tokens at a time.
+    static_for<0, NT>([&](auto N) {
+      constexpr int nt = decltype(N)::value;
+      auto sums_of = [&](int w) { return reinterpret_cast<f32x4*>(lds + w * UP_RING<FP4, RT> + UP_W_SLOTS * STEP); };
+      meet();  // every wave has read its tokens, and the sums before these
 #pragma unroll
-  for (int i = 0; i < TILES; ++i)
+      for (int i = 0; i < TILES; ++i) sums_of(wave)[i * 64 + lane] = acc[i][nt];
+      meet();
+      for (int i = wave; i < RT; i += UP_WAVES) {
+        f32x4 gate = sums_of(0)[i * 64 + lane], up = sums_of(0)[(RT + i) * 64 + lane];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) red[(wave * UNITS + i * NT + nt) * 64 + lane] = acc[i][nt];
-  __syncthreads();
-  const int tile = act_tile(p, expert, number, slots[0]), tile2 = NT > 1 && count > 16 ? act_tile(p, expert, number + 1, slots[16]) : 0;
-  for (int unit = wave; unit < RT * NT; unit += UP_WAVES) {
-    f32x4 gate = red[unit * 64 + lane], up = red[(RT * NT + unit) * 64 + lane];
+        for (int w = 1; w < UP_WAVES; ++w) {
+          gate += sums_of(w)[i * 64 + lane];
+          up += sums_of(w)[(RT + i) * 64 + lane];
+        }
+        f32x4 a;
 #pragma unroll
-    for (int w = 1; w < UP_WAVES; ++w) {
-      gate += red[(w * UNITS + unit) * 64 + lane];
-      up += red[(w * UNITS + RT * NT + unit) * 64 + lane];
-    }
-    f32x4 a;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = gate[i] * sigmoid(gate[i]) * up[i];
-    const int i = unit / NT, nt = unit % NT;
-    if (nt * 16 + r < count) {
-      const u32x2 packed = {pack2((f32x2){a[0], a[1]}), pack2((f32x2){a[2], a[3]})};
-      uint16_t* const at = p.act + (size_t)(nt ? tile2 : tile) * ROWS * p.inner;
-      *reinterpret_cast<u32x2*>(at + act_at<FP4, ROWS>(f0 + 16 * i + 4 * g, r)) = packed;
-    }
+        for (int k = 0; k < 4; ++k) a[k] = gate[k] * sigmoid(gate[k]) * up[k];
+        if (nt * 16 + r < count) {
+          const u32x2 packed = {pack2((f32x2){a[0], a[1]}), pack2((f32x2){a[2], a[3]})};
+          uint16_t* const at = p.act + (size_t)act_tiles[nt] * ROWS * p.inner;
+          *reinterpret_cast<u32x2*>(at + act_at<FP4, ROWS>(tile * 16 * RT + 16 * i + 4 * g, r)) = packed;
+        }
+      }
+    });
+    meet();  // the sums have been read: tokens may come
   }
-  __syncthreads();  // the sums have been read: the rings are free
+  wait_loads<0>();  // (the last step's weights once more)
+  meet();
 }
 
-// A workgroup takes 16 RT gate rows and as many up rows of one expert: an expert by its
-// number, or with no more slots than experts the expert of a slot that is the first to
-// name it. The first one makes the plan as well.
+// The tiles of all experts that have tokens, in order, are dealt to the workgroups in
+// runs of the same length. The first workgroup writes the plan as well.
 template <bool FP4, int RT, int ROWS>
 __global__ __launch_bounds__(UP_THREADS, 1) void experts_up_kernel(ExpertsArgs p) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[UP_WAVES * UP_RING<FP4, RT>];
-  __shared__ int ids[MAX_FEW_PAIRS];
-  __shared__ int list[MAX_FEW_PAIRS];  // the plan's owners; then the expert's slots
-  __shared__ int waves_before[UP_WAVES];
+  __shared__ UpLists l;
+  static_assert(UP_WAVES * UP_RING<FP4, RT> >= 2 * MAX_GROUPS * 4, "the tables of groups in the rings' place");
   const int n = p.tokens * p.top_k, tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int tiles = p.inner / (16 * RT), item = blockIdx.x / tiles, f0 = blockIdx.x % tiles * 16 * RT;
-  const bool by_slot = n <= p.num_groups;
-  const int e = __builtin_amdgcn_readfirstlane(by_slot ? p.ids[item] : item);
-  const bool named = e >= 0 && e < p.num_groups;
-  const int row0[2] = {f0, p.inner + f0};
-  const UpWeights<FP4, RT> weights(p.b1, p.sfb1, named ? e : 0, 2 * p.inner, p.hidden, row0, lane);
-  const int steps = wave_blocks<FP4>(wave, p.hidden / QBLOCK), last = max(steps - 1, 0);
-  const uint32_t base = (uint32_t)(uintptr_t)(lds_void*)(lds + wave * UP_RING<FP4, RT>);
-  auto first_weights = [&]() {  // (a wave without steps loads blocks that nobody reads)
-    if (steps == 0) return;
-    weights.load(wave_block<FP4>(wave, 0), base);
-    weights.load(wave_block<FP4>(wave, min(1, last)), base + UpWeights<FP4, RT>::BYTES);
-  };
-  if (named) first_weights();
+  int* const first = reinterpret_cast<int*>(lds);  // of each group's slots
+  for (int i = tid; i < n; i += UP_THREADS) {
+    const int e = p.ids[i];
+    l.ids[i] = (short)(e >= 0 && e < p.num_groups ? e : -1);
+  }
+  for (int e = tid; e < p.num_groups; e += UP_THREADS) first[e] = n;
+  meet();
+  for (int i = tid; i < n; i += UP_THREADS)
+    if (l.ids[i] >= 0) atomicMin(&first[l.ids[i]], i);
+  meet();
+  const int experts = gather(l, n, [&](int i) { return l.ids[i] >= 0 && first[l.ids[i]] == i; },
+                             [&](int i, int at) { l.active[at] = (uint16_t)l.ids[i]; });
+  if (blockIdx.x == 0) {
+    if (tid < 64) write_plan(p, l, experts, first, first + MAX_GROUPS);
+    meet();
+  }
 
-  for (int i = tid; i < n; i += UP_THREADS) ids[i] = p.ids[i];
-  __syncthreads();
-  if (blockIdx.x == 0) build_plan<UP_THREADS>(p, reinterpret_cast<ExpertPlan*>(p.plan), ids, list);
-  if (!named) return;
-  // The expert's slots in order, counted 256 at a time.
-  int count = 0;
-  bool earlier = false;
-  for (int i0 = 0; i0 < n; i0 += UP_THREADS) {
-    const int i = i0 + tid;
-    const bool mine = i < n && ids[i] == e;
-    const bool take = mine && first_of_token(ids, i, p.top_k);
-    earlier |= mine && by_slot && i < item;
-    const uint64_t votes = __ballot(take);
-    if (lane == 0) waves_before[wave] = __popcll(votes);
-    __syncthreads();
-    int before = count;
-    for (int w = 0; w < UP_WAVES; ++w) {
-      if (w < wave) before += waves_before[w];
-      count += waves_before[w];
+  const int tiles = p.inner / (16 * RT), all = experts * tiles;  // at most 2^22
+  const int grid = gridDim.x, share = all / grid, more = all % grid, b = blockIdx.x;
+  int at = b * share + min(b, more);
+  const int end = at + share + (b < more);
+  UpWeights<FP4, RT> weights(p.b1, p.sfb1, 2 * p.inner, p.hidden, lane);
+  while (at < end) {
+    const int expert = __builtin_amdgcn_readfirstlane((int)l.active[at / tiles]);
+    const int tile = at % tiles, tile_end = min(tile + end - at, tiles);
+    at += tile_end - tile;
+    const int count = gather(l, n, [&](int i) { return l.ids[i] == expert && first_of_token(l.ids, i, p.top_k); },
+                             [&](int i, int place) { l.list[place] = (uint16_t)i; });
+    // The tokens 16 at a time, the last 17 to 24 at once.
+    for (int t0 = 0; t0 < count;) {
+      const int left = count - t0, here = left <= 4 * UP_MOST_FOURS ? left : 16;
+      const uint16_t* const slots = l.list + t0;
+      if constexpr (ROWS == 4) {
+        up_tiles<FP4, RT, 1, ROWS>(p, weights, tile, tile_end, expert, t0 / 16, slots, here, lds);
+      } else {
+        if (here <= 4) up_tiles<FP4, RT, 1, ROWS>(p, weights, tile, tile_end, expert, t0 / 16, slots, here, lds);
+        else if (here <= 8) up_tiles<FP4, RT, 2, ROWS>(p, weights, tile, tile_end, expert, t0 / 16, slots, here, lds);
+        else if (here <= 16) up_tiles<FP4, RT, 4, ROWS>(p, weights, tile, tile_end, expert, t0 / 16, slots, here, lds);
+        else up_tiles<FP4, RT, 6, ROWS>(p, weights, tile, tile_end, expert, t0 / 16, slots, here, lds);
+      }
+      t0 += here;
     }
-    if (take) list[before + __popcll(votes & ((1ull << lane) - 1))] = i;
-    __syncthreads();
   }
-  const bool none = __syncthreads_or(earlier) || count == 0;
-  // The tokens 16 at a time, the last 17 to 24 at once.
-  for (int t0 = 0; !none && t0 < count;) {
-    const int left = count - t0, here = left <= 4 * UP_MOST_FOURS ? left : 16;
-    if (t0 > 0) first_weights();
-    if constexpr (ROWS == 4) {
-      up_pass<FP4, RT, 1, ROWS>(p, weights, f0, e, t0 / 16, list + t0, here, lds);
-    } else {
-      if (here <= 4) up_pass<FP4, RT, 1, ROWS>(p, weights, f0, e, t0 / 16, list + t0, here, lds);
-      else if (here <= 8) up_pass<FP4, RT, 2, ROWS>(p, weights, f0, e, t0 / 16, list + t0, here, lds);
-      else if (here <= 16) up_pass<FP4, RT, 4, ROWS>(p, weights, f0, e, t0 / 16, list + t0, here, lds);
-      else up_pass<FP4, RT, 6, ROWS>(p, weights, f0, e, t0 / 16, list + t0, here, lds);
-    }
-    t0 += here;
-  }
-  wait_loads<0>();  // no wave may end while a load can still write its LDS
 }
 
 // ---------------------------------------------------------------------------
@@ -577,7 +644,8 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
     Cursor ahead{}, now{};
     start(now);
     const int first = start(ahead);
-    DownWeights<FP4> weights(p.b2, p.sfb2, first, p.hidden, p.inner, row0, lane);
+    DownWeights<FP4> weights(p.b2, p.sfb2, p.hidden, p.inner, lane);
+    weights.place(first, row0, lane);
     const uint16_t* act = p.act + (size_t)ahead.tile * ROWS * p.inner;
     const uint32_t act_lane = (uint32_t)(g * ROWS + (r & (ROWS - 1))) * 8;
     f32x4 acc[DOWN_RT][1] = {};
@@ -591,7 +659,7 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
       if (++loaded < steps && ++ahead.block == ahead.end) {  // (past the last step it is loaded again)
         ++ahead.turn;
         const int e = start(ahead);
-        weights = DownWeights<FP4>(p.b2, p.sfb2, e, p.hidden, p.inner, row0, lane);
+        weights.place(e, row0, lane);
         act = p.act + (size_t)ahead.tile * ROWS * p.inner;
       }
     };
@@ -648,7 +716,7 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
 
 template <bool FP4, int RT, int ROWS>
 hipError_t launch_up(const ExpertsArgs& a, hipStream_t stream) {
-  const int workgroups = std::min(a.tokens * a.top_k, a.num_groups) * (a.inner / (16 * RT));
+  const int workgroups = std::min(std::min(a.tokens * a.top_k, a.num_groups) * (a.inner / (16 * RT)), a.cus);
   hipLaunchKernelGGL((experts_up_kernel<FP4, RT, ROWS>), dim3(workgroups), dim3(UP_THREADS), 0, stream, a);
   return hipGetLastError();
 }
@@ -658,7 +726,7 @@ template <bool FP4, int ROWS>
 hipError_t launch_both(const ExpertsArgs& a, hipStream_t stream) {
   constexpr int RT = FP4 ? 4 : 2;
   // Half as many rows a workgroup where there would not be one for every compute unit.
-  const bool few = std::min(a.tokens * a.top_k, a.num_groups) * (a.inner / (16 * RT)) < 256;
+  const bool few = std::min(a.tokens * a.top_k, a.num_groups) * (a.inner / (16 * RT)) < a.cus;
   if (hipError_t e = few ? launch_up<FP4, RT / 2, ROWS>(a, stream) : launch_up<FP4, RT, ROWS>(a, stream)) return e;
   void (*down)(ExpertsArgs);
   if constexpr (ROWS == 4) down = experts_down_kernel<FP4, ROWS, 4>;

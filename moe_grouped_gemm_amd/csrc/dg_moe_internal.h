@@ -68,6 +68,7 @@ struct ExpertsArgs {
   void* plan;            // EXPERT_PLAN_BYTES
   uint16_t* act;         // experts_act_bytes()
   int fp4, tokens, top_k, num_groups, hidden, inner;
+  int cus;               // compute units to spread over
 };
 // Grows with tokens.
 long long experts_act_bytes(int tokens, int top_k, int num_groups, int inner);
