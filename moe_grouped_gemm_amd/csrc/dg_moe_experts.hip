@@ -145,14 +145,16 @@ struct Weights {
 #pragma unroll
     for (int i = 0; i < GROUPS; ++i) rows[i] = buffer_rsrc(w + (size_t)row0[i] * row_bytes, 0xFFFFFFFFu);
     scales = buffer_rsrc(sf + (size_t)e * (FP4 ? values / QBLOCK : values / QBLOCK / 128), 0xFFFFFFFFu);
+    // (By value: a choice between the array's elements would put it in memory.)
+    const int run0 = row0[0], run1 = row0[GROUPS - 1];
     if constexpr (FP4) {
 #pragma unroll
       for (int q = 0; q < SCALE_LOADS; ++q) {
         const int tile = min(4 * q + (lane >> 4), TILES - 1), group = tile / PER_GROUP;
-        sf_at[q] = ((GROUPS == 2 && group ? row0[GROUPS - 1] : row0[0]) + (tile - group * PER_GROUP) * 16 + (lane & 15)) * 4;
+        sf_at[q] = ((group ? run1 : run0) + (tile - group * PER_GROUP) * 16 + (lane & 15)) * 4;
       }
     } else {
-      sf_at[0] = (GROUPS == 2 && (lane & 1) ? row0[GROUPS - 1] : row0[0]) / 128 * (k / QBLOCK) * 4;
+      sf_at[0] = (lane & 1 ? run1 : run0) / 128 * (k / QBLOCK) * 4;
     }
   }
 
