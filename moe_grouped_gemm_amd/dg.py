@@ -365,51 +365,96 @@ def k_grouped_fp8_gemm_nt_contiguous(a, sfa, b, sfb, d, ks, c=None, ue8m0: bool 
 # FP4: E2M1 values with one power-of-two scale per 32 (MXFP4)
 # ---------------------------------------------------------------------------
 
-def _fp4_operand(q, sf, name: str, ndim: int, dev):
-    """(rows, k) of packed codes [..., rows, k/2] uint8 with their scale words
-    [..., k/128, tma_aligned(rows)] int32."""
-    _need(q, name, torch.uint8, ndim, dev)
-    _need(sf, "sf" + name, torch.int32, ndim, dev)
-    *lead, rows, half = q.shape
-    k = 2 * half
-    if k % 128:
-        raise ValueError(f"{name}: k must be a multiple of 128")
-    if any(size >= 2 ** 31 for size in q.shape):  # (the library's sizes are ints)
+def _is(t, dtype, shape, index: int) -> bool:
+    """Whether t is a contiguous tensor of that type and shape on that GPU: the
+    cheapest way to ask (a decode step's calls take a few microseconds each)."""
+    try:
+        return t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
+    except AttributeError:
+        return False
+
+
+_U8, _I32 = torch.uint8, torch.int32
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call(name: str, index: int, *args) -> None:
+    """Calls an entry point on device `index`'s current stream, with that device current."""
+    entry = getattr(lib(), name)
+    if _current_device() == index and _raw_stream is not None:
+        status = entry(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = entry(*args, torch.cuda.current_stream(index).cuda_stream)
+    if status:
+        _check(status, name)
+
+
+def _refuse_fp4(q, sf, name: str, shape, dev) -> None:
+    """Says what is wrong with an FP4 operand of `shape` values [..., rows, k]."""
+    _need(q, name, _U8, len(shape), dev)
+    _need(sf, "sf" + name, _I32, len(shape), dev)
+    *lead, rows, k = shape
+    if k % 128 or not k:
+        raise ValueError(f"{name}: k must be a multiple of 128, got {k}")
+    if tuple(q.shape) != (*lead, rows, k // 2):
+        raise ValueError(f"{name} must have shape {(*lead, rows, k // 2)}, got {tuple(q.shape)}")
+    raise ValueError(f"sf{name} must have shape {(*lead, k // 128, (rows + 3) // 4 * 4)}, got {tuple(sf.shape)}")
+
+
+def _want_fp4(q, sf, name: str, shape, index: int) -> None:
+    """Checks packed codes [..., rows, k/2] uint8 with their scale words [..., k/128,
+    tma_aligned(rows)] int32."""
+    *lead, rows, k = shape
+    if k % 128 or not _is(q, _U8, (*lead, rows, k // 2), index) \
+            or not _is(sf, _I32, (*lead, k // 128, (rows + 3) // 4 * 4), index):
+        _refuse_fp4(q, sf, name, shape, _device(index))
+    if rows >= 2 ** 31:  # (the library's sizes are ints)
         raise ValueError(f"{name}: sizes past 32 bits")
-    want = (*lead, k // 128, get_tma_aligned_size(rows, 4))
-    if tuple(sf.shape) != want:
-        raise ValueError(f"sf{name} must have shape {want}, got {tuple(sf.shape)}")
-    return rows, k
+
+
+def _device(index: int) -> torch.device:
+    return torch.device("cuda", index) if index >= 0 else torch.device("cuda")
+
+
+def _codes_of(q, name: str, ndim: int):
+    """(device index, shape of the values) of an operand's codes."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if q.dim() != ndim or q.get_device() < 0:
+        _need(q, name, _U8, ndim, _device(-1))
+    *lead, half = q.shape
+    return q.get_device(), (*lead, 2 * half)
 
 
 def _fp4_gemm(name, a, sfa, b, sfb, d, rows=None, masked=False):
-    dev = a.device
-    m, k = _fp4_operand(a, sfa, "a", 3 if masked else 2, dev)
-    n, kb = _fp4_operand(b, sfb, "b", 2 if rows is None else 3, dev)
-    _need(d, "d", torch.bfloat16, a.dim(), dev)
-    if kb != k or tuple(d.shape) != (*a.shape[:-1], n):
-        raise ValueError("shape mismatch between a, b and d")
-    if n % 128:
-        raise ValueError("n must be a multiple of 128")
-    args = [a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), d.data_ptr()]
+    index, shape_a = _codes_of(a, "a", 3 if masked else 2)
+    _, shape_b = _codes_of(b, "b", 2 if rows is None else 3)
+    *lead, m, k = shape_a
+    n = shape_b[-2]
+    _want_fp4(a, sfa, "a", shape_a, index)
+    _want_fp4(b, sfb, "b", shape_b, index)
+    if shape_b[-1] != k or n % 128:
+        raise ValueError("a and b differ in k" if shape_b[-1] != k else "n must be a multiple of 128")
+    if not _is(d, torch.bfloat16, (*lead, m, n), index):
+        _need(d, "d", torch.bfloat16, len(shape_a), _device(index))
+        raise ValueError(f"d must have shape {(*lead, m, n)}, got {tuple(d.shape)}")
+    args = (a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), d.data_ptr())
     if rows is None:
-        sizes = (m, n, k)
+        args += (m, n, k)
     else:
-        _need(rows, "the layout's rows", torch.int32, 1, dev)
-        g = b.shape[0]
-        if masked and a.shape[0] != g:
+        g = shape_b[0]
+        if masked and lead != [g]:
             raise ValueError("a and b differ in groups")
-        if rows.shape[0] != (m if name.endswith("contiguous") else g):
+        if not _is(rows, _I32, (m if name.endswith("contiguous") else g,), index):
+            _need(rows, "the layout's rows", _I32, 1, _device(index))
             raise ValueError("the layout's rows have the wrong length")
-        args.append(rows.data_ptr())
-        sizes = (g, m, n, k) if masked else (m, n, k, g)
-    if not d.numel():  # nothing to compute, and empty tensors have no address
-        return d
-    _check(getattr(lib(), name)(*args, *sizes, _stream(a)), name)
+        args += (rows.data_ptr(), g, m, n, k) if masked else (rows.data_ptr(), m, n, k, g)
+    if d.numel():  # else nothing to compute, and empty tensors have no address
+        _call(name, index, *args)
     return d
 
 
-@_on_its_device
 def fp4_gemm_nt(a, sfa, b, sfb, d) -> torch.Tensor:
     """d[m, n] = bf16(sum_k a[m,k] sfa[m,k/32] * b[n,k] sfb[n,k/32]) of FP4 values.
 
@@ -420,14 +465,12 @@ def fp4_gemm_nt(a, sfa, b, sfb, d) -> torch.Tensor:
     return _fp4_gemm("dg_fp4_gemm_nt", a, sfa, b, sfb, d)
 
 
-@_on_its_device
 def m_grouped_fp4_gemm_nt_contiguous(a, sfa, b, sfb, d, grouped_layout) -> torch.Tensor:
     """Contiguous-layout grouped FP4 GEMM; grouped_layout [M] int32 holds each
     row's group (-1 for padding). b [G, N, K/2], sfb [G, K/128, tma_aligned(N)]."""
     return _fp4_gemm("dg_m_grouped_fp4_gemm_nt_contiguous", a, sfa, b, sfb, d, grouped_layout)
 
 
-@_on_its_device
 def m_grouped_fp4_gemm_nt_masked(a, sfa, b, sfb, d, masked_m) -> torch.Tensor:
     """Masked-layout grouped FP4 GEMM; masked_m [G] int32 (device) holds each
     group's valid rows. a [G, max_m, K/2], sfa [G, K/128, tma_aligned(max_m)],
@@ -435,28 +478,11 @@ def m_grouped_fp4_gemm_nt_masked(a, sfa, b, sfb, d, masked_m) -> torch.Tensor:
     return _fp4_gemm("dg_m_grouped_fp4_gemm_nt_masked", a, sfa, b, sfb, d, masked_m, masked=True)
 
 
-@_on_its_device
 def m_grouped_fp4_gemm_nt_nopad(a, sfa, b, sfb, d, group_rows) -> torch.Tensor:
     """No-padding grouped FP4 GEMM; group_rows [G] int32 (device) holds each
     group's row count, the groups' rows following one another from row 0 of a.
     b [G, N, K/2], sfb [G, K/128, tma_aligned(N)]."""
     return _fp4_gemm("dg_m_grouped_fp4_gemm_nt_nopad", a, sfa, b, sfb, d, group_rows)
-
-
-def _fp4_rows(x, q, sf, types, first):
-    """(groups, rows, k) of rows x [rows, k] or [groups, rows, k] and their FP4
-    operand, on the device of the call's first tensor."""
-    if not isinstance(x, torch.Tensor) or not isinstance(q, torch.Tensor):
-        raise TypeError("x and q must be torch.Tensors")
-    if x.dtype not in types:
-        raise TypeError(f"x must be {' or '.join(map(str, types))}, got {x.dtype}")
-    if first.dim() not in (2, 3):
-        raise ValueError(f"rows have 2 or 3 dims, got shape {tuple(first.shape)}")
-    _need(x, "x", x.dtype, first.dim(), first.device)
-    rows, k = _fp4_operand(q, sf, "q", first.dim(), first.device)
-    if tuple(x.shape) != (*q.shape[:-1], k):
-        raise ValueError("shape mismatch between x and q")
-    return (x.shape[0] if x.dim() == 3 else 1), rows, k
 
 
 def quantize_fp4(x, q, sf):
@@ -465,28 +491,29 @@ def quantize_fp4(x, q, sf):
     Per 32 values one scale, the smallest power of two not below amax / 6; codes
     round to the nearest value, ties to the even code. An infinity or NaN makes its
     32 values NaN. Words of sf past the last row are not written."""
-    return _quantize_fp4(x, q, sf)
+    if not isinstance(x, torch.Tensor) or not isinstance(q, torch.Tensor):
+        raise TypeError("x and q must be torch.Tensors")
+    if x.dtype is not torch.bfloat16 and x.dtype is not torch.float32:
+        raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
+    shape, index = x.shape, x.get_device()
+    if not 2 <= len(shape) <= 3 or index < 0 or not x.is_contiguous():
+        _need(x, "x", x.dtype, 3 if len(shape) != 2 else 2, _device(index))
+    _want_fp4(q, sf, "q", shape, index)
+    _call("dg_quantize_fp4", index, x.data_ptr(), x.dtype is torch.float32, q.data_ptr(), sf.data_ptr(),
+          shape[0] if len(shape) == 3 else 1, *shape[-2:])
+    return q, sf
 
 
 def dequantize_fp4(q, sf, x) -> torch.Tensor:
     """The values that an FP4 operand (q, sf as quantize_fp4 makes them) stands
     for, into x [M, K] (or [G, M, K]) bfloat16."""
-    return _dequantize_fp4(q, sf, x)
-
-
-@_on_its_device
-def _quantize_fp4(x, q, sf):
-    groups, rows, k = _fp4_rows(x, q, sf, (torch.bfloat16, torch.float32), x)
-    _check(lib().dg_quantize_fp4(x.data_ptr(), int(x.dtype is torch.float32), q.data_ptr(), sf.data_ptr(), groups,
-                                 rows, k, _stream(x)), "dg_quantize_fp4")
-    return q, sf
-
-
-@_on_its_device
-def _dequantize_fp4(q, sf, x):
-    groups, rows, k = _fp4_rows(x, q, sf, (torch.bfloat16,), q)
-    _check(lib().dg_dequantize_fp4(q.data_ptr(), sf.data_ptr(), x.data_ptr(), groups, rows, k, _stream(q)),
-           "dg_dequantize_fp4")
+    index, shape = _codes_of(q, "q", 3 if isinstance(q, torch.Tensor) and q.dim() == 3 else 2)
+    _want_fp4(q, sf, "q", shape, index)
+    if not _is(x, torch.bfloat16, shape, index):
+        _need(x, "x", torch.bfloat16, len(shape), _device(index))
+        raise ValueError(f"x must have shape {shape}, got {tuple(x.shape)}")
+    _call("dg_dequantize_fp4", index, q.data_ptr(), sf.data_ptr(), x.data_ptr(), shape[0] if len(shape) == 3 else 1,
+          *shape[-2:])
     return x
 
 
