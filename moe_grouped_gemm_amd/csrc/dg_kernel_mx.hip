@@ -4,10 +4,18 @@
 //   D[m][n] = bf16( sum_k e2m1(A[m][k]) 2^(ea[m][k/32] - 127) * e2m1(B[n][k]) 2^(eb[n][k/32] - 127) )
 //
 // v_mfma_scale_f32_16x16x128_f8f6f4 takes packed E2M1 for both operands: lane
-// group g = lane / 16 holds K positions 32g .. 32g + 31 of row lane % 16 (16
-// bytes, even k in the low nibble), which are one scale block, and applies the
-// block's two scales itself. Its float32 accumulator holds the sums: no step of
-// the kernel's own follows the products but the one rounding to BF16.
+// group g = lane / 16 holds 32 successive values of row lane % 16 (16 bytes, even
+// k in the low nibble), which are one scale block, and applies the block's two
+// scales itself: a byte of the lane's scale register, the same byte in all lanes.
+// Its float32 accumulator holds the sums: no step of the kernel's own follows the
+// products but the one rounding to BF16.
+//
+// Which 32 values a group holds is free as long as both operands hold the same. Of a
+// step's 256 the j-th of two MFMAs (j = 0, 1) takes blocks 2g + j: a group's two
+// blocks have two successive bytes of one scale word, and a 16-bit read per 16 rows
+// gives the lanes all that both MFMAs need, byte j of it for the j-th. (With the j-th
+// MFMA on blocks 4j + g every lane would need another byte of its word: a transpose
+// between lanes, 36 instructions a step, that cost 8% of the time.)
 //
 // A persistent kernel over 256 x 256 tiles; a K step is 256 values, 128-byte rows of
 // either operand, in one of two LDS stages that direct-to-LDS loads fill one to two
@@ -25,11 +33,15 @@ struct Cfg {
   static constexpr int WM = 128, WN = 64, MT = WM / 16, NT = WN / 16;
 };
 constexpr int STEP_BLOCKS = 2;                          // 128-value blocks of K a step: 128-byte rows
-constexpr int A_BYTES = Cfg::BM * ROW_BYTES;            // 32 KB
+// LDS of a stage, in two buffers that are refilled at different times (see the K loop):
+// HIGH the later halves of the two wave rows' A rows (64 .. 127 and 192 .. 255), LOW all
+// else.
+enum { LOW = 0, HIGH = 1 };
+constexpr int A_HALF = Cfg::BM / 2 * ROW_BYTES;         // 16 KB
 constexpr int B_BYTES = Cfg::BN * ROW_BYTES;            // 32 KB
-constexpr int SA_OFF = A_BYTES + B_BYTES;               // [block of the step][256] LHS scale words
+constexpr int SA_OFF = A_HALF + B_BYTES;                // [128 values of the step][4][16][4] LHS scale words: row 64 i + 16 j + r at [i][r][j]
 constexpr int SB_OFF = SA_OFF + STEP_BLOCKS * Cfg::BM * 4;
-constexpr int STAGE_BYTES = SB_OFF + STEP_BLOCKS * Cfg::BN * 4;
+constexpr int LOW_BYTES = SB_OFF + STEP_BLOCKS * Cfg::BN * 4;
 static_assert(Cfg::NW == 8 && Cfg::BM == 256 && Cfg::BN == 256, "load split below");
 
 }  // namespace mx
@@ -39,15 +51,16 @@ constexpr int A_PACK_SHIFT<mx::Cfg> = 1;
 
 namespace mx {
 
-// One LDS buffer per stage, and its byte address.
-template <int S>
+// An LDS buffer of its own for each stage and half (the compiler makes a read wait for
+// the loads in flight into the buffer that it reads, and only for those).
+template <int S, int PART>
 __device__ __forceinline__ uint8_t* stage_buf() {
-  __shared__ __attribute__((aligned(1024))) uint8_t buf[STAGE_BYTES];
+  __shared__ __attribute__((aligned(1024))) uint8_t buf[PART == LOW ? LOW_BYTES : A_HALF];
   return buf;
 }
-template <int S>
+template <int S, int PART>
 __device__ __forceinline__ uint32_t stage_addr() {
-  return (uint32_t)(uintptr_t)(lds_void*)stage_buf<S>();
+  return (uint32_t)(uintptr_t)(lds_void*)stage_buf<S, PART>();
 }
 
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t lds_base) {
@@ -66,9 +79,11 @@ struct LaneOffsets {
 __device__ __forceinline__ LaneOffsets lane_offsets(int k, int wave, int lane) {
   LaneOffsets o;
   const int row0 = wave * 8 + (lane >> 3);
-  o.ab = (uint32_t)row0 * ((uint32_t)k / 2) + (uint32_t)(((lane & 7) ^ ((row0 >> 1) & 7)) * 16);  // the same for every j
+  // Of the row's eight 16-byte blocks 2g + j lies where lds_offset() has chunk g + 4j.
+  const int chunk = (lane & 7) ^ ((row0 >> 1) & 7);  // the same for every j
+  o.ab = (uint32_t)row0 * ((uint32_t)k / 2) + (uint32_t)((chunk & 3) * 2 + (chunk >> 2)) * 16u;
   o.ab_step = 64u * ((uint32_t)k / 2);
-  o.sc = (uint32_t)(64 * (wave & 3) + lane) * 4u;
+  o.sc = (uint32_t)(64 * (wave & 3) + (lane & 3) * 16 + (lane >> 2)) * 4u;
   return o;
 }
 
@@ -132,163 +147,154 @@ __device__ __forceinline__ StageSrc refill_src(const GemmArgs& p, const TileSrc&
   return stage_src(p, t, in0 ? ahead : (in1 ? ahead - steps : ahead - 2 * steps), wave);
 }
 
-// The loads of one step into stage S, in four parts (see the K loop): 0 and 1 the A
-// tile, 2 and 3 the B tile, 3 also the scale words.
+// The loads of one step into stage S: 0 and 1 the B tile, 2 the LOW half of the A tile,
+// 3 the scale words, 4 the HIGH half of the A tile; two instructions of a wave each.
+constexpr int LOW_LOADS = 8, HIGH_LOADS = 2;
 template <int S, int PART>
 __device__ __forceinline__ void issue_part(const StageSrc& r, int wave, const LaneOffsets& lo) {
-  const uint32_t st = stage_addr<S>();
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int j = PART % 2 * 2 + i;
-    dma16(PART < 2 ? r.a : r.b, lo.ab + j * lo.ab_step, st + (PART < 2 ? 0 : A_BYTES) + (j * Cfg::NW + wave) * 1024);
-  }
+  const uint32_t st = stage_addr<S, PART == 4 ? HIGH : LOW>();
   if constexpr (PART == 3) {
     const int at = ((wave >> 2) * 256 + 64 * (wave & 3)) * 4;
     dma4(r.sa, lo.sc, st + SA_OFF + at);
     dma4(r.sb, lo.sc, st + SB_OFF + at);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = PART < 2 ? PART * 2 + i : i * 2 + (PART == 4);  // which 64 rows
+      const int slot = PART < 2 ? j : i;
+      dma16(PART < 2 ? r.b : r.a, lo.ab + j * lo.ab_step,
+            st + (PART < 2 ? A_HALF : 0) + (slot * Cfg::NW + wave) * 1024);
+    }
   }
 }
 
 // A lane's LDS byte offsets within a stage, fixed for the kernel (a 16-row band adds
 // 2048 bytes; see lds_offset() for the swizzle).
 struct LdsOffsets {
-  uint32_t a0, a1, b0, b1;  // the pieces of K block 0 and 1 of the step, of the wave's first band or columns
-  uint32_t sa, sb;          // its words, 64 rows a read
+  uint32_t a0, a1, b0, b1;  // what the lane holds for the two MFMAs, of the wave's first band or columns
+  uint32_t sa, sb;          // its scale words of four bands or column blocks
+  uint32_t pick;            // byte selector: of two words, the two bytes of each that the lane needs
 };
 
 __device__ __forceinline__ LdsOffsets lds_offsets(int wm0, int wn0, int lane) {
   LdsOffsets o;
   const int r = lane & 15, g = lane >> 4;
   const uint32_t c0 = (uint32_t)lds_offset(r, g), c1 = (uint32_t)lds_offset(r, g + 4);
-  o.a0 = (uint32_t)wm0 * ROW_BYTES + c0;
-  o.a1 = (uint32_t)wm0 * ROW_BYTES + c1;
-  o.b0 = A_BYTES + (uint32_t)wn0 * ROW_BYTES + c0;
-  o.b1 = A_BYTES + (uint32_t)wn0 * ROW_BYTES + c1;
-  o.sa = SA_OFF + (uint32_t)(wm0 + lane) * 4;
-  o.sb = SB_OFF + (uint32_t)(wn0 + lane) * 4;
+  o.a0 = (uint32_t)wm0 / 2 * ROW_BYTES + c0;
+  o.a1 = (uint32_t)wm0 / 2 * ROW_BYTES + c1;
+  o.b0 = A_HALF + (uint32_t)wn0 * ROW_BYTES + c0;
+  o.b1 = A_HALF + (uint32_t)wn0 * ROW_BYTES + c1;
+  o.sa = SA_OFF + (uint32_t)((g >> 1) * 1024 + wm0 * 4 + r * 16);
+  o.sb = SB_OFF + (uint32_t)((g >> 1) * 1024 + wn0 * 4 + r * 16);
+  o.pick = (g & 1) ? 0x07060302u : 0x05040100u;
   return o;
 }
 
-// A 16-row fragment of both K blocks of a step: piece g of the row's first half and of
-// its second.
+// A 16-row fragment for both MFMAs of a step.
 struct Frag {
-  i32x4 h[STEP_BLOCKS];
+  i32x4 h[2];
 };
-template <int S>
+template <int S, int PART = LOW>
 __device__ __forceinline__ Frag frag_at(uint32_t off0, uint32_t off1, int band) {
-  const uint8_t* st = stage_buf<S>();
+  const uint8_t* st = stage_buf<S, PART>();
   Frag f;
   f.h[0] = *reinterpret_cast<const i32x4*>(st + off0 + band * 16 * ROW_BYTES);
   f.h[1] = *reinterpret_cast<const i32x4*>(st + off1 + band * 16 * ROW_BYTES);
   return f;
 }
+template <int S, int BAND>
+__device__ __forceinline__ Frag band_at(const LdsOffsets& lds) {
+  return frag_at<S, BAND / 4>(lds.a0, lds.a1, BAND % 4);
+}
 __device__ __forceinline__ i32x8 operand(const i32x4& v) { return (i32x8){v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
 
-// The scale words of a wave's rows and columns as they lie in LDS, lane l the word of
-// the l-th of 64 rows: of either K block, rows 0 .. 63 and 64 .. 127, and the columns.
-struct Words {
-  uint32_t a[STEP_BLOCKS][2], b[STEP_BLOCKS];
+// The scales of the wave's bands and column blocks, two of them a register: byte
+// 2 (i % 2) + j of register i / 2 for the j-th MFMA.
+struct Scales {
+  int a[Cfg::MT / 2], b[Cfg::NT / 2];
 };
-template <int S>
-__device__ __forceinline__ Words words_at(const LdsOffsets& lds) {
-  const uint8_t* st = stage_buf<S>();
-  Words w;
-#pragma unroll
-  for (int h = 0; h < STEP_BLOCKS; ++h) {
-    w.a[h][0] = *reinterpret_cast<const uint32_t*>(st + lds.sa + h * 1024);
-    w.a[h][1] = *reinterpret_cast<const uint32_t*>(st + lds.sa + h * 1024 + 256);
-    w.b[h] = *reinterpret_cast<const uint32_t*>(st + lds.sb + h * 1024);
-  }
-  return w;
-}
-
-// Lane (r, g) of four groups of 16 gives the scale word of row 16g + r, and gets
-// byte g of the words of rows r, 16 + r, 32 + r and 48 + r: the codes of its K
-// positions in four successive 16-row fragments, in the order in which the
-// MFMA's byte select counts.
-__device__ __forceinline__ int scale_codes(uint32_t w, uint32_t pick_lo, uint32_t pick_hi) {
-  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-  const u32x2 half = __builtin_amdgcn_permlane32_swap(w, w, false, false);
-  const u32x2 lo = __builtin_amdgcn_permlane16_swap(half[0], half[0], false, false);
-  const u32x2 hi = __builtin_amdgcn_permlane16_swap(half[1], half[1], false, false);
-  return (int)(__builtin_amdgcn_perm(lo[1], lo[0], pick_lo) | __builtin_amdgcn_perm(hi[1], hi[0], pick_hi));
-}
-struct Codes {
-  int a[STEP_BLOCKS][2], b[STEP_BLOCKS];
-};
-__device__ __forceinline__ Codes codes_of(const Words& w, int lane) {
-  const uint32_t g = lane >> 4;
-  const uint32_t pick_lo = g | (4 + g) << 8 | 0x0C0C0000u, pick_hi = 0x0C0Cu | g << 16 | (4 + g) << 24;
-  Codes c;
-#pragma unroll
-  for (int h = 0; h < STEP_BLOCKS; ++h) {
-    c.a[h][0] = scale_codes(w.a[h][0], pick_lo, pick_hi);
-    c.a[h][1] = scale_codes(w.a[h][1], pick_lo, pick_hi);
-    c.b[h] = scale_codes(w.b[h], pick_lo, pick_hi);
-  }
-  return c;
+// The scales of four bands or column blocks, from index 2 I of `to`.
+template <int S, int I, int N>
+__device__ __forceinline__ void scales_at(int (&to)[N], uint32_t off, uint32_t pick) {
+  const i32x4 w = *reinterpret_cast<const i32x4*>(stage_buf<S, LOW>() + off + I * 256);
+  to[2 * I] = __builtin_amdgcn_perm(w[1], w[0], pick);
+  to[2 * I + 1] = __builtin_amdgcn_perm(w[3], w[2], pick);
 }
 
 template <int MT, int NT, int H>
-__device__ __forceinline__ f32x4 mfma(const Frag& b, const Frag& a, const f32x4& c, const Codes& s) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(b.h[H]), operand(a.h[H]), c, 4, 4, NT, s.b[H], MT & 3,
-                                                          s.a[H][MT >> 2]);
+__device__ __forceinline__ f32x4 mfma(const Frag& b, const Frag& a, const f32x4& c, const Scales& s) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(b.h[H]), operand(a.h[H]), c, 4, 4, 2 * (NT & 1) + H,
+                                                          s.b[NT / 2], 2 * (MT & 1) + H, s.a[MT / 2]);
 }
 
 // Writes a wave's finished 128 x 64 sub-tile as BF16 (round to nearest even), valid rows
-// only. Each 16-row band goes through LDS, so that every store covers whole 128-byte
-// row segments (8 lanes per row), in two of this wave's own 1 KB B slots of stage S,
-// the stage the tile's last step read: no wave reads it again before the next barrier,
-// and only this wave's own refill loads, issued later, overwrite these slots. 16-byte
-// slots are XOR-swizzled by row.
-template <int KIND, int S>
+// only. A lane has 4 columns of a row of each 16-column block; exchanges between lane
+// halves, quarters and halves of quarters give it 8 of a row's 64, so that each store
+// covers whole 128-byte segments of 8 rows. (Without the last exchange, 64 bytes of 16
+// rows a store, the masked decode took 1 to 2% more.)
+template <int KIND>
 __device__ __forceinline__ void store_tile(const GemmArgs& p, const TileRef& cur, const RowMask& cm,
-                                           const f32x4 (&acc)[Cfg::MT][Cfg::NT], int wave, int wm0, int wn0,
-                                           int lane) {
-  static_assert(Cfg::WN * 2 == ROW_BYTES, "one 128-byte row segment per wave and row");
-  typedef int i32x2 __attribute__((ext_vector_type(2)));
-  uint8_t* const st = stage_buf<S>();
-  const int wbase = A_BYTES + wave * 1024;  // slot j of the wave at + j * NW * 1024
+                                           const f32x4 (&acc)[Cfg::MT][Cfg::NT], int wm0, int wn0, int lane) {
   const int r = lane & 15, q = lane >> 4;
-  auto slot_off = [](int row, int sl) { return (row >> 3) * Cfg::NW * 1024 + (row & 7) * 128 + ((sl ^ (row & 7)) << 4); };
 #pragma unroll
   for (int mt = 0; mt < Cfg::MT; ++mt) {
     const uint32_t valid = band_rows<Cfg, KIND>(cur, cm, wm0, mt);
     if (valid == 0) continue;
+    i32x4 w[2];  // columns 32 np + 8 q .. + 7 of row r
 #pragma unroll
-    for (int nt = 0; nt < Cfg::NT; ++nt) {
-      const f32x4 v = acc[mt][nt];
-      const i32x2 packed = {(int)pack_bf16x2(v[0], v[1]), (int)pack_bf16x2(v[2], v[3])};
-      // columns 16 nt + 4 q .. + 3: half (q & 1) of 16-byte slot 2 nt + q / 2
-      *reinterpret_cast<i32x2*>(st + (wbase + slot_off(r, 2 * nt + (q >> 1)) + (q & 1) * 8)) = packed;
+    for (int np = 0; np < 2; ++np) {
+      const f32x4 u = acc[mt][2 * np], v = acc[mt][2 * np + 1];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        // Lanes of quarter q hold columns 4 q + 2 i of either block. The lanes' upper
+        // half's first block against the lower half's second, then odd quarters' against
+        // even ones': quarter q has columns 8 q .. 8 q + 7 of the 32.
+        const auto h = __builtin_amdgcn_permlane32_swap(pack_bf16x2(u[2 * i], u[2 * i + 1]),
+                                                        pack_bf16x2(v[2 * i], v[2 * i + 1]), false, false);
+        const auto t = __builtin_amdgcn_permlane16_swap(h[0], h[1], false, false);
+        w[np][i] = (int)t[0];
+        w[np][2 + i] = (int)t[1];
+      }
+    }
+    // The second 32 columns of rows 0 .. 7 against the first of rows 8 .. 15 (a rotation of
+    // each 16 lanes by 8, written to 8 of them).
+    i32x4 out[2];  // columns 32 (r / 8) + 8 q .. + 7 of rows r % 8 and 8 + r % 8
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      out[0][i] = __builtin_amdgcn_update_dpp(w[0][i], w[1][i], 0x128, 0xF, 0xC, false);
+      out[1][i] = __builtin_amdgcn_update_dpp(w[1][i], w[0][i], 0x128, 0xF, 0x3, false);
     }
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const int row = (lane >> 3) + 8 * half;
-      const int sl = lane & 7;
-      const i32x4 v = *reinterpret_cast<const i32x4*>(st + (wbase + slot_off(row, sl)));
+      const int row = (r & 7) + 8 * half;
       if ((valid >> row) & 1) {
-        uint16_t* drow = cur.d + (size_t)(cur.m0 + wm0 + mt * 16 + row) * p.n + cur.n0 + wn0 + 8 * sl;
-        if constexpr (KIND == KIND_DENSE) *(global_i32x4*)drow = v;
-        else __builtin_nontemporal_store(v, (global_i32x4*)drow);
+        uint16_t* at = cur.d + (size_t)(cur.m0 + wm0 + mt * 16 + row) * p.n + cur.n0 + wn0 + 32 * (r >> 3) + 8 * q;
+        // Past the caches' reach: the operands stay there (4096 x 7168 x 2048: 43 us, with
+        // plain stores 46; the masked decode 39 and 41).
+        __builtin_nontemporal_store(out[half], (global_i32x4*)at);
       }
     }
   }
 }
 
 // The K loop of one tile; its first step reads stage PHASE. Step i of the global
-// sequence of steps reads stage s = i % 2:
-//   entry:     the first step's operands are read (its stage was completed before the
+// sequence of steps reads stage s = i % 2, and issues the loads of step i + 2 into it as
+// its parts fall free:
+//   entry:     the first step's first operands are read (they were complete before the
 //              last barrier);
-//   bands 0-5: the A fragment two bands ahead from stage s, 8 MFMAs of the band (4
-//              column blocks, 2 K blocks); bands 0 and 1 also issue parts 2 and 3 of the
-//              refill of stage 1 - s (step i + 1);
-//   barrier:   after it every wave's loads of step i + 1 have landed and no wave reads
-//              stage s any more (bands 6 and 7 work from registers);
+//   bands 0-1: the A fragment two bands ahead from LOW, 8 MFMAs of the band (4 column
+//              blocks, 2 halves of K);
+//   barrier:   after it no wave reads LOW of stage s any more (its fragments of B, the
+//              scales and bands 2 and 3 are in registers), and every wave's loads of HIGH
+//              of stage s have landed;
+//   bands 2-5: the same from HIGH; a quarter of LOW's refill is issued with each;
+//   barrier:   after it no wave reads HIGH of stage s any more, and every wave's loads of
+//              step i + 1 into LOW have landed;
 //   bands 6-7: column block by column block, so that a B fragment is read again for step
 //              i + 1 as soon as its last MFMA of step i has issued, then the next step's
-//              first A fragments and its scale words; parts 0 and 1 of the refill of stage
-//              s (step i + 2) are issued.
+//              first A fragments and its scales; HIGH's refill is issued.
+// So every load has a step and a half to land. (One barrier a step, at band 6, gave it
+// 0.6 to 1 step, and took 229 us where this takes 221 for 16384 x 4096 x 7168.)
 // Only bands below NB are computed (the rows of the others are not stored).
 template <int KIND, int PHASE, int NB>
 __device__ __forceinline__ void mainloop(const GemmArgs& p, const TileSrc& t0, const TileSrc& t1, const TileSrc& t2,
@@ -308,9 +314,12 @@ __device__ __forceinline__ void mainloop(const GemmArgs& p, const TileSrc& t0, c
   Frag af[4], bf[Cfg::NT];  // A ring: band mt's fragment in slot mt % 4
 #pragma unroll
   for (int nt = 0; nt < Cfg::NT; ++nt) bf[nt] = frag_at<PHASE>(lds.b0, lds.b1, nt);
-  af[0] = frag_at<PHASE>(lds.a0, lds.a1, 0);
-  af[1] = frag_at<PHASE>(lds.a0, lds.a1, 1);
-  Words words = words_at<PHASE>(lds);
+  af[0] = band_at<PHASE, 0>(lds);
+  af[1] = band_at<PHASE, 1>(lds);
+  Scales scales;
+  scales_at<PHASE, 0>(scales.b, lds.sb, lds.pick);
+  scales_at<PHASE, 0>(scales.a, lds.sa, lds.pick);
+  scales_at<PHASE, 1>(scales.a, lds.sa, lds.pick);
   for (int i0 = 0; i0 < steps; i0 += 2) {
     static_for<0, 2>([&](auto si) {
       constexpr int s = (decltype(si)::value + PHASE) % 2, sn = 1 - s;
@@ -319,62 +328,70 @@ __device__ __forceinline__ void mainloop(const GemmArgs& p, const TileSrc& t0, c
       // The refills are issued unconditionally (past the last tile they load a step nobody
       // reads): a branch here would make the compiler wait for them before reading the
       // current stage.
-      const StageSrc r1 = refill_src(p, t0, t1, t2, i + 1, steps, wave);
       const StageSrc r2 = refill_src(p, t0, t1, t2, i + 2, steps, wave);
       if (!on) {
-        issue_part<sn, 2>(r1, wave, lo);
-        issue_part<sn, 3>(r1, wave, lo);
-        wait_vmcnt_0();
+        wait_vmcnt<LOW_LOADS + HIGH_LOADS>();
         wait_lgkmcnt_0();
         barrier();
-        next_rows();
         issue_part<s, 0>(r2, wave, lo);
         issue_part<s, 1>(r2, wave, lo);
+        issue_part<s, 2>(r2, wave, lo);
+        issue_part<s, 3>(r2, wave, lo);
+        wait_vmcnt<LOW_LOADS + HIGH_LOADS>();
+        barrier();
+        next_rows();
+        issue_part<s, 4>(r2, wave, lo);
         return;
       }
-      const Codes codes = codes_of(words, lane);
       static_for<0, 6>([&](auto MT) {
         constexpr int mt = decltype(MT)::value;
-        if constexpr (mt + 2 < NB) af[(mt + 2) % 4] = frag_at<s>(lds.a0, lds.a1, mt + 2);
-        if constexpr (mt == 0) issue_part<sn, 2>(r1, wave, lo);
-        if constexpr (mt == 1) issue_part<sn, 3>(r1, wave, lo);
+        if constexpr (mt == 2) {
+          wait_lgkmcnt_0();
+          wait_vmcnt<LOW_LOADS + HIGH_LOADS>();  // all but the last refills of LOW and HIGH
+          barrier();
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (mt + 2 < NB) af[(mt + 2) % 4] = band_at<s, mt + 2>(lds);
+        if constexpr (mt >= 2) issue_part<s, mt - 2>(r2, wave, lo);
         if constexpr (mt < NB) {
-          static_for<0, STEP_BLOCKS * Cfg::NT>([&](auto I) {
+          static_for<0, 2 * Cfg::NT>([&](auto I) {
             constexpr int h = decltype(I)::value / Cfg::NT, nt = decltype(I)::value % Cfg::NT;
-            acc[mt][nt] = mfma<mt, nt, h>(bf[nt], af[mt % 4], acc[mt][nt], codes);
+            acc[mt][nt] = mfma<mt, nt, h>(bf[nt], af[mt % 4], acc[mt][nt], scales);
           });
           // The reads two bands ahead and this band's share of the refill first.
           if constexpr (mt + 2 < NB) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // DS reads
-          if constexpr (mt == 0) __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);      // VMEM loads
-          if constexpr (mt == 1) __builtin_amdgcn_sched_group_barrier(0x020, 4, 0);
-          __builtin_amdgcn_sched_group_barrier(0x008, STEP_BLOCKS * Cfg::NT, 0);  // MFMA
+          if constexpr (mt >= 2) __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);      // VMEM loads
+          __builtin_amdgcn_sched_group_barrier(0x008, 2 * Cfg::NT, 0);  // MFMA
         }
         __builtin_amdgcn_sched_barrier(0);
       });
       static_for<0, Cfg::NT>([&](auto NT) {
         constexpr int nt = decltype(NT)::value;
         if constexpr (NB == Cfg::MT) {
-          acc[6][nt] = mfma<6, nt, 0>(bf[nt], af[2], acc[6][nt], codes);
-          acc[7][nt] = mfma<7, nt, 0>(bf[nt], af[3], acc[7][nt], codes);
-          acc[6][nt] = mfma<6, nt, 1>(bf[nt], af[2], acc[6][nt], codes);
-          acc[7][nt] = mfma<7, nt, 1>(bf[nt], af[3], acc[7][nt], codes);
+          acc[6][nt] = mfma<6, nt, 0>(bf[nt], af[2], acc[6][nt], scales);
+          acc[7][nt] = mfma<7, nt, 0>(bf[nt], af[3], acc[7][nt], scales);
+          acc[6][nt] = mfma<6, nt, 1>(bf[nt], af[2], acc[6][nt], scales);
+          acc[7][nt] = mfma<7, nt, 1>(bf[nt], af[3], acc[7][nt], scales);
         }
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (nt == 0) {
           wait_lgkmcnt_0();
-          wait_vmcnt_0();
+          wait_vmcnt<LOW_LOADS + HIGH_LOADS>();  // the same
           barrier();
           next_rows();
           __builtin_amdgcn_sched_barrier(0);
-          issue_part<s, 0>(r2, wave, lo);
+          issue_part<s, 4>(r2, wave, lo);
         }
-        if constexpr (nt == 1) issue_part<s, 1>(r2, wave, lo);
         // The next step's operands (past a tile's last step: the next tile's first, which
         // its entry reads again).
         bf[nt] = frag_at<sn>(lds.b0, lds.b1, nt);
-        if constexpr (nt == 1) af[0] = frag_at<sn>(lds.a0, lds.a1, 0);
-        if constexpr (nt == 2) words = words_at<sn>(lds);
-        if constexpr (nt == 3) af[1] = frag_at<sn>(lds.a0, lds.a1, 1);
+        if constexpr (nt == 1) af[0] = band_at<sn, 0>(lds);
+        if constexpr (nt == 3) {  // bands 6 and 7 are done
+          af[1] = band_at<sn, 1>(lds);
+          scales_at<sn, 0>(scales.b, lds.sb, lds.pick);
+          scales_at<sn, 0>(scales.a, lds.sa, lds.pick);
+          scales_at<sn, 1>(scales.a, lds.sa, lds.pick);
+        }
         __builtin_amdgcn_sched_barrier(0);
       });
     });
@@ -429,18 +446,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) fp4_gemm_nt_kernel(GemmArgs p
   [[maybe_unused]] RowGroups crg{-1, -1};
   if constexpr (KIND == KIND_CONTIGUOUS) crg = load_row_groups<Cfg>(p, cur, wm0, lane);
 
-  // Step 0 into stage 0 and parts 0 and 1 of step 1 into stage 1 (the first step issues
-  // the rest); step 0 must have landed for every wave before it is read.
+  // Steps 0 and 1; of step 0 LOW must have landed for every wave before it is read.
   {
     const StageSrc r0 = refill_src(p, c0, c1, c2, 0, steps, wave);
     const StageSrc r1 = refill_src(p, c0, c1, c2, 1, steps, wave);
-    issue_part<0, 0>(r0, wave, lo);
-    issue_part<0, 1>(r0, wave, lo);
-    issue_part<0, 2>(r0, wave, lo);
-    issue_part<0, 3>(r0, wave, lo);
-    issue_part<1, 0>(r1, wave, lo);
-    issue_part<1, 1>(r1, wave, lo);
-    wait_vmcnt<4>();  // all but step 1's parts 0 and 1
+    static_for<0, 5>([&](auto I) { issue_part<0, decltype(I)::value>(r0, wave, lo); });
+    static_for<0, 5>([&](auto I) { issue_part<1, decltype(I)::value>(r1, wave, lo); });
+    wait_vmcnt<LOW_LOADS + 2 * HIGH_LOADS>();
     barrier();
   }
   int phase = 0;
@@ -473,12 +485,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) fp4_gemm_nt_kernel(GemmArgs p
     }
     phase = (phase + steps) & 1;
 
-    // Epilogue (the next tile's first step has landed, its second is in flight), from the
-    // stage the tile's last step read.
-    if (on) {
-      if (phase == 0) store_tile<KIND, 1>(p, cur, cmask, acc, wave, wm0, wn0, lane);
-      else store_tile<KIND, 0>(p, cur, cmask, acc, wave, wm0, wn0, lane);
-    }
+    if (on) store_tile<KIND>(p, cur, cmask, acc, wm0, wn0, lane);
     // Slide the window.
     cmask = nmask;
     cur = nxt;
