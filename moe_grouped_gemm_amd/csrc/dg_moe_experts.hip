@@ -549,24 +549,25 @@ __global__ __launch_bounds__(UP_THREADS, 1) void experts_up_kernel(ExpertsArgs p
 
 constexpr int DOWN_WAVES = 4, DOWN_THREADS = DOWN_WAVES * 64, DOWN_RT = 2;
 
-// Steps on their way and in use: of 4 KB (FP8) or 2, as many as leave the sums room.
-template <bool FP4, int TOKENS>
-constexpr int DOWN_DEPTH = FP4 ? 8 : TOKENS > 64 ? 4 : 5;
+// Steps on their way and in use: of 4 KB (FP8) or 2, as many as leave the sums room (and
+// as vmcnt can count).
+template <bool FP4, int TOKENS, int NT>
+constexpr int DOWN_DEPTH = FP4 ? (NT > 1 ? 6 : 8) : TOKENS > 64 ? 4 : 5;
 template <bool FP4>
 using DownWeights = Weights<FP4, DOWN_RT, 1>;
 
 struct DownItem {
-  int expert, begin, count, tile;  // pairs of the plan, at most 16, and their activations
+  int expert_count, begin, tile, tile2;  // pairs of the plan (expert << 8 | how many), and their activations
 };
 
-// A workgroup takes 32 columns of y for all tokens. Its waves share the experts, 16
-// tokens of one at a time, and, where these do not come out even, their K in parts;
+// A workgroup takes 32 columns of y for all tokens. Its waves share the experts, 16 NT
+// tokens of one at a time (NT is 2 for more than 16 tokens), and, where these do not come out even, their K in parts;
 // each wave keeps sums of its own in LDS, which are added in order at the end. A wave's
 // items follow one another in one pipeline of steps.
-template <bool FP4, int ROWS, int TOKENS>
+template <bool FP4, int ROWS, int TOKENS, int NT>
 __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsArgs p) {
   constexpr int STRIDE = 16 * DOWN_RT + (TOKENS > 64 ? 0 : 4);  // floats; 4 past a power of two where there is room
-  constexpr int DEPTH = DOWN_DEPTH<FP4, TOKENS>, W = DownWeights<FP4>::LOADS, STEP = DownWeights<FP4>::BYTES;
+  constexpr int DEPTH = DOWN_DEPTH<FP4, TOKENS, NT>, W = DownWeights<FP4>::LOADS, STEP = DownWeights<FP4>::BYTES;
   __shared__ __attribute__((aligned(1024))) uint8_t rings[DOWN_WAVES * DEPTH * STEP];
   __shared__ __attribute__((aligned(16))) float sums[DOWN_WAVES * TOKENS * STRIDE];
   // Of the pairs; read from memory in the loop, they would be waited for with all the
@@ -586,13 +587,13 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
     sums_at[i] = (uint16_t)(plan->slot[i] / p.top_k * (STRIDE / 4));
     pair_weights[i] = plan->weight[i];
   }
-  // The items: an expert's pairs 16 at a time, in order.
+  // The items: an expert's pairs 16 NT at a time, in order.
   int total = 0;
   for (int r0 = 0; r0 < experts; r0 += DOWN_THREADS) {
     const int at = r0 + tid;
     ExpertEntry entry{0, 0, 0, 0};
     if (at < experts) entry = plan->entry[at];
-    const int has = (entry.count + 15) / 16;
+    const int has = (entry.count + 16 * NT - 1) / (16 * NT);
     int upto = has;
     for (int d = 1; d < 64; d <<= 1) {
       const int v = __shfl_up(upto, d);
@@ -605,9 +606,12 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
       if (w < wave) before += items_of[w];
       total += items_of[w];
     }
-    for (int i = 0; i < has; ++i)
-      items[before + i] = DownItem{entry.expert, entry.begin + 16 * i, min(entry.count - 16 * i, 16),
-                                   act_tile(p, entry.expert, i, plan->slot[entry.begin + 16 * i])};
+    for (int i = 0; i < has; ++i) {
+      const int begin = entry.begin + 16 * NT * i, count = min(entry.count - 16 * NT * i, 16 * NT);
+      const int tile = act_tile(p, entry.expert, NT * i, plan->slot[begin]);
+      const int tile2 = count > 16 ? act_tile(p, entry.expert, NT * i + 1, plan->slot[begin + 16]) : tile;
+      items[before + i] = DownItem{entry.expert << 8 | count, begin, tile, tile2};
+    }
     __syncthreads();
   }
   total = __builtin_amdgcn_readfirstlane(total);
@@ -621,17 +625,19 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
 
   // Where the loads and the products are: the turn, its item and its blocks.
   struct Cursor {
-    int turn, block, end, begin, count, tile;
+    int turn, block, end, begin, count, tile, tile2;
   };
   auto start = [&](Cursor& c) {
     const int item = wave + c.turn * DOWN_WAVES, part = item % parts;
     const DownItem at = items[item / parts];
     c.begin = __builtin_amdgcn_readfirstlane(at.begin);
-    c.count = __builtin_amdgcn_readfirstlane(at.count);
     c.tile = __builtin_amdgcn_readfirstlane(at.tile);
+    c.tile2 = __builtin_amdgcn_readfirstlane(at.tile2);
+    const int expert_count = __builtin_amdgcn_readfirstlane(at.expert_count);
+    c.count = expert_count & 0xFF;
     c.block = units * part / parts * unit;
     c.end = min(units * (part + 1) / parts * unit, blocks);
-    return __builtin_amdgcn_readfirstlane(at.expert);
+    return expert_count >> 8;
   };
   int steps = 0;
   for (int turn = 0; turn < turns; ++turn) {
@@ -648,42 +654,60 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
     const int first = start(ahead);
     DownWeights<FP4> weights(p.b2, p.sfb2, p.hidden, p.inner, lane);
     weights.place(first, row0, lane);
-    const uint16_t* act = p.act + (size_t)ahead.tile * ROWS * p.inner;
-    const uint32_t act_lane = (uint32_t)(g * ROWS + (r & (ROWS - 1))) * 8;
-    f32x4 acc[DOWN_RT][1] = {};
-    int loaded = 0, w_next = 0, w_slot = 0;
-    u32x4 t[DEPTH][1][4];
-    auto load = [&](u32x4 (&to)[1][4]) {
+    // The item's activations; rows past its pairs are not loaded (they lie past the end).
+    __amdgpu_buffer_rsrc_t act[NT];
+    uint32_t act_at[NT];
+    auto place_act = [&]() {
+      const uint32_t tile_values = (uint32_t)ROWS * p.inner;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) to[0][j] = load16(act + (ahead.block * QBLOCK * ROWS + j * 4 * ROWS * 8) + act_lane);
+      for (int nt = 0; nt < NT; ++nt) {
+        act[nt] = buffer_rsrc(p.act + (size_t)(nt ? ahead.tile2 : ahead.tile) * tile_values, tile_values * 2);
+        act_at[nt] = 16 * nt + r < ahead.count ? (uint32_t)(g * ROWS + (r & (ROWS - 1))) * 16 : 0x80000000u;
+      }
+    };
+    place_act();
+    f32x4 acc[DOWN_RT][NT] = {};
+    int loaded = 0, w_next = 0, w_slot = 0;
+    u32x4 t[DEPTH][NT][4];
+    auto load = [&](u32x4 (&to)[NT][4]) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          to[nt][j] = __builtin_amdgcn_raw_buffer_load_b128(act[nt], act_at[nt] + j * 64 * ROWS,
+                                                            ahead.block * QBLOCK * ROWS * 2, 0);
       weights.load(ahead.block, base + w_next * STEP);
       w_next = w_next == DEPTH - 1 ? 0 : w_next + 1;
       if (++loaded < steps && ++ahead.block == ahead.end) {  // (past the last step it is loaded again)
         ++ahead.turn;
         const int e = start(ahead);
         weights.place(e, row0, lane);
-        act = p.act + (size_t)ahead.tile * ROWS * p.inner;
+        place_act();
       }
     };
-    auto use = [&](const u32x4 (&from)[1][4]) {
+    auto use = [&](const u32x4 (&from)[NT][4]) {
       const uint8_t* const st = ring + w_slot * STEP;
       w_slot = w_slot == DEPTH - 1 ? 0 : w_slot + 1;
 #pragma unroll
-      for (int k = 0; k < DOWN_RT; ++k) weights.template multiply<1>(acc[k], st, k, from, lane);
+      for (int k = 0; k < DOWN_RT; ++k) weights.template multiply<NT>(acc[k], st, k, from, lane);
       if (++now.block < now.end) return;
-      if (r < now.count) {  // the item's tokens differ from one another
-        const float w = pair_weights[now.begin + r];
-        float* const at = mine + 4 * (sums_at[now.begin + r] + g);
 #pragma unroll
-        for (int k = 0; k < DOWN_RT; ++k) {
-          f32x4 sum = *reinterpret_cast<f32x4*>(at + 16 * k);
+      for (int nt = 0; nt < NT; ++nt)
+        if (16 * nt + r < now.count) {  // the item's tokens differ from one another
+          const float w = pair_weights[now.begin + 16 * nt + r];
+          float* const at = mine + 4 * (sums_at[now.begin + 16 * nt + r] + g);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) sum[v] = __builtin_fmaf(w, acc[k][0][v], sum[v]);
-          *reinterpret_cast<f32x4*>(at + 16 * k) = sum;
+          for (int k = 0; k < DOWN_RT; ++k) {
+            f32x4 sum = *reinterpret_cast<f32x4*>(at + 16 * k);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) sum[v] = __builtin_fmaf(w, acc[k][nt][v], sum[v]);
+            *reinterpret_cast<f32x4*>(at + 16 * k) = sum;
+          }
         }
-      }
 #pragma unroll
-      for (int k = 0; k < DOWN_RT; ++k) acc[k][0] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      for (int k = 0; k < DOWN_RT; ++k)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) acc[k][nt] = (f32x4){0.f, 0.f, 0.f, 0.f};
       if (++now.turn < turns) start(now);
     };
     // Rounds that are left at their end only, so that on every path to a use the compiler
@@ -695,7 +719,7 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
         constexpr int j = decltype(I)::value;
         before_loads();
         load(t[(j + DEPTH - 1) % DEPTH]);
-        wait_loads<(DEPTH - 1) * (4 + W)>();
+        wait_loads<(DEPTH - 1) * (4 * NT + W)>();
         use(t[j]);
       });
     }
@@ -731,8 +755,10 @@ hipError_t launch_both(const ExpertsArgs& a, hipStream_t stream) {
   const bool few = std::min(a.tokens * a.top_k, a.num_groups) * (a.inner / (16 * RT)) < a.cus;
   if (hipError_t e = few ? launch_up<FP4, RT / 2, ROWS>(a, stream) : launch_up<FP4, RT, ROWS>(a, stream)) return e;
   void (*down)(ExpertsArgs);
-  if constexpr (ROWS == 4) down = experts_down_kernel<FP4, ROWS, 4>;
-  else down = a.tokens <= 64 ? experts_down_kernel<FP4, ROWS, 64> : experts_down_kernel<FP4, ROWS, MAX_FEW_TOKENS>;
+  if constexpr (ROWS == 4) down = experts_down_kernel<FP4, ROWS, 4, 1>;
+  else if (a.tokens <= 16) down = experts_down_kernel<FP4, ROWS, 64, 1>;
+  else if (a.tokens <= 64) down = experts_down_kernel<FP4, ROWS, 64, 2>;
+  else down = experts_down_kernel<FP4, ROWS, MAX_FEW_TOKENS, 2>;
   hipLaunchKernelGGL(down, dim3(a.hidden / (16 * DOWN_RT)), dim3(DOWN_THREADS), 0, stream, a);
   return hipGetLastError();
 }
