@@ -17,6 +17,8 @@
 // cores' registers, lane by lane a row, take the L1 four times the accesses: one
 // 16-byte piece each, 3.4 TB/s where tokens' rows come the same way.
 //
+// A step is 128 bytes of each row: 128 values of FP8, or two blocks of 128 of FP4.
+//
 // v_mfma_f32_16x16x32_bf16: the first operand's lane (r, g) = (lane % 16, lane /
 // 16) holds 8 values of K of weight row r, the second's of token r, and result i of
 // the lane is weight row 4g + i for token r. Lane group g takes a quarter of a
@@ -95,21 +97,22 @@ __device__ __forceinline__ void before_loads() {
   asm volatile("" ::: "memory");
 }
 
-// One step of the weights: a 128-value block of K of TILES 16-row tiles, GROUPS
-// (1 or 2) runs of successive rows, with their scales.
+// One step of the weights: 128 bytes of each row of TILES 16-row tiles, GROUPS (1 or 2)
+// runs of successive rows, with their scales.
 template <bool FP4, int TILES_, int GROUPS>
 struct Weights {
   static constexpr int TILES = TILES_, PER_GROUP = TILES / GROUPS;
-  static constexpr int TILE_BYTES = FP4 ? 1024 : 2048, BLOCK_BYTES = FP4 ? 64 : 128;
-  static constexpr int SCALE_LOADS = FP4 ? (TILES + 3) / 4 : 1;
-  static constexpr int BYTES = TILES * TILE_BYTES + SCALE_LOADS * 256;  // of a step in LDS
-  static constexpr int LOADS = TILES * (TILE_BYTES / 1024) + SCALE_LOADS;
+  static constexpr int BLOCKS = FP4 ? 2 : 1;  // of 128 values, in a step
+  static constexpr int TILE_BYTES = 2048, SCALES_AT = TILES * TILE_BYTES;
+  static constexpr int SCALE_LOADS = FP4 ? (TILES + 1) / 2 : 1;
+  static constexpr int BYTES = SCALES_AT + SCALE_LOADS * 256;  // of a step in LDS
+  static constexpr int LOADS = TILES * 2 + SCALE_LOADS;
 
   const uint8_t* b;
   const uint32_t* sf;
   int n, k;                                      // the matrix is [n][k]
-  uint32_t row_bytes, scale_step;                // bytes between rows; between a block's scales and the next's
-  uint32_t w_at[TILE_BYTES / 1024];              // the lane's offsets,
+  uint32_t row_bytes, scale_step;                // bytes between rows; between a step's scales and the next's
+  uint32_t w_at[2];                              // the lane's offsets,
   uint32_t read_at, read_sf;                     // and in LDS
   __amdgpu_buffer_rsrc_t rows[GROUPS], scales;   // of the place at hand
   uint32_t sf_at[SCALE_LOADS];
@@ -118,68 +121,67 @@ struct Weights {
       : b(static_cast<const uint8_t*>(b_)), sf(static_cast<const uint32_t*>(sf_)), n(n_), k(k_) {
     const int r = lane & 15, g = lane >> 4;
     row_bytes = FP4 ? k / 2 : k;
-    scale_step = FP4 ? n * 4 : 4;
-    if constexpr (FP4) {
-      // A load is 16 rows of 64 bytes; pieces of 16 are swizzled so that a fragment
-      // read's 16 lanes of a pass (see lds_offset()) lie on 16 different slots.
-      const int row = lane >> 2, piece = (lane & 3) ^ (-(row >> 2) & 3);
-      w_at[0] = row * row_bytes + piece * 16;
-      read_at = r * 64 + ((g ^ (-(r >> 2) & 3)) << 4);
-      read_sf = r * 4;
-    } else {
-      // A load is 8 rows of 128 bytes.
+    scale_step = FP4 ? n * 8 : 4;
+    // A load is 8 rows of 128 bytes; pieces of 16 are swizzled for the fragment reads.
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = 8 * h + (lane >> 3), piece = (lane & 7) ^ ((row >> 1) & 7);
-        w_at[h] = row * row_bytes + piece * 16;
-      }
-      read_at = lds_offset(r, g);  // and, with bit 6 flipped, lds_offset(r, g + 4)
-      read_sf = 0;
+    for (int h = 0; h < 2; ++h) {
+      const int row = 8 * h + (lane >> 3), piece = (lane & 7) ^ ((row >> 1) & 7);
+      w_at[h] = row * row_bytes + piece * 16;
     }
+    read_at = lds_offset(r, g);  // and, with bit 6 flipped, lds_offset(r, g + 4)
+    read_sf = r * 4;
   }
 
   // Turns to the runs of rows from row0[.] of expert e's matrix.
   __device__ __forceinline__ void place(int e, const int (&row0)[GROUPS], int lane) {
-    const size_t values = (size_t)n * k;
-    const uint8_t* w = b + (size_t)e * (FP4 ? values / 2 : values);
+    // What lies past the expert's matrix (a last block of FP4 may have no second one) reads
+    // as zero.
+    const size_t values = (size_t)n * k, bytes = FP4 ? values / 2 : values;
+    const size_t sf_words = FP4 ? values / QBLOCK : values / QBLOCK / 128;
+    auto extent = [](size_t left) { return (uint32_t)min(left, (size_t)0xFFFFFFFFu); };
 #pragma unroll
-    for (int i = 0; i < GROUPS; ++i) rows[i] = buffer_rsrc(w + (size_t)row0[i] * row_bytes, 0xFFFFFFFFu);
-    scales = buffer_rsrc(sf + (size_t)e * (FP4 ? values / QBLOCK : values / QBLOCK / 128), 0xFFFFFFFFu);
+    for (int i = 0; i < GROUPS; ++i) {
+      const size_t at = (size_t)row0[i] * row_bytes;
+      rows[i] = buffer_rsrc(b + e * bytes + at, extent(bytes - at));
+    }
+    scales = buffer_rsrc(sf + e * sf_words, extent(sf_words * 4));
     // (By value: a choice between the array's elements would put it in memory.)
     const int run0 = row0[0], run1 = row0[GROUPS - 1];
     if constexpr (FP4) {
+      // Words of the first block's rows, then the second's.
 #pragma unroll
       for (int q = 0; q < SCALE_LOADS; ++q) {
-        const int tile = min(4 * q + (lane >> 4), TILES - 1), group = tile / PER_GROUP;
-        sf_at[q] = ((group ? run1 : run0) + (tile - group * PER_GROUP) * 16 + (lane & 15)) * 4;
+        const int at = min(4 * q + (lane >> 4), 2 * TILES - 1), block = at / TILES, tile = at % TILES;
+        const int group = tile / PER_GROUP;
+        sf_at[q] = (block * n + (group ? run1 : run0) + (tile - group * PER_GROUP) * 16 + (lane & 15)) * 4;
       }
     } else {
       sf_at[0] = (lane & 1 ? run1 : run0) / 128 * (k / QBLOCK) * 4;
     }
   }
 
-  __device__ __forceinline__ void load(int block, uint32_t lds) const {
+  __device__ __forceinline__ void load(int step, uint32_t lds) const {
 #pragma unroll
     for (int i = 0; i < TILES; ++i)
 #pragma unroll
-      for (int h = 0; h < TILE_BYTES / 1024; ++h)
-        dma16(rows[i / PER_GROUP], w_at[h], (uint32_t)(i % PER_GROUP) * 16 * row_bytes + (uint32_t)block * BLOCK_BYTES,
+      for (int h = 0; h < 2; ++h)
+        dma16(rows[i / PER_GROUP], w_at[h], (uint32_t)(i % PER_GROUP) * 16 * row_bytes + (uint32_t)step * 128,
               lds + i * TILE_BYTES + h * 1024);
 #pragma unroll
-    for (int q = 0; q < SCALE_LOADS; ++q)
-      dma4(scales, sf_at[q], (uint32_t)block * scale_step, lds + TILES * TILE_BYTES + q * 256);
+    for (int q = 0; q < SCALE_LOADS; ++q) dma4(scales, sf_at[q], (uint32_t)step * scale_step, lds + SCALES_AT + q * 256);
   }
 
-  // acc += tile i of the step at `st` times the tokens' operands.
+  // acc += tile i of block `block` of the step at `st` times the tokens' operands.
   template <int NT>
-  __device__ __forceinline__ void multiply(f32x4 (&acc)[NT], const uint8_t* st, int i, const u32x4 (&t)[NT][4],
-                                           int lane) const {
+  __device__ __forceinline__ void multiply(f32x4 (&acc)[NT], const uint8_t* st, int i, int block,
+                                           const u32x4 (&t)[NT][4], int lane) const {
     const uint8_t* tile = st + i * TILE_BYTES;
-    const uint8_t* sf = st + TILES * TILE_BYTES;
+    const uint8_t* sf = st + SCALES_AT;
     bf16x8 w[4];
     if constexpr (FP4) {
-      const u32x4 v = *reinterpret_cast<const u32x4*>(tile + read_at);
-      const uint32_t code = (*reinterpret_cast<const uint32_t*>(sf + i * 64 + read_sf) >> (8 * (lane >> 4))) & 0xFF;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(tile + (block ? read_at ^ 64 : read_at));
+      const uint32_t word = *reinterpret_cast<const uint32_t*>(sf + (block * TILES + i) * 64 + read_sf);
+      const uint32_t code = (word >> (8 * (lane >> 4))) & 0xFF;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t dword = v[j];
@@ -221,26 +223,13 @@ struct Weights {
 // ---------------------------------------------------------------------------
 
 constexpr int UP_WAVES = 4, UP_THREADS = UP_WAVES * 64;
-constexpr int UP_W_SLOTS = 3;   // steps of weights in a wave's ring
-constexpr int UP_T_BYTES = 12288;  // and bytes of tokens: two steps of 24, three of up to 16
-constexpr int UP_MOST_FOURS = 6;   // most tokens of a pass, in fours
+constexpr int UP_W_SLOTS = 2;      // steps of weights in a wave's ring: one is on its way, one in use
+constexpr int UP_T_BYTES = 16384;  // and bytes of tokens: two steps of 24 or 32, three of up to 16
+constexpr int UP_MOST_FOURS = 8;   // most tokens of a pass, in fours
 
 // Tokens' rows of a block come in loads of 4 rows of 256 bytes; their 16-byte pieces
 // are swizzled for the fragment reads, as the weights' are.
 __device__ __forceinline__ int token_swizzle(int row) { return (row & 3) | ((-(row >> 2) & 3) << 2); }
-
-// The i-th block of K that a wave takes, and how many there are: turn by turn, for
-// FP4 two successive ones, which share a 128-byte line of a row.
-template <bool FP4>
-__device__ __forceinline__ int wave_block(int wave, int i) {
-  return FP4 ? (i >> 1) * 2 * UP_WAVES + 2 * wave + (i & 1) : i * UP_WAVES + wave;
-}
-template <bool FP4>
-__device__ __forceinline__ int wave_blocks(int wave, int blocks) {
-  if (!FP4) return max((blocks - wave + UP_WAVES - 1) / UP_WAVES, 0);
-  const int rounds = blocks / (2 * UP_WAVES);
-  return 2 * rounds + min(max(blocks - rounds * 2 * UP_WAVES - 2 * wave, 0), 2);
-}
 
 template <bool FP4, int RT>
 using UpWeights = Weights<FP4, 2 * RT, 2>;
@@ -358,22 +347,31 @@ __device__ __forceinline__ void up_tiles(const ExpertsArgs& p, UpWeights<FP4, RT
   constexpr int NT = (FOURS + 3) / 4, W = UpWeights<FP4, RT>::LOADS, T = FOURS, TILES = 2 * RT;
   constexpr int STEP = UpWeights<FP4, RT>::BYTES, TOKENS = FOURS * 1024;
   constexpr int T_AHEAD = FOURS <= 4 ? 2 : 1, T_SLOTS = T_AHEAD + 1;
-  static_assert(T_SLOTS * TOKENS <= UP_T_BYTES && TILES * 1024 <= UP_T_BYTES, "tokens, and sums in their place");
+  // The waves' sums lie at the end of their tokens' place; before them the next tile's
+  // first tokens are on their way meanwhile.
+  constexpr int SUMS = TILES * NT * 1024, SUMS_AT = UP_W_SLOTS * STEP + UP_T_BYTES - SUMS;
+  static_assert(T_SLOTS * TOKENS <= UP_T_BYTES && T_AHEAD * TOKENS + SUMS <= UP_T_BYTES, "room for both");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   uint8_t* const ring = lds + wave * UP_RING<FP4, RT>;
   const uint32_t base = (uint32_t)(uintptr_t)(lds_void*)ring, token_base = base + UP_W_SLOTS * STEP;
   const __amdgpu_buffer_rsrc_t x = buffer_rsrc(p.x, 0xFFFFFFFFu);
-  const int steps = wave_blocks<FP4>(wave, p.hidden / QBLOCK);
+  constexpr int BLOCKS = UpWeights<FP4, RT>::BLOCKS;
+  // Steps of K go to the waves turn by turn: the wave's i-th, of which the last of all may
+  // have one block only.
+  const int all_blocks = p.hidden / QBLOCK, all_steps = (all_blocks + BLOCKS - 1) / BLOCKS;
+  const int steps = max((all_steps - wave + UP_WAVES - 1) / UP_WAVES, 0);
+  auto step_of = [&](int i) { return i * UP_WAVES + wave; };
+  const int blocks = steps * BLOCKS - (steps > 0 && (step_of(steps - 1) + 1) * BLOCKS > all_blocks);
 
-  // The weights' loads: where they are, two steps ahead of the products.
+  // The weights' loads: where they are, a step ahead of the products.
   int w_tile = tile, w_i = 0, w_next = 0;
   auto place = [&]() {
     const int row0[2] = {w_tile * 16 * RT, p.inner + w_tile * 16 * RT};
     weights.place(expert, row0, lane);
   };
   auto load_weights = [&]() {  // (past the last step it is loaded again)
-    weights.load(wave_block<FP4>(wave, w_i), base + w_next * STEP);
+    weights.load(step_of(w_i), base + w_next * STEP);
     w_next = w_next == UP_W_SLOTS - 1 ? 0 : w_next + 1;
     if (w_i + 1 < steps) {
       ++w_i;
@@ -384,10 +382,7 @@ __device__ __forceinline__ void up_tiles(const ExpertsArgs& p, UpWeights<FP4, RT
     }
   };
   place();
-  if (steps > 0) {
-    load_weights();
-    load_weights();
-  }
+  if (steps > 0) load_weights();
 
   uint32_t x_at[FOURS];
 #pragma unroll
@@ -403,17 +398,25 @@ __device__ __forceinline__ void up_tiles(const ExpertsArgs& p, UpWeights<FP4, RT
     read_at[nt] = row * 256;
     swizzle[nt] = token_swizzle(row & 15);
   }
-  const int act_tiles[2] = {act_tile(p, expert, number, slots[0]),
-                            NT > 1 && count > 16 ? act_tile(p, expert, number + 1, slots[16]) : 0};
+  const int act_tile0 = act_tile(p, expert, number, slots[0]);
+  const int act_tile1 = NT > 1 && count > 16 ? act_tile(p, expert, number + 1, slots[16]) : 0;
   int t_next = 0;
   auto load_tokens = [&](int i) {
-    const int block = wave_block<FP4>(wave, i);
+    const int block = step_of(i / BLOCKS) * BLOCKS + i % BLOCKS;
 #pragma unroll
     for (int q = 0; q < FOURS; ++q) dma16(x, x_at[q], (uint32_t)block * 256, token_base + t_next * TOKENS + q * 1024);
     t_next = t_next == T_SLOTS - 1 ? 0 : t_next + 1;
   };
 
+  auto first_tokens = [&]() {
+    t_next = 0;
+#pragma unroll
+    for (int i = 0; i < T_AHEAD; ++i)
+      if (i < blocks) load_tokens(i);
+  };
+
   int w_slot = 0;
+  first_tokens();
   for (; tile < tile_end; ++tile) {
     f32x4 acc[TILES][NT];
 #pragma unroll
@@ -421,28 +424,19 @@ __device__ __forceinline__ void up_tiles(const ExpertsArgs& p, UpWeights<FP4, RT
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) acc[i][nt] = (f32x4){0.f, 0.f, 0.f, 0.f};
     int t_slot = 0;
-    t_next = 0;
-#pragma unroll
-    for (int i = 0; i < T_AHEAD; ++i)
-      if (i < steps) load_tokens(i);
-    for (int i = 0; i < steps; ++i) {
+    // Block by block: its tokens' loads go T_AHEAD blocks ahead, those of the weights a step.
+    auto multiply = [&](int i, auto BLOCK) {
+      constexpr int block = decltype(BLOCK)::value;
+      // In this order what may still be on its way is the next step's weights and the tokens
+      // of the blocks after this, whichever came first.
       before_loads();
-      const bool more = i + T_AHEAD < steps;
-      if (more) load_tokens(i + T_AHEAD);
-      load_weights();
-      // What may still be on its way: the next two steps' weights (at a tile's first step,
-      // whose tokens came after the second one's weights, one step's), and the tokens of the
-      // steps after this.
-      const int tokens_after = more ? T_AHEAD : steps - 1 - i;
-      if (i == 0) {
-        if (tokens_after == 0) wait_loads<W>();
-        else if (tokens_after == 1) wait_loads<W + T>();
-        else wait_loads<W + T_AHEAD * T>();
-      } else {
-        if (tokens_after == 0) wait_loads<2 * W>();
-        else if (tokens_after == 1) wait_loads<2 * W + T>();
-        else wait_loads<2 * W + T_AHEAD * T>();
-      }
+      if constexpr (BLOCKS == 1) load_weights();
+      if (i + T_AHEAD < blocks) load_tokens(i + T_AHEAD);
+      if constexpr (BLOCKS == 2 && block == 0) load_weights();
+      const int tokens_after = min(T_AHEAD, blocks - 1 - i);
+      if (tokens_after == 0) wait_loads<W>();
+      else if (tokens_after == 1) wait_loads<W + T>();
+      else wait_loads<W + T_AHEAD * T>();
       const uint8_t* const st = ring + w_slot * STEP;
       const uint8_t* const tok = ring + UP_W_SLOTS * STEP + t_slot * TOKENS;
       u32x4 t[NT][4];
@@ -454,36 +448,41 @@ __device__ __forceinline__ void up_tiles(const ExpertsArgs& p, UpWeights<FP4, RT
           t[nt][j] = *reinterpret_cast<const u32x4*>(tok + read_at[nt] + ((piece ^ swizzle[nt]) << 4));
         }
 #pragma unroll
-      for (int k = 0; k < TILES; ++k) weights.template multiply<NT>(acc[k], st, k, t, lane);
-      w_slot = w_slot == UP_W_SLOTS - 1 ? 0 : w_slot + 1;
+      for (int k = 0; k < TILES; ++k) weights.template multiply<NT>(acc[k], st, k, block, t, lane);
       t_slot = t_slot == T_SLOTS - 1 ? 0 : t_slot + 1;
+    };
+    for (int i = 0; i < steps; ++i) {
+      multiply(i * BLOCKS, std::integral_constant<int, 0>{});
+      if constexpr (BLOCKS == 2)
+        if (i * 2 + 1 < blocks) multiply(i * 2 + 1, std::integral_constant<int, 1>{});
+      w_slot = w_slot == UP_W_SLOTS - 1 ? 0 : w_slot + 1;
     }
 
-    // The waves' sums, in the tokens' place, 16 tokens at a time.
-    static_for<0, NT>([&](auto N) {
-      constexpr int nt = decltype(N)::value;
-      auto sums_of = [&](int w) { return reinterpret_cast<f32x4*>(lds + w * UP_RING<FP4, RT> + UP_W_SLOTS * STEP); };
-      meet();  // every wave has read its tokens, and the sums before these
+    before_loads();
+    if (tile + 1 < tile_end) first_tokens();
+    auto sums_of = [&](int w) { return reinterpret_cast<f32x4*>(lds + w * UP_RING<FP4, RT> + SUMS_AT); };
 #pragma unroll
-      for (int i = 0; i < TILES; ++i) sums_of(wave)[i * 64 + lane] = acc[i][nt];
-      meet();
-      for (int i = wave; i < RT; i += UP_WAVES) {
-        f32x4 gate = sums_of(0)[i * 64 + lane], up = sums_of(0)[(RT + i) * 64 + lane];
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int w = 1; w < UP_WAVES; ++w) {
-          gate += sums_of(w)[i * 64 + lane];
-          up += sums_of(w)[(RT + i) * 64 + lane];
-        }
-        f32x4 a;
+      for (int i = 0; i < TILES; ++i) sums_of(wave)[(nt * TILES + i) * 64 + lane] = acc[i][nt];
+    meet();
+    for (int item = wave; item < RT * NT; item += UP_WAVES) {
+      const int nt = item / RT, i = item % RT, at = nt * TILES + i;
+      f32x4 gate = sums_of(0)[at * 64 + lane], up = sums_of(0)[(at + RT) * 64 + lane];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) a[k] = gate[k] * sigmoid(gate[k]) * up[k];
-        if (nt * 16 + r < count) {
-          const u32x2 packed = {pack2((f32x2){a[0], a[1]}), pack2((f32x2){a[2], a[3]})};
-          uint16_t* const at = p.act + (size_t)act_tiles[nt] * ROWS * p.inner;
-          *reinterpret_cast<u32x2*>(at + act_at<FP4, ROWS>(tile * 16 * RT + 16 * i + 4 * g, r)) = packed;
-        }
+      for (int w = 1; w < UP_WAVES; ++w) {
+        gate += sums_of(w)[at * 64 + lane];
+        up += sums_of(w)[(at + RT) * 64 + lane];
       }
-    });
+      f32x4 a;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) a[k] = gate[k] * sigmoid(gate[k]) * up[k];
+      if (nt * 16 + r < count) {
+        const u32x2 packed = {pack2((f32x2){a[0], a[1]}), pack2((f32x2){a[2], a[3]})};
+        uint16_t* const to = p.act + (size_t)(nt ? act_tile1 : act_tile0) * ROWS * p.inner;
+        *reinterpret_cast<u32x2*>(to + act_at<FP4, ROWS>(tile * 16 * RT + 16 * i + 4 * g, r)) = packed;
+      }
+    }
     meet();  // the sums have been read: tokens may come
   }
   wait_loads<0>();  // (the last step's weights once more)
@@ -526,9 +525,9 @@ __global__ __launch_bounds__(UP_THREADS, 1) void experts_up_kernel(ExpertsArgs p
     at += tile_end - tile;
     const int count = gather(l, n, [&](int i) { return l.ids[i] == expert && first_of_token(l.ids, i, p.top_k); },
                              [&](int i, int place) { l.list[place] = (uint16_t)i; });
-    // The tokens 16 at a time, the last 17 to 24 at once.
+    // The tokens 32 at a time.
     for (int t0 = 0; t0 < count;) {
-      const int left = count - t0, here = left <= 4 * UP_MOST_FOURS ? left : 16;
+      const int left = count - t0, here = min(left, 4 * UP_MOST_FOURS);
       const uint16_t* const slots = l.list + t0;
       if constexpr (ROWS == 4) {
         up_tiles<FP4, RT, 1, ROWS>(p, weights, tile, tile_end, expert, t0 / 16, slots, here, lds);
@@ -536,7 +535,8 @@ __global__ __launch_bounds__(UP_THREADS, 1) void experts_up_kernel(ExpertsArgs p
         if (here <= 4) up_tiles<FP4, RT, 1, ROWS>(p, weights, tile, tile_end, expert, t0 / 16, slots, here, lds);
         else if (here <= 8) up_tiles<FP4, RT, 2, ROWS>(p, weights, tile, tile_end, expert, t0 / 16, slots, here, lds);
         else if (here <= 16) up_tiles<FP4, RT, 4, ROWS>(p, weights, tile, tile_end, expert, t0 / 16, slots, here, lds);
-        else up_tiles<FP4, RT, 6, ROWS>(p, weights, tile, tile_end, expert, t0 / 16, slots, here, lds);
+        else if (here <= 24) up_tiles<FP4, RT, 6, ROWS>(p, weights, tile, tile_end, expert, t0 / 16, slots, here, lds);
+        else up_tiles<FP4, RT, 8, ROWS>(p, weights, tile, tile_end, expert, t0 / 16, slots, here, lds);
       }
       t0 += here;
     }
@@ -547,27 +547,27 @@ __global__ __launch_bounds__(UP_THREADS, 1) void experts_up_kernel(ExpertsArgs p
 // Down
 // ---------------------------------------------------------------------------
 
-constexpr int DOWN_WAVES = 4, DOWN_THREADS = DOWN_WAVES * 64, DOWN_RT = 2;
+constexpr int DOWN_WAVES = 4, DOWN_THREADS = DOWN_WAVES * 64;
 
-// Steps on their way and in use: of 4 KB (FP8) or 2, as many as leave the sums room (and
-// as vmcnt can count).
+// Steps on their way and in use: as many as leave the sums room (and as vmcnt can count).
 template <bool FP4, int TOKENS, int NT>
-constexpr int DOWN_DEPTH = FP4 ? (NT > 1 ? 6 : 8) : TOKENS > 64 ? 4 : 5;
-template <bool FP4>
-using DownWeights = Weights<FP4, DOWN_RT, 1>;
+constexpr int DOWN_DEPTH = FP4 ? (NT > 1 ? 3 : 4) : TOKENS > 64 ? 4 : 5;
+template <bool FP4, int RT>
+using DownWeights = Weights<FP4, RT, 1>;
 
 struct DownItem {
   int expert_count, begin, tile, tile2;  // pairs of the plan (expert << 8 | how many), and their activations
 };
 
-// A workgroup takes 32 columns of y for all tokens. Its waves share the experts, 16 NT
+// A workgroup takes 16 RT columns of y for all tokens. Its waves share the experts, 16 NT
 // tokens of one at a time (NT is 2 for more than 16 tokens), and, where these do not come out even, their K in parts;
 // each wave keeps sums of its own in LDS, which are added in order at the end. A wave's
 // items follow one another in one pipeline of steps.
-template <bool FP4, int ROWS, int TOKENS, int NT>
+template <bool FP4, int ROWS, int TOKENS, int NT, int RT>
 __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsArgs p) {
-  constexpr int STRIDE = 16 * DOWN_RT + (TOKENS > 64 ? 0 : 4);  // floats; 4 past a power of two where there is room
-  constexpr int DEPTH = DOWN_DEPTH<FP4, TOKENS, NT>, W = DownWeights<FP4>::LOADS, STEP = DownWeights<FP4>::BYTES;
+  constexpr int STRIDE = 16 * RT + (TOKENS > 64 ? 0 : 4);  // floats; 4 past a power of two where there is room
+  constexpr int DEPTH = DOWN_DEPTH<FP4, TOKENS, NT>, W = DownWeights<FP4, RT>::LOADS, STEP = DownWeights<FP4, RT>::BYTES;
+  constexpr int BLOCKS = DownWeights<FP4, RT>::BLOCKS, ACT_LOADS = 4 * NT * BLOCKS;
   __shared__ __attribute__((aligned(1024))) uint8_t rings[DOWN_WAVES * DEPTH * STEP];
   __shared__ __attribute__((aligned(16))) float sums[DOWN_WAVES * TOKENS * STRIDE];
   // Of the pairs; read from memory in the loop, they would be waited for with all the
@@ -578,7 +578,7 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
   __shared__ int items_of[DOWN_WAVES];
   const ExpertPlan* plan = reinterpret_cast<const ExpertPlan*>(p.plan);
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), c0 = blockIdx.x * 16 * DOWN_RT;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), c0 = blockIdx.x * 16 * RT;
   float* const mine = sums + wave * TOKENS * STRIDE;
   for (int i = lane; i < p.tokens * STRIDE; i += 64) mine[i] = 0.0f;
 
@@ -616,16 +616,16 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
   }
   total = __builtin_amdgcn_readfirstlane(total);
 
-  // Parts of K (of pairs of blocks, see wave_block): so many that the waves have the
-  // same number of items, or that they have eight each.
-  const int blocks = p.inner / QBLOCK, unit = FP4 ? 2 : 1, units = (blocks + unit - 1) / unit;
+  // Parts of K: so many that the waves have the same number of items, or that they have
+  // eight each.
+  const int item_steps = (p.inner / QBLOCK + BLOCKS - 1) / BLOCKS;
   int parts = 1;
-  while (parts < 8 && parts * 2 <= units && total * parts % DOWN_WAVES && total * parts < 8 * DOWN_WAVES) parts *= 2;
+  while (parts < 8 && parts * 2 <= item_steps && total * parts % DOWN_WAVES && total * parts < 8 * DOWN_WAVES) parts *= 2;
   const int all = total * parts, turns = wave < all ? (all - wave + DOWN_WAVES - 1) / DOWN_WAVES : 0;
 
-  // Where the loads and the products are: the turn, its item and its blocks.
+  // Where the loads and the products are: the turn, its item and its steps.
   struct Cursor {
-    int turn, block, end, begin, count, tile, tile2;
+    int turn, step, end, begin, count, tile, tile2;
   };
   auto start = [&](Cursor& c) {
     const int item = wave + c.turn * DOWN_WAVES, part = item % parts;
@@ -635,14 +635,14 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
     c.tile2 = __builtin_amdgcn_readfirstlane(at.tile2);
     const int expert_count = __builtin_amdgcn_readfirstlane(at.expert_count);
     c.count = expert_count & 0xFF;
-    c.block = units * part / parts * unit;
-    c.end = min(units * (part + 1) / parts * unit, blocks);
+    c.step = item_steps * part / parts;
+    c.end = item_steps * (part + 1) / parts;
     return expert_count >> 8;
   };
   int steps = 0;
   for (int turn = 0; turn < turns; ++turn) {
     const int part = (wave + turn * DOWN_WAVES) % parts;
-    steps += min(units * (part + 1) / parts * unit, blocks) - units * part / parts * unit;
+    steps += item_steps * (part + 1) / parts - item_steps * part / parts;
   }
 
   if (steps > 0) {
@@ -652,9 +652,10 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
     Cursor ahead{}, now{};
     start(now);
     const int first = start(ahead);
-    DownWeights<FP4> weights(p.b2, p.sfb2, p.hidden, p.inner, lane);
+    DownWeights<FP4, RT> weights(p.b2, p.sfb2, p.hidden, p.inner, lane);
     weights.place(first, row0, lane);
-    // The item's activations; rows past its pairs are not loaded (they lie past the end).
+    // The item's activations; rows past its pairs are not loaded (they lie past the end, as
+    // does a second block past the last).
     __amdgpu_buffer_rsrc_t act[NT];
     uint32_t act_at[NT];
     auto place_act = [&]() {
@@ -666,38 +667,42 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
       }
     };
     place_act();
-    f32x4 acc[DOWN_RT][NT] = {};
+    f32x4 acc[RT][NT] = {};
     int loaded = 0, w_next = 0, w_slot = 0;
-    u32x4 t[DEPTH][NT][4];
-    auto load = [&](u32x4 (&to)[NT][4]) {
+    u32x4 t[DEPTH][BLOCKS][NT][4];
+    auto load = [&](u32x4 (&to)[BLOCKS][NT][4]) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int b = 0; b < BLOCKS; ++b)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          to[nt][j] = __builtin_amdgcn_raw_buffer_load_b128(act[nt], act_at[nt] + j * 64 * ROWS,
-                                                            ahead.block * QBLOCK * ROWS * 2, 0);
-      weights.load(ahead.block, base + w_next * STEP);
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            to[b][nt][j] = __builtin_amdgcn_raw_buffer_load_b128(
+                act[nt], act_at[nt] + (b * QBLOCK * 2 + j * 64) * ROWS, ahead.step * BLOCKS * QBLOCK * ROWS * 2, 0);
+      weights.load(ahead.step, base + w_next * STEP);
       w_next = w_next == DEPTH - 1 ? 0 : w_next + 1;
-      if (++loaded < steps && ++ahead.block == ahead.end) {  // (past the last step it is loaded again)
+      if (++loaded < steps && ++ahead.step == ahead.end) {  // (past the last step it is loaded again)
         ++ahead.turn;
         const int e = start(ahead);
         weights.place(e, row0, lane);
         place_act();
       }
     };
-    auto use = [&](const u32x4 (&from)[NT][4]) {
+    auto use = [&](const u32x4 (&from)[BLOCKS][NT][4]) {
       const uint8_t* const st = ring + w_slot * STEP;
       w_slot = w_slot == DEPTH - 1 ? 0 : w_slot + 1;
 #pragma unroll
-      for (int k = 0; k < DOWN_RT; ++k) weights.template multiply<NT>(acc[k], st, k, from, lane);
-      if (++now.block < now.end) return;
+      for (int b = 0; b < BLOCKS; ++b)
+#pragma unroll
+        for (int k = 0; k < RT; ++k) weights.template multiply<NT>(acc[k], st, k, b, from[b], lane);
+      if (++now.step < now.end) return;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
         if (16 * nt + r < now.count) {  // the item's tokens differ from one another
           const float w = pair_weights[now.begin + 16 * nt + r];
           float* const at = mine + 4 * (sums_at[now.begin + 16 * nt + r] + g);
 #pragma unroll
-          for (int k = 0; k < DOWN_RT; ++k) {
+          for (int k = 0; k < RT; ++k) {
             f32x4 sum = *reinterpret_cast<f32x4*>(at + 16 * k);
 #pragma unroll
             for (int v = 0; v < 4; ++v) sum[v] = __builtin_fmaf(w, acc[k][nt][v], sum[v]);
@@ -705,7 +710,7 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
           }
         }
 #pragma unroll
-      for (int k = 0; k < DOWN_RT; ++k)
+      for (int k = 0; k < RT; ++k)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) acc[k][nt] = (f32x4){0.f, 0.f, 0.f, 0.f};
       if (++now.turn < turns) start(now);
@@ -719,7 +724,7 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
         constexpr int j = decltype(I)::value;
         before_loads();
         load(t[(j + DEPTH - 1) % DEPTH]);
-        wait_loads<(DEPTH - 1) * (4 * NT + W)>();
+        wait_loads<(DEPTH - 1) * (ACT_LOADS + W)>();
         use(t[j]);
       });
     }
@@ -729,8 +734,8 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
     });
   }
   __syncthreads();
-  for (int i = tid; i < p.tokens * 8 * DOWN_RT; i += DOWN_THREADS) {
-    const int t = i / (8 * DOWN_RT), c = i % (8 * DOWN_RT) * 2;
+  for (int i = tid; i < p.tokens * 8 * RT; i += DOWN_THREADS) {
+    const int t = i / (8 * RT), c = i % (8 * RT) * 2;
     f32x2 s = {0.f, 0.f};
 #pragma unroll
     for (int w = 0; w < DOWN_WAVES; ++w)
@@ -747,20 +752,28 @@ hipError_t launch_up(const ExpertsArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <bool FP4, int ROWS, int TOKENS, int NT>
+hipError_t launch_down(const ExpertsArgs& a, hipStream_t stream) {
+  // 16 columns a workgroup, and the activations read twice as often, where 32 would leave
+  // half the compute units without one. 128 tokens, 64 experts of 4096 x 1536 in FP8: 121
+  // us, with 32 columns 147; 16 tokens: 74 and 105. With hidden 7168 (448 workgroups for
+  // 224) 61 tokens and 32 experts took 140 us for 100.
+  const int rt = a.hidden / 32 <= a.cus / 2 ? 1 : 2;
+  const auto down = rt == 1 ? experts_down_kernel<FP4, ROWS, TOKENS, NT, 1> : experts_down_kernel<FP4, ROWS, TOKENS, NT, 2>;
+  hipLaunchKernelGGL(down, dim3(a.hidden / (16 * rt)), dim3(DOWN_THREADS), 0, stream, a);
+  return hipGetLastError();
+}
+
 // ROWS: 4 for up to 4 tokens, else 16.
 template <bool FP4, int ROWS>
 hipError_t launch_both(const ExpertsArgs& a, hipStream_t stream) {
-  constexpr int RT = FP4 ? 4 : 2;
   // Half as many rows a workgroup where there would not be one for every compute unit.
-  const bool few = std::min(a.tokens * a.top_k, a.num_groups) * (a.inner / (16 * RT)) < a.cus;
-  if (hipError_t e = few ? launch_up<FP4, RT / 2, ROWS>(a, stream) : launch_up<FP4, RT, ROWS>(a, stream)) return e;
-  void (*down)(ExpertsArgs);
-  if constexpr (ROWS == 4) down = experts_down_kernel<FP4, ROWS, 4, 1>;
-  else if (a.tokens <= 16) down = experts_down_kernel<FP4, ROWS, 64, 1>;
-  else if (a.tokens <= 64) down = experts_down_kernel<FP4, ROWS, 64, 2>;
-  else down = experts_down_kernel<FP4, ROWS, MAX_FEW_TOKENS, 2>;
-  hipLaunchKernelGGL(down, dim3(a.hidden / (16 * DOWN_RT)), dim3(DOWN_THREADS), 0, stream, a);
-  return hipGetLastError();
+  const bool few = std::min(a.tokens * a.top_k, a.num_groups) * (a.inner / 32) < a.cus;
+  if (hipError_t e = few ? launch_up<FP4, 1, ROWS>(a, stream) : launch_up<FP4, 2, ROWS>(a, stream)) return e;
+  if constexpr (ROWS == 4) return launch_down<FP4, ROWS, 4, 1>(a, stream);
+  else if (a.tokens <= 16) return launch_down<FP4, ROWS, 64, 1>(a, stream);
+  else if (a.tokens <= 64) return launch_down<FP4, ROWS, 64, 2>(a, stream);
+  else return launch_down<FP4, ROWS, MAX_FEW_TOKENS, 2>(a, stream);
 }
 
 }  // namespace
