@@ -399,7 +399,9 @@ __device__ __forceinline__ void mainloop(const GemmArgs& p, const TileSrc& t0, c
 }
 
 // A wave whose valid rows lie in its first HALF_BANDS bands runs a copy of the K loop
-// without the other bands' MFMAs (their rows are never stored).
+// without the other bands' MFMAs (their rows are never stored). 32 groups of up to 64
+// rows, 4096 x 7168: 93 us, without the copy 99; 16 groups of up to 256 rows, 7168 x
+// 2048: 40 with either.
 constexpr int HALF_BANDS = 4;
 
 template <int KIND>

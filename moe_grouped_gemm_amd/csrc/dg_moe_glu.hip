@@ -80,13 +80,14 @@ __global__ __launch_bounds__(GLU_THREADS) void swiglu_fp8_kernel(GluArgs p, int 
 }
 
 // To FP4, one step of which is a quarter to a half of a value: the codes are those of
-// the formula itself, whatever the last places of its float32 terms. These are
-// good to well below SLACK (the exponential's argument rounds by |g| 2^-24, |g| < 89,
-// the rest by a few 2^-24), so a code or scale that comes out the same for values
-// that much smaller and larger is the formula's. The others, one value in 10^5, are
-// computed again in 64 bits, a wave at a time, and so are blocks so small and gates so
-// far below zero that float32 terms lose their precision.
-constexpr float SLACK = 0x1p-17f;
+// the formula itself, whatever the last places of its float32 terms. With n = max(-g,
+// 0) these are off by less than (1.5 n + 8) 2^-24: log2(e) g and its product round by 1.5
+// |g| 2^-24 (no matter above zero, where the exponential is below 1 in a sum with 1), the
+// exponential and the reciprocal by 2^-23 each, four operations by 2^-24. So a code or
+// scale that comes out the same for values (n + 8) 2^-23 smaller and larger, n the
+// block's largest, is the formula's. The others, a few values in 10^6, are computed again
+// in 64 bits, a wave at a time, and so are blocks so small and gates so far below zero
+// that float32 terms lose their precision.
 constexpr uint32_t TINY = 0x0D800000u;  // 2^-100
 constexpr float LOW_GATE = -87.0f;
 
@@ -146,13 +147,14 @@ __global__ __launch_bounds__(GLU_THREADS) void swiglu_fp4_kernel(GluArgs p, int 
     for (int i = 0; i < 8; ++i) a.v[i] = gate.v[i] * sigmoid(gate.v[i]) * up.v[i];
     const uint32_t top = max4(abs_top(a));
     uint32_t code = fp4_scale(top);
-    uint32_t q = fp4_codes(scaled(a, 1.0f - SLACK), code);
-    const float amax = __builtin_bit_cast(float, top);
-    bool near = q != fp4_codes(scaled(a, 1.0f + SLACK), code);
-    near |= fp4_scale(abs_bits(amax * (1.0f - SLACK))) != fp4_scale(abs_bits(amax * (1.0f + SLACK)));
-    float low = gate.v[0];
+    float low = 0.0f;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) low = fminf(low, gate.v[i]);
+    for (int i = 0; i < 8; ++i) low = fminf(low, gate.v[i]);
+    const float slack = __builtin_fmaf(__builtin_bit_cast(float, max4(abs_bits(low))), 0x1p-23f, 0x1p-20f);
+    uint32_t q = fp4_codes(scaled(a, 1.0f - slack), code);
+    const float amax = __builtin_bit_cast(float, top);
+    bool near = q != fp4_codes(scaled(a, 1.0f + slack), code);
+    near |= fp4_scale(abs_bits(amax * (1.0f - slack))) != fp4_scale(abs_bits(amax * (1.0f + slack)));
     if (__any(low < LOW_GATE || top < TINY)) {  // but a block of zeros is exact
       bool zero = true;
 #pragma unroll
