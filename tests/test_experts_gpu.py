@@ -310,3 +310,41 @@ def test_agrees_with_the_grouped_products(dev):
     # FP8 rounds x and a by 2^-4 at most each, by about 0.6 2^-4 / sqrt(3) in the 2-norm; x enters both g and u
     off = (y.double() - z.double()).norm() / y.double().norm()
     assert off < 3 * 2.0 ** -4, off.item()
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("case", LAYERS)
+def test_few_compute_units_give_the_same_bits(dev, case, fp4):
+    """As few compute units as make every workgroup take more rows of the weights, several
+    tiles and several experts in turn."""
+    _say(f"experts on few compute units {case} fp4={fp4}")
+    t, k, g, hidden, inner = case
+    g = min(g, 64)
+    b1, sfb1, _ = _weights(fp4, g, 2 * inner, hidden, 1, dev)
+    b2, sfb2, _ = _weights(fp4, g, hidden, inner, 2, dev)
+    ids = _ids(t, k, g, t + g)
+    x = torch.randn(t, hidden, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).to(dev)
+    w = torch.rand(t, k, generator=torch.Generator().manual_seed(4)).to(dev)
+    want = _run(x, ids, w, b1, sfb1, b2, sfb2, dev)
+    for cus in (1, 3):
+        dg.set_num_cus(cus)
+        try:
+            y = _run(x, ids, w, b1, sfb1, b2, sfb2, dev)
+        finally:
+            dg.set_num_cus(0)
+        assert torch.equal(y.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("t", [2, 11, 31, 90])
+def test_long_rows(dev, t, fp4):
+    """Rows of 4224, the first length that takes 32 columns a workgroup on 256 compute units,
+    with an odd number of blocks."""
+    _say(f"experts, long rows t={t} fp4={fp4}")
+    g, k, hidden, inner = 3, 2, 4224, 384
+    b1, sfb1, v1 = _weights(fp4, g, 2 * inner, hidden, 1, dev)
+    b2, sfb2, v2 = _weights(fp4, g, hidden, inner, 2, dev)
+    ids = _ids(t, k, g, t)
+    x = torch.randn(t, hidden, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).to(dev)
+    w = torch.rand(t, k, generator=torch.Generator().manual_seed(4)).to(dev)
+    _check(_run(x, ids, w, b1, sfb1, b2, sfb2, dev), x, ids, w.cpu().numpy(), v1, v2)

@@ -356,3 +356,37 @@ def test_two_streams_at_once(dev):
     torch.cuda.synchronize()
     for o, d in zip(ops, outs):
         _check(_bits(d).view(np.uint16), *o, k, False, "stream")
+
+
+@pytest.mark.parametrize("k", [128, 256, 384, 640])
+def test_few_workgroups_give_the_same_bits(dev, k):
+    """One, three and eight workgroups for all tiles: tiles of one, two and three steps that
+    follow one another in a workgroup's pipeline, valid rows that end next to the copies of
+    the K loop."""
+    _say(f"few workgroups, k={k}")
+    n, g = 640, 5
+    b, sfb = _codes(4, (g,), n, k)
+    flat, sf_flat = _codes(5, (), 1280, k)
+    many, sf_many = _codes(6, (g,), 300, k)
+    bd, sfbd, ad, sfad, md, sfmd = _put(dev, b, sfb, flat, sf_flat, many, sf_many)
+    ids = torch.from_numpy(_layout([200, 0, 129, 512, 100], 1280)).to(dev)
+    counts = torch.tensor([64, 65, 300, 0, 193], dtype=torch.int32, device=dev)
+
+    def calls():
+        d = [_out(1280, n), _out(1280, n), _out(g, 300, n), _out(1280, n)]
+        dg.fp4_gemm_nt(ad, sfad, bd[1], sfbd[1], d[0])
+        dg.m_grouped_fp4_gemm_nt_contiguous(ad, sfad, bd, sfbd, d[1], ids)
+        dg.m_grouped_fp4_gemm_nt_masked(md, sfmd, bd, sfbd, d[2], counts)
+        dg.m_grouped_fp4_gemm_nt_nopad(ad, sfad, bd, sfbd, d[3], counts)
+        return [_bits(v) for v in d]
+
+    want = calls()
+    _check(want[0].view(np.uint16), flat, sf_flat, b[1], sfb[1], k, False, "dense")
+    for cus in (1, 3, 8):
+        dg.set_num_cus(cus)
+        try:
+            got = calls()
+        finally:
+            dg.set_num_cus(0)
+        for what, x, y in zip(("dense", "contiguous", "masked", "no padding"), got, want):
+            np.testing.assert_array_equal(x, y, f"{what}, {cus} workgroups")

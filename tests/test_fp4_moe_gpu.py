@@ -233,3 +233,62 @@ def test_a_block_in_fp4(dev, layout):
         want[i] += float(weights[i, j]) * flat_yp[r]
     err = 8 * 2.0 ** -24 * M.combine_mag(flat_yp, row_of, _f64(weights))
     assert np.all(np.abs(_f64(y) - want) <= bf16_ulp(np.abs(want) + err) / 2 + err)
+
+
+@pytest.mark.parametrize("layout", ["masked", "nopad", "contiguous"])
+def test_a_captured_block(dev, layout):
+    """Quantiser, dispatch, products, activation, combine and an expert layer over the same
+    weights in one graph, replayed between eager calls with other tokens, ids and weights: each
+    replay gives the eager calls' bits."""
+    _say(f"a captured block in FP4, {layout}")
+    t, k, g, hidden, inner = 20, 3, 5, 256, 384
+    plan, _, ids = _moved(layout, t, k, g, hidden, {"masked": t}.get(layout), dev)
+    master = _randn(g, hidden, inner, seed=5, scale=0.06, dtype=torch.float32)
+    x = _randn(t, hidden, seed=3)
+    weights = torch.rand(t, k, device=dev)
+
+    def operand(*shape):
+        *lead, m, c = shape
+        return (torch.zeros(*lead, m, c // 2, dtype=torch.uint8, device=dev),
+                torch.zeros(*lead, c // 128, dg.get_tma_aligned_size(m, 4), dtype=torch.int32, device=dev))
+
+    b1 = dg.quantize_fp4(_randn(g, 2 * inner, hidden, seed=4, scale=0.06), *operand(g, 2 * inner, hidden))
+    b2 = operand(g, hidden, inner)
+    gemm = getattr(dg, f"m_grouped_fp4_gemm_nt_{layout}")
+    lead = plan.rows_shape[:-1]
+    gu, yp = (torch.zeros(*lead, n, dtype=torch.bfloat16, device=dev) for n in (2 * inner, hidden))
+    q1, q2 = operand(*lead, hidden), operand(*lead, inner)
+    y, z = (torch.zeros(t, hidden, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    back = torch.zeros(g, hidden, inner, dtype=torch.bfloat16, device=dev)
+    of = plan.grouped_layout if layout == "contiguous" else plan.group_rows
+    ws = moe.experts_workspace(t, k, g, inner, dev)
+
+    def block():
+        dg.quantize_fp4(master, *b2)
+        moe.dispatch_fp4(plan, x, *q1, topk_ids=ids)
+        gemm(*q1, *b1, gu, of)
+        moe.swiglu_fp4(gu, *q2, rows=of, layout=layout)
+        gemm(*q2, *b2, yp, of)
+        moe.combine(plan, yp, y, weights=weights)
+        moe.experts(x, ids, weights, *b1, *b2, z, ws)
+        dg.dequantize_fp4(*b2, back)
+
+    block()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        block()
+    for seed in range(4):
+        x.copy_(_randn(t, hidden, seed=70 + seed))
+        ids.copy_(torch.from_numpy(np.random.default_rng(seed).integers(-1, g, (t, k)).astype(np.int32)))
+        master.mul_(-1.25)
+        weights.uniform_()
+        block()
+        want = [v.clone() for v in (y, z, back)]
+        for v in (y, z, back, gu, yp, ws, *b2):
+            v.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, ref in zip((y, z, back), want):
+            assert torch.equal(got.view(torch.int16), ref.view(torch.int16))
+        assert y.abs().sum() > 0 and z.abs().sum() > 0
