@@ -12,15 +12,24 @@
 //
 // Which 32 values a group holds is free as long as both operands hold the same. Of a
 // step's 256 the j-th of two MFMAs (j = 0, 1) takes blocks 2g + j: a group's two
-// blocks have two successive bytes of one scale word, and a 16-bit read per 16 rows
-// gives the lanes all that both MFMAs need, byte j of it for the j-th. (With the j-th
-// MFMA on blocks 4j + g every lane would need another byte of its word: a transpose
-// between lanes, 36 instructions a step, that cost 8% of the time.)
+// blocks have two successive bytes of one scale word, so that a byte permutation puts
+// the scales of two 16-row bands and both MFMAs into one register: 6 of them and 3
+// reads a step, the words lying in LDS with a row of four bands side by side. (With the
+// j-th MFMA on blocks 4j + g every lane would need another byte of its word: a
+// transpose between lanes, 36 instructions a step, that cost 8% of the time.)
 //
-// A persistent kernel over 256 x 256 tiles; a K step is 256 values, 128-byte rows of
-// either operand, in one of two LDS stages that direct-to-LDS loads fill one to two
-// steps ahead, with one barrier a step (see the K loop): the pipeline of
-// dg_kernel.hip, whose stages hold as many bytes and half the values.
+// A persistent kernel over 256 x 256 tiles, a 128 x 64 part of one a wave; a K step is
+// 256 values, 128-byte rows of either operand, in one of two LDS stages that
+// direct-to-LDS loads fill a step and a half ahead (see the K loop). Two stages of 68
+// KB are what LDS holds; smaller tiles read more of either operand for a product.
+//
+// What bounds it (16384 x 4096 x 7168 in 221 us, 4.35 PFLOP/s): matrix cores and
+// LDS reads alone take 147 us (6.5 PFLOP/s; a loop of these MFMAs alone, with operands
+// of random bits, 7.3: they draw the power), a stream of operands that all hit the L1
+// 25 us more, from L2 another 26 (its misses 5 of them), the stores 18. 4096 x 7168 x
+// 2048 (43 us) is two rounds of 224 tiles of 256 possible and 10 us of stores. With
+// few rows (16 groups of up to 32 rows, 7168 x 2048, 25 us) reading B bounds it, at 4.9
+// TB/s.
 
 #include "dg_device.h"
 

@@ -17,6 +17,14 @@
 // cores' registers, lane by lane a row, take the L1 four times the accesses: one
 // 16-byte piece each, 3.4 TB/s where tokens' rows come the same way.
 //
+// What bounds it: a compute unit takes some 40 GB/s together, whether two or five
+// steps are on their way, so the tokens' or activations' bytes (16 tokens: half the
+// weights' in the first launch, as many in the second) and the processors' turns add to
+// the weights' time. An FP8 batch, 61 tokens and 32 experts of 7168 x 2048:
+// 180 us (5.2 TB/s of weights) and 101 (4.7); weights alone 164 and 79. One token,
+// eight experts in FP4: 28 and 18 us, of which about 5 each are a launch's lists of
+// who is where, one read from memory after the other.
+//
 // A step is 128 bytes of each row: 128 values of FP8, or two blocks of 128 of FP4.
 //
 // v_mfma_f32_16x16x32_bf16: the first operand's lane (r, g) = (lane % 16, lane /

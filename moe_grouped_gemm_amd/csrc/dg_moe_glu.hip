@@ -133,7 +133,10 @@ __device__ __forceinline__ F8 scaled(const F8& a, float by) {
   return r;
 }
 
-// Bound by memory: 4 bytes read and 1/2 + 1/32 written a value.
+// Bound by memory and the vector units about alike: 4 bytes read and 1/2 + 1/32
+// written a value, and some 90 operations (exponential, reciprocal, two roundings to
+// codes). 32000 rows of 2048: 57 us, 5.2 TB/s (295 MB); with a margin of 2^-17 for
+// all gates, 6 times as many recomputed values, 61.
 template <bool MANY>
 __global__ __launch_bounds__(GLU_THREADS) void swiglu_fp4_kernel(GluArgs p, int row_step, int chunk) {
   const size_t I = p.inner;

