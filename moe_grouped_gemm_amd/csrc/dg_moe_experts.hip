@@ -51,10 +51,10 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 // A pair is known by its first slot; a token that names an expert twice is one pair
 // with the weights' sum.
 struct ExpertEntry {
-  int expert, begin, count, pad;
+  int expert, begin, count, first;  // its pairs, and the slot of the first
 };
 struct ExpertPlan {
-  int experts, pairs, pad[2];
+  int experts, pad[3];
   ExpertEntry entry[MAX_FEW_PAIRS];
   int slot[MAX_FEW_PAIRS];
   float weight[MAX_FEW_PAIRS];
@@ -316,7 +316,9 @@ __device__ void write_plan(const ExpertsArgs& p, const UpLists& l, int experts, 
       if (pair) f(i, e, before + rank);
     }
   };
-  for_pairs([](int, int, int) {});
+  for_pairs([&](int i, int e, int at) {
+    if (at == 0) plan->entry[order[e]].first = i;
+  });
   int pairs = 0;
   for (int r0 = 0; r0 < experts; r0 += 64) {
     const int r = r0 + lane, e = r < experts ? l.active[r] : 0, has = r < experts ? next[e] : 0;
@@ -326,7 +328,9 @@ __device__ void write_plan(const ExpertsArgs& p, const UpLists& l, int experts, 
       if (lane >= d) upto += v;
     }
     if (r < experts) {
-      plan->entry[r] = ExpertEntry{e, pairs + upto - has, has, 0};
+      plan->entry[r].expert = e;
+      plan->entry[r].begin = pairs + upto - has;
+      plan->entry[r].count = has;
       next[e] = pairs + upto - has;
     }
     pairs += __shfl(upto, 63);
@@ -342,7 +346,6 @@ __device__ void write_plan(const ExpertsArgs& p, const UpLists& l, int experts, 
   });
   if (lane == 0) {
     plan->experts = experts;
-    plan->pairs = pairs;
   }
 }
 
@@ -590,18 +593,19 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
   float* const mine = sums + wave * TOKENS * STRIDE;
   for (int i = lane; i < p.tokens * STRIDE; i += 64) mine[i] = 0.0f;
 
-  const int experts = plan->experts, pairs = plan->pairs;
-  for (int i = tid; i < pairs; i += DOWN_THREADS) {
+  // What the plan may hold is read before it is known how much of that it does hold: one
+  // way to memory, not three.
+  const int n = p.tokens * p.top_k, most = min(n, p.num_groups), experts = plan->experts;
+  for (int i = tid; i < n; i += DOWN_THREADS) {
     sums_at[i] = (uint16_t)(plan->slot[i] / p.top_k * (STRIDE / 4));
     pair_weights[i] = plan->weight[i];
   }
   // The items: an expert's pairs 16 NT at a time, in order.
   int total = 0;
-  for (int r0 = 0; r0 < experts; r0 += DOWN_THREADS) {
+  for (int r0 = 0; r0 < most; r0 += DOWN_THREADS) {
     const int at = r0 + tid;
-    ExpertEntry entry{0, 0, 0, 0};
-    if (at < experts) entry = plan->entry[at];
-    const int has = (entry.count + 16 * NT - 1) / (16 * NT);
+    const ExpertEntry entry = plan->entry[min(at, most - 1)];
+    const int has = at < experts ? (entry.count + 16 * NT - 1) / (16 * NT) : 0;
     int upto = has;
     for (int d = 1; d < 64; d <<= 1) {
       const int v = __shfl_up(upto, d);
@@ -616,7 +620,7 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
     }
     for (int i = 0; i < has; ++i) {
       const int begin = entry.begin + 16 * NT * i, count = min(entry.count - 16 * NT * i, 16 * NT);
-      const int tile = act_tile(p, entry.expert, NT * i, plan->slot[begin]);
+      const int tile = act_tile(p, entry.expert, NT * i, i == 0 ? entry.first : plan->slot[begin]);
       const int tile2 = count > 16 ? act_tile(p, entry.expert, NT * i + 1, plan->slot[begin + 16]) : tile;
       items[before + i] = DownItem{entry.expert << 8 | count, begin, tile, tile2};
     }

@@ -145,9 +145,9 @@ __global__ __launch_bounds__(GLU_THREADS) void swiglu_fp4_kernel(GluArgs p, int 
     const uint16_t* src = p.gu + row * 2 * I + b * QBLOCK + l16 * 8;
     const u32x4 gate_raw = load_stream16(src), up_raw = load_stream16(src + I);
     const F8 gate = unpack8(gate_raw), up = unpack8(up_raw);
-    F8 a;
+    F8 a;  // (with a sigmoid that is one operation short, and too small below LOW_GATE)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a.v[i] = gate.v[i] * sigmoid(gate.v[i]) * up.v[i];
+    for (int i = 0; i < 8; ++i) a.v[i] = gate.v[i] * __builtin_amdgcn_rcpf(1.0f + __expf(-gate.v[i])) * up.v[i];
     const uint32_t top = max4(abs_top(a));
     uint32_t code = fp4_scale(top);
     float low = 0.0f;
