@@ -121,6 +121,16 @@ def test_swiglu_fp4_many_values(dev, scale):
     _glu(dev, ("dense", 1, 3000, 2048), gu)
 
 
+def test_swiglu_fp4_many_values_of_low_gates(dev):
+    """Gates between -87 and -20, whose exponential is off by up to 2^-16: two million values."""
+    _say("swiglu_fp4 many values of low gates")
+    gen = torch.Generator().manual_seed(9)
+    base = -21.0 - 65.0 * torch.rand(1000, 64, 1, generator=gen)               # a block's gates are alike
+    gate = (base + 2.0 * torch.rand(1000, 64, 32, generator=gen) - 1.0).reshape(1000, 2048)
+    up = torch.randn(1000, 2048, generator=gen) * 2.0 ** 60
+    _glu(dev, ("dense", 1, 1000, 2048), torch.cat([gate, up], 1).to(torch.bfloat16).to(dev))
+
+
 def test_swiglu_fp4_on_the_borders(dev):
     """silu(g) u of chosen g and u next to borders between codes, and next to those
     between scales."""
