@@ -31,6 +31,8 @@
 // few rows (16 groups of up to 32 rows, 7168 x 2048, 25 us) reading B bounds it, at 4.9
 // TB/s.
 
+#include <algorithm>
+
 #include "dg_device.h"
 
 namespace dg {
@@ -55,8 +57,20 @@ static_assert(Cfg::NW == 8 && Cfg::BM == 256 && Cfg::BN == 256, "load split belo
 
 }  // namespace mx
 
+namespace mx {
+
+// The kernel for few tiles (see there).
+struct Few {
+  static constexpr int BM = 64, BN = 64, SLOTS = 1;
+  static constexpr int NW = 4, THREADS = NW * 64;
+};
+
+}  // namespace mx
+
 template <>
 constexpr int A_PACK_SHIFT<mx::Cfg> = 1;
+template <>
+constexpr int A_PACK_SHIFT<mx::Few> = 1;
 
 namespace mx {
 
@@ -231,58 +245,61 @@ __device__ __forceinline__ void scales_at(int (&to)[N], uint32_t off, uint32_t p
 }
 
 template <int MT, int NT, int H>
-__device__ __forceinline__ f32x4 mfma(const Frag& b, const Frag& a, const f32x4& c, const Scales& s) {
+__device__ __forceinline__ f32x4 mfma(const Frag& b, const Frag& a, const f32x4& c, int sb, int sa) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(b.h[H]), operand(a.h[H]), c, 4, 4, 2 * (NT & 1) + H,
-                                                          s.b[NT / 2], 2 * (MT & 1) + H, s.a[MT / 2]);
+                                                          sb, 2 * (MT & 1) + H, sa);
 }
 
-// Writes a wave's finished 128 x 64 sub-tile as BF16 (round to nearest even), valid rows
-// only. A lane has 4 columns of a row of each 16-column block; exchanges between lane
-// halves, quarters and halves of quarters give it 8 of a row's 64, so that each store
-// covers whole 128-byte segments of 8 rows. (Without the last exchange, 64 bytes of 16
-// rows a store, the masked decode took 1 to 2% more.)
+// Writes 16 rows of 64 columns as BF16 (round to nearest even), the rows of `valid` only;
+// `rows` is the first row's first column. A lane has 4 columns of a row of each 16-column
+// block; exchanges between lane halves, quarters and halves of quarters give it 8 of a
+// row's 64, so that each store covers whole 128-byte segments of 8 rows. (Without the
+// last exchange, 64 bytes of 16 rows a store, the masked decode took 1 to 2% more.)
+__device__ __forceinline__ void store_band(uint16_t* rows, int n, uint32_t valid, const f32x4 (&v)[4], int lane) {
+  const int r = lane & 15, q = lane >> 4;
+  i32x4 w[2];  // columns 32 np + 8 q .. + 7 of row r
+#pragma unroll
+  for (int np = 0; np < 2; ++np)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      // Lanes of quarter q hold columns 4 q + 2 i of either block. The lanes' upper
+      // half's first block against the lower half's second, then odd quarters' against
+      // even ones': quarter q has columns 8 q .. 8 q + 7 of the 32.
+      const f32x4 &x = v[2 * np], &y = v[2 * np + 1];
+      const auto h = __builtin_amdgcn_permlane32_swap(pack_bf16x2(x[2 * i], x[2 * i + 1]),
+                                                      pack_bf16x2(y[2 * i], y[2 * i + 1]), false, false);
+      const auto t = __builtin_amdgcn_permlane16_swap(h[0], h[1], false, false);
+      w[np][i] = (int)t[0];
+      w[np][2 + i] = (int)t[1];
+    }
+  // The second 32 columns of rows 0 .. 7 against the first of rows 8 .. 15 (a rotation of
+  // each 16 lanes by 8, written to 8 of them).
+  i32x4 out[2];  // columns 32 (r / 8) + 8 q .. + 7 of rows r % 8 and 8 + r % 8
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    out[0][i] = __builtin_amdgcn_update_dpp(w[0][i], w[1][i], 0x128, 0xF, 0xC, false);
+    out[1][i] = __builtin_amdgcn_update_dpp(w[1][i], w[0][i], 0x128, 0xF, 0x3, false);
+  }
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int row = (r & 7) + 8 * half;
+    // Past the caches' reach: the operands stay there (4096 x 7168 x 2048: 43 us, with
+    // plain stores 46; the masked decode 39 and 41).
+    if ((valid >> row) & 1)
+      __builtin_nontemporal_store(out[half], (global_i32x4*)(rows + (size_t)row * n + 32 * (r >> 3) + 8 * q));
+  }
+}
+
+// A wave's finished 128 x 64 sub-tile.
 template <int KIND>
 __device__ __forceinline__ void store_tile(const GemmArgs& p, const TileRef& cur, const RowMask& cm,
                                            const f32x4 (&acc)[Cfg::MT][Cfg::NT], int wm0, int wn0, int lane) {
-  const int r = lane & 15, q = lane >> 4;
+  static_assert(Cfg::NT == 4, "a band of 64 columns");
 #pragma unroll
   for (int mt = 0; mt < Cfg::MT; ++mt) {
     const uint32_t valid = band_rows<Cfg, KIND>(cur, cm, wm0, mt);
-    if (valid == 0) continue;
-    i32x4 w[2];  // columns 32 np + 8 q .. + 7 of row r
-#pragma unroll
-    for (int np = 0; np < 2; ++np) {
-      const f32x4 u = acc[mt][2 * np], v = acc[mt][2 * np + 1];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        // Lanes of quarter q hold columns 4 q + 2 i of either block. The lanes' upper
-        // half's first block against the lower half's second, then odd quarters' against
-        // even ones': quarter q has columns 8 q .. 8 q + 7 of the 32.
-        const auto h = __builtin_amdgcn_permlane32_swap(pack_bf16x2(u[2 * i], u[2 * i + 1]),
-                                                        pack_bf16x2(v[2 * i], v[2 * i + 1]), false, false);
-        const auto t = __builtin_amdgcn_permlane16_swap(h[0], h[1], false, false);
-        w[np][i] = (int)t[0];
-        w[np][2 + i] = (int)t[1];
-      }
-    }
-    // The second 32 columns of rows 0 .. 7 against the first of rows 8 .. 15 (a rotation of
-    // each 16 lanes by 8, written to 8 of them).
-    i32x4 out[2];  // columns 32 (r / 8) + 8 q .. + 7 of rows r % 8 and 8 + r % 8
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      out[0][i] = __builtin_amdgcn_update_dpp(w[0][i], w[1][i], 0x128, 0xF, 0xC, false);
-      out[1][i] = __builtin_amdgcn_update_dpp(w[1][i], w[0][i], 0x128, 0xF, 0x3, false);
-    }
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int row = (r & 7) + 8 * half;
-      if ((valid >> row) & 1) {
-        uint16_t* at = cur.d + (size_t)(cur.m0 + wm0 + mt * 16 + row) * p.n + cur.n0 + wn0 + 32 * (r >> 3) + 8 * q;
-        // Past the caches' reach: the operands stay there (4096 x 7168 x 2048: 43 us, with
-        // plain stores 46; the masked decode 39 and 41).
-        __builtin_nontemporal_store(out[half], (global_i32x4*)at);
-      }
-    }
+    if (valid != 0)
+      store_band(cur.d + (size_t)(cur.m0 + wm0 + mt * 16) * p.n + cur.n0 + wn0, p.n, valid, acc[mt], lane);
   }
 }
 
@@ -365,7 +382,7 @@ __device__ __forceinline__ void mainloop(const GemmArgs& p, const TileSrc& t0, c
         if constexpr (mt < NB) {
           static_for<0, 2 * Cfg::NT>([&](auto I) {
             constexpr int h = decltype(I)::value / Cfg::NT, nt = decltype(I)::value % Cfg::NT;
-            acc[mt][nt] = mfma<mt, nt, h>(bf[nt], af[mt % 4], acc[mt][nt], scales);
+            acc[mt][nt] = mfma<mt, nt, h>(bf[nt], af[mt % 4], acc[mt][nt], scales.b[nt / 2], scales.a[mt / 2]);
           });
           // The reads two bands ahead and this band's share of the refill first.
           if constexpr (mt + 2 < NB) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // DS reads
@@ -377,10 +394,10 @@ __device__ __forceinline__ void mainloop(const GemmArgs& p, const TileSrc& t0, c
       static_for<0, Cfg::NT>([&](auto NT) {
         constexpr int nt = decltype(NT)::value;
         if constexpr (NB == Cfg::MT) {
-          acc[6][nt] = mfma<6, nt, 0>(bf[nt], af[2], acc[6][nt], scales);
-          acc[7][nt] = mfma<7, nt, 0>(bf[nt], af[3], acc[7][nt], scales);
-          acc[6][nt] = mfma<6, nt, 1>(bf[nt], af[2], acc[6][nt], scales);
-          acc[7][nt] = mfma<7, nt, 1>(bf[nt], af[3], acc[7][nt], scales);
+          acc[6][nt] = mfma<6, nt, 0>(bf[nt], af[2], acc[6][nt], scales.b[nt / 2], scales.a[6 / 2]);
+          acc[7][nt] = mfma<7, nt, 0>(bf[nt], af[3], acc[7][nt], scales.b[nt / 2], scales.a[7 / 2]);
+          acc[6][nt] = mfma<6, nt, 1>(bf[nt], af[2], acc[6][nt], scales.b[nt / 2], scales.a[6 / 2]);
+          acc[7][nt] = mfma<7, nt, 1>(bf[nt], af[3], acc[7][nt], scales.b[nt / 2], scales.a[7 / 2]);
         }
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (nt == 0) {
@@ -514,10 +531,212 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) fp4_gemm_nt_kernel(GemmArgs p
   wait_vmcnt_0();
 }
 
-}  // namespace mx
+// ---------------------------------------------------------------------------
+// Few tiles
+// ---------------------------------------------------------------------------
+
+// 64 x 64 tiles, the K of each shared by a workgroup's four waves, step by step in
+// turn: each wave loads both operands of its steps into a ring of its own, one step ahead,
+// and needs no barrier; at a tile's end their sums meet in LDS, added in order. Sixteen
+// times the tiles and a fourth of the steps of the kernel above, and four times its
+// operand traffic.
+constexpr int FEW_SA = (Few::BM + Few::BN) * ROW_BYTES;  // LDS of a step: A, B, the words of A [block][r][band] and B
+constexpr int FEW_SB = FEW_SA + STEP_BLOCKS * Few::BM * 4;
+constexpr int FEW_STEP = FEW_SB + STEP_BLOCKS * Few::BN * 4;
+constexpr int FEW_LOADS = 2 * 8 + 2 * STEP_BLOCKS;
+static_assert(2 * FEW_STEP >= 4 * 4 * 64 * 16, "a wave's sums in its ring's place");
+
+// Tile t of the contiguous layout: a 128-row block belongs to its first row's group.
+__device__ __forceinline__ TileRef few_contiguous_tile(const GemmArgs& p, int t) {
+  TileRef tr;
+  int mb, nb;
+  raster(t, p.m_blocks, p.n_blocks, 4, mb, nb);
+  tr.m0 = uniform_int(mb * Few::BM);
+  tr.n0 = uniform_int(nb * Few::BN);
+  tr.load_rows = tr.valid_rows = p.m;
+  tr.a = p.a;
+  tr.sfa = p.sfa;
+  tr.d = p.d;
+  tr.group = aux_scalar(p.aux, tr.m0 & ~127);
+  tr.active = tr.group >= 0 && tr.group < p.num_groups;
+  return tr;
+}
 
 template <int KIND>
-static hipError_t launch_mx(const GemmArgs& args, int num_cus, hipStream_t stream) {
+__global__ void __launch_bounds__(Few::THREADS, 1) fp4_gemm_few_kernel(GemmArgs p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Few::NW * 2 * FEW_STEP];
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int k_blocks = p.k / BK, steps = (k_blocks + STEP_BLOCKS - 1) / STEP_BLOCKS;
+  const int mine = max((steps - wave + Few::NW - 1) / Few::NW, 0);
+  int num_tiles = p.num_tiles;
+  [[maybe_unused]] int* s_prefix = nullptr;
+  if constexpr (counts_on_device(KIND)) {
+    s_prefix = group_table<Few, KIND>(p, tid);
+    num_tiles = s_prefix[p.num_groups];
+  }
+  uint8_t* const ring = lds + wave * 2 * FEW_STEP;
+  const uint32_t base = (uint32_t)(uintptr_t)(lds_void*)ring, row = (uint32_t)p.k / 2;
+  // The lane's 16 bytes of each 8 rows of a load, rows 8 j .. (see lane_offsets()).
+  uint32_t load_at[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int row0 = 8 * j + (lane >> 3), chunk = (lane & 7) ^ ((row0 >> 1) & 7);
+    load_at[j] = (uint32_t)(lane >> 3) * row + (uint32_t)((chunk & 3) * 2 + (chunk >> 2)) * 16u;
+  }
+  const uint32_t word_row = (uint32_t)((lane & 3) * 16 + (lane >> 2));
+  const uint32_t c0 = (uint32_t)lds_offset(r, g), c1 = (uint32_t)lds_offset(r, g + 4);
+  const uint32_t words_at = (uint32_t)((g >> 1) * 256 + r * 16), pick = (g & 1) ? 0x07060302u : 0x05040100u;
+
+  for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
+    TileRef cur;
+    [[maybe_unused]] int id = 0;
+    if constexpr (KIND == KIND_CONTIGUOUS) {
+      cur = few_contiguous_tile(p, t);
+      if (!cur.active) continue;
+      cur.b = p.b + (size_t)cur.group * p.n * p.k;
+      id = p.aux[cur.m0 + lane];
+    } else {
+      int at = t;
+      cur = next_active<Few, KIND>(p, at, gridDim.x, num_tiles, s_prefix);  // (every tile is active)
+    }
+    const int rows = uniform_int(min(cur.load_rows - cur.m0, Few::BM)), bands = (rows + 15) / 16;
+    const __amdgpu_buffer_rsrc_t a = buffer_rsrc(cur.a + (size_t)cur.m0 * row, (uint32_t)rows * row);
+    const __amdgpu_buffer_rsrc_t b = buffer_rsrc(p.b + ((size_t)cur.group * p.n + cur.n0) * row, Few::BN * row);
+    // The group's words. Those of rows past the tile's are other rows', and reach no row
+    // that is stored; a second block past the last reads as zero (see stage_src()).
+    const uint32_t sa_bytes = (uint32_t)k_blocks * p.ld_sfa * 4, sb_bytes = (uint32_t)k_blocks * p.ld_sfb * 4;
+    const float* const sfa = KIND == KIND_MASKED ? cur.sfa : p.sfa;
+    const __amdgpu_buffer_rsrc_t sa = buffer_rsrc(sfa, sa_bytes);
+    const __amdgpu_buffer_rsrc_t sb = buffer_rsrc(p.sfb + (size_t)cur.group * k_blocks * p.ld_sfb, sb_bytes);
+    const uint32_t sa_at = ((uint32_t)(cur.sfa - sfa) + cur.m0 + word_row) * 4, sb_at = (cur.n0 + word_row) * 4;
+    auto load = [&](int i) {
+      const int step = i * Few::NW + wave;
+      const uint32_t st = base + (i & 1) * FEW_STEP, skip = (uint32_t)step * ROW_BYTES;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(a, lds_dest(st + j * 1024), 16, load_at[j & 1] + 8 * j * row, skip, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(b, lds_dest(st + Few::BM * ROW_BYTES + j * 1024), 16,
+                                                 load_at[j & 1] + 8 * j * row, skip, 0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < STEP_BLOCKS; ++j) {
+        const uint32_t blk = (uint32_t)(step * STEP_BLOCKS + j);
+        dma4(sa, sa_at + blk * p.ld_sfa * 4, st + FEW_SA + j * 256);
+        dma4(sb, sb_at + blk * p.ld_sfb * 4, st + FEW_SB + j * 256);
+      }
+    };
+    f32x4 acc[4][4];
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) acc[mt][nt] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    if (mine > 0) load(0);
+    for (int i = 0; i < mine; ++i) {
+      wait_lgkmcnt_0();  // the step before has been read
+      asm volatile("" ::: "memory");
+      if (i + 1 < mine) {
+        load(i + 1);
+        wait_vmcnt<FEW_LOADS>();
+      } else {
+        wait_vmcnt_0();
+      }
+      asm volatile("" ::: "memory");
+      const uint8_t* const st = ring + (i & 1) * FEW_STEP;
+      auto frag = [&](int at) {
+        Frag f;
+        f.h[0] = *reinterpret_cast<const i32x4*>(st + at + c0);
+        f.h[1] = *reinterpret_cast<const i32x4*>(st + at + c1);
+        return f;
+      };
+      const i32x4 wa = *reinterpret_cast<const i32x4*>(st + FEW_SA + words_at);
+      const i32x4 wb = *reinterpret_cast<const i32x4*>(st + FEW_SB + words_at);
+      const int scales_a[2] = {(int)__builtin_amdgcn_perm(wa[1], wa[0], pick), (int)__builtin_amdgcn_perm(wa[3], wa[2], pick)};
+      const int scales_b[2] = {(int)__builtin_amdgcn_perm(wb[1], wb[0], pick), (int)__builtin_amdgcn_perm(wb[3], wb[2], pick)};
+      Frag bf[4];
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) bf[nt] = frag(Few::BM * ROW_BYTES + nt * 16 * ROW_BYTES);
+      static_for<0, 4>([&](auto MT) {
+        constexpr int mt = decltype(MT)::value;
+        if (mt >= bands) return;
+        const Frag af = frag(mt * 16 * ROW_BYTES);
+        static_for<0, 8>([&](auto I) {
+          constexpr int h = decltype(I)::value / 4, nt = decltype(I)::value % 4;
+          acc[mt][nt] = mfma<mt, nt, h>(bf[nt], af, acc[mt][nt], scales_b[nt / 2], scales_a[mt / 2]);
+        });
+      });
+    }
+    // The waves' sums, a band a wave.
+    auto sums_of = [&](int w) { return reinterpret_cast<f32x4*>(lds + w * 2 * FEW_STEP); };
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt)
+        if (mt < bands) sums_of(wave)[(mt * 4 + nt) * 64 + lane] = acc[mt][nt];
+    __syncthreads();
+    uint32_t valid;
+    if constexpr (KIND == KIND_CONTIGUOUS)
+      valid = (uint32_t)(__builtin_amdgcn_ballot_w64(id == cur.group) >> (16 * wave)) & 0xFFFFu;
+    else
+      valid = band_rows<Few, KIND>(cur, RowMask{0, 0}, 16 * wave, 0);
+    if (wave < bands && valid != 0) {
+      f32x4 v[4];
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+        v[nt] = sums_of(0)[(wave * 4 + nt) * 64 + lane];
+#pragma unroll
+        for (int w = 1; w < Few::NW; ++w) v[nt] += sums_of(w)[(wave * 4 + nt) * 64 + lane];
+      }
+      store_band(cur.d + (size_t)(cur.m0 + 16 * wave) * p.n + cur.n0, p.n, valid, v, lane);
+    }
+    __syncthreads();  // the sums have been read
+  }
+}
+
+}  // namespace mx
+
+// Tiles of 64 x 64 up to which a call takes those: three rounds of a whole chip's. In us,
+// with these and with the large ones: 512 x 2048 x 7168 (256 tiles) 10.1, 42.5; 1024 x 1024
+// x 1024 (256) 4.7, 12.9; 16 x 2176 x 2432 (34) 4.8, 14.0; 12 groups of 16 x 2304 x 640 (432)
+// 5.8, 8.1; 18 of 8 x 2304 x 5632 (648) 22.4, 26.6; 2048^3 (1024) 15.6, 18.4; 8 of up to 256
+// x 2048 x 2048 (1024) 20.0, 18.8; 16 of up to 32 x 7168 x 2048 (1792) 28.1, 25.3; 2048 x
+// 4096 x 4096 (2048) 44.8, 29.8. (Not by dg_get_num_cus(): the order of the sums differs.)
+constexpr long long FEW_TILES = 768;
+
+// Tiles that a call may have, of C's size.
+template <class C>
+static long long most_tiles(int kind, const GemmArgs& p) {
+  const long long m_blocks = (p.m + C::BM - 1) / C::BM, n_blocks = (p.n + C::BN - 1) / C::BN;
+  switch (kind) {
+    case KIND_MASKED:  // an upper bound for the grid's size, as for no padding; the kernel counts the tiles
+      return p.num_groups * m_blocks * n_blocks;
+    case KIND_NOPAD:  // each group adds at most one partial row block
+      return (m_blocks + p.num_groups) * n_blocks;
+    case KIND_CONTIGUOUS:
+      return C::SLOTS * m_blocks * n_blocks;
+    default:
+      return m_blocks * n_blocks;
+  }
+}
+
+template <int KIND>
+static hipError_t launch_few(GemmArgs args, int num_cus, hipStream_t stream) {
+  using C = mx::Few;
+  args.m_blocks = (args.m + C::BM - 1) / C::BM;
+  args.n_blocks = args.n / C::BN;
+  args.num_tiles = (int)most_tiles<C>(KIND, args);
+  const int grid = std::min(args.num_tiles, num_cus);
+  hipLaunchKernelGGL(mx::fp4_gemm_few_kernel<KIND>, dim3(grid), dim3(C::THREADS), 0, stream, args);
+  return hipGetLastError();
+}
+
+template <int KIND>
+static hipError_t launch_mx(GemmArgs args, int num_cus, hipStream_t stream) {
+  if (most_tiles<mx::Few>(KIND, args) <= FEW_TILES) return launch_few<KIND>(args, num_cus, stream);
+  using C = mx::Cfg;
+  args.m_blocks = (args.m + C::BM - 1) / C::BM;
+  args.n_blocks = (args.n + C::BN - 1) / C::BN;
+  args.num_tiles = (int)most_tiles<C>(KIND, args);
   auto kern = mx::fp4_gemm_nt_kernel<KIND>;
   int per_cu = 1;
   hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, kern, mx::Cfg::THREADS, 0);
@@ -530,21 +749,14 @@ static hipError_t launch_mx(const GemmArgs& args, int num_cus, hipStream_t strea
 }
 
 hipError_t launch_fp4(int kind, GemmArgs args, int num_cus, hipStream_t stream) {
-  using C = mx::Cfg;
-  args.m_blocks = (args.m + C::BM - 1) / C::BM;
-  args.n_blocks = (args.n + C::BN - 1) / C::BN;
   switch (kind) {
-    case KIND_MASKED:  // an upper bound for the grid's size, as for no padding; the kernel counts the tiles
-      args.num_tiles = args.num_groups * args.m_blocks * args.n_blocks;
+    case KIND_MASKED:
       return launch_mx<KIND_MASKED>(args, num_cus, stream);
-    case KIND_NOPAD:  // each group adds at most one partial row block
-      args.num_tiles = (args.m_blocks + args.num_groups) * args.n_blocks;
+    case KIND_NOPAD:
       return launch_mx<KIND_NOPAD>(args, num_cus, stream);
     case KIND_CONTIGUOUS:
-      args.num_tiles = C::SLOTS * args.m_blocks * args.n_blocks;
       return launch_mx<KIND_CONTIGUOUS>(args, num_cus, stream);
     default:
-      args.num_tiles = args.m_blocks * args.n_blocks;
       return launch_mx<KIND_DENSE>(args, num_cus, stream);
   }
 }

@@ -152,7 +152,9 @@ def _check(got_bits, a, sfa, b, sfb, k, whole, what):
         check_close(got_bits, ref, what, mag, k)
 
 
-DENSE = [(1, 128, 128), (15, 128, 384), (130, 384, 256), (257, 256, 512), (300, 640, 1152), (513, 128, 2048), (64, 512, 7168)]
+# Few tiles, and as many as take the large ones.
+DENSE = [(1, 128, 128), (15, 128, 384), (130, 384, 256), (257, 256, 512), (300, 640, 1152), (513, 128, 2048), (64, 512, 7168),
+         (1, 49280, 128), (15, 49280, 640), (257, 9984, 384), (513, 5632, 256), (64, 49280, 1152), (700, 4608, 2048)]
 
 
 @pytest.mark.parametrize("whole", [False, True])
@@ -182,10 +184,11 @@ def test_dense_many_tiles(dev):
     check_close(got[np.ix_(rows, cols)], ref, "sampled", mag, k)
 
 
+@pytest.mark.parametrize("n", [256, 24832])
 @pytest.mark.parametrize("k", [128, 896])
-def test_nan_scales_stay_in_their_rows(dev, k):
-    _say(f"NaN scales, K {k}")
-    m, n = 70, 256
+def test_nan_scales_stay_in_their_rows(dev, k, n):
+    _say(f"NaN scales, K {k}, N {n}")
+    m = 70
     a, sfa = _codes(5, (), m, k)
     b, sfb = _codes(6, (), n, k)
     sfa[k // 128 - 1, 3] |= 0xFF00                   # the second block of the last 128 values
@@ -198,10 +201,11 @@ def test_nan_scales_stay_in_their_rows(dev, k):
     np.testing.assert_array_equal(nan, want)
 
 
-def test_scales_at_their_ends(dev):
+@pytest.mark.parametrize("n", [128, 49280])
+def test_scales_at_their_ends(dev, n):
     """2^-127 times 2^127, and sums below BF16's smallest."""
-    _say("extreme scales")
-    m, n, k = 16, 128, 384
+    _say(f"extreme scales, N {n}")
+    m, k = 16, 384
     a, sfa = _codes(7, (), m, k, True)
     b, sfb = _codes(8, (), n, k, True)
     ones = sfa.copy(), sfb.copy()
@@ -224,7 +228,8 @@ def _layout(counts, m):
 
 
 @pytest.mark.parametrize("whole", [False, True])
-@pytest.mark.parametrize("counts,n,k", [([5, 0, 300, 128, 1], 256, 384), ([700], 128, 128), ([127, 129, 640], 640, 1024)])
+@pytest.mark.parametrize("counts,n,k", [([5, 0, 300, 128, 1], 256, 384), ([700], 128, 128), ([127, 129, 640], 640, 1024),
+                                        ([5, 0, 300, 128, 1], 3584, 384), ([700], 4992, 128), ([127, 129, 640], 2816, 1024)])
 def test_contiguous(dev, counts, n, k, whole):
     _say(f"contiguous {counts} n={n} k={k} whole={whole}")
     m, g = sum(-(-c // 128) * 128 for c in counts) + 128, len(counts)
@@ -241,10 +246,11 @@ def test_contiguous(dev, counts, n, k, whole):
         _check(got[rows], a[rows], sfa[:, :m][:, rows], b[e], sfb[e], k, whole, f"group {e}")
 
 
-def test_contiguous_ids_that_change_inside_blocks(dev):
+@pytest.mark.parametrize("n", [128, 4992])
+def test_contiguous_ids_that_change_inside_blocks(dev, n):
     """The row rule of the layout: a 128-row block is its first row's group's."""
-    _say("contiguous, ids that change inside blocks")
-    m, n, k, g = 640, 128, 256, 3
+    _say(f"contiguous, ids that change inside blocks, n={n}")
+    m, k, g = 640, 256, 3
     ids = np.random.default_rng(0).integers(-1, 5, m).astype(np.int32)
     ids[0], ids[128], ids[256], ids[384], ids[512] = 1, -1, 7, 2, 0
     a, sfa = _codes(3, (), m, k, True)
@@ -259,7 +265,9 @@ def test_contiguous_ids_that_change_inside_blocks(dev):
 
 @pytest.mark.parametrize("whole", [False, True])
 @pytest.mark.parametrize("counts,max_m,n,k", [([5, 0, 64, 63], 64, 128, 384), ([300, -2, 17, 999, 129], 300, 384, 256),
-                                              ([1] * 40, 8, 256, 1152), ([0, 0], 16, 128, 128), ([97, 160], 257, 128, 512)])
+                                              ([1] * 40, 8, 256, 1152), ([0, 0], 16, 128, 128), ([97, 160], 257, 128, 512),
+                                              ([300, -2, 17, 999, 129], 300, 2048, 256), ([1, 8] * 20, 8, 1280, 1152),
+                                              ([0, 0], 16, 24704, 128), ([97, 160], 257, 4992, 512)])
 def test_masked(dev, counts, max_m, n, k, whole):
     _say(f"masked {counts} of {max_m} n={n} k={k} whole={whole}")
     g = len(counts)
@@ -279,7 +287,9 @@ def test_masked(dev, counts, max_m, n, k, whole):
 
 @pytest.mark.parametrize("whole", [False, True])
 @pytest.mark.parametrize("counts,m,n,k", [([3, 0, 200, 31], 240, 256, 384), ([5, -4, 90, 400, 7], 260, 128, 640),
-                                          ([1, 2, 3] * 20, 120, 128, 256), ([513], 513, 384, 128)])
+                                          ([1, 2, 3] * 20, 120, 128, 256), ([513], 513, 384, 128),
+                                          ([5, -4, 90, 400, 7], 260, 4992, 640), ([1, 2, 3] * 20, 120, 896, 256),
+                                          ([513], 513, 4992, 128)])
 def test_nopad(dev, counts, m, n, k, whole):
     _say(f"nopad {counts} of {m} n={n} k={k} whole={whole}")
     g = len(counts)
@@ -358,13 +368,14 @@ def test_two_streams_at_once(dev):
         _check(_bits(d).view(np.uint16), *o, k, False, "stream")
 
 
+@pytest.mark.parametrize("n", [640, 2560])
 @pytest.mark.parametrize("k", [128, 256, 384, 640])
-def test_few_workgroups_give_the_same_bits(dev, k):
+def test_few_workgroups_give_the_same_bits(dev, k, n):
     """One, three and eight workgroups for all tiles: tiles of one, two and three steps that
     follow one another in a workgroup's pipeline, valid rows that end next to the copies of
     the K loop."""
-    _say(f"few workgroups, k={k}")
-    n, g = 640, 5
+    _say(f"few workgroups, n={n} k={k}")
+    g = 5
     b, sfb = _codes(4, (g,), n, k)
     flat, sf_flat = _codes(5, (), 1280, k)
     many, sf_many = _codes(6, (g,), 300, k)
