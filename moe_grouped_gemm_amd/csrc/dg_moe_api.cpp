@@ -110,7 +110,8 @@ dg_status experts_sizes(int tokens, int top_k, int num_groups, int inner) {
 }
 
 long long experts_workspace(int tokens, int top_k, int num_groups, int inner) {
-  return EXPERT_PLAN_BYTES + experts_act_bytes(tokens, top_k, num_groups, inner);
+  return EXPERT_PLAN_BYTES + experts_act_bytes(tokens, top_k, num_groups, inner) +
+         (long long)tokens * EXPERT_DOWN_COLUMNS * 4;
 }
 
 bool gate_aligned(const void* gate, int kind) { return kind == DG_MOE_GATE_TOKEN ? aligned4b(gate) : aligned16(gate); }
@@ -284,6 +285,8 @@ dg_status dg_moe_experts(const dg_moe_experts_args* args, void* stream) {
   e.y = static_cast<uint16_t*>(a.y);
   e.plan = a.workspace;
   e.act = reinterpret_cast<uint16_t*>(static_cast<char*>(a.workspace) + EXPERT_PLAN_BYTES);
+  e.partial = reinterpret_cast<float*>(reinterpret_cast<char*>(e.act) +
+                                       experts_act_bytes(a.tokens, a.top_k, a.num_groups, a.inner));
   e.fp4 = a.weight_type == DG_MOE_WEIGHTS_FP4;
   e.tokens = a.tokens;
   e.top_k = a.top_k;

@@ -44,6 +44,10 @@ namespace dg {
 namespace moe {
 namespace {
 
+// Columns that the second launch spreads over the chip, 16 to a compute unit: with fewer
+// columns of y, several workgroups share the experts of 16 columns.
+constexpr int DOWN_COLUMNS = EXPERT_DOWN_COLUMNS;
+
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 // What the first launch leaves for the second, before the activations: the experts
@@ -58,6 +62,7 @@ struct ExpertPlan {
   ExpertEntry entry[MAX_FEW_PAIRS];
   int slot[MAX_FEW_PAIRS];
   float weight[MAX_FEW_PAIRS];
+  int done[DOWN_COLUMNS / 16];  // of each 16 columns of y: workgroups whose sums are there
 };
 static_assert(sizeof(ExpertPlan) == EXPERT_PLAN_BYTES, "room for the plan");
 
@@ -344,9 +349,8 @@ __device__ void write_plan(const ExpertsArgs& p, const UpLists& l, int experts, 
     plan->slot[at] = i;
     plan->weight[at] = w;
   });
-  if (lane == 0) {
-    plan->experts = experts;
-  }
+  for (int i = lane; i < DOWN_COLUMNS / 16; i += 64) plan->done[i] = 0;
+  if (lane == 0) plan->experts = experts;
 }
 
 // The tiles [tile, tile_end) of 16 RT gate rows and as many up rows of one expert, with up
@@ -587,7 +591,8 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
   __shared__ uint16_t sums_at[MAX_FEW_PAIRS];  // of the pair's token, in 16 bytes
   __shared__ float pair_weights[MAX_FEW_PAIRS];
   __shared__ int items_of[DOWN_WAVES];
-  const ExpertPlan* plan = reinterpret_cast<const ExpertPlan*>(p.plan);
+  __shared__ bool last;
+  ExpertPlan* const plan = reinterpret_cast<ExpertPlan*>(p.plan);
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), c0 = blockIdx.x * 16 * RT;
   float* const mine = sums + wave * TOKENS * STRIDE;
@@ -629,18 +634,19 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
   total = __builtin_amdgcn_readfirstlane(total);
 
   // Parts of K: so many that the waves have the same number of items, or that they have
-  // eight each.
+  // eight each. The workgroups of the same columns share them like waves.
+  const int waves = DOWN_WAVES * p.splits, me = blockIdx.y * DOWN_WAVES + wave;
   const int item_steps = (p.inner / QBLOCK + BLOCKS - 1) / BLOCKS;
   int parts = 1;
-  while (parts < 8 && parts * 2 <= item_steps && total * parts % DOWN_WAVES && total * parts < 8 * DOWN_WAVES) parts *= 2;
-  const int all = total * parts, turns = wave < all ? (all - wave + DOWN_WAVES - 1) / DOWN_WAVES : 0;
+  while (parts < 8 && parts * 2 <= item_steps && total * parts % waves && total * parts < 8 * waves) parts *= 2;
+  const int all = total * parts, turns = me < all ? (all - me + waves - 1) / waves : 0;
 
   // Where the loads and the products are: the turn, its item and its steps.
   struct Cursor {
     int turn, step, end, begin, count, tile, tile2;
   };
   auto start = [&](Cursor& c) {
-    const int item = wave + c.turn * DOWN_WAVES, part = item % parts;
+    const int item = me + c.turn * waves, part = item % parts;
     const DownItem at = items[item / parts];
     c.begin = __builtin_amdgcn_readfirstlane(at.begin);
     c.tile = __builtin_amdgcn_readfirstlane(at.tile);
@@ -653,7 +659,7 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
   };
   int steps = 0;
   for (int turn = 0; turn < turns; ++turn) {
-    const int part = (wave + turn * DOWN_WAVES) % parts;
+    const int part = (me + turn * waves) % parts;
     steps += item_steps * (part + 1) / parts - item_steps * part / parts;
   }
 
@@ -753,6 +759,32 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
     for (int w = 0; w < DOWN_WAVES; ++w)
 #pragma unroll
       for (int k = 0; k < 2; ++k) s[k] += sums[(w * TOKENS + t) * STRIDE + c + k];
+    if (p.splits == 1)
+      *reinterpret_cast<uint32_t*>(p.y + (size_t)t * p.hidden + c0 + c) = pack2(s);
+    else
+      __hip_atomic_store(reinterpret_cast<uint64_t*>(p.partial + ((size_t)blockIdx.y * p.tokens + t) * p.hidden + c0 + c),
+                         __builtin_bit_cast(uint64_t, s), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if (p.splits == 1) return;
+  // The last of the columns' workgroups to be done adds their sums, in order. They go
+  // past the L2s by accesses of agent scope, and are there once waited for: a fence would
+  // write back and drop a whole L2 for each workgroup (20 us of 50).
+  wait_vmcnt_0();
+  __syncthreads();
+  if (tid == 0)
+    last = __hip_atomic_fetch_add(&plan->done[blockIdx.x], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == p.splits - 1;
+  __syncthreads();
+  if (!last) return;
+  for (int i = tid; i < p.tokens * 8 * RT; i += DOWN_THREADS) {
+    const int t = i / (8 * RT), c = i % (8 * RT) * 2;
+    f32x2 s = {0.f, 0.f};
+    for (int w = 0; w < p.splits; ++w) {
+      const f32x2 v = __builtin_bit_cast(
+          f32x2, __hip_atomic_load(reinterpret_cast<uint64_t*>(p.partial + ((size_t)w * p.tokens + t) * p.hidden + c0 + c),
+                                   __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+#pragma unroll
+      for (int k = 0; k < 2; ++k) s[k] += v[k];
+    }
     *reinterpret_cast<uint32_t*>(p.y + (size_t)t * p.hidden + c0 + c) = pack2(s);
   }
 }
@@ -772,8 +804,18 @@ hipError_t launch_down(const ExpertsArgs& a, hipStream_t stream) {
   // 224) 61 tokens and 32 experts took 140 us for 100.
   const int rt = a.hidden / 32 <= a.cus / 2 ? 1 : 2;
   const auto down = rt == 1 ? experts_down_kernel<FP4, ROWS, TOKENS, NT, 1> : experts_down_kernel<FP4, ROWS, TOKENS, NT, 2>;
-  hipLaunchKernelGGL(down, dim3(a.hidden / (16 * rt)), dim3(DOWN_THREADS), 0, stream, a);
+  hipLaunchKernelGGL(down, dim3(a.hidden / (16 * rt), a.splits), dim3(DOWN_THREADS), 0, stream, a);
   return hipGetLastError();
+}
+
+// How many workgroups of the second launch share the experts of their columns: as many as
+// there is room for, while each wave keeps eight steps. Whole layers, in us, with and
+// without: 57 tokens, 82 experts of 1536 x 1536 in FP8 149, 197; 8 tokens, 43 experts of
+// 768 x 1664 in FP4 27, 39; 5 tokens, 26 experts of 512 x 896 in FP8 20, 26. (Not by the
+// compute units that are set: the order of the sums differs.)
+int down_splits(const ExpertsArgs& a) {
+  const int experts = std::min(a.tokens * a.top_k, a.num_groups), steps = a.inner / (a.fp4 ? 2 * QBLOCK : QBLOCK);
+  return std::max(std::min(DOWN_COLUMNS / a.hidden, experts * steps / (8 * DOWN_WAVES)), 1);
 }
 
 // ROWS: 4 for up to 4 tokens, else 16.
@@ -795,7 +837,8 @@ long long experts_act_bytes(int tokens, int top_k, int num_groups, int inner) {
   return (long long)tiles * (tokens <= 4 ? 4 : 16) * inner * 2;
 }
 
-hipError_t launch_experts(const ExpertsArgs& a, hipStream_t stream) {
+hipError_t launch_experts(ExpertsArgs a, hipStream_t stream) {
+  a.splits = down_splits(a);
   if (a.tokens <= 4) return a.fp4 ? launch_both<true, 4>(a, stream) : launch_both<false, 4>(a, stream);
   return a.fp4 ? launch_both<true, 16>(a, stream) : launch_both<false, 16>(a, stream);
 }

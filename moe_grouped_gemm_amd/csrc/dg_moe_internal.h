@@ -55,7 +55,9 @@ hipError_t launch_swiglu_bwd(const GluArgs& a, hipStream_t stream);
 // A whole expert layer for a few tokens (dg_moe_experts.hip).
 constexpr int MAX_FEW_TOKENS = 128;
 constexpr int MAX_FEW_PAIRS = 1024;                            // tokens * top_k
-constexpr int EXPERT_PLAN_BYTES = 16 + MAX_FEW_PAIRS * 24;     // the workspace's head; a multiple of 16
+constexpr int EXPERT_DOWN_COLUMNS = 4096;
+// The workspace's head; a multiple of 16.
+constexpr int EXPERT_PLAN_BYTES = 16 + MAX_FEW_PAIRS * 24 + EXPERT_DOWN_COLUMNS / 16 * 4;
 struct ExpertsArgs {
   const uint16_t* x;
   const int32_t* ids;
@@ -69,10 +71,12 @@ struct ExpertsArgs {
   uint16_t* act;         // experts_act_bytes()
   int fp4, tokens, top_k, num_groups, hidden, inner;
   int cus;               // compute units to spread over
+  float* partial;        // EXPERT_DOWN_COLUMNS floats a token
+  int splits;            // set by launch_experts()
 };
 // Grows with tokens.
 long long experts_act_bytes(int tokens, int top_k, int num_groups, int inner);
-hipError_t launch_experts(const ExpertsArgs& a, hipStream_t stream);
+hipError_t launch_experts(ExpertsArgs a, hipStream_t stream);
 
 // Norms around the block (dg_moe_norm.hip).
 // Most workgroups of the gradient's row loop (and rows of its partial sums).

@@ -87,6 +87,8 @@ LAYERS = [
     (1, 1, 1, 128, 128), (1, 8, 16, 640, 256), (3, 2, 8, 2048, 512), (5, 8, 16, 384, 128), (16, 4, 6, 256, 384),
     (17, 3, 40, 512, 256), (33, 8, 9, 384, 128), (64, 2, 3, 256, 256), (100, 8, 12, 128, 256), (128, 8, 64, 256, 128),
     (7, 32, 32, 256, 128), (2, 3, 4096, 128, 128), (40, 1, 1, 896, 1152), (128, 1, 2, 128, 128),
+    # rows so short that several workgroups share the experts of their columns
+    (30, 8, 40, 256, 1024), (9, 4, 30, 384, 1280), (100, 3, 20, 128, 2048), (3, 8, 40, 2048, 640),
 ]
 
 
@@ -348,3 +350,48 @@ def test_long_rows(dev, t, fp4):
     x = torch.randn(t, hidden, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).to(dev)
     w = torch.rand(t, k, generator=torch.Generator().manual_seed(4)).to(dev)
     _check(_run(x, ids, w, b1, sfb1, b2, sfb2, dev), x, ids, w.cpu().numpy(), v1, v2)
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+def test_workgroups_that_share_columns_captured_and_on_two_streams(dev, fp4):
+    """Short rows, whose sums meet in the workspace: replays of two graphs over one workspace
+    and calls on two streams give the bits of calls made alone."""
+    _say(f"experts, shared columns, fp4={fp4}")
+    k, g, hidden, inner = 4, 30, 256, 1024
+    b1, sfb1, _ = _weights(fp4, g, 2 * inner, hidden, 1, dev)
+    b2, sfb2, _ = _weights(fp4, g, hidden, inner, 2, dev)
+    sent = (b1, sfb1, b2, sfb2)
+    ws = moe.experts_workspace(40, k, g, inner, dev)
+    calls = []
+    for t in (40, 7):
+        x, w = torch.zeros(t, hidden, dtype=torch.bfloat16, device=dev), torch.ones(t, k, device=dev)
+        ids, y = torch.zeros(t, k, dtype=torch.int32, device=dev), torch.zeros(t, hidden, dtype=torch.bfloat16, device=dev)
+        moe.experts(x, ids, w, *sent, y, ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            moe.experts(x, ids, w, *sent, y, ws)
+        calls.append((graph, x, ids, w, y))
+    streams = [torch.cuda.Stream() for _ in calls]
+    spaces = [moe.experts_workspace(40, k, g, inner, dev) for _ in calls]
+    for seed in range(4):
+        want = []
+        for _, x, ids, w, _ in calls:
+            x.copy_(torch.randn(x.shape, generator=torch.Generator().manual_seed(seed)))
+            ids.copy_(torch.from_numpy(_ids(*ids.shape, g, seed)))
+            w.uniform_()
+            want.append(_run(x, ids.cpu().numpy(), w, *sent, dev).view(torch.int16))
+        for (graph, *_, y), ref in zip(calls, want):
+            y.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y.view(torch.int16), ref)
+        outs = [torch.zeros_like(c[4]) for c in calls]
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for s, space, (_, x, ids, w, _), out in zip(streams, spaces, calls, outs):
+                with torch.cuda.stream(s):
+                    moe.experts(x, ids, w, *sent, out, space)
+        torch.cuda.synchronize()
+        for out, ref in zip(outs, want):
+            assert torch.equal(out.view(torch.int16), ref)
