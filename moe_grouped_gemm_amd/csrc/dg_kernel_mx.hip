@@ -18,7 +18,8 @@
 // j-th MFMA on blocks 4j + g every lane would need another byte of its word: a
 // transpose between lanes, 36 instructions a step, that cost 8% of the time.)
 //
-// A persistent kernel over 256 x 256 tiles, a 128 x 64 part of one a wave; a K step is
+// Two kernels: for few tiles see the second. The first is persistent over 256 x 256
+// tiles, a 128 x 64 part of one a wave; a K step is
 // 256 values, 128-byte rows of either operand, in one of two LDS stages that
 // direct-to-LDS loads fill a step and a half ahead (see the K loop). Two stages of 68
 // KB are what LDS holds; smaller tiles read more of either operand for a product.

@@ -22,7 +22,7 @@
 // weights' in the first launch, as many in the second) and the processors' turns add to
 // the weights' time. An FP8 batch, 61 tokens and 32 experts of 7168 x 2048:
 // 180 us (5.2 TB/s of weights) and 101 (4.7); weights alone 164 and 79. One token,
-// eight experts in FP4: 28 and 18 us, of which about 5 each are a launch's lists of
+// eight experts in FP4: 28 and 17 us, of which about 5 each are a launch's lists of
 // who is where, one read from memory after the other.
 //
 // A step is 128 bytes of each row: 128 values of FP8, or two blocks of 128 of FP4.
