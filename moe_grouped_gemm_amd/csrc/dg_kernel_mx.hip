@@ -19,7 +19,7 @@
 // transpose between lanes, 36 instructions a step, that cost 8% of the time.)
 //
 // Two kernels: for few tiles see the second. The first is persistent over 256 x 256
-// tiles, a 128 x 64 part of one a wave; a K step is 256 values, 128-byte rows of either
+// tiles (or, for fewer of them, 128 x 256), a 128 x 64 part of one a wave; a K step is 256 values, 128-byte rows of either
 // operand, in one of two LDS stages that direct-to-LDS loads fill a step and a half
 // ahead (see the K loop). Two stages of 68 KB are what LDS holds; smaller tiles read
 // more of either operand for a product, and four waves of 128 x 128 (a third fewer LDS
@@ -40,22 +40,27 @@
 namespace dg {
 namespace mx {
 
+// A workgroup's tile: BM x 256, a wave 128 x 64 of it.
+template <int BM_>
 struct Cfg {
-  static constexpr int BM = 256, BN = 256, SLOTS = BM / 128;
-  static constexpr int WAVES_N = 4, NW = 8, THREADS = NW * 64;
+  static constexpr int BM = BM_, BN = 256, SLOTS = BM / 128;
+  static constexpr int WAVES_N = 4, NW = BM / 32, THREADS = NW * 64;
   static constexpr int WM = 128, WN = 64, MT = WM / 16, NT = WN / 16;
 };
-constexpr int STEP_BLOCKS = 2;                          // 128-value blocks of K a step: 128-byte rows
+using Big = Cfg<256>;
+using Half = Cfg<128>;
+constexpr int STEP_BLOCKS = 2;  // 128-value blocks of K a step: 128-byte rows
 // LDS of a stage, in two buffers that are refilled at different times (see the K loop):
-// HIGH the later halves of the two wave rows' A rows (64 .. 127 and 192 .. 255), LOW all
-// else.
+// HIGH the later halves of the wave rows' A rows (64 .. 127 of each 128), LOW all else.
 enum { LOW = 0, HIGH = 1 };
-constexpr int A_HALF = Cfg::BM / 2 * ROW_BYTES;         // 16 KB
-constexpr int B_BYTES = Cfg::BN * ROW_BYTES;            // 32 KB
-constexpr int SA_OFF = A_HALF + B_BYTES;                // [128 values of the step][4][16][4] LHS scale words: row 64 i + 16 j + r at [i][r][j]
-constexpr int SB_OFF = SA_OFF + STEP_BLOCKS * Cfg::BM * 4;
-constexpr int LOW_BYTES = SB_OFF + STEP_BLOCKS * Cfg::BN * 4;
-static_assert(Cfg::NW == 8 && Cfg::BM == 256 && Cfg::BN == 256, "load split below");
+template <class C>
+constexpr int A_HALF = C::BM / 2 * ROW_BYTES;
+template <class C>
+constexpr int SA_OFF = A_HALF<C> + C::BN * ROW_BYTES;  // [128 values of the step][BM / 64][16][4] LHS scale words: row 64 i + 16 j + r at [i][r][j]
+template <class C>
+constexpr int SB_OFF = SA_OFF<C> + STEP_BLOCKS * C::BM * 4;
+template <class C>
+constexpr int LOW_BYTES = SB_OFF<C> + STEP_BLOCKS * C::BN * 4;
 
 }  // namespace mx
 
@@ -69,8 +74,8 @@ struct Few {
 
 }  // namespace mx
 
-template <>
-constexpr int A_PACK_SHIFT<mx::Cfg> = 1;
+template <int BM>
+constexpr int A_PACK_SHIFT<mx::Cfg<BM>> = 1;
 template <>
 constexpr int A_PACK_SHIFT<mx::Few> = 1;
 
@@ -78,14 +83,14 @@ namespace mx {
 
 // An LDS buffer of its own for each stage and half (the compiler makes a read wait for
 // the loads in flight into the buffer that it reads, and only for those).
-template <int S, int PART>
+template <class C, int S, int PART>
 __device__ __forceinline__ uint8_t* stage_buf() {
-  __shared__ __attribute__((aligned(1024))) uint8_t buf[PART == LOW ? LOW_BYTES : A_HALF];
+  __shared__ __attribute__((aligned(1024))) uint8_t buf[PART == LOW ? LOW_BYTES<C> : A_HALF<C>];
   return buf;
 }
-template <int S, int PART>
+template <class C, int S, int PART>
 __device__ __forceinline__ uint32_t stage_addr() {
-  return (uint32_t)(uintptr_t)(lds_void*)stage_buf<S, PART>();
+  return (uint32_t)(uintptr_t)(lds_void*)stage_buf<C, S, PART>();
 }
 
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t lds_base) {
@@ -95,20 +100,23 @@ __device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, uint32_t voff, ui
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds_dest(lds_base), 4, voff, 0, 0, 0);
 }
 
-// This lane's byte offsets within a tile: of its A and B loads (the j-th adds 64 j
+// This lane's byte offsets within a tile: of its A and B loads (the j-th adds 8 NW j
 // rows) and of its scale words.
 struct LaneOffsets {
-  uint32_t ab, ab_step, sc;
+  uint32_t ab, ab_step, sa, sb;
 };
 
+template <class C>
 __device__ __forceinline__ LaneOffsets lane_offsets(int k, int wave, int lane) {
   LaneOffsets o;
   const int row0 = wave * 8 + (lane >> 3);
   // Of the row's eight 16-byte blocks 2g + j lies where lds_offset() has chunk g + 4j.
   const int chunk = (lane & 7) ^ ((row0 >> 1) & 7);  // the same for every j
   o.ab = (uint32_t)row0 * ((uint32_t)k / 2) + (uint32_t)((chunk & 3) * 2 + (chunk >> 2)) * 16u;
-  o.ab_step = 64u * ((uint32_t)k / 2);
-  o.sc = (uint32_t)(64 * (wave & 3) + (lane & 3) * 16 + (lane >> 2)) * 4u;
+  o.ab_step = 8u * C::NW * ((uint32_t)k / 2);
+  const int word = (lane & 3) * 16 + (lane >> 2);
+  o.sa = (uint32_t)(64 * (wave % (C::BM / 64)) + word) * 4u;
+  o.sb = (uint32_t)(64 * (wave & 3) + word) * 4u;
   return o;
 }
 
@@ -122,11 +130,12 @@ struct TileSrc {
   uint32_t a_rows, b_rows;
 };
 
+template <class C>
 __device__ __forceinline__ TileSrc tile_src(const GemmArgs& p, const TileRef& tr) {
   TileSrc s;
   const size_t row = (size_t)p.k / 2;
-  s.a_rows = uniform_int(min(max(tr.load_rows - tr.m0, 0), Cfg::BM));
-  s.b_rows = uniform_int(min(p.n - tr.n0, Cfg::BN));
+  s.a_rows = uniform_int(min(max(tr.load_rows - tr.m0, 0), C::BM));
+  s.b_rows = uniform_int(min(p.n - tr.n0, C::BN));
   s.a = uniform_ptr(tr.a + (size_t)tr.m0 * row);
   s.sa = uniform_ptr(tr.sfa + tr.m0);
   s.b = uniform_ptr(p.b + ((size_t)tr.group * p.n + tr.n0) * row);
@@ -138,19 +147,25 @@ __device__ __forceinline__ TileSrc tile_src(const GemmArgs& p, const TileRef& tr
 // everything of an odd last block's second half: the scale words by their
 // descriptors, and codes that are other rows' (no code is infinite or NaN) come to
 // nothing under two scales of 2^-127.
+template <class C>
 struct StageSrc {
-  __amdgpu_buffer_rsrc_t a, b, sa, sb;
+  static constexpr int SB_LOADS = 8 / C::NW;  // of 64 words each
+  __amdgpu_buffer_rsrc_t a, b, sa, sb[SB_LOADS];
 };
 
-__device__ __forceinline__ StageSrc stage_src(const GemmArgs& p, const TileSrc& t, int step, int wave) {
-  StageSrc r;
+template <class C>
+__device__ __forceinline__ StageSrc<C> stage_src(const GemmArgs& p, const TileSrc& t, int step, int wave) {
+  StageSrc<C> r;
   const uint32_t row = (uint32_t)p.k / 2, skip = (uint32_t)step * ROW_BYTES;
-  const int blk = step * STEP_BLOCKS + (wave >> 2);  // the 128-value block whose scales this wave loads
-  const bool in = blk < p.k / BK;
+  auto words = [&](const float* w, int block, int ld, uint32_t rows) {  // `block` of the step's
+    const int blk = step * STEP_BLOCKS + block;
+    return buffer_rsrc(w + (size_t)blk * ld, blk < p.k / BK ? rows * 4u : 0);
+  };
   r.a = buffer_rsrc(t.a + skip, t.a_rows ? t.a_rows * row - skip : 0);
   r.b = buffer_rsrc(t.b + skip, t.b_rows * row - skip);
-  r.sa = buffer_rsrc(t.sa + (size_t)blk * p.ld_sfa, in ? t.a_rows * 4u : 0);
-  r.sb = buffer_rsrc(t.sb + (size_t)blk * p.ld_sfb, in ? t.b_rows * 4u : 0);
+  r.sa = words(t.sa, wave / (C::BM / 64), p.ld_sfa, t.a_rows);
+#pragma unroll
+  for (int i = 0; i < r.SB_LOADS; ++i) r.sb[i] = words(t.sb, (i * C::NW + wave) >> 2, p.ld_sfb, t.b_rows);
   return r;
 }
 
@@ -158,7 +173,8 @@ __device__ __forceinline__ StageSrc stage_src(const GemmArgs& p, const TileSrc& 
 // this tile, of the next one, or (with a single step per tile) of the one after.
 // With no such tile the window's entries repeat the previous one and the loads fetch
 // a step nobody reads.
-__device__ __forceinline__ StageSrc refill_src(const GemmArgs& p, const TileSrc& t0, const TileSrc& t1,
+template <class C>
+__device__ __forceinline__ StageSrc<C> refill_src(const GemmArgs& p, const TileSrc& t0, const TileSrc& t1,
                                                const TileSrc& t2, int ahead, int steps, int wave) {
   const bool in0 = ahead < steps, in1 = ahead < 2 * steps;
   // Field by field (a select between references would put the tiles in memory).
@@ -169,26 +185,31 @@ __device__ __forceinline__ StageSrc refill_src(const GemmArgs& p, const TileSrc&
   t.sb = in0 ? t0.sb : (in1 ? t1.sb : t2.sb);
   t.a_rows = in0 ? t0.a_rows : (in1 ? t1.a_rows : t2.a_rows);
   t.b_rows = in0 ? t0.b_rows : (in1 ? t1.b_rows : t2.b_rows);
-  return stage_src(p, t, in0 ? ahead : (in1 ? ahead - steps : ahead - 2 * steps), wave);
+  return stage_src<C>(p, t, in0 ? ahead : (in1 ? ahead - steps : ahead - 2 * steps), wave);
 }
 
 // The loads of one step into stage S: 0 and 1 the B tile, 2 the LOW half of the A tile,
-// 3 the scale words, 4 the HIGH half of the A tile; two instructions of a wave each.
-constexpr int LOW_LOADS = 8, HIGH_LOADS = 2;
-template <int S, int PART>
-__device__ __forceinline__ void issue_part(const StageSrc& r, int wave, const LaneOffsets& lo) {
-  const uint32_t st = stage_addr<S, PART == 4 ? HIGH : LOW>();
+// 3 the scale words, 4 the HIGH half of the A tile. How many of a wave each takes:
+template <class C, int PART>
+constexpr int PART_LOADS = PART < 2 ? 16 / C::NW : PART == 3 ? 1 + StageSrc<C>::SB_LOADS : 2;
+template <class C>
+constexpr int LOW_LOADS = 2 * PART_LOADS<C, 0> + PART_LOADS<C, 2> + PART_LOADS<C, 3>;
+constexpr int HIGH_LOADS = 2;
+template <class C, int S, int PART>
+__device__ __forceinline__ void issue_part(const StageSrc<C>& r, int wave, const LaneOffsets& lo) {
+  const uint32_t st = stage_addr<C, S, PART == 4 ? HIGH : LOW>();
   if constexpr (PART == 3) {
-    const int at = ((wave >> 2) * 256 + 64 * (wave & 3)) * 4;
-    dma4(r.sa, lo.sc, st + SA_OFF + at);
-    dma4(r.sb, lo.sc, st + SB_OFF + at);
-  } else {
+    dma4(r.sa, lo.sa, st + SA_OFF<C> + wave * 256);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int j = PART < 2 ? PART * 2 + i : i * 2 + (PART == 4);  // which 64 rows
-      const int slot = PART < 2 ? j : i;
-      dma16(PART < 2 ? r.b : r.a, lo.ab + j * lo.ab_step,
-            st + (PART < 2 ? A_HALF : 0) + (slot * Cfg::NW + wave) * 1024);
+    for (int i = 0; i < r.SB_LOADS; ++i) dma4(r.sb[i], lo.sb, st + SB_OFF<C> + (i * C::NW + wave) * 256);
+  } else {
+    constexpr int ROUNDS = 8 / C::NW;  // that 64 rows take
+#pragma unroll
+    for (int i = 0; i < PART_LOADS<C, PART>; ++i) {
+      // Which 8 NW rows of the tile, and of its place in LDS.
+      const int slot = PART < 2 ? PART * PART_LOADS<C, PART> + i : i;
+      const int j = PART < 2 ? slot : i / ROUNDS * 2 * ROUNDS + i % ROUNDS + (PART == 4) * ROUNDS;
+      dma16(PART < 2 ? r.b : r.a, lo.ab + j * lo.ab_step, st + (PART < 2 ? A_HALF<C> : 0) + (slot * C::NW + wave) * 1024);
     }
   }
 }
@@ -201,16 +222,17 @@ struct LdsOffsets {
   uint32_t pick;            // byte selector: of two words, the two bytes of each that the lane needs
 };
 
+template <class C>
 __device__ __forceinline__ LdsOffsets lds_offsets(int wm0, int wn0, int lane) {
   LdsOffsets o;
   const int r = lane & 15, g = lane >> 4;
   const uint32_t c0 = (uint32_t)lds_offset(r, g), c1 = (uint32_t)lds_offset(r, g + 4);
   o.a0 = (uint32_t)wm0 / 2 * ROW_BYTES + c0;
   o.a1 = (uint32_t)wm0 / 2 * ROW_BYTES + c1;
-  o.b0 = A_HALF + (uint32_t)wn0 * ROW_BYTES + c0;
-  o.b1 = A_HALF + (uint32_t)wn0 * ROW_BYTES + c1;
-  o.sa = SA_OFF + (uint32_t)((g >> 1) * 1024 + wm0 * 4 + r * 16);
-  o.sb = SB_OFF + (uint32_t)((g >> 1) * 1024 + wn0 * 4 + r * 16);
+  o.b0 = A_HALF<C> + (uint32_t)wn0 * ROW_BYTES + c0;
+  o.b1 = A_HALF<C> + (uint32_t)wn0 * ROW_BYTES + c1;
+  o.sa = SA_OFF<C> + (uint32_t)((g >> 1) * C::BM * 4 + wm0 * 4 + r * 16);
+  o.sb = SB_OFF<C> + (uint32_t)((g >> 1) * C::BN * 4 + wn0 * 4 + r * 16);
   o.pick = (g & 1) ? 0x07060302u : 0x05040100u;
   return o;
 }
@@ -219,29 +241,29 @@ __device__ __forceinline__ LdsOffsets lds_offsets(int wm0, int wn0, int lane) {
 struct Frag {
   i32x4 h[2];
 };
-template <int S, int PART = LOW>
+template <class C, int S, int PART = LOW>
 __device__ __forceinline__ Frag frag_at(uint32_t off0, uint32_t off1, int band) {
-  const uint8_t* st = stage_buf<S, PART>();
+  const uint8_t* st = stage_buf<C, S, PART>();
   Frag f;
   f.h[0] = *reinterpret_cast<const i32x4*>(st + off0 + band * 16 * ROW_BYTES);
   f.h[1] = *reinterpret_cast<const i32x4*>(st + off1 + band * 16 * ROW_BYTES);
   return f;
 }
-template <int S, int BAND>
+template <class C, int S, int BAND>
 __device__ __forceinline__ Frag band_at(const LdsOffsets& lds) {
-  return frag_at<S, BAND / 4>(lds.a0, lds.a1, BAND % 4);
+  return frag_at<C, S, BAND / 4>(lds.a0, lds.a1, BAND % 4);
 }
 __device__ __forceinline__ i32x8 operand(const i32x4& v) { return (i32x8){v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
 
 // The scales of the wave's bands and column blocks, two of them a register: byte
 // 2 (i % 2) + j of register i / 2 for the j-th MFMA.
 struct Scales {
-  int a[Cfg::MT / 2], b[Cfg::NT / 2];
+  int a[Big::MT / 2], b[Big::NT / 2];
 };
 // The scales of four bands or column blocks, from index 2 I of `to`.
-template <int S, int I, int N>
+template <class C, int S, int I, int N>
 __device__ __forceinline__ void scales_at(int (&to)[N], uint32_t off, uint32_t pick) {
-  const i32x4 w = *reinterpret_cast<const i32x4*>(stage_buf<S, LOW>() + off + I * 256);
+  const i32x4 w = *reinterpret_cast<const i32x4*>(stage_buf<C, S, LOW>() + off + I * 256);
   to[2 * I] = __builtin_amdgcn_perm(w[1], w[0], pick);
   to[2 * I + 1] = __builtin_amdgcn_perm(w[3], w[2], pick);
 }
@@ -293,13 +315,13 @@ __device__ __forceinline__ void store_band(uint16_t* rows, int n, uint32_t valid
 }
 
 // A wave's finished 128 x 64 sub-tile.
-template <int KIND>
+template <class C, int KIND>
 __device__ __forceinline__ void store_tile(const GemmArgs& p, const TileRef& cur, const RowMask& cm,
-                                           const f32x4 (&acc)[Cfg::MT][Cfg::NT], int wm0, int wn0, int lane) {
-  static_assert(Cfg::NT == 4, "a band of 64 columns");
+                                           const f32x4 (&acc)[C::MT][C::NT], int wm0, int wn0, int lane) {
+  static_assert(C::NT == 4, "a band of 64 columns");
 #pragma unroll
-  for (int mt = 0; mt < Cfg::MT; ++mt) {
-    const uint32_t valid = band_rows<Cfg, KIND>(cur, cm, wm0, mt);
+  for (int mt = 0; mt < C::MT; ++mt) {
+    const uint32_t valid = band_rows<C, KIND>(cur, cm, wm0, mt);
     if (valid != 0)
       store_band(cur.d + (size_t)(cur.m0 + wm0 + mt * 16) * p.n + cur.n0 + wn0, p.n, valid, acc[mt], lane);
   }
@@ -324,12 +346,12 @@ __device__ __forceinline__ void store_tile(const GemmArgs& p, const TileRef& cur
 // So every load has a step and a half to land. (One barrier a step, at band 6, gave it
 // 0.6 to 1 step, and took 229 us where this takes 221 for 16384 x 4096 x 7168.)
 // Only bands below NB are computed (the rows of the others are not stored).
-template <int KIND, int PHASE, int NB>
+template <class C, int KIND, int PHASE, int NB>
 __device__ __forceinline__ void mainloop(const GemmArgs& p, const TileSrc& t0, const TileSrc& t1, const TileSrc& t2,
-                                         f32x4 (&acc)[Cfg::MT][Cfg::NT], bool on, int wave, int lane,
+                                         f32x4 (&acc)[C::MT][C::NT], bool on, int wave, int lane,
                                          const LdsOffsets& lds, const LaneOffsets& lo, const RowGroups& nrg, int ngroup,
                                          RowMask& nmask) {
-  static_assert(NB == Cfg::MT || (NB >= 2 && NB <= 6), "a partial copy computes bands 0 .. NB-1 before the barrier");
+  static_assert(NB == C::MT || (NB >= 2 && NB <= 6), "a partial copy computes bands 0 .. NB-1 before the barrier");
   // The next tile's row mask (contiguous layout), after a barrier: see RowGroups.
   auto next_rows = [&]() {
     if constexpr (KIND == KIND_CONTIGUOUS) {
@@ -339,15 +361,15 @@ __device__ __forceinline__ void mainloop(const GemmArgs& p, const TileSrc& t0, c
     }
   };
   const int steps = (p.k / BK + STEP_BLOCKS - 1) / STEP_BLOCKS;
-  Frag af[4], bf[Cfg::NT];  // A ring: band mt's fragment in slot mt % 4
+  Frag af[4], bf[C::NT];  // A ring: band mt's fragment in slot mt % 4
 #pragma unroll
-  for (int nt = 0; nt < Cfg::NT; ++nt) bf[nt] = frag_at<PHASE>(lds.b0, lds.b1, nt);
-  af[0] = band_at<PHASE, 0>(lds);
-  af[1] = band_at<PHASE, 1>(lds);
+  for (int nt = 0; nt < C::NT; ++nt) bf[nt] = frag_at<C, PHASE>(lds.b0, lds.b1, nt);
+  af[0] = band_at<C, PHASE, 0>(lds);
+  af[1] = band_at<C, PHASE, 1>(lds);
   Scales scales;
-  scales_at<PHASE, 0>(scales.b, lds.sb, lds.pick);
-  scales_at<PHASE, 0>(scales.a, lds.sa, lds.pick);
-  scales_at<PHASE, 1>(scales.a, lds.sa, lds.pick);
+  scales_at<C, PHASE, 0>(scales.b, lds.sb, lds.pick);
+  scales_at<C, PHASE, 0>(scales.a, lds.sa, lds.pick);
+  scales_at<C, PHASE, 1>(scales.a, lds.sa, lds.pick);
   for (int i0 = 0; i0 < steps; i0 += 2) {
     static_for<0, 2>([&](auto si) {
       constexpr int s = (decltype(si)::value + PHASE) % 2, sn = 1 - s;
@@ -356,46 +378,46 @@ __device__ __forceinline__ void mainloop(const GemmArgs& p, const TileSrc& t0, c
       // The refills are issued unconditionally (past the last tile they load a step nobody
       // reads): a branch here would make the compiler wait for them before reading the
       // current stage.
-      const StageSrc r2 = refill_src(p, t0, t1, t2, i + 2, steps, wave);
+      const StageSrc<C> r2 = refill_src<C>(p, t0, t1, t2, i + 2, steps, wave);
       if (!on) {
-        wait_vmcnt<LOW_LOADS + HIGH_LOADS>();
+        wait_vmcnt<LOW_LOADS<C> + HIGH_LOADS>();
         wait_lgkmcnt_0();
         barrier();
-        issue_part<s, 0>(r2, wave, lo);
-        issue_part<s, 1>(r2, wave, lo);
-        issue_part<s, 2>(r2, wave, lo);
-        issue_part<s, 3>(r2, wave, lo);
-        wait_vmcnt<LOW_LOADS + HIGH_LOADS>();
+        issue_part<C, s, 0>(r2, wave, lo);
+        issue_part<C, s, 1>(r2, wave, lo);
+        issue_part<C, s, 2>(r2, wave, lo);
+        issue_part<C, s, 3>(r2, wave, lo);
+        wait_vmcnt<LOW_LOADS<C> + HIGH_LOADS>();
         barrier();
         next_rows();
-        issue_part<s, 4>(r2, wave, lo);
+        issue_part<C, s, 4>(r2, wave, lo);
         return;
       }
       static_for<0, 6>([&](auto MT) {
         constexpr int mt = decltype(MT)::value;
         if constexpr (mt == 2) {
           wait_lgkmcnt_0();
-          wait_vmcnt<LOW_LOADS + HIGH_LOADS>();  // all but the last refills of LOW and HIGH
+          wait_vmcnt<LOW_LOADS<C> + HIGH_LOADS>();  // all but the last refills of LOW and HIGH
           barrier();
           __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (mt + 2 < NB) af[(mt + 2) % 4] = band_at<s, mt + 2>(lds);
-        if constexpr (mt >= 2) issue_part<s, mt - 2>(r2, wave, lo);
+        if constexpr (mt + 2 < NB) af[(mt + 2) % 4] = band_at<C, s, mt + 2>(lds);
+        if constexpr (mt >= 2) issue_part<C, s, mt - 2>(r2, wave, lo);
         if constexpr (mt < NB) {
-          static_for<0, 2 * Cfg::NT>([&](auto I) {
-            constexpr int h = decltype(I)::value / Cfg::NT, nt = decltype(I)::value % Cfg::NT;
+          static_for<0, 2 * C::NT>([&](auto I) {
+            constexpr int h = decltype(I)::value / C::NT, nt = decltype(I)::value % C::NT;
             acc[mt][nt] = mfma<mt, nt, h>(bf[nt], af[mt % 4], acc[mt][nt], scales.b[nt / 2], scales.a[mt / 2]);
           });
           // The reads two bands ahead and this band's share of the refill first.
           if constexpr (mt + 2 < NB) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // DS reads
-          if constexpr (mt >= 2) __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);      // VMEM loads
-          __builtin_amdgcn_sched_group_barrier(0x008, 2 * Cfg::NT, 0);  // MFMA
+          if constexpr (mt >= 2) __builtin_amdgcn_sched_group_barrier(0x020, PART_LOADS<C, mt - 2>, 0);  // VMEM loads
+          __builtin_amdgcn_sched_group_barrier(0x008, 2 * C::NT, 0);  // MFMA
         }
         __builtin_amdgcn_sched_barrier(0);
       });
-      static_for<0, Cfg::NT>([&](auto NT) {
+      static_for<0, C::NT>([&](auto NT) {
         constexpr int nt = decltype(NT)::value;
-        if constexpr (NB == Cfg::MT) {
+        if constexpr (NB == C::MT) {
           acc[6][nt] = mfma<6, nt, 0>(bf[nt], af[2], acc[6][nt], scales.b[nt / 2], scales.a[6 / 2]);
           acc[7][nt] = mfma<7, nt, 0>(bf[nt], af[3], acc[7][nt], scales.b[nt / 2], scales.a[7 / 2]);
           acc[6][nt] = mfma<6, nt, 1>(bf[nt], af[2], acc[6][nt], scales.b[nt / 2], scales.a[6 / 2]);
@@ -404,21 +426,21 @@ __device__ __forceinline__ void mainloop(const GemmArgs& p, const TileSrc& t0, c
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (nt == 0) {
           wait_lgkmcnt_0();
-          wait_vmcnt<LOW_LOADS + HIGH_LOADS>();  // the same
+          wait_vmcnt<LOW_LOADS<C> + HIGH_LOADS>();  // the same
           barrier();
           next_rows();
           __builtin_amdgcn_sched_barrier(0);
-          issue_part<s, 4>(r2, wave, lo);
+          issue_part<C, s, 4>(r2, wave, lo);
         }
         // The next step's operands (past a tile's last step: the next tile's first, which
         // its entry reads again).
-        bf[nt] = frag_at<sn>(lds.b0, lds.b1, nt);
-        if constexpr (nt == 1) af[0] = band_at<sn, 0>(lds);
+        bf[nt] = frag_at<C, sn>(lds.b0, lds.b1, nt);
+        if constexpr (nt == 1) af[0] = band_at<C, sn, 0>(lds);
         if constexpr (nt == 3) {  // bands 6 and 7 are done
-          af[1] = band_at<sn, 1>(lds);
-          scales_at<sn, 0>(scales.b, lds.sb, lds.pick);
-          scales_at<sn, 0>(scales.a, lds.sa, lds.pick);
-          scales_at<sn, 1>(scales.a, lds.sa, lds.pick);
+          af[1] = band_at<C, sn, 1>(lds);
+          scales_at<C, sn, 0>(scales.b, lds.sb, lds.pick);
+          scales_at<C, sn, 0>(scales.a, lds.sa, lds.pick);
+          scales_at<C, sn, 1>(scales.a, lds.sa, lds.pick);
         }
         __builtin_amdgcn_sched_barrier(0);
       });
@@ -432,19 +454,19 @@ __device__ __forceinline__ void mainloop(const GemmArgs& p, const TileSrc& t0, c
 // 2048: 40 with either.
 constexpr int HALF_BANDS = 4;
 
-template <int KIND>
-__global__ void __launch_bounds__(Cfg::THREADS, 1) fp4_gemm_nt_kernel(GemmArgs p) {
+template <class C, int KIND>
+__global__ void __launch_bounds__(C::THREADS, 1) fp4_gemm_nt_kernel(GemmArgs p) {
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm0 = (wave / Cfg::WAVES_N) * Cfg::WM;
-  const int wn0 = (wave % Cfg::WAVES_N) * Cfg::WN;
+  const int wm0 = (wave / C::WAVES_N) * C::WM;
+  const int wn0 = (wave % C::WAVES_N) * C::WN;
   const int steps = (p.k / BK + STEP_BLOCKS - 1) / STEP_BLOCKS;
 
   int num_tiles = p.num_tiles;
   [[maybe_unused]] int* s_prefix = nullptr;
   if constexpr (counts_on_device(KIND)) {
-    s_prefix = group_table<Cfg, KIND>(p, tid);
+    s_prefix = group_table<C, KIND>(p, tid);
     num_tiles = s_prefix[p.num_groups];
   }
 
@@ -457,32 +479,32 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) fp4_gemm_nt_kernel(GemmArgs p
   // ahead, which reaches the tile after next when a tile has a single step). Missing
   // tiles repeat the previous window entry.
   int t = rank;
-  TileRef cur = next_active<Cfg, KIND>(p, t, grid, num_tiles, s_prefix);
+  TileRef cur = next_active<C, KIND>(p, t, grid, num_tiles, s_prefix);
   if (!cur.active) return;
   int t1 = t + grid;
-  TileRef nxt = next_active<Cfg, KIND>(p, t1, grid, num_tiles, s_prefix);
+  TileRef nxt = next_active<C, KIND>(p, t1, grid, num_tiles, s_prefix);
   int t2 = t1 + grid;
   TileRef nx2;
   nx2.active = false;
-  if (nxt.active) nx2 = next_active<Cfg, KIND>(p, t2, grid, num_tiles, s_prefix);
-  const LaneOffsets lo = lane_offsets(p.k, wave, lane);
-  const LdsOffsets lds = lds_offsets(wm0, wn0, lane);
-  TileSrc c0 = tile_src(p, cur);
-  TileSrc c1 = nxt.active ? tile_src(p, nxt) : c0;
-  TileSrc c2 = nx2.active ? tile_src(p, nx2) : c1;
+  if (nxt.active) nx2 = next_active<C, KIND>(p, t2, grid, num_tiles, s_prefix);
+  const LaneOffsets lo = lane_offsets<C>(p.k, wave, lane);
+  const LdsOffsets lds = lds_offsets<C>(wm0, wn0, lane);
+  TileSrc c0 = tile_src<C>(p, cur);
+  TileSrc c1 = nxt.active ? tile_src<C>(p, nxt) : c0;
+  TileSrc c2 = nx2.active ? tile_src<C>(p, nx2) : c1;
 
   // The first tile's row groups (contiguous layout) are loaded before the prologue's
   // loads, so that waiting for them never waits for those.
   [[maybe_unused]] RowGroups crg{-1, -1};
-  if constexpr (KIND == KIND_CONTIGUOUS) crg = load_row_groups<Cfg>(p, cur, wm0, lane);
+  if constexpr (KIND == KIND_CONTIGUOUS) crg = load_row_groups<C>(p, cur, wm0, lane);
 
   // Steps 0 and 1; of step 0 LOW must have landed for every wave before it is read.
   {
-    const StageSrc r0 = refill_src(p, c0, c1, c2, 0, steps, wave);
-    const StageSrc r1 = refill_src(p, c0, c1, c2, 1, steps, wave);
-    static_for<0, 5>([&](auto I) { issue_part<0, decltype(I)::value>(r0, wave, lo); });
-    static_for<0, 5>([&](auto I) { issue_part<1, decltype(I)::value>(r1, wave, lo); });
-    wait_vmcnt<LOW_LOADS + 2 * HIGH_LOADS>();
+    const StageSrc<C> r0 = refill_src<C>(p, c0, c1, c2, 0, steps, wave);
+    const StageSrc<C> r1 = refill_src<C>(p, c0, c1, c2, 1, steps, wave);
+    static_for<0, 5>([&](auto I) { issue_part<C, 0, decltype(I)::value>(r0, wave, lo); });
+    static_for<0, 5>([&](auto I) { issue_part<C, 1, decltype(I)::value>(r1, wave, lo); });
+    wait_vmcnt<LOW_LOADS<C> + 2 * HIGH_LOADS>();
     barrier();
   }
   int phase = 0;
@@ -495,27 +517,27 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) fp4_gemm_nt_kernel(GemmArgs p
     if constexpr (KIND == KIND_CONTIGUOUS) any_row = (cmask.even | cmask.odd) != 0;
     else any_row = cur.valid_rows > cur.m0 + wm0;
     const bool on = any_row && cur.n0 + wn0 < p.n;
-    int bands = Cfg::MT;
+    int bands = C::MT;
     if constexpr (counts_on_device(KIND))
-      bands = uniform_int(min(max((cur.valid_rows - cur.m0 - wm0 + 15) / 16, 0), Cfg::MT));
+      bands = uniform_int(min(max((cur.valid_rows - cur.m0 - wm0 + 15) / 16, 0), C::MT));
     RowGroups nrg{-1, -1};
-    if constexpr (KIND == KIND_CONTIGUOUS) nrg = load_row_groups<Cfg>(p, nxt, wm0, lane);
-    f32x4 acc[Cfg::MT][Cfg::NT];
+    if constexpr (KIND == KIND_CONTIGUOUS) nrg = load_row_groups<C>(p, nxt, wm0, lane);
+    f32x4 acc[C::MT][C::NT];
 #pragma unroll
-    for (int mt = 0; mt < Cfg::MT; ++mt)
+    for (int mt = 0; mt < C::MT; ++mt)
 #pragma unroll
-      for (int nt = 0; nt < Cfg::NT; ++nt) acc[mt][nt] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      for (int nt = 0; nt < C::NT; ++nt) acc[mt][nt] = (f32x4){0.f, 0.f, 0.f, 0.f};
 
     if (counts_on_device(KIND) && bands <= HALF_BANDS) {
-      if (phase == 0) mainloop<KIND, 0, HALF_BANDS>(p, c0, c1, c2, acc, on, wave, lane, lds, lo, nrg, nxt.group, nmask);
-      else mainloop<KIND, 1, HALF_BANDS>(p, c0, c1, c2, acc, on, wave, lane, lds, lo, nrg, nxt.group, nmask);
+      if (phase == 0) mainloop<C, KIND, 0, HALF_BANDS>(p, c0, c1, c2, acc, on, wave, lane, lds, lo, nrg, nxt.group, nmask);
+      else mainloop<C, KIND, 1, HALF_BANDS>(p, c0, c1, c2, acc, on, wave, lane, lds, lo, nrg, nxt.group, nmask);
     } else {
-      if (phase == 0) mainloop<KIND, 0, Cfg::MT>(p, c0, c1, c2, acc, on, wave, lane, lds, lo, nrg, nxt.group, nmask);
-      else mainloop<KIND, 1, Cfg::MT>(p, c0, c1, c2, acc, on, wave, lane, lds, lo, nrg, nxt.group, nmask);
+      if (phase == 0) mainloop<C, KIND, 0, C::MT>(p, c0, c1, c2, acc, on, wave, lane, lds, lo, nrg, nxt.group, nmask);
+      else mainloop<C, KIND, 1, C::MT>(p, c0, c1, c2, acc, on, wave, lane, lds, lo, nrg, nxt.group, nmask);
     }
     phase = (phase + steps) & 1;
 
-    if (on) store_tile<KIND>(p, cur, cmask, acc, wm0, wn0, lane);
+    if (on) store_tile<C, KIND>(p, cur, cmask, acc, wm0, wn0, lane);
     // Slide the window.
     cmask = nmask;
     cur = nxt;
@@ -524,9 +546,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) fp4_gemm_nt_kernel(GemmArgs p
     c1 = c2;
     if (nx2.active) {
       t2 += grid;
-      nx2 = next_active<Cfg, KIND>(p, t2, grid, num_tiles, s_prefix);
+      nx2 = next_active<C, KIND>(p, t2, grid, num_tiles, s_prefix);
     }
-    c2 = nx2.active ? tile_src(p, nx2) : c1;
+    c2 = nx2.active ? tile_src<C>(p, nx2) : c1;
   }
   // The last refills loaded steps nobody reads; no wave may end while such a load can
   // still write its LDS.
@@ -732,22 +754,36 @@ static hipError_t launch_few(GemmArgs args, int num_cus, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int KIND>
-static hipError_t launch_mx(GemmArgs args, int num_cus, hipStream_t stream) {
-  if (most_tiles<mx::Few>(KIND, args) <= FEW_TILES) return launch_few<KIND>(args, num_cus, stream);
-  using C = mx::Cfg;
+template <class C, int KIND>
+static hipError_t launch_tiles(GemmArgs args, int num_cus, hipStream_t stream) {
   args.m_blocks = (args.m + C::BM - 1) / C::BM;
   args.n_blocks = (args.n + C::BN - 1) / C::BN;
   args.num_tiles = (int)most_tiles<C>(KIND, args);
-  auto kern = mx::fp4_gemm_nt_kernel<KIND>;
+  auto kern = mx::fp4_gemm_nt_kernel<C, KIND>;
   int per_cu = 1;
-  hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, kern, mx::Cfg::THREADS, 0);
+  hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, kern, C::THREADS, 0);
   if (e != hipSuccess) return e;
   if (per_cu < 1) per_cu = 1;
   const int grid = balanced_grid(args.num_tiles, (long long)num_cus * per_cu);
   if (grid < 1) return hipSuccess;
-  hipLaunchKernelGGL(kern, dim3(grid), dim3(mx::Cfg::THREADS), 0, stream, args);
+  hipLaunchKernelGGL(kern, dim3(grid), dim3(C::THREADS), 0, stream, args);
   return hipGetLastError();
+}
+
+// Tiles of 128 x 256 up to which a call takes those, one to a compute unit: 2048 x 4096 x
+// 4096 (256) 23.9 us, with 256 x 256 30.0; 2048^3 (128) 13.9, 18.5; 8 groups of up to 256 x
+// 2048 x 2048 (128) 14.5, 18.5; but 3000 x 4096 x 2048 (384) 25.0, 19.9. So do masked calls
+// of at most 128 rows a group, half of whose larger tiles would be empty: 32 groups of up
+// to 64 x 4096 x 7168 92, 96; 29 of up to 48 x 2688 x 640 12.6, 13.5; but 32 of up to 256 x
+// 4096 x 7168 163, 131.
+constexpr long long HALF_TILES = 256;
+
+template <int KIND>
+static hipError_t launch_mx(const GemmArgs& args, int num_cus, hipStream_t stream) {
+  if (most_tiles<mx::Few>(KIND, args) <= FEW_TILES) return launch_few<KIND>(args, num_cus, stream);
+  if (most_tiles<mx::Half>(KIND, args) <= HALF_TILES || (KIND == KIND_MASKED && args.m <= mx::Half::BM))
+    return launch_tiles<mx::Half, KIND>(args, num_cus, stream);
+  return launch_tiles<mx::Big, KIND>(args, num_cus, stream);
 }
 
 hipError_t launch_fp4(int kind, GemmArgs args, int num_cus, hipStream_t stream) {

@@ -152,9 +152,10 @@ def _check(got_bits, a, sfa, b, sfb, k, whole, what):
         check_close(got_bits, ref, what, mag, k)
 
 
-# Few tiles, and as many as take the large ones.
+# Few tiles, more, and as many as take the largest ones.
 DENSE = [(1, 128, 128), (15, 128, 384), (130, 384, 256), (257, 256, 512), (300, 640, 1152), (513, 128, 2048), (64, 512, 7168),
-         (1, 49280, 128), (15, 49280, 640), (257, 9984, 384), (513, 5632, 256), (64, 49280, 1152), (700, 4608, 2048)]
+         (1, 49280, 128), (15, 49280, 640), (257, 9984, 384), (513, 5632, 256), (64, 49280, 1152), (700, 4608, 2048),
+         (1, 65792, 128), (15, 65792, 640), (257, 22272, 384), (513, 13312, 256), (64, 65792, 1152), (700, 11008, 640)]
 
 
 @pytest.mark.parametrize("whole", [False, True])
@@ -184,7 +185,7 @@ def test_dense_many_tiles(dev):
     check_close(got[np.ix_(rows, cols)], ref, "sampled", mag, k)
 
 
-@pytest.mark.parametrize("n", [256, 24832])
+@pytest.mark.parametrize("n", [256, 24832, 65792])
 @pytest.mark.parametrize("k", [128, 896])
 def test_nan_scales_stay_in_their_rows(dev, k, n):
     _say(f"NaN scales, K {k}, N {n}")
@@ -201,7 +202,7 @@ def test_nan_scales_stay_in_their_rows(dev, k, n):
     np.testing.assert_array_equal(nan, want)
 
 
-@pytest.mark.parametrize("n", [128, 49280])
+@pytest.mark.parametrize("n", [128, 49280, 65792])
 def test_scales_at_their_ends(dev, n):
     """2^-127 times 2^127, and sums below BF16's smallest."""
     _say(f"extreme scales, N {n}")
@@ -229,7 +230,8 @@ def _layout(counts, m):
 
 @pytest.mark.parametrize("whole", [False, True])
 @pytest.mark.parametrize("counts,n,k", [([5, 0, 300, 128, 1], 256, 384), ([700], 128, 128), ([127, 129, 640], 640, 1024),
-                                        ([5, 0, 300, 128, 1], 3584, 384), ([700], 4992, 128), ([127, 129, 640], 2816, 1024)])
+                                        ([5, 0, 300, 128, 1], 3584, 384), ([700], 4992, 128), ([127, 129, 640], 2816, 1024),
+                                        ([5, 0, 300, 128, 1], 9472, 384), ([700], 9472, 128), ([127, 129, 640], 7424, 512)])
 def test_contiguous(dev, counts, n, k, whole):
     _say(f"contiguous {counts} n={n} k={k} whole={whole}")
     m, g = sum(-(-c // 128) * 128 for c in counts) + 128, len(counts)
@@ -246,7 +248,7 @@ def test_contiguous(dev, counts, n, k, whole):
         _check(got[rows], a[rows], sfa[:, :m][:, rows], b[e], sfb[e], k, whole, f"group {e}")
 
 
-@pytest.mark.parametrize("n", [128, 4992])
+@pytest.mark.parametrize("n", [128, 4992, 13312])
 def test_contiguous_ids_that_change_inside_blocks(dev, n):
     """The row rule of the layout: a 128-row block is its first row's group's."""
     _say(f"contiguous, ids that change inside blocks, n={n}")
@@ -267,7 +269,9 @@ def test_contiguous_ids_that_change_inside_blocks(dev, n):
 @pytest.mark.parametrize("counts,max_m,n,k", [([5, 0, 64, 63], 64, 128, 384), ([300, -2, 17, 999, 129], 300, 384, 256),
                                               ([1] * 40, 8, 256, 1152), ([0, 0], 16, 128, 128), ([97, 160], 257, 128, 512),
                                               ([300, -2, 17, 999, 129], 300, 2048, 256), ([1, 8] * 20, 8, 1280, 1152),
-                                              ([0, 0], 16, 24704, 128), ([97, 160], 257, 4992, 512)])
+                                              ([0, 0], 16, 24704, 128), ([97, 160], 257, 4992, 512),
+                                              ([300, -2, 17, 999, 129], 300, 4608, 256), ([97, 160], 257, 11008, 512),
+                                              ([128, 1] * 20, 128, 1792, 384)])
 def test_masked(dev, counts, max_m, n, k, whole):
     _say(f"masked {counts} of {max_m} n={n} k={k} whole={whole}")
     g = len(counts)
@@ -289,7 +293,8 @@ def test_masked(dev, counts, max_m, n, k, whole):
 @pytest.mark.parametrize("counts,m,n,k", [([3, 0, 200, 31], 240, 256, 384), ([5, -4, 90, 400, 7], 260, 128, 640),
                                           ([1, 2, 3] * 20, 120, 128, 256), ([513], 513, 384, 128),
                                           ([5, -4, 90, 400, 7], 260, 4992, 640), ([1, 2, 3] * 20, 120, 896, 256),
-                                          ([513], 513, 4992, 128)])
+                                          ([513], 513, 4992, 128), ([5, -4, 90, 400, 7], 260, 8448, 640),
+                                          ([1, 2, 3] * 20, 120, 1280, 256), ([513], 513, 11008, 128)])
 def test_nopad(dev, counts, m, n, k, whole):
     _say(f"nopad {counts} of {m} n={n} k={k} whole={whole}")
     g = len(counts)
@@ -368,7 +373,7 @@ def test_two_streams_at_once(dev):
         _check(_bits(d).view(np.uint16), *o, k, False, "stream")
 
 
-@pytest.mark.parametrize("n", [640, 2560])
+@pytest.mark.parametrize("n", [640, 2560, 6912])
 @pytest.mark.parametrize("k", [128, 256, 384, 640])
 def test_few_workgroups_give_the_same_bits(dev, k, n):
     """One, three and eight workgroups for all tiles: tiles of one, two and three steps that
