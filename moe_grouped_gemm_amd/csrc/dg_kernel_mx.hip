@@ -81,8 +81,7 @@ constexpr int A_PACK_SHIFT<mx::Few> = 1;
 
 namespace mx {
 
-// An LDS buffer of its own for each stage and half (the compiler makes a read wait for
-// the loads in flight into the buffer that it reads, and only for those).
+// An LDS buffer for each stage and half, and its byte address.
 template <class C, int S, int PART>
 __device__ __forceinline__ uint8_t* stage_buf() {
   __shared__ __attribute__((aligned(1024))) uint8_t buf[PART == LOW ? LOW_BYTES<C> : A_HALF<C>];
@@ -450,7 +449,7 @@ __device__ __forceinline__ void mainloop(const GemmArgs& p, const TileSrc& t0, c
 
 // A wave whose valid rows lie in its first HALF_BANDS bands runs a copy of the K loop
 // without the other bands' MFMAs (their rows are never stored). 32 groups of up to 64
-// rows, 4096 x 7168: 93 us, without the copy 99; 16 groups of up to 256 rows, 7168 x
+// rows, 4096 x 7168: 97 us, without the copy 112; 16 groups of up to 256 rows, 7168 x
 // 2048: 40 with either.
 constexpr int HALF_BANDS = 4;
 
