@@ -264,10 +264,9 @@ dg_status dg_moe_block_norm_bwd(const dg_moe_norm_bwd* args, void* stream);
  *   workspace  16-byte aligned, dg_moe_experts_workspace_bytes() bytes;
  *            contents need not be kept between calls; calls that use one must be
  *            ordered (one stream, or events)
- * The weights of the experts that have tokens are read once. Neither x nor the
- * weights are quantised on the way: weights stand for their exact values (of FP4
- * in BF16's range), products sum in float32 and silu(g) * u is rounded once to
- * BF16. (The order of a token's sums goes by the sizes and by how many experts the
+ * The weights of the experts that have tokens are read once. Neither x nor the weights are quantised on the way: weights stand for their
+ * exact values (of FP4 in BF16's range), products sum in float32 and silu(g) * u is held
+ * to 2^-16 of itself (as the sum of two BF16 values). (The order of a token's sums goes by the sizes and by how many experts the
  * call's tokens name.)
  * tokens <= 128, top_k <= 32, tokens * top_k <= 1024, num_groups <= 4096,
  * hidden and inner multiples of 128 up to 2^16. tokens == 0 is a no-op.

@@ -5,9 +5,8 @@
 //
 // with the experts' weights in FP8 (one float32 scale per 128 x 128) or FP4 (one
 // power-of-two scale per 32 values of a row) and everything else as it comes: x in
-// BF16, sums in float32, a rounded once to BF16 (the rounding of y itself is as
-// large; a grouped product's path rounds g, u and then a to FP8). The weights of
-// the experts that have tokens are read once, and that bounds both launches.
+// BF16, sums in float32, a held to 2^-16 of it in two BF16 values, y rounded once. The
+// weights of the experts that have tokens are read once, and that bounds both launches.
 //
 // Every wave streams weights of its own through a ring in LDS, without a barrier:
 // direct-to-LDS loads whose successive lanes read a row's successive 16 bytes, some
@@ -19,11 +18,12 @@
 //
 // What bounds it: a compute unit takes some 40 GB/s together, whether two or five
 // steps are on their way, so the tokens' or activations' bytes (16 tokens: half the
-// weights' in the first launch, as many in the second) and the processors' turns add to
-// the weights' time. An FP8 batch, 61 tokens and 32 experts of 7168 x 2048:
-// 180 us (5.2 TB/s of weights) and 101 (4.7); weights alone 164 and 79. One token,
-// eight experts in FP4: 28 and 17 us, of which about 5 each are a launch's lists of
-// who is where, one read from memory after the other.
+// weights' in the first launch, twice as many in the second) and the processors' turns
+// add to the weights' time. An FP8 batch, 61 tokens and 32 experts of 7168 x 2048:
+// 186 us (5.1 TB/s of weights) and 129 (3.6); weights alone 164 and 79, and the second
+// launch 102 with activations of one BF16 value. One token, eight experts in FP4: 28 and 18
+// us, of which about 5 each are a launch's lists of who is where, one read from memory
+// after the other.
 //
 // A step is 128 bytes of each row: 128 values of FP8, or two blocks of 128 of FP4.
 //
@@ -70,21 +70,39 @@ static_assert(sizeof(ExpertPlan) == EXPERT_PLAN_BYTES, "room for the plan");
 // Activations between the launches
 // ---------------------------------------------------------------------------
 
-// They lie in tiles of one expert's up to 16 tokens, in the order in which the second
-// launch's lanes load them, 16 bytes each: block b of 128 values, instruction j, lane
-// group g, row. `rows` is 4 where the call has no more tokens (the lanes of other rows
-// repeat them), else 16. With no more slots than experts a tile is known by its first
-// pair's slot, else by the expert and its number.
+// A value is held as the sum of two in BF16, float32's upper 16 bits and what those leave
+// out, which is good to 2^-16 of it (one BF16 value, 2^-8 of it, would double the
+// layer's error). The second products multiply the two side by side, as neighbouring
+// columns of a token operand: a tile is one expert's up to 8 tokens.
+//
+// Tiles lie in the order in which the second launch's lanes load them, 16 bytes each: block
+// b of 128 values, instruction j, lane group g, row: each token's upper part, then its
+// lower one, so that few tokens take few cache lines (with all upper parts first, 16 tokens
+// and 64 experts took 88 us for 69). TOKENS, of a tile, is 4 where the call has no more,
+// else 8. With no more slots than experts a tile is known by its first pair's slot, else by
+// the expert and its number.
+constexpr int TILE_TOKENS = 8;
+__device__ __forceinline__ bool tiles_by_slot(const ExpertsArgs& p) { return p.tokens * p.top_k <= p.num_groups; }
 __device__ __forceinline__ int act_tile(const ExpertsArgs& p, int expert, int number, int first_slot) {
-  const bool by_slot = p.tokens * p.top_k <= p.num_groups;
-  return by_slot ? first_slot : expert * ((p.tokens + 15) / 16) + number;
+  return tiles_by_slot(p) ? first_slot : expert * ((p.tokens + TILE_TOKENS - 1) / TILE_TOKENS) + number;
 }
-// Of value k of a tile's row, in values.
-template <bool FP4, int ROWS>
+// Of value k of a tile's row, in BF16 values.
+template <bool FP4, int TOKENS>
 __device__ __forceinline__ int act_at(int k, int row) {
   const int b = k / QBLOCK, in = k % QBLOCK;
   const int g = FP4 ? in / 32 : in / 16 % 4, j = FP4 ? in / 8 % 4 : in / 64 * 2 + in / 8 % 2;
-  return b * QBLOCK * ROWS + ((j * 4 + g) * ROWS + row) * 8 + in % 8;
+  return b * QBLOCK * 2 * TOKENS + ((j * 4 + g) * 2 * TOKENS + row) * 8 + in % 8;
+}
+
+// The upper parts of two values, and the lower ones (nothing is left of an infinity).
+__device__ __forceinline__ uint32_t upper2(float a, float b) {
+  return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, a), 0x07060302u);
+}
+__device__ __forceinline__ uint32_t lower2(float a, float b) {
+  auto rest = [](float v) {
+    return __builtin_isfinite(v) ? v - __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & 0xFFFF0000u) : 0.0f;
+  };
+  return pack2((f32x2){rest(a), rest(b)});
 }
 
 // ---------------------------------------------------------------------------
@@ -184,8 +202,9 @@ struct Weights {
     for (int q = 0; q < SCALE_LOADS; ++q) dma4(scales, sf_at[q], (uint32_t)step * scale_step, lds + SCALES_AT + q * 256);
   }
 
-  // acc += tile i of block `block` of the step at `st` times the tokens' operands.
-  template <int NT>
+  // acc += tile i of block `block` of the step at `st` times the first USED of the tokens'
+  // operands.
+  template <int USED, int NT>
   __device__ __forceinline__ void multiply(f32x4 (&acc)[NT], const uint8_t* st, int i, int block,
                                            const u32x4 (&t)[NT][4], int lane) const {
     const uint8_t* tile = st + i * TILE_BYTES;
@@ -201,7 +220,7 @@ struct Weights {
         w[j] = __builtin_bit_cast(bf16x8, fp4_values(dword, code));
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < USED; ++nt)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           acc[nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j], __builtin_bit_cast(bf16x8, t[nt][j]), acc[nt], 0, 0, 0);
@@ -219,7 +238,7 @@ struct Weights {
         w[j] = __builtin_bit_cast(bf16x8, o);
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int nt = 0; nt < USED; ++nt) {
         f32x4 part = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -356,16 +375,16 @@ __device__ void write_plan(const ExpertsArgs& p, const UpLists& l, int experts, 
 // The tiles [tile, tile_end) of 16 RT gate rows and as many up rows of one expert, with up
 // to 4 FOURS of its tokens: the waves share K and their sums meet in LDS at a tile's end.
 // The weights go on from one tile to the next; tokens' rows are fetched again, from L2.
-template <bool FP4, int RT, int FOURS, int ROWS>
+template <bool FP4, int RT, int FOURS, int TOKENS>
 __device__ __forceinline__ void up_tiles(const ExpertsArgs& p, UpWeights<FP4, RT>& weights, int tile, int tile_end,
                                          int expert, int number, const uint16_t* slots, int count, uint8_t* lds) {
   constexpr int NT = (FOURS + 3) / 4, W = UpWeights<FP4, RT>::LOADS, T = FOURS, TILES = 2 * RT;
-  constexpr int STEP = UpWeights<FP4, RT>::BYTES, TOKENS = FOURS * 1024;
+  constexpr int STEP = UpWeights<FP4, RT>::BYTES, TOKEN_BYTES = FOURS * 1024;
   constexpr int T_AHEAD = FOURS <= 4 ? 2 : 1, T_SLOTS = T_AHEAD + 1;
   // The waves' sums lie at the end of their tokens' place; before them the next tile's
   // first tokens are on their way meanwhile.
   constexpr int SUMS = TILES * NT * 1024, SUMS_AT = UP_W_SLOTS * STEP + UP_T_BYTES - SUMS;
-  static_assert(T_SLOTS * TOKENS <= UP_T_BYTES && T_AHEAD * TOKENS + SUMS <= UP_T_BYTES, "room for both");
+  static_assert(T_SLOTS * TOKEN_BYTES <= UP_T_BYTES && T_AHEAD * TOKEN_BYTES + SUMS <= UP_T_BYTES, "room for both");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   uint8_t* const ring = lds + wave * UP_RING<FP4, RT>;
@@ -413,13 +432,18 @@ __device__ __forceinline__ void up_tiles(const ExpertsArgs& p, UpWeights<FP4, RT
     read_at[nt] = row * 256;
     swizzle[nt] = token_swizzle(row & 15);
   }
-  const int act_tile0 = act_tile(p, expert, number, slots[0]);
-  const int act_tile1 = NT > 1 && count > 16 ? act_tile(p, expert, number + 1, slots[16]) : 0;
+  uint16_t* act[NT];  // where the lane's tokens' activations go (a row past the last: not used)
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int token = min(nt * 16 + r, count - 1), first = token / TILE_TOKENS * TILE_TOKENS;
+    const int to = act_tile(p, expert, number + first / TILE_TOKENS, slots[first]);
+    act[nt] = p.act + (size_t)to * 2 * TOKENS * p.inner + token % TILE_TOKENS * 16;
+  }
   int t_next = 0;
   auto load_tokens = [&](int i) {
     const int block = step_of(i / BLOCKS) * BLOCKS + i % BLOCKS;
 #pragma unroll
-    for (int q = 0; q < FOURS; ++q) dma16(x, x_at[q], (uint32_t)block * 256, token_base + t_next * TOKENS + q * 1024);
+    for (int q = 0; q < FOURS; ++q) dma16(x, x_at[q], (uint32_t)block * 256, token_base + t_next * TOKEN_BYTES + q * 1024);
     t_next = t_next == T_SLOTS - 1 ? 0 : t_next + 1;
   };
 
@@ -453,7 +477,7 @@ __device__ __forceinline__ void up_tiles(const ExpertsArgs& p, UpWeights<FP4, RT
       else if (tokens_after == 1) wait_loads<W + T>();
       else wait_loads<W + T_AHEAD * T>();
       const uint8_t* const st = ring + w_slot * STEP;
-      const uint8_t* const tok = ring + UP_W_SLOTS * STEP + t_slot * TOKENS;
+      const uint8_t* const tok = ring + UP_W_SLOTS * STEP + t_slot * TOKEN_BYTES;
       u32x4 t[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -493,9 +517,11 @@ __device__ __forceinline__ void up_tiles(const ExpertsArgs& p, UpWeights<FP4, RT
 #pragma unroll
       for (int k = 0; k < 4; ++k) a[k] = gate[k] * sigmoid(gate[k]) * up[k];
       if (nt * 16 + r < count) {
-        const u32x2 packed = {pack2((f32x2){a[0], a[1]}), pack2((f32x2){a[2], a[3]})};
-        uint16_t* const to = p.act + (size_t)(nt ? act_tile1 : act_tile0) * ROWS * p.inner;
-        *reinterpret_cast<u32x2*>(to + act_at<FP4, ROWS>(tile * 16 * RT + 16 * i + 4 * g, r)) = packed;
+        uint16_t* to = act[0];  // (a choice by an index would put them in memory)
+        if constexpr (NT > 1) to = nt ? act[1] : to;
+        const int k = tile * 16 * RT + 16 * i + 4 * g;
+        *reinterpret_cast<u32x2*>(to + act_at<FP4, TOKENS>(k, 0)) = (u32x2){upper2(a[0], a[1]), upper2(a[2], a[3])};
+        *reinterpret_cast<u32x2*>(to + act_at<FP4, TOKENS>(k, 1)) = (u32x2){lower2(a[0], a[1]), lower2(a[2], a[3])};
       }
     }
     meet();  // the sums have been read: tokens may come
@@ -506,7 +532,7 @@ __device__ __forceinline__ void up_tiles(const ExpertsArgs& p, UpWeights<FP4, RT
 
 // The tiles of all experts that have tokens, in order, are dealt to the workgroups in
 // runs of the same length. The first workgroup writes the plan as well.
-template <bool FP4, int RT, int ROWS>
+template <bool FP4, int RT, int TOKENS>
 __global__ __launch_bounds__(UP_THREADS, 1) void experts_up_kernel(ExpertsArgs p) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[UP_WAVES * UP_RING<FP4, RT>];
   __shared__ UpLists l;
@@ -544,14 +570,15 @@ __global__ __launch_bounds__(UP_THREADS, 1) void experts_up_kernel(ExpertsArgs p
     for (int t0 = 0; t0 < count;) {
       const int left = count - t0, here = min(left, 4 * UP_MOST_FOURS);
       const uint16_t* const slots = l.list + t0;
-      if constexpr (ROWS == 4) {
-        up_tiles<FP4, RT, 1, ROWS>(p, weights, tile, tile_end, expert, t0 / 16, slots, here, lds);
+      const int number = t0 / TILE_TOKENS;
+      if constexpr (TOKENS == 4) {
+        up_tiles<FP4, RT, 1, TOKENS>(p, weights, tile, tile_end, expert, number, slots, here, lds);
       } else {
-        if (here <= 4) up_tiles<FP4, RT, 1, ROWS>(p, weights, tile, tile_end, expert, t0 / 16, slots, here, lds);
-        else if (here <= 8) up_tiles<FP4, RT, 2, ROWS>(p, weights, tile, tile_end, expert, t0 / 16, slots, here, lds);
-        else if (here <= 16) up_tiles<FP4, RT, 4, ROWS>(p, weights, tile, tile_end, expert, t0 / 16, slots, here, lds);
-        else if (here <= 24) up_tiles<FP4, RT, 6, ROWS>(p, weights, tile, tile_end, expert, t0 / 16, slots, here, lds);
-        else up_tiles<FP4, RT, 8, ROWS>(p, weights, tile, tile_end, expert, t0 / 16, slots, here, lds);
+        if (here <= 4) up_tiles<FP4, RT, 1, TOKENS>(p, weights, tile, tile_end, expert, number, slots, here, lds);
+        else if (here <= 8) up_tiles<FP4, RT, 2, TOKENS>(p, weights, tile, tile_end, expert, number, slots, here, lds);
+        else if (here <= 16) up_tiles<FP4, RT, 4, TOKENS>(p, weights, tile, tile_end, expert, number, slots, here, lds);
+        else if (here <= 24) up_tiles<FP4, RT, 6, TOKENS>(p, weights, tile, tile_end, expert, number, slots, here, lds);
+        else up_tiles<FP4, RT, 8, TOKENS>(p, weights, tile, tile_end, expert, number, slots, here, lds);
       }
       t0 += here;
     }
@@ -564,53 +591,64 @@ __global__ __launch_bounds__(UP_THREADS, 1) void experts_up_kernel(ExpertsArgs p
 
 constexpr int DOWN_WAVES = 4, DOWN_THREADS = DOWN_WAVES * 64;
 
-// Steps on their way and in use: as many as leave the sums room (and as vmcnt can count).
-template <bool FP4, int TOKENS, int NT>
-constexpr int DOWN_DEPTH = FP4 ? (NT > 1 ? 3 : 4) : TOKENS > 64 ? 4 : 5;
+// Steps on their way and in use: as many as leave the sums and the operands' registers room.
+template <bool FP4, int NT>
+constexpr int DOWN_DEPTH = (FP4 ? 4 : 5) - (NT == 4 ? 2 : NT == 2 ? 1 : 0);
 template <bool FP4, int RT>
 using DownWeights = Weights<FP4, RT, 1>;
 
+// Of the other lane of a pair (DPP quad_perm 1, 0, 3, 2).
+__device__ __forceinline__ float neighbour(float v) {
+  return __builtin_bit_cast(float, quad<0xB1>(__builtin_bit_cast(uint32_t, v)));
+}
+
 struct DownItem {
-  int expert_count, begin, tile, tile2;  // pairs of the plan (expert << 8 | how many), and their activations
+  int expert_count, begin, tile;  // pairs of the plan (expert << 8 | how many), and their first activations
 };
 
-// A workgroup takes 16 RT columns of y for all tokens. Its waves share the experts, 16 NT
-// tokens of one at a time (NT is 2 for more than 16 tokens), and, where these do not come out even, their K in parts;
-// each wave keeps sums of its own in LDS, which are added in order at the end. A wave's
-// items follow one another in one pipeline of steps.
-template <bool FP4, int ROWS, int TOKENS, int NT, int RT>
+// A workgroup takes 16 RT columns of y for all tokens (of which a call has at most MOST).
+// Its waves share the experts, NT tiles of 8 tokens of one at a time (NT is as many as the
+// call's tokens fill, up to 4), and, where these do not come out even, their K in parts; each
+// wave keeps sums of its own in LDS, which are added in order at the end. A wave's items
+// follow one another in one pipeline of steps.
+template <bool FP4, int TOKENS, int MOST, int NT, int RT>
 __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsArgs p) {
-  constexpr int STRIDE = 16 * RT + (TOKENS > 64 ? 0 : 4);  // floats; 4 past a power of two where there is room
-  constexpr int DEPTH = DOWN_DEPTH<FP4, TOKENS, NT>, W = DownWeights<FP4, RT>::LOADS, STEP = DownWeights<FP4, RT>::BYTES;
-  constexpr int BLOCKS = DownWeights<FP4, RT>::BLOCKS, ACT_LOADS = 4 * NT * BLOCKS;
+  constexpr int STRIDE = 16 * RT + (MOST > 64 ? 0 : 4);  // floats; 4 past a power of two where there is room
+  constexpr int DEPTH = DOWN_DEPTH<FP4, NT>, W = DownWeights<FP4, RT>::LOADS, STEP = DownWeights<FP4, RT>::BYTES;
+  // (loads of activations: at least one tile's)
+  constexpr int BLOCKS = DownWeights<FP4, RT>::BLOCKS, ACT_LOADS = 4 * BLOCKS;
   __shared__ __attribute__((aligned(1024))) uint8_t rings[DOWN_WAVES * DEPTH * STEP];
-  __shared__ __attribute__((aligned(16))) float sums[DOWN_WAVES * TOKENS * STRIDE];
+  __shared__ __attribute__((aligned(16))) float sums[DOWN_WAVES * MOST * STRIDE];
   // Of the pairs; read from memory in the loop, they would be waited for with all the
   // weights that are on their way.
   __shared__ DownItem items[MAX_FEW_PAIRS];
-  __shared__ uint16_t sums_at[MAX_FEW_PAIRS];  // of the pair's token, in 16 bytes
+  __shared__ uint16_t slots[MAX_FEW_PAIRS];     // the pair's slot,
+  __shared__ uint16_t sums_at[MAX_FEW_PAIRS];  // where its token's sums are, in 16 bytes
   __shared__ float pair_weights[MAX_FEW_PAIRS];
   __shared__ int items_of[DOWN_WAVES];
   __shared__ bool last;
   ExpertPlan* const plan = reinterpret_cast<ExpertPlan*>(p.plan);
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), c0 = blockIdx.x * 16 * RT;
-  float* const mine = sums + wave * TOKENS * STRIDE;
+  float* const mine = sums + wave * MOST * STRIDE;
   for (int i = lane; i < p.tokens * STRIDE; i += 64) mine[i] = 0.0f;
 
   // What the plan may hold is read before it is known how much of that it does hold: one
   // way to memory, not three.
   const int n = p.tokens * p.top_k, most = min(n, p.num_groups), experts = plan->experts;
   for (int i = tid; i < n; i += DOWN_THREADS) {
-    sums_at[i] = (uint16_t)(plan->slot[i] / p.top_k * (STRIDE / 4));
+    const int slot = plan->slot[i];
+    slots[i] = (uint16_t)slot;
+    sums_at[i] = (uint16_t)(slot / p.top_k * (STRIDE / 4));
     pair_weights[i] = plan->weight[i];
   }
-  // The items: an expert's pairs 16 NT at a time, in order.
+  // The items: an expert's pairs 8 NT at a time, in order.
+  constexpr int ITEM = TILE_TOKENS * NT;
   int total = 0;
   for (int r0 = 0; r0 < most; r0 += DOWN_THREADS) {
     const int at = r0 + tid;
     const ExpertEntry entry = plan->entry[min(at, most - 1)];
-    const int has = at < experts ? (entry.count + 16 * NT - 1) / (16 * NT) : 0;
+    const int has = at < experts ? (entry.count + ITEM - 1) / ITEM : 0;
     int upto = has;
     for (int d = 1; d < 64; d <<= 1) {
       const int v = __shfl_up(upto, d);
@@ -624,10 +662,9 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
       total += items_of[w];
     }
     for (int i = 0; i < has; ++i) {
-      const int begin = entry.begin + 16 * NT * i, count = min(entry.count - 16 * NT * i, 16 * NT);
+      const int begin = entry.begin + ITEM * i, count = min(entry.count - ITEM * i, ITEM);
       const int tile = act_tile(p, entry.expert, NT * i, i == 0 ? entry.first : plan->slot[begin]);
-      const int tile2 = count > 16 ? act_tile(p, entry.expert, NT * i + 1, plan->slot[begin + 16]) : tile;
-      items[before + i] = DownItem{entry.expert << 8 | count, begin, tile, tile2};
+      items[before + i] = DownItem{entry.expert << 8 | count, begin, tile};
     }
     __syncthreads();
   }
@@ -643,14 +680,13 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
 
   // Where the loads and the products are: the turn, its item and its steps.
   struct Cursor {
-    int turn, step, end, begin, count, tile, tile2;
+    int turn, step, end, begin, count, tile;
   };
   auto start = [&](Cursor& c) {
     const int item = me + c.turn * waves, part = item % parts;
     const DownItem at = items[item / parts];
     c.begin = __builtin_amdgcn_readfirstlane(at.begin);
     c.tile = __builtin_amdgcn_readfirstlane(at.tile);
-    c.tile2 = __builtin_amdgcn_readfirstlane(at.tile2);
     const int expert_count = __builtin_amdgcn_readfirstlane(at.expert_count);
     c.count = expert_count & 0xFF;
     c.step = item_steps * part / parts;
@@ -672,31 +708,38 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
     const int first = start(ahead);
     DownWeights<FP4, RT> weights(p.b2, p.sfb2, p.hidden, p.inner, lane);
     weights.place(first, row0, lane);
-    // The item's activations; rows past its pairs are not loaded (they lie past the end, as
-    // does a second block past the last).
+    // The item's activations: lanes 2 t and 2 t + 1 load the two parts of a token's. Rows past
+    // its pairs are not loaded (they lie past the end, as does a second block past the last).
     __amdgpu_buffer_rsrc_t act[NT];
     uint32_t act_at[NT];
     auto place_act = [&]() {
-      const uint32_t tile_values = (uint32_t)ROWS * p.inner;
+      const uint32_t tile_values = (uint32_t)(2 * TOKENS) * p.inner;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        act[nt] = buffer_rsrc(p.act + (size_t)(nt ? ahead.tile2 : ahead.tile) * tile_values, tile_values * 2);
-        act_at[nt] = 16 * nt + r < ahead.count ? (uint32_t)(g * ROWS + (r & (ROWS - 1))) * 16 : 0x80000000u;
+        const int first = TILE_TOKENS * nt, token = first + r / 2;
+        int tile = ahead.tile;
+        if (nt > 0 && first < ahead.count) tile = tiles_by_slot(p) ? slots[ahead.begin + first] : tile + nt;
+        act[nt] = buffer_rsrc(p.act + (size_t)tile * tile_values, tile_values * 2);
+        act_at[nt] = token < ahead.count ? (uint32_t)(g * 2 * TOKENS + r) * 16 : 0x80000000u;
       }
     };
     place_act();
     f32x4 acc[RT][NT] = {};
     int loaded = 0, w_next = 0, w_slot = 0;
     u32x4 t[DEPTH][BLOCKS][NT][4];
-    auto load = [&](u32x4 (&to)[BLOCKS][NT][4]) {
+    auto load = [&](u32x4 (&to)[BLOCKS][NT][4]) __attribute__((always_inline)) {
+      // Tiles that the item does not have are not asked for: a load takes its turn at the L1
+      // whether it has rows or not (57 tokens, 82 experts of 1536 x 1536: 184 us for 148).
 #pragma unroll
-      for (int b = 0; b < BLOCKS; ++b)
+      for (int nt = 0; nt < NT; ++nt)
+        if (nt == 0 || TILE_TOKENS * nt < ahead.count) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int b = 0; b < BLOCKS; ++b)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            to[b][nt][j] = __builtin_amdgcn_raw_buffer_load_b128(
-                act[nt], act_at[nt] + (b * QBLOCK * 2 + j * 64) * ROWS, ahead.step * BLOCKS * QBLOCK * ROWS * 2, 0);
+            for (int j = 0; j < 4; ++j)
+              to[b][nt][j] = __builtin_amdgcn_raw_buffer_load_b128(
+                  act[nt], act_at[nt] + (b * QBLOCK + j * 32) * TOKENS * 4, ahead.step * BLOCKS * QBLOCK * TOKENS * 4, 0);
+        }
       weights.load(ahead.step, base + w_next * STEP);
       w_next = w_next == DEPTH - 1 ? 0 : w_next + 1;
       if (++loaded < steps && ++ahead.step == ahead.end) {  // (past the last step it is loaded again)
@@ -706,19 +749,33 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
         place_act();
       }
     };
-    auto use = [&](const u32x4 (&from)[BLOCKS][NT][4]) {
+    auto use = [&](const u32x4 (&from)[BLOCKS][NT][4]) __attribute__((always_inline)) {
       const uint8_t* const st = ring + w_slot * STEP;
       w_slot = w_slot == DEPTH - 1 ? 0 : w_slot + 1;
+      // As many tiles as the item has.
+      auto multiply = [&](auto TILES) __attribute__((always_inline)) {
 #pragma unroll
-      for (int b = 0; b < BLOCKS; ++b)
+        for (int b = 0; b < BLOCKS; ++b)
 #pragma unroll
-        for (int k = 0; k < RT; ++k) weights.template multiply<NT>(acc[k], st, k, b, from[b], lane);
+          for (int k = 0; k < RT; ++k)
+            weights.template multiply<decltype(TILES)::value>(acc[k], st, k, b, from[b], lane);
+      };
+      if (NT > 3 && now.count > 3 * TILE_TOKENS) multiply(std::integral_constant<int, NT>{});
+      else if (NT > 2 && now.count > 2 * TILE_TOKENS) multiply(std::integral_constant<int, std::min(NT, 3)>{});
+      else if (NT > 1 && now.count > TILE_TOKENS) multiply(std::integral_constant<int, std::min(NT, 2)>{});
+      else multiply(std::integral_constant<int, 1>{});
       if (++now.step < now.end) return;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        if (16 * nt + r < now.count) {  // the item's tokens differ from one another
-          const float w = pair_weights[now.begin + 16 * nt + r];
-          float* const at = mine + 4 * (sums_at[now.begin + 16 * nt + r] + g);
+      for (int nt = 0; nt < NT; ++nt) {
+        // The sums of the lower parts to those of the upper ones.
+#pragma unroll
+        for (int k = 0; k < RT; ++k)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[k][nt][v] += neighbour(acc[k][nt][v]);
+        const int pair = TILE_TOKENS * nt + r / 2;
+        if (r % 2 == 0 && pair < now.count) {  // the item's tokens differ from one another
+          const float w = pair_weights[now.begin + pair];
+          float* const at = mine + 4 * (sums_at[now.begin + pair] + g);
 #pragma unroll
           for (int k = 0; k < RT; ++k) {
             f32x4 sum = *reinterpret_cast<f32x4*>(at + 16 * k);
@@ -727,6 +784,7 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
             *reinterpret_cast<f32x4*>(at + 16 * k) = sum;
           }
         }
+      }
 #pragma unroll
       for (int k = 0; k < RT; ++k)
 #pragma unroll
@@ -734,7 +792,8 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
       if (++now.turn < turns) start(now);
     };
     // Rounds that are left at their end only, so that on every path to a use the compiler
-    // knows how many loads follow the ones that it waits for.
+    // knows how many loads follow the ones that it waits for: those of steps with one tile
+    // (the waits for the weights go by these as well).
     static_for<0, DEPTH - 1>([&](auto I) { load(t[decltype(I)::value]); });
     const int rounds = steps / DEPTH * DEPTH;
     for (int i0 = 0; i0 < rounds; i0 += DEPTH) {
@@ -758,7 +817,7 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
 #pragma unroll
     for (int w = 0; w < DOWN_WAVES; ++w)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) s[k] += sums[(w * TOKENS + t) * STRIDE + c + k];
+      for (int k = 0; k < 2; ++k) s[k] += sums[(w * MOST + t) * STRIDE + c + k];
     if (p.splits == 1)
       *reinterpret_cast<uint32_t*>(p.y + (size_t)t * p.hidden + c0 + c) = pack2(s);
     else
@@ -789,21 +848,21 @@ __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsAr
   }
 }
 
-template <bool FP4, int RT, int ROWS>
+template <bool FP4, int RT, int TOKENS>
 hipError_t launch_up(const ExpertsArgs& a, hipStream_t stream) {
   const int workgroups = std::min(std::min(a.tokens * a.top_k, a.num_groups) * (a.inner / (16 * RT)), a.cus);
-  hipLaunchKernelGGL((experts_up_kernel<FP4, RT, ROWS>), dim3(workgroups), dim3(UP_THREADS), 0, stream, a);
+  hipLaunchKernelGGL((experts_up_kernel<FP4, RT, TOKENS>), dim3(workgroups), dim3(UP_THREADS), 0, stream, a);
   return hipGetLastError();
 }
 
-template <bool FP4, int ROWS, int TOKENS, int NT>
+template <bool FP4, int TOKENS, int MOST, int NT>
 hipError_t launch_down(const ExpertsArgs& a, hipStream_t stream) {
   // 16 columns a workgroup, and the activations read twice as often, where 32 would leave
   // half the compute units without one. 128 tokens, 64 experts of 4096 x 1536 in FP8: 121
-  // us, with 32 columns 147; 16 tokens: 74 and 105. With hidden 7168 (448 workgroups for
-  // 224) 61 tokens and 32 experts took 140 us for 100.
+  // us, with 32 columns 186; 16 tokens: 72 and 100. With hidden 7168 (448 workgroups for
+  // 224) 61 tokens and 32 experts took 198 us for 129.
   const int rt = a.hidden / 32 <= a.cus / 2 ? 1 : 2;
-  const auto down = rt == 1 ? experts_down_kernel<FP4, ROWS, TOKENS, NT, 1> : experts_down_kernel<FP4, ROWS, TOKENS, NT, 2>;
+  const auto down = rt == 1 ? experts_down_kernel<FP4, TOKENS, MOST, NT, 1> : experts_down_kernel<FP4, TOKENS, MOST, NT, 2>;
   hipLaunchKernelGGL(down, dim3(a.hidden / (16 * rt), a.splits), dim3(DOWN_THREADS), 0, stream, a);
   return hipGetLastError();
 }
@@ -818,29 +877,30 @@ int down_splits(const ExpertsArgs& a) {
   return std::max(std::min(DOWN_COLUMNS / a.hidden, experts * steps / (8 * DOWN_WAVES)), 1);
 }
 
-// ROWS: 4 for up to 4 tokens, else 16.
-template <bool FP4, int ROWS>
+// TOKENS: 4 for up to 4 tokens, else 8.
+template <bool FP4, int TOKENS>
 hipError_t launch_both(const ExpertsArgs& a, hipStream_t stream) {
   // Half as many rows a workgroup where there would not be one for every compute unit.
   const bool few = std::min(a.tokens * a.top_k, a.num_groups) * (a.inner / 32) < a.cus;
-  if (hipError_t e = few ? launch_up<FP4, 1, ROWS>(a, stream) : launch_up<FP4, 2, ROWS>(a, stream)) return e;
-  if constexpr (ROWS == 4) return launch_down<FP4, ROWS, 4, 1>(a, stream);
-  else if (a.tokens <= 16) return launch_down<FP4, ROWS, 64, 1>(a, stream);
-  else if (a.tokens <= 64) return launch_down<FP4, ROWS, 64, 2>(a, stream);
-  else return launch_down<FP4, ROWS, MAX_FEW_TOKENS, 2>(a, stream);
+  if (hipError_t e = few ? launch_up<FP4, 1, TOKENS>(a, stream) : launch_up<FP4, 2, TOKENS>(a, stream)) return e;
+  if constexpr (TOKENS == 4) return launch_down<FP4, TOKENS, 4, 1>(a, stream);
+  else if (a.tokens <= 8) return launch_down<FP4, TOKENS, 64, 1>(a, stream);
+  else if (a.tokens <= 16) return launch_down<FP4, TOKENS, 64, 2>(a, stream);
+  else if (a.tokens <= 64) return launch_down<FP4, TOKENS, 64, 4>(a, stream);
+  else return launch_down<FP4, TOKENS, MAX_FEW_TOKENS, 4>(a, stream);
 }
 
 }  // namespace
 
 long long experts_act_bytes(int tokens, int top_k, int num_groups, int inner) {
-  const int n = tokens * top_k, tiles = n <= num_groups ? n : num_groups * ((tokens + 15) / 16);
-  return (long long)tiles * (tokens <= 4 ? 4 : 16) * inner * 2;
+  const int n = tokens * top_k, tiles = n <= num_groups ? n : num_groups * ((tokens + TILE_TOKENS - 1) / TILE_TOKENS);
+  return (long long)tiles * (tokens <= 4 ? 4 : TILE_TOKENS) * inner * 4;
 }
 
 hipError_t launch_experts(ExpertsArgs a, hipStream_t stream) {
   a.splits = down_splits(a);
   if (a.tokens <= 4) return a.fp4 ? launch_both<true, 4>(a, stream) : launch_both<false, 4>(a, stream);
-  return a.fp4 ? launch_both<true, 16>(a, stream) : launch_both<false, 16>(a, stream);
+  return a.fp4 ? launch_both<true, 8>(a, stream) : launch_both<false, 8>(a, stream);
 }
 
 }  // namespace moe

@@ -162,6 +162,66 @@ def test_exact_layer(dev, t, k, g, hidden, inner, fp4):
 
 
 @pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("t,k,g,hidden,inner", [(1, 2, 4, 384, 128), (3, 4, 9, 256, 1024), (9, 3, 5, 256, 384), (16, 2, 4, 4224, 128),
+                                                (30, 4, 40, 256, 512), (61, 4, 8, 640, 256), (128, 4, 10, 128, 384)])
+def test_activations_of_more_bits_than_bf16_has(dev, t, k, g, hidden, inner, fp4):
+    """As _exact_layer, with ups 6 a + b / 2 of whole a and b up to 127: silu(g) u = 32 u has up to 11
+    significant bits, which reach the second products whole. Everything is a multiple of 4."""
+    _say(f"experts, long activations: {(t, k, g, hidden, inner)} fp4={fp4}")
+    x, sent, v1, v2 = _exact_layer(fp4, t, g, hidden, inner, t, dev)
+    r = np.random.default_rng(t + 1)
+    x[:, 1:] = torch.from_numpy(r.integers(-127, 128, (t, hidden - 1))).to(x)
+    v1[:, inner:] = 0.0
+    for e in range(g):
+        two = np.stack([1 + r.permutation(hidden - 1)[:2] for _ in range(inner)])
+        v1[e, inner + np.arange(inner), two[:, 0]] = 6.0
+        v1[e, inner + np.arange(inner), two[:, 1]] = 0.5
+    if fp4:
+        scale = np.full((g, 2 * inner, hidden // 32), 127, np.uint8)
+        sent[0] = torch.from_numpy(F.pack(F.codes(v1, scale))).to(dev)
+    else:
+        sent[0] = torch.from_numpy(v1).to(torch.float8_e4m3fn).to(dev)
+    ids = _ids(t, k, g, t)
+    w = r.choice([0.25, 0.5, 1.0, -1.0], (t, k))
+    y = _run(x, ids, torch.from_numpy(w).float().to(dev), *sent, dev)
+    xs = x.double().cpu().numpy()
+    ref, mag = np.zeros((t, hidden)), np.zeros((t, hidden))
+    long = 0
+    for i, j in np.argwhere(ids >= 0):
+        gu = v1[ids[i, j]] @ xs[i]
+        a = gu[:inner] * gu[inner:]
+        long += (O.bf16_round(a) != a).sum()
+        ref[i] += w[i, j] * (v2[ids[i, j]] @ a)
+        mag[i] += abs(w[i, j]) * (np.abs(v2[ids[i, j]]) @ np.abs(a))
+    assert mag.max() / 4 < 2 ** 24 and long > inner // 4
+    np.testing.assert_array_equal(y.view(torch.int16).cpu().numpy().view(np.uint16), O.bf16_bits(ref))
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("t", [1, 6, 20])
+def test_infinite_activations_stay_infinite(dev, t, fp4):
+    """An activation past float32's range is infinite, with nothing left over beside it: so are
+    the outputs that it reaches through weights of one sign, and no other token's."""
+    _say(f"experts, infinite activations t={t} fp4={fp4}")
+    g, hidden, inner = 2, 256, 128
+    x, sent, v1, v2 = _exact_layer(fp4, t, g, hidden, inner, t, dev)
+    ids = np.zeros((t, 1), np.int32)
+    first = int(np.flatnonzero(v1[0, inner])[0])         # what the first activation's up is picked from
+    x[:, 1:] = x[:, 1:].abs()
+    x[0, first] = 2.0 ** 127
+    up, ones = np.abs(v1), np.ones_like(v2)
+    for i, v in ((0, up), (2, ones)):
+        if fp4:
+            sent[i] = torch.from_numpy(F.pack(F.codes(v, np.full((g, v.shape[1], v.shape[2] // 32), 127, np.uint8)))).to(dev)
+        else:
+            sent[i] = torch.from_numpy(v).to(torch.float8_e4m3fn).to(dev)
+    y = _run(x, ids, None, *sent, dev)
+    assert torch.equal(y[0], torch.full_like(y[0], float("inf")))
+    ref = _exact(x[1:].double().cpu().numpy(), ids[1:], np.ones((t - 1, 1)), up, ones)
+    np.testing.assert_array_equal(y[1:].view(torch.int16).cpu().numpy().view(np.uint16), O.bf16_bits(ref))
+
+
+@pytest.mark.parametrize("fp4", [False, True])
 def test_ids_and_weights_at_their_ends(dev, fp4):
     """An expert named twice by a token, ids outside the experts with weights that are not
     numbers, tokens without experts, one expert for all."""
