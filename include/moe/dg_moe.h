@@ -264,10 +264,11 @@ dg_status dg_moe_block_norm_bwd(const dg_moe_norm_bwd* args, void* stream);
  *   workspace  16-byte aligned, dg_moe_experts_workspace_bytes() bytes;
  *            contents need not be kept between calls; calls that use one must be
  *            ordered (one stream, or events)
- * The weights of the experts that have tokens are read once. Neither x nor the weights are quantised on the way: weights stand for their
- * exact values (of FP4 in BF16's range), products sum in float32 and silu(g) * u is held
- * to 2^-16 of itself (as the sum of two BF16 values). (The order of a token's sums goes by the sizes and by how many experts the
- * call's tokens name.)
+ * The weights of an expert are read once for each 32 of its tokens. Neither x nor the
+ * weights are quantised on the way: weights stand for their exact values (of FP4 in
+ * BF16's range), products sum in float32 and silu(g) * u is held to 2^-16 of itself (as
+ * the sum of two BF16 values). (The order of a token's sums goes by the sizes and by how
+ * many experts the call's tokens name.)
  * tokens <= 128, top_k <= 32, tokens * top_k <= 1024, num_groups <= 4096,
  * hidden and inner multiples of 128 up to 2^16. tokens == 0 is a no-op.
  */

@@ -6,7 +6,8 @@
 // with the experts' weights in FP8 (one float32 scale per 128 x 128) or FP4 (one
 // power-of-two scale per 32 values of a row) and everything else as it comes: x in
 // BF16, sums in float32, a held to 2^-16 of it in two BF16 values, y rounded once. The
-// weights of the experts that have tokens are read once, and that bounds both launches.
+// weights of an expert are read once for each 32 of its tokens, and that bounds both
+// launches.
 //
 // Every wave streams weights of its own through a ring in LDS, without a barrier:
 // direct-to-LDS loads whose successive lanes read a row's successive 16 bytes, some

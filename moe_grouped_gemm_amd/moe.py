@@ -399,7 +399,7 @@ def experts(x, topk_ids, weights, b1, sfb1, b2, sfb2, y, workspace) -> torch.Ten
     float8_e4m3fn with float32 sfb [G, N/128, K/128], or uint8 (packed FP4, half as
     many columns) with int32 sfb [G, K/128, N]. What decode steps call in place of
     dispatch, two products, the activation and combine: nothing is quantised on the
-    way."""
+    way, and an expert's weights are read once for each 32 of its tokens."""
     index = _first(x, "x", _BF16, 2)
     t, hidden = shape = x.shape
     fp4 = isinstance(b1, torch.Tensor) and b1.dtype is torch.uint8
