@@ -92,6 +92,16 @@ def _check(status: int, what: str) -> None:
         raise DGError(status, what)
 
 
+def _int32(v: int) -> int:
+    """A size as the library's int takes it; -1, which every call refuses, where it
+    does not fit (ctypes would take it modulo 2^32)."""
+    return v if -2 ** 31 <= v < 2 ** 31 else -1
+
+
+def _int32s(*sizes: int):
+    return sizes if max(sizes) < 2 ** 31 else tuple(_int32(v) for v in sizes)
+
+
 def _stream(t: torch.Tensor) -> int:
     return torch.cuda.current_stream(t.device).cuda_stream
 
@@ -199,7 +209,7 @@ def fp8_gemm_nt(a, sfa, b, sfb, d, ue8m0: bool = False) -> torch.Tensor:
     if tuple(sfa.shape) != (k // 128, get_tma_aligned_size(m, 4)) or tuple(sfb.shape) != (n // 128, k // 128):
         raise ValueError("scale shapes do not match the (1, 128, 128) recipe layout")
     _check(_entry("dg_fp8_gemm_nt", ue8m0)(a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), d.data_ptr(),
-                                m, n, k, _stream(a)), "dg_fp8_gemm_nt")
+                                *_int32s(m, n, k), _stream(a)), "dg_fp8_gemm_nt")
     return d
 
 
@@ -222,7 +232,7 @@ def m_grouped_fp8_gemm_nt_contiguous(a, sfa, b, sfb, d, grouped_layout, ue8m0: b
         raise ValueError("scale shapes do not match the (1, 128, 128) recipe layout")
     _check(_entry("dg_m_grouped_fp8_gemm_nt_contiguous", ue8m0)(
         a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), d.data_ptr(), grouped_layout.data_ptr(),
-        m, n, k, g, _stream(a)), "dg_m_grouped_fp8_gemm_nt_contiguous")
+        *_int32s(m, n, k, g), _stream(a)), "dg_m_grouped_fp8_gemm_nt_contiguous")
     return d
 
 
@@ -247,7 +257,7 @@ def m_grouped_fp8_gemm_nt_masked(a, sfa, b, sfb, d, masked_m, ue8m0: bool = Fals
         raise ValueError("scale shapes do not match the (1, 128, 128) recipe layout")
     _check(_entry("dg_m_grouped_fp8_gemm_nt_masked", ue8m0)(
         a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), d.data_ptr(), masked_m.data_ptr(),
-        g, max_m, n, k, _stream(a)), "dg_m_grouped_fp8_gemm_nt_masked")
+        *_int32s(g, max_m, n, k), _stream(a)), "dg_m_grouped_fp8_gemm_nt_masked")
     return d
 
 
@@ -272,7 +282,7 @@ def m_grouped_fp8_gemm_nt_nopad(a, sfa, b, sfb, d, group_rows, ue8m0: bool = Fal
         raise ValueError("scale shapes do not match the (1, 128, 128) recipe layout")
     _check(_entry("dg_m_grouped_fp8_gemm_nt_nopad", ue8m0)(
         a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), d.data_ptr(), group_rows.data_ptr(),
-        m, n, k, g, _stream(a)), "dg_m_grouped_fp8_gemm_nt_nopad")
+        *_int32s(m, n, k, g), _stream(a)), "dg_m_grouped_fp8_gemm_nt_nopad")
     return d
 
 
@@ -297,7 +307,7 @@ def m_grouped_fp8_fp4_gemm_nt_contiguous(a, sfa, b, sfb, d, grouped_layout) -> t
         raise ValueError("scale shapes do not match the (1, 128) x (1, 32) layout")
     _check(lib().dg_m_grouped_fp8_fp4_gemm_nt_contiguous(
         a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), d.data_ptr(), grouped_layout.data_ptr(),
-        m, n, k, g, _stream(a)), "dg_m_grouped_fp8_fp4_gemm_nt_contiguous")
+        *_int32s(m, n, k, g), _stream(a)), "dg_m_grouped_fp8_fp4_gemm_nt_contiguous")
     return d
 
 
@@ -322,7 +332,7 @@ def m_grouped_fp8_fp4_gemm_nt_masked(a, sfa, b, sfb, d, masked_m) -> torch.Tenso
         raise ValueError("scale shapes do not match the (1, 128) x (1, 32) layout")
     _check(lib().dg_m_grouped_fp8_fp4_gemm_nt_masked(
         a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), d.data_ptr(), masked_m.data_ptr(),
-        g, max_m, n, k, _stream(a)), "dg_m_grouped_fp8_fp4_gemm_nt_masked")
+        *_int32s(g, max_m, n, k), _stream(a)), "dg_m_grouped_fp8_fp4_gemm_nt_masked")
     return d
 
 
@@ -354,10 +364,10 @@ def k_grouped_fp8_gemm_nt_contiguous(a, sfa, b, sfb, d, ks, c=None, ue8m0: bool 
     if (tuple(sfa.shape) != (k // 128, get_tma_aligned_size(m, 4))
             or tuple(sfb.shape) != (k // 128, get_tma_aligned_size(n, 4))):
         raise ValueError("scale shapes do not match the (1, 1, 128) recipe layout")
-    ks_arr = (ctypes.c_int * max(g, 1))(*ks)
+    ks_arr = (ctypes.c_int * max(g, 1))(*(_int32(v) for v in ks))
     _check(_entry("dg_k_grouped_fp8_gemm_nt_contiguous", ue8m0)(
         a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), None if c is None else c.data_ptr(),
-        d.data_ptr(), ks_arr, g, m, n, _stream(a)), "dg_k_grouped_fp8_gemm_nt_contiguous")
+        d.data_ptr(), ks_arr, *_int32s(g, m, n), _stream(a)), "dg_k_grouped_fp8_gemm_nt_contiguous")
     return d
 
 
@@ -409,7 +419,7 @@ def _want_fp4(q, sf, name: str, shape, index: int) -> None:
     if k % 128 or not _is(q, _U8, (*lead, rows, k // 2), index) \
             or not _is(sf, _I32, (*lead, k // 128, (rows + 3) // 4 * 4), index):
         _refuse_fp4(q, sf, name, shape, _device(index))
-    if rows >= 2 ** 31:  # (the library's sizes are ints)
+    if max(shape) >= 2 ** 31:  # (the library's sizes are ints)
         raise ValueError(f"{name}: sizes past 32 bits")
 
 

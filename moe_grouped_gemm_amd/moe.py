@@ -31,7 +31,7 @@ from typing import Optional
 import torch
 
 from . import dg
-from .dg import DGError, _check, _current_device, _need  # noqa: F401  (DGError: what a failed call raises)
+from .dg import DGError, _check, _current_device, _int32, _int32s, _need  # noqa: F401  (DGError: what a failed call raises)
 
 _LAYOUTS = {"dense": 0, "contiguous": 1, "masked": 2, "nopad": 3}
 _BF16, _F32, _I32, _FP8 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
@@ -84,12 +84,6 @@ def lib() -> ctypes.CDLL:
             fn.restype = restype
         _lib = handle
     return _lib
-
-
-def _int32(v: int) -> int:
-    """A size as the library's int takes it; -1, which every call refuses, where it
-    does not fit (ctypes would take it modulo 2^32)."""
-    return v if -2 ** 31 <= v < 2 ** 31 else -1
 
 
 def _ptr(t) -> int:
@@ -321,6 +315,8 @@ def _glu(gu, rows, layout: str):
     m, width = gu.shape[-2:]
     if width % 256:
         raise ValueError("gu must hold 2 * inner columns, inner a multiple of 128")
+    if max(m, width) >= 2 ** 31:
+        raise ValueError("gu: sizes past 32 bits")
     if layout == "dense":
         if rows is not None:
             raise ValueError("the dense layout takes no rows")
@@ -421,8 +417,8 @@ def experts(x, topk_ids, weights, b1, sfb1, b2, sfb2, y, workspace) -> torch.Ten
     if _first(workspace, "workspace", torch.uint8, 1) != index:
         raise ValueError(f"workspace must be on {x.device}")
     args = _EXPERTS.pack(x.data_ptr(), topk_ids.data_ptr(), _ptr(weights), b1.data_ptr(), sfb1.data_ptr(), b2.data_ptr(),
-                         sfb2.data_ptr(), y.data_ptr(), workspace.data_ptr(), workspace.numel(), fp4, t, top_k,
-                         _int32(g), hidden, inner)
+                         sfb2.data_ptr(), y.data_ptr(), workspace.data_ptr(), workspace.numel(), fp4,
+                         *_int32s(t, top_k, g, hidden, inner))
     _call("dg_moe_experts", index, args)
     return y
 

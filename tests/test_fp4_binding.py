@@ -80,3 +80,49 @@ def test_calls_run_on_their_tensors_device(monkeypatch, name):
     current[0] = 1
     _calls()[name]()
     assert seen == [(name.split()[0], 1, 1000)] * 2 and current[0] == 1
+
+
+def _vast(*shape, dtype):
+    """A tensor on the second GPU with sizes and without memory."""
+    return torch.empty(*shape, dtype=dtype, device="meta").as_subclass(_OnDevice1)
+
+
+def _vast_calls():
+    u8, i32, bf, f32, f8 = torch.uint8, torch.int32, torch.bfloat16, torch.float32, torch.float8_e4m3fn
+    k = 2 ** 32 + 128                                # 128, taken modulo 2^32
+    x, q, sf = _vast(1, k, dtype=bf), _vast(1, k // 2, dtype=u8), _vast(k // 128, 4, dtype=i32)
+    b, sfb, d = _vast(128, k // 2, dtype=u8), _vast(k // 128, 128, dtype=i32), _vast(1, 128, dtype=bf)
+    n = _vast(k, 64, dtype=u8), _vast(1, k, dtype=i32)
+    one, a, sfa = _vast(1, dtype=i32), _vast(1, 64, dtype=u8), _vast(1, 4, dtype=i32)
+    a8, sfa8, b8, sfb8 = _vast(1, k, dtype=f8), _vast(k // 128, 4, dtype=f32), _vast(128, k, dtype=f8), _vast(1, k // 128, dtype=f32)
+    t, ids, w = _vast(1, 128, dtype=bf), _vast(1, 2 ** 32 + 2, dtype=i32), _vast(64, dtype=u8)
+    e1, s1, e2, s2 = _vast(1, 256, 128, dtype=f8), _vast(1, 2, 1, dtype=f32), _vast(1, 128, 128, dtype=f8), _vast(1, 1, 1, dtype=f32)
+    return {
+        "quantize_fp4": lambda: dg.quantize_fp4(x, q, sf),
+        "quantize_fp4 of groups": lambda: dg.quantize_fp4(_vast(k, 1, 128, dtype=bf), _vast(k, 1, 64, dtype=u8), _vast(k, 1, 4, dtype=i32)),
+        "dequantize_fp4": lambda: dg.dequantize_fp4(q, sf, x),
+        "fp4_gemm_nt, k": lambda: dg.fp4_gemm_nt(q, sf, b, sfb, d),
+        "fp4_gemm_nt, n": lambda: dg.fp4_gemm_nt(a, sfa, *n, _vast(1, k, dtype=bf)),
+        "fp4_gemm_nt_nopad": lambda: dg.m_grouped_fp4_gemm_nt_nopad(q, sf, b[None], sfb[None], d, one),
+        "fp8_gemm_nt": lambda: dg.fp8_gemm_nt(a8, sfa8, b8, sfb8, d),
+        "fp8_gemm_nt_nopad": lambda: dg.m_grouped_fp8_gemm_nt_nopad(a8, sfa8, b8[None], sfb8[None], d, one),
+        "swiglu_fp4": lambda: moe.swiglu_fp4(_vast(1, 2 * k, dtype=bf), q, sf),
+        "swiglu_fp8": lambda: moe.swiglu_fp8(_vast(1, 2 * k, dtype=bf), a8, sfa8),
+        "experts": lambda: moe.experts(t, ids, None, e1, s1, e2, s2, t, w),
+    }
+
+
+@pytest.mark.parametrize("name", sorted(_vast_calls()))
+def test_sizes_past_32_bits_are_refused(monkeypatch, name):
+    """The library's sizes are ints, which ctypes takes modulo 2^32: such a call would work on
+    a corner of its tensors and succeed."""
+    for module in (dg, moe):
+        monkeypatch.setattr(module, "_current_device", lambda: 1)
+        monkeypatch.setattr(module, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(dg, "_stream", lambda t: 0)
+    monkeypatch.setattr(dg, "_need", lambda *args: None)
+    monkeypatch.setattr(torch.Tensor, "data_ptr", lambda self: 0x10000)
+    with pytest.raises((ValueError, dg.DGError)) as refused:
+        _vast_calls()[name]()
+    if refused.type is dg.DGError:
+        assert refused.value.status in (2, 4)        # shape, unsupported: before the device is asked
