@@ -721,8 +721,9 @@ __global__ void __launch_bounds__(Few::THREADS, 1) fp4_gemm_few_kernel(GemmArgs 
 // Tiles of 64 x 64 up to which a call takes those: three rounds of a whole chip's. In us,
 // with these and with the large ones: 512 x 2048 x 7168 (256 tiles) 10.1, 42.5; 1024 x 1024
 // x 1024 (256) 4.7, 12.9; 16 x 2176 x 2432 (34) 4.8, 14.0; 12 groups of 16 x 2304 x 640 (432)
-// 5.8, 8.1; 18 of 8 x 2304 x 5632 (648) 22.4, 26.6; 2048^3 (1024) 15.6, 18.4; 8 of up to 256
-// x 2048 x 2048 (1024) 20.0, 18.8; 16 of up to 32 x 7168 x 2048 (1792) 28.1, 25.3; 2048 x
+// 5.8, 8.1; 18 of 8 x 2304 x 5632 (648) 22.4, 26.6; single rows of 8 groups among 128,
+// without padding, x 2048 x 7168 (256) 14.4, 39.9, and of 40 among 128 (1280) 56.8, 77.9, x
+// 2048 x 2048 23.7, 23.8; 2048^3 (1024) 15.6, 18.4; 8 of up to 256 x 2048 x 2048 (1024) 20.0, 18.8; 16 of up to 32 x 7168 x 2048 (1792) 28.1, 25.3; 2048 x
 // 4096 x 4096 (2048) 44.8, 29.8. (Not by dg_get_num_cus(): the order of the sums differs.)
 constexpr long long FEW_TILES = 768;
 
@@ -730,11 +731,12 @@ constexpr long long FEW_TILES = 768;
 template <class C>
 static long long most_tiles(int kind, const GemmArgs& p) {
   const long long m_blocks = (p.m + C::BM - 1) / C::BM, n_blocks = (p.n + C::BN - 1) / C::BN;
+  const long long held = std::min(p.num_groups, p.m);  // groups that can have rows
   switch (kind) {
     case KIND_MASKED:  // an upper bound for the grid's size, as for no padding; the kernel counts the tiles
       return p.num_groups * m_blocks * n_blocks;
-    case KIND_NOPAD:  // each group adds at most one partial row block
-      return (m_blocks + p.num_groups) * n_blocks;
+    case KIND_NOPAD:  // a row block for each of them, and one for each BM of the other rows
+      return (held + (p.m - held) / C::BM) * n_blocks;
     case KIND_CONTIGUOUS:
       return C::SLOTS * m_blocks * n_blocks;
     default:

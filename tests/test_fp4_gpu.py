@@ -310,6 +310,31 @@ def test_nopad(dev, counts, m, n, k, whole):
         _check(got[lo:hi], a[lo:hi], sfa[:, lo:hi], b[e], sfb[e], k, whole, f"group {e}")
 
 
+@pytest.mark.parametrize("whole", [False, True])
+@pytest.mark.parametrize("m,g,n,k", [(1, 2048, 128, 384), (8, 128, 2048, 512), (8, 128, 2048, 7168), (3, 40, 8448, 256),
+                                     (40, 256, 4096, 256), (100, 300, 2560, 128), (300, 200, 512, 384)])
+def test_nopad_of_more_groups_than_most_have_rows(dev, m, g, n, k, whole):
+    """A step of few tokens over many experts: most groups have none, in runs and by turns."""
+    _say(f"nopad, {m} rows of {g} groups, n={n} k={k} whole={whole}")
+    r = np.random.default_rng(m + g)
+    counts = np.bincount(r.choice(g, m), minlength=g).astype(np.int32)
+    if m < g:                                        # as many groups as rows, the last one among them
+        counts[:] = 0
+        counts[np.r_[r.permutation(g - 1)[:m - 1], g - 1]] = 1
+    a, sfa = _codes(7, (), m, k, whole)
+    b, sfb = _codes(8, (min(g, 3),), n, k, whole)
+    pick = np.arange(g) % len(b)                     # groups share three matrices' values
+    ad, sfad, bd, sfbd = _put(dev, a, sfa, b, sfb)
+    every = torch.from_numpy(pick).to(dev)
+    d = _out(m, n)
+    dg.m_grouped_fp4_gemm_nt_nopad(ad, sfad, bd[every].contiguous(), sfbd[every].contiguous(), d, torch.from_numpy(counts).to(dev))
+    got = _bits(d).view(np.uint16)
+    owner = np.repeat(np.arange(g), counts)
+    for e in range(len(b)):
+        mine = pick[owner] == e
+        _check(got[mine], a[mine], sfa[:, :m][:, mine], b[e], sfb[e], k, whole, f"matrix {e}")
+
+
 def test_no_rows_no_groups(dev):
     _say("empty products")
     a, sfa = _codes(1, (), 0, 256)
