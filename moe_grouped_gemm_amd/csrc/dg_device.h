@@ -108,12 +108,17 @@ __device__ __forceinline__ int e8m0_code(float s) {
 template <class C>
 constexpr int A_PACK_SHIFT = 0;
 
+// Whether its RHS is FP8 with a scale per 128 x 128, whose place in a group resolve_tile()
+// gives. Kernels with a packed FP4 RHS locate theirs from the group's number.
+template <class C>
+constexpr bool FP8_RHS = true;
+
 // Where one output tile's operands live, and which of its rows are valid.
 struct TileRef {
   const uint8_t* a;    // row 0 of the group's A
   const float* sfa;    // the group's transposed LHS scales
-  const uint8_t* b;    // the group's B [n][k]
-  const float* sfb;    // the group's RHS scales [n/128][k/128]
+  const uint8_t* b;    // the group's B [n][k] (FP8_RHS only, else null)
+  const float* sfb;    // the group's RHS scales [n/128][k/128] (the same)
   uint16_t* d;         // row 0 of the group's D
   int group;
   int m0, n0;          // first row (within the group) and column of the tile
@@ -223,6 +228,13 @@ __device__ int* group_table(const GemmArgs& p, int tid) {
   return tab;
 }
 
+template <class C>
+__device__ __forceinline__ void set_group(TileRef& tr, const GemmArgs& p, int g) {
+  tr.group = g;
+  tr.b = FP8_RHS<C> ? p.b + (size_t)g * p.n * p.k : nullptr;
+  tr.sfb = FP8_RHS<C> ? p.sfb + (size_t)g * (p.n / BK) * (p.k / BK) : nullptr;
+}
+
 // Resolves linear tile index t of layout KIND. Tile order:
 //   dense:      raster over (M block, N block);
 //   contiguous: slot-major, then raster over (BM-row block, N block); slot j
@@ -237,9 +249,9 @@ __device__ __forceinline__ TileRef resolve_tile(const GemmArgs& p, int t, int nu
   TileRef tr;
   tr.active = false;
   if (t >= num_tiles) return tr;
-  const size_t K = (size_t)p.k;
-  const int k_blocks = p.k / BK;
   if constexpr (counts_on_device(KIND)) {
+    const size_t K = (size_t)p.k;
+    const int k_blocks = p.k / BK;
     int lo = 0, hi = p.num_groups - 1;  // last g with prefix[g] <= t: a group with tiles
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -265,9 +277,7 @@ __device__ __forceinline__ TileRef resolve_tile(const GemmArgs& p, int t, int nu
     const int local = t - s_prefix[g];
     const int nb = local / mblocks;
     const int mb = local - nb * mblocks;
-    tr.group = g;
-    tr.b = p.b + (size_t)g * p.n * K;
-    tr.sfb = p.sfb + (size_t)g * (p.n / BK) * k_blocks;
+    set_group<C>(tr, p, g);
     tr.m0 = mb * C::BM;
     tr.n0 = nb * C::BN;
     tr.load_rows = v;        // rows past the group's count are never fetched
@@ -285,9 +295,7 @@ __device__ __forceinline__ TileRef resolve_tile(const GemmArgs& p, int t, int nu
     tr.a = p.a;
     tr.sfa = p.sfa;
     tr.d = p.d;
-    tr.group = 0;
-    tr.b = p.b;
-    tr.sfb = p.sfb;
+    set_group<C>(tr, p, 0);
     if constexpr (KIND == KIND_CONTIGUOUS) {
       // The distinct valid groups of this block's 128-row segment blocks, in order.
       int found = 0, g_sel = -1;
@@ -307,9 +315,7 @@ __device__ __forceinline__ TileRef resolve_tile(const GemmArgs& p, int t, int nu
         }
       }
       if (g_sel < 0) return tr;  // nothing for this slot: inactive
-      tr.group = g_sel;
-      tr.b = p.b + (size_t)g_sel * p.n * K;
-      tr.sfb = p.sfb + (size_t)g_sel * (p.n / BK) * k_blocks;
+      set_group<C>(tr, p, g_sel);
     }
     tr.active = true;
   }

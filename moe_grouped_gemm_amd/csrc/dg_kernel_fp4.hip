@@ -30,6 +30,14 @@ struct Cfg {
   static constexpr int WAVES_N = 4, NW = 8, THREADS = NW * 64;
   static constexpr int WM = 128, WN = 64, MT = WM / 16, NT = WN / 16;
 };
+
+}  // namespace w4a8
+
+template <>
+constexpr bool FP8_RHS<w4a8::Cfg> = false;
+
+namespace w4a8 {
+
 constexpr int B_ROW = BK / 2;                      // packed E2M1 bytes per row and K block
 constexpr int A_BYTES = Cfg::BM * ROW_BYTES;       // 32 KB
 constexpr int B_BYTES = Cfg::BN * B_ROW;           // 16 KB
@@ -37,6 +45,7 @@ constexpr int SA_OFF = A_BYTES + B_BYTES;          // 256 LHS scales
 constexpr int SB_OFF = SA_OFF + Cfg::BM * 4;       // 4 x 256 RHS scales: [32-K block][column]
 constexpr int STAGE_BYTES = SB_OFF + 4 * Cfg::BN * 4;
 static_assert(Cfg::NW == 8 && Cfg::BM == 256 && Cfg::BN == 256, "load split below");
+static_assert(!FP8_RHS<Cfg> && A_PACK_SHIFT<Cfg> == 0, "the RHS alone is packed");
 
 __device__ __forceinline__ uint8_t* lds() {
   __shared__ __attribute__((aligned(1024))) uint8_t buf[2 * STAGE_BYTES];

@@ -62,10 +62,6 @@ constexpr int SB_OFF = SA_OFF<C> + STEP_BLOCKS * C::BM * 4;
 template <class C>
 constexpr int LOW_BYTES = SB_OFF<C> + STEP_BLOCKS * C::BN * 4;
 
-}  // namespace mx
-
-namespace mx {
-
 // The kernel for few tiles (see there).
 struct Few {
   static constexpr int BM = 64, BN = 64, SLOTS = 1;
@@ -78,6 +74,10 @@ template <int BM>
 constexpr int A_PACK_SHIFT<mx::Cfg<BM>> = 1;
 template <>
 constexpr int A_PACK_SHIFT<mx::Few> = 1;
+template <int BM>
+constexpr bool FP8_RHS<mx::Cfg<BM>> = false;
+template <>
+constexpr bool FP8_RHS<mx::Few> = false;
 
 namespace mx {
 
@@ -131,6 +131,7 @@ struct TileSrc {
 
 template <class C>
 __device__ __forceinline__ TileSrc tile_src(const GemmArgs& p, const TileRef& tr) {
+  static_assert(!FP8_RHS<C> && A_PACK_SHIFT<C> == 1, "both operands are packed");
   TileSrc s;
   const size_t row = (size_t)p.k / 2;
   s.a_rows = uniform_int(min(max(tr.load_rows - tr.m0, 0), C::BM));
@@ -587,6 +588,7 @@ __device__ __forceinline__ TileRef few_contiguous_tile(const GemmArgs& p, int t)
 
 template <int KIND>
 __global__ void __launch_bounds__(Few::THREADS, 1) fp4_gemm_few_kernel(GemmArgs p) {
+  static_assert(!FP8_RHS<Few> && A_PACK_SHIFT<Few> == 1, "both operands are packed");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Few::NW * 2 * FEW_STEP];
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -617,7 +619,6 @@ __global__ void __launch_bounds__(Few::THREADS, 1) fp4_gemm_few_kernel(GemmArgs 
     if constexpr (KIND == KIND_CONTIGUOUS) {
       cur = few_contiguous_tile(p, t);
       if (!cur.active) continue;
-      cur.b = p.b + (size_t)cur.group * p.n * p.k;
       id = p.aux[cur.m0 + lane];
     } else {
       int at = t;

@@ -312,7 +312,7 @@ def test_nopad(dev, counts, m, n, k, whole):
 
 @pytest.mark.parametrize("whole", [False, True])
 @pytest.mark.parametrize("m,g,n,k", [(1, 2048, 128, 384), (8, 128, 2048, 512), (8, 128, 2048, 7168), (3, 40, 8448, 256),
-                                     (40, 256, 4096, 256), (100, 300, 2560, 128), (300, 200, 512, 384)])
+                                     (14, 60, 4096, 384), (40, 256, 4096, 256), (100, 300, 2560, 128), (300, 200, 512, 384)])
 def test_nopad_of_more_groups_than_most_have_rows(dev, m, g, n, k, whole):
     """A step of few tokens over many experts: most groups have none, in runs and by turns."""
     _say(f"nopad, {m} rows of {g} groups, n={n} k={k} whole={whole}")
