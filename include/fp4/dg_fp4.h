@@ -31,7 +31,7 @@ extern "C" {
  *   D = bf16( sum_k e2m1(A[m][k]) sfa[m][k/32] * e2m1(B[n][k]) sfb[n][k/32] )
  * Products accumulate in float32 inside the MFMA. dg_quantize_fp4 makes such
  * operands, dg_moe.h's steps the left ones of a mixture-of-experts block.
- * At most 2^30 rows (num_groups * max_m) and 2^29 tiles of 128 x 128.
+ * Fewer than 2^30 rows (masked: num_groups * max_m); a, b and d below 2^40 bytes each.
  */
 dg_status dg_fp4_gemm_nt(const void* a, const uint32_t* sfa,
                          const void* b, const uint32_t* sfb,

@@ -59,9 +59,9 @@ int effective_cus() {
 
 constexpr long long kMaxDim = 1 << 20;
 constexpr long long kMaxBytes = 1LL << 40;
-// FP4: rows, and 128 x 128 tiles, which the kernels count in ints with room to step past the last.
+// FP4: rows, which the kernels count in ints with room to step past the last. (So are their
+// tiles, of 64 x 64 at least: fewer than 2^29 where D and B are below kMaxBytes.)
 constexpr long long kMaxFp4Rows = 1LL << 30;
-constexpr long long kMaxFp4Tiles = 1LL << 29;
 constexpr int kMaxMaskedGroups = dg::MAX_MASKED_GROUPS;
 constexpr int kMaxNopadGroups = dg::MAX_NOPAD_GROUPS;
 
@@ -308,8 +308,7 @@ dg_status fp4(int kind, const void* a, const uint32_t* sfa, const void* b, const
   if (kind == dg::KIND_MASKED && num_groups > kMaxMaskedGroups) return DG_ERR_UNSUPPORTED;
   if (kind == dg::KIND_NOPAD && num_groups > kMaxNopadGroups) return DG_ERR_UNSUPPORTED;
   const long long all = (kind == dg::KIND_MASKED ? (long long)num_groups : 1LL) * m;
-  // The kernel's row and tile numbers are ints.
-  if (all >= kMaxFp4Rows || (all / 128 + num_groups + 1) * (n / 128) >= kMaxFp4Tiles) return DG_ERR_UNSUPPORTED;
+  if (all >= kMaxFp4Rows) return DG_ERR_UNSUPPORTED;
   if (all * (k / 2) >= kMaxBytes || all * n * 2 >= kMaxBytes || (long long)num_groups * n * (k / 2) >= kMaxBytes)
     return DG_ERR_UNSUPPORTED;
   if (m == 0 || num_groups == 0) return DG_OK;

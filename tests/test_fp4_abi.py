@@ -67,6 +67,17 @@ def test_valid_calls_need_a_device():
     assert _quantize() == DEVICE and _back() == DEVICE
 
 
+@no_gpu
+@pytest.mark.parametrize("name", sorted(CALLS))
+def test_the_largest_products_are_taken(name):
+    """The limits as documented: rows below 2^30, groups as far as the layout's rows go."""
+    g = {"dense": {}, "contiguous": {"g": 1 << 26}, "masked": {"g": 4096}, "nopad": {"g": 2048}}[name]
+    m = {"masked": (1 << 18) - 1, "contiguous": (1 << 30) - 128}.get(name, (1 << 30) - 1)
+    assert CALLS[name](m=m, n=128, k=128, **g) == DEVICE
+    assert CALLS[name](m=128, n=1 << 20, k=128, **{k: min(v, 1 << 13) for k, v in g.items()}) == DEVICE
+    assert CALLS[name](m=128, n=128, k=1 << 20, **{k: min(v, 1 << 13) for k, v in g.items()}) == DEVICE
+
+
 def _quantize(x=A, kind=0, q=B, sf=C, groups=2, rows=5, k=256):
     return dg.lib().dg_quantize_fp4(x, kind, q, sf, groups, rows, k, None)
 
