@@ -74,8 +74,9 @@ def test_the_largest_products_are_taken(name):
     g = {"dense": {}, "contiguous": {"g": 1 << 26}, "masked": {"g": 4096}, "nopad": {"g": 2048}}[name]
     m = {"masked": (1 << 18) - 1, "contiguous": (1 << 30) - 128}.get(name, (1 << 30) - 1)
     assert CALLS[name](m=m, n=128, k=128, **g) == DEVICE
-    assert CALLS[name](m=128, n=1 << 20, k=128, **{k: min(v, 1 << 13) for k, v in g.items()}) == DEVICE
-    assert CALLS[name](m=128, n=128, k=1 << 20, **{k: min(v, 1 << 13) for k, v in g.items()}) == DEVICE
+    few = {k: min(v, 2048) for k, v in g.items()}     # b is 2^37 bytes, and d (masked) 2^39
+    assert CALLS[name](m=128, n=1 << 20, k=128, **few) == DEVICE
+    assert CALLS[name](m=128, n=128, k=1 << 20, **few) == DEVICE
 
 
 def _quantize(x=A, kind=0, q=B, sf=C, groups=2, rows=5, k=256):
