@@ -13,9 +13,9 @@
  * every result is rounded once, to nearest even. Results do not depend on
  * timing: the same inputs give the same bits. The norms and their gradient
  * spread over dg_get_num_cus() compute units (the order of the gradient's
- * column sums goes by their number), and so does the first launch of the expert
- * layer (its results do not depend on it), the other calls over as many workgroups
- * as they have work for.
+ * column sums goes by their number). The launches of the expert layer go by it too, the
+ * first one's workgroups and the columns that one of the second takes (its results do not
+ * depend on it); the other calls spread over as many workgroups as they have work for.
  */
 #ifndef DG_MOE_H
 #define DG_MOE_H
