@@ -135,6 +135,52 @@ def _need(t: torch.Tensor, name: str, dtype, ndim: int, device) -> None:
         raise ValueError(f"{name} must be contiguous")
 
 
+def _device(index: int) -> torch.device:
+    return torch.device("cuda", index) if index >= 0 else torch.device("cuda")
+
+
+def _want(t: torch.Tensor, name: str, dtype, shape, index: int) -> None:
+    """As _need, with the whole shape and the device by its index (the cheapest way
+    to ask: get_device() is -1 on the host; a decode step's calls take a few
+    microseconds each)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _need(t, name, dtype, len(shape), _device(index))
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _current_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The handle of a device's current stream without the Stream object that
+# torch.cuda.current_stream() builds first (0.1 us for 1.9).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+
+
+def _caller(scope):
+    """The _call() of a binding module, by the module's own lib(), _current_device()
+    and _raw_stream() (scope: its globals)."""
+    def call(name: str, index: int, *args) -> None:
+        """Calls an entry point on device `index`'s current stream, with that device
+        current: the handle of a default stream is 0 on every device."""
+        entry, stream = getattr(scope["lib"](), name), scope["_raw_stream"]
+        if scope["_current_device"]() == index:
+            status = entry(*args, stream(index))
+        else:
+            with torch.cuda.device(index):
+                status = entry(*args, stream(index))
+        if status:
+            _check(status, name)
+    return call
+
+
+_call = _caller(globals())
+
+
 # ---------------------------------------------------------------------------
 # Utilities (include/dg.h)
 # ---------------------------------------------------------------------------
@@ -375,56 +421,19 @@ def k_grouped_fp8_gemm_nt_contiguous(a, sfa, b, sfb, d, ks, c=None, ue8m0: bool 
 # FP4: E2M1 values with one power-of-two scale per 32 (MXFP4)
 # ---------------------------------------------------------------------------
 
-def _is(t, dtype, shape, index: int) -> bool:
-    """Whether t is a contiguous tensor of that type and shape on that GPU: the
-    cheapest way to ask (a decode step's calls take a few microseconds each)."""
-    try:
-        return t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
-    except AttributeError:
-        return False
-
-
 _U8, _I32 = torch.uint8, torch.int32
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _call(name: str, index: int, *args) -> None:
-    """Calls an entry point on device `index`'s current stream, with that device current."""
-    entry = getattr(lib(), name)
-    if _current_device() == index and _raw_stream is not None:
-        status = entry(*args, _raw_stream(index))
-    else:
-        with torch.cuda.device(index):
-            status = entry(*args, torch.cuda.current_stream(index).cuda_stream)
-    if status:
-        _check(status, name)
-
-
-def _refuse_fp4(q, sf, name: str, shape, dev) -> None:
-    """Says what is wrong with an FP4 operand of `shape` values [..., rows, k]."""
-    _need(q, name, _U8, len(shape), dev)
-    _need(sf, "sf" + name, _I32, len(shape), dev)
-    *lead, rows, k = shape
-    if k % 128 or not k:
-        raise ValueError(f"{name}: k must be a multiple of 128, got {k}")
-    if tuple(q.shape) != (*lead, rows, k // 2):
-        raise ValueError(f"{name} must have shape {(*lead, rows, k // 2)}, got {tuple(q.shape)}")
-    raise ValueError(f"sf{name} must have shape {(*lead, k // 128, (rows + 3) // 4 * 4)}, got {tuple(sf.shape)}")
 
 
 def _want_fp4(q, sf, name: str, shape, index: int) -> None:
     """Checks packed codes [..., rows, k/2] uint8 with their scale words [..., k/128,
     tma_aligned(rows)] int32."""
     *lead, rows, k = shape
-    if k % 128 or not _is(q, _U8, (*lead, rows, k // 2), index) \
-            or not _is(sf, _I32, (*lead, k // 128, (rows + 3) // 4 * 4), index):
-        _refuse_fp4(q, sf, name, shape, _device(index))
+    if k % 128 or not k:
+        raise ValueError(f"{name}: k must be a multiple of 128, got {k}")
     if max(shape) >= 2 ** 31:  # (the library's sizes are ints)
         raise ValueError(f"{name}: sizes past 32 bits")
-
-
-def _device(index: int) -> torch.device:
-    return torch.device("cuda", index) if index >= 0 else torch.device("cuda")
+    _want(q, name, _U8, (*lead, rows, k // 2), index)
+    _want(sf, "sf" + name, _I32, (*lead, k // 128, (rows + 3) // 4 * 4), index)
 
 
 def _codes_of(q, name: str, ndim: int):
@@ -446,9 +455,7 @@ def _fp4_gemm(name, a, sfa, b, sfb, d, rows=None, masked=False):
     _want_fp4(b, sfb, "b", shape_b, index)
     if shape_b[-1] != k or n % 128:
         raise ValueError("a and b differ in k" if shape_b[-1] != k else "n must be a multiple of 128")
-    if not _is(d, torch.bfloat16, (*lead, m, n), index):
-        _need(d, "d", torch.bfloat16, len(shape_a), _device(index))
-        raise ValueError(f"d must have shape {(*lead, m, n)}, got {tuple(d.shape)}")
+    _want(d, "d", torch.bfloat16, (*lead, m, n), index)
     args = (a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), d.data_ptr())
     if rows is None:
         args += (m, n, k)
@@ -456,9 +463,7 @@ def _fp4_gemm(name, a, sfa, b, sfb, d, rows=None, masked=False):
         g = shape_b[0]
         if masked and lead != [g]:
             raise ValueError("a and b differ in groups")
-        if not _is(rows, _I32, (m if name.endswith("contiguous") else g,), index):
-            _need(rows, "the layout's rows", _I32, 1, _device(index))
-            raise ValueError("the layout's rows have the wrong length")
+        _want(rows, "the layout's rows", _I32, (m if name.endswith("contiguous") else g,), index)
         args += (rows.data_ptr(), g, m, n, k) if masked else (rows.data_ptr(), m, n, k, g)
     if d.numel():  # else nothing to compute, and empty tensors have no address
         _call(name, index, *args)
@@ -519,9 +524,7 @@ def dequantize_fp4(q, sf, x) -> torch.Tensor:
     for, into x [M, K] (or [G, M, K]) bfloat16."""
     index, shape = _codes_of(q, "q", 3 if isinstance(q, torch.Tensor) and q.dim() == 3 else 2)
     _want_fp4(q, sf, "q", shape, index)
-    if not _is(x, torch.bfloat16, shape, index):
-        _need(x, "x", torch.bfloat16, len(shape), _device(index))
-        raise ValueError(f"x must have shape {shape}, got {tuple(x.shape)}")
+    _want(x, "x", torch.bfloat16, shape, index)
     _call("dg_dequantize_fp4", index, q.data_ptr(), sf.data_ptr(), x.data_ptr(), shape[0] if len(shape) == 3 else 1,
           *shape[-2:])
     return x

@@ -31,7 +31,8 @@ from typing import Optional
 import torch
 
 from . import dg
-from .dg import DGError, _check, _current_device, _int32, _int32s, _need  # noqa: F401  (DGError: what a failed call raises)
+from .dg import _device, _int32, _int32s, _need, _want
+from .dg import DGError, _current_device, _raw_stream  # noqa: F401  (what a failed call raises; what _call() looks up here)
 
 _LAYOUTS = {"dense": 0, "contiguous": 1, "masked": 2, "nopad": 3}
 _BF16, _F32, _I32, _FP8 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
@@ -90,38 +91,7 @@ def _ptr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
 
-# The handle of a device's current stream: a decode step's calls take a few
-# microseconds each, of which torch.cuda.current_stream(...).cuda_stream, which
-# builds a Stream object first, took 1.9 (this: 0.1).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _stream(index: int) -> int:
-    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
-
-
-def _call(name: str, index: int, *args) -> None:
-    """Calls an entry point on device `index`'s current stream, with that device
-    current: the handle of a default stream is 0 on every device."""
-    if _current_device() == index:
-        status = getattr(lib(), name)(*args, _stream(index))
-    else:
-        with torch.cuda.device(index):
-            status = getattr(lib(), name)(*args, _stream(index))
-    if status:
-        _check(status, name)
-
-
-def _want(t: torch.Tensor, name: str, dtype, shape, index: int) -> None:
-    """As dg._need, with the whole shape and the device by its index (the
-    cheapest way to ask: get_device() is -1 on the host)."""
-    try:
-        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
-            return
-    except AttributeError:
-        pass
-    _need(t, name, dtype, len(shape), _device(index))
-    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+_call = dg._caller(globals())
 
 
 def _optional(index: int, dtype, shape, **tensors) -> None:
@@ -134,10 +104,6 @@ def _optional(index: int, dtype, shape, **tensors) -> None:
             except AttributeError:
                 pass
             _want(t, name, dtype, shape, index)
-
-
-def _device(index: int) -> torch.device:
-    return torch.device("cuda", index) if index >= 0 else torch.device("cpu")
 
 
 def _first(t: torch.Tensor, name: str, dtype, ndim: int) -> int:
