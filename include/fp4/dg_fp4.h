@@ -63,7 +63,10 @@ dg_status dg_m_grouped_fp4_gemm_nt_nopad(const void* a, const uint32_t* sfa,
  *      words, both as the GEMMs take them (groups = 1: one operand)
  * Per 32 values the scale is the smallest power of two that is not below
  * amax / 6, so that nothing saturates, and at least 2^-127; codes are
- * e2m1(x / scale), rounded to nearest, ties to the even code. An infinity or a NaN
+ * e2m1(x / scale), rounded to nearest, ties to the even code. (The conversion that the
+ * microscaling text itself gives takes 2^(floor(log2 amax) - 2): half this scale where
+ * amax is above 1.5 times its power of two, values above 6 times that cut to it. Its codes
+ * differ there; the products take either.) An infinity or a NaN
  * makes its block's scale NaN, and with it all of its 32 values. Words past
  * the last row are not written. Read back, a value is exact, but for one past
  * BF16's largest, which becomes infinite (a value from 1.75 2^127 on rounds up to

@@ -503,7 +503,9 @@ def m_grouped_fp4_gemm_nt_nopad(a, sfa, b, sfb, d, group_rows) -> torch.Tensor:
 def quantize_fp4(x, q, sf):
     """Rows x [M, K] (or [G, M, K]) bfloat16 or float32 to an FP4 GEMM operand:
     q [M, K/2] uint8 and sf [K/128, tma_aligned(M)] int32 (or with the leading G).
-    Per 32 values one scale, the smallest power of two not below amax / 6; codes
+    Per 32 values one scale, the smallest power of two not below amax / 6 (nothing
+    saturates; where amax is above 1.5 times its power of two that is twice the
+    scale 2^(floor(log2 amax) - 2) of an encoder that lets values saturate); codes
     round to the nearest value, ties to the even code. An infinity or NaN makes its
     32 values NaN. Words of sf past the last row are not written."""
     if not isinstance(x, torch.Tensor) or not isinstance(q, torch.Tensor):
