@@ -165,6 +165,19 @@ def test_swiglu_fp4_special_values(dev):
     _glu(dev, ("dense", 1, 9, inner), gu)
 
 
+def test_swiglu_fp4_next_to_overflow(dev):
+    """Gates and ups whose product is 2^128 (1 - 1.1e-7), the largest below float32's overflow of all BF16 pairs
+    and finite, 2^128 (1 - 1.3e-14) and 2^128, which round to infinity, and 2^128 (1 + 6e-6)."""
+    _say("swiglu_fp4 next to overflow")
+    inner = 256
+    gu = _randn(8, 2 * inner, seed=52)
+    for row, (g, u) in enumerate(((16.0, 2.0 ** 124), (32.0, 2.0 ** 123), (2.0 ** 64, 2.0 ** 64), (5.96875, 1.34375 * 2.0 ** 125))):
+        for i, sign in ((row, 1.0), (row + 4, -1.0)):
+            gu[i, 40], gu[i, inner + 40] = g, sign * u
+            gu[i, 200], gu[i, inner + 200] = g, sign * u / 2
+    _glu(dev, ("dense", 1, 8, inner), gu)
+
+
 def test_offsets_past_32_bits(dev):
     """Rows and values past 2^31: the last ones."""
     _say("fp4 offsets past 32 bits")
