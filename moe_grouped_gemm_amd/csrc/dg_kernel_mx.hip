@@ -25,13 +25,13 @@
 // more of either operand for a product, and four waves of 128 x 128 (a third fewer LDS
 // reads) took 6% more.
 //
-// What bounds it (16384 x 4096 x 7168 in 221 us, 4.35 PFLOP/s): matrix cores and
+// What bounds it (16384 x 4096 x 7168 in 215 us, 4.48 PFLOP/s): matrix cores and
 // LDS reads alone take 147 us (6.5 PFLOP/s; a loop of these MFMAs alone, with operands
 // of random bits, 7.3: they draw the power), a stream of operands that all hit the L1
 // 25 us more, from L2 another 26 (its misses 5 of them), the stores 18. 4096 x 7168 x
-// 2048 (43 us) is two rounds of 224 tiles of 256 possible and 10 us of stores. With
-// few rows (16 groups of up to 32 rows, 7168 x 2048, 25 us) reading B bounds it, at 4.9
-// TB/s.
+// 2048 (37 to 40 us by the inputs' power) is two rounds of 224 tiles of 256 possible and
+// 10 us of stores. With few rows (16 groups of up to 32 rows, 7168 x 2048, 28 us a call)
+// reading B bounds it, at 4.4 TB/s.
 
 #include <algorithm>
 
@@ -307,8 +307,8 @@ __device__ __forceinline__ void store_band(uint16_t* rows, int n, uint32_t valid
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const int row = (r & 7) + 8 * half;
-    // Past the caches' reach: the operands stay there (4096 x 7168 x 2048: 43 us, with
-    // plain stores 46; the masked decode 39 and 41).
+    // Past the caches' reach: the operands stay there (4096 x 7168 x 2048: 40 us, with
+    // plain stores 42; 16 masked groups of up to 256 x 7168 x 2048 43 and 46).
     if ((valid >> row) & 1)
       __builtin_nontemporal_store(out[half], (global_i32x4*)(rows + (size_t)row * n + 32 * (r >> 3) + 8 * q));
   }
@@ -344,7 +344,7 @@ __device__ __forceinline__ void store_tile(const GemmArgs& p, const TileRef& cur
 //              i + 1 as soon as its last MFMA of step i has issued, then the next step's
 //              first A fragments and its scales; HIGH's refill is issued.
 // So every load has a step and a half to land. (One barrier a step, at band 6, gave it
-// 0.6 to 1 step, and took 229 us where this takes 221 for 16384 x 4096 x 7168.)
+// 0.6 to 1 step, and took 3.6% more for 16384 x 4096 x 7168.)
 // Only bands below NB are computed (the rows of the others are not stored).
 template <class C, int KIND, int PHASE, int NB>
 __device__ __forceinline__ void mainloop(const GemmArgs& p, const TileSrc& t0, const TileSrc& t1, const TileSrc& t2,
@@ -450,8 +450,8 @@ __device__ __forceinline__ void mainloop(const GemmArgs& p, const TileSrc& t0, c
 
 // A wave whose valid rows lie in its first HALF_BANDS bands runs a copy of the K loop
 // without the other bands' MFMAs (their rows are never stored). 32 groups of up to 64
-// rows, 4096 x 7168: 97 us, without the copy 112; 16 groups of up to 256 rows, 7168 x
-// 2048: 40 with either.
+// rows, 4096 x 7168: 90 us, without the copy 96; 16 groups of up to 256 rows, 7168 x
+// 2048: 43 with either.
 constexpr int HALF_BANDS = 4;
 
 template <class C, int KIND>

@@ -21,7 +21,7 @@
 // steps are on their way, so the tokens' or activations' bytes (16 tokens: half the
 // weights' in the first launch, twice as many in the second) and the processors' turns
 // add to the weights' time. An FP8 batch, 61 tokens and 32 experts of 7168 x 2048:
-// 186 us (5.1 TB/s of weights) and 129 (3.6); weights alone 164 and 79, and the second
+// 183 us (5.1 TB/s of weights) and 129 (3.7); weights alone 164 and 79, and the second
 // launch 102 with activations of one BF16 value. One token, eight experts in FP4: 28 and 18
 // us, of which about 5 each are a launch's lists of who is where, one read from memory
 // after the other.
@@ -870,8 +870,8 @@ hipError_t launch_down(const ExpertsArgs& a, hipStream_t stream) {
 
 // How many workgroups of the second launch share the experts of their columns: as many as
 // there is room for, while each wave keeps eight steps. Whole layers, in us, with and
-// without: 57 tokens, 82 experts of 1536 x 1536 in FP8 149, 197; 8 tokens, 43 experts of
-// 768 x 1664 in FP4 27, 39; 5 tokens, 26 experts of 512 x 896 in FP8 20, 26. (Not by the
+// without: 57 tokens, 82 experts of 1536 x 1536 in FP8 135, 175; 8 tokens, 43 experts of
+// 768 x 1664 in FP4 38, 56; 5 tokens, 26 experts of 512 x 896 in FP8 25, 33. (Not by the
 // compute units that are set: the order of the sums differs.)
 int down_splits(const ExpertsArgs& a) {
   const int experts = std::min(a.tokens * a.top_k, a.num_groups), steps = a.inner / (a.fp4 ? 2 * QBLOCK : QBLOCK);
