@@ -198,6 +198,23 @@ def test_activations_of_more_bits_than_bf16_has(dev, t, k, g, hidden, inner, fp4
 
 
 @pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("t,k,g", [(9, 2, 24), (16, 1, 17), (17, 4, 70), (24, 2, 48), (33, 2, 96), (128, 1, 128)])
+def test_many_tokens_of_an_expert_among_more_experts_than_slots(dev, t, k, g, fp4):
+    """Tiles of activations known by their first pairs' slots, several an expert."""
+    _say(f"experts, crowded: {(t, k, g)} fp4={fp4}")
+    hidden, inner = 256, 256
+    x, sent, v1, v2 = _exact_layer(fp4, t, g, hidden, inner, t, dev)
+    r = np.random.default_rng(t)
+    for crowd in (1, 2):
+        ids = np.asarray(r.choice(r.permutation(g)[:crowd], (t, k)), np.int32)
+        ids[:, 1:][r.random((t, k - 1)) < 0.3] = -1
+        w = r.choice([0.25, 0.5, 1.0, -2.0], (t, k))
+        y = _run(x, ids, torch.from_numpy(w).float().to(dev), *sent, dev)
+        ref = _exact(x.double().cpu().numpy(), ids, w, v1, v2)
+        np.testing.assert_array_equal(y.view(torch.int16).cpu().numpy().view(np.uint16), O.bf16_bits(ref))
+
+
+@pytest.mark.parametrize("fp4", [False, True])
 @pytest.mark.parametrize("t", [1, 6, 20])
 def test_infinite_activations_stay_infinite(dev, t, fp4):
     """An activation past float32's range is infinite, with nothing left over beside it: so are
