@@ -72,8 +72,8 @@ static_assert(sizeof(ExpertPlan) == EXPERT_PLAN_BYTES, "room for the plan");
 // ---------------------------------------------------------------------------
 
 // A value is held as the sum of two in BF16, float32's upper 16 bits and what those leave
-// out, which is good to 2^-16 of it (one BF16 value, 2^-8 of it, would double the
-// layer's error). The second products multiply the two side by side, as neighbouring
+// out, which is good to 2^-16 of it (with one BF16 value, good to 2^-8, the layer's error
+// was 0.0023 in the 2-norm, where y's own rounding makes 0.0017). The second products multiply the two side by side, as neighbouring
 // columns of a token operand: a tile is one expert's up to 8 tokens.
 //
 // Tiles lie in the order in which the second launch's lanes load them, 16 bytes each: block
@@ -616,14 +616,14 @@ template <bool FP4, int TOKENS, int MOST, int NT, int RT>
 __global__ __launch_bounds__(DOWN_THREADS, 1) void experts_down_kernel(ExpertsArgs p) {
   constexpr int STRIDE = 16 * RT + (MOST > 64 ? 0 : 4);  // floats; 4 past a power of two where there is room
   constexpr int DEPTH = DOWN_DEPTH<FP4, NT>, W = DownWeights<FP4, RT>::LOADS, STEP = DownWeights<FP4, RT>::BYTES;
-  // (loads of activations: at least one tile's)
+  // Loads of activations in a step: at least one tile's.
   constexpr int BLOCKS = DownWeights<FP4, RT>::BLOCKS, ACT_LOADS = 4 * BLOCKS;
   __shared__ __attribute__((aligned(1024))) uint8_t rings[DOWN_WAVES * DEPTH * STEP];
   __shared__ __attribute__((aligned(16))) float sums[DOWN_WAVES * MOST * STRIDE];
   // Of the pairs; read from memory in the loop, they would be waited for with all the
   // weights that are on their way.
   __shared__ DownItem items[MAX_FEW_PAIRS];
-  __shared__ uint16_t slots[MAX_FEW_PAIRS];     // the pair's slot,
+  __shared__ uint16_t slots[MAX_FEW_PAIRS];    // the pair's slot,
   __shared__ uint16_t sums_at[MAX_FEW_PAIRS];  // where its token's sums are, in 16 bytes
   __shared__ float pair_weights[MAX_FEW_PAIRS];
   __shared__ int items_of[DOWN_WAVES];
